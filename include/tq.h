@@ -63,6 +63,12 @@
  *     kb c), 2 kb d bytes, followed by KSM; with key_bits 16 KQ holds the
  *     fp16 keys (32 d bytes) and there is no KSM.  VI is a dense vb-bit
  *     stream per token, 2 vb d bytes.  tq_config_check gives the size.
+ *
+ * Dense layout (uncompressed or 8-bit float pages, for the layers a model keeps
+ * out of the compression; read by tq_paged_attention):
+ *   16-bit tile, 64 d bytes: keys [16][d], then values [16][d], fp16 or bf16;
+ *   8-bit tile, 32 d + 32 bytes: key codes [16][d], value codes [16][d] (e4m3), then
+ *     int8 exponents of the 16 keys and of the 16 values: entry = code * 2^exponent.
  */
 #ifndef TQ_H_
 #define TQ_H_
@@ -83,7 +89,7 @@ typedef enum {
   TQ_ERR_CUDA = 4         /* a CUDA runtime call or launch failed */
 } tq_status;
 
-typedef enum { TQ_LAYOUT_MAIN = 0, TQ_LAYOUT_ALT = 1 } tq_layout;
+typedef enum { TQ_LAYOUT_MAIN = 0, TQ_LAYOUT_ALT = 1, TQ_LAYOUT_DENSE = 2 } tq_layout;
 
 /* Device error word bits (tq_get_device_errors). */
 #define TQ_DEVERR_BLOCK_ID   0x1u /* block-table entry outside [0, num_blocks) */
@@ -92,6 +98,8 @@ typedef enum { TQ_LAYOUT_MAIN = 0, TQ_LAYOUT_ALT = 1 } tq_layout;
 #define TQ_DEVERR_CHUNKS     0x8u /* n_compressed larger than the max_ctx given to decode */
 #define TQ_DEVERR_TIMEOUT    0x10u /* a decode CTA gave up waiting (about a second) for its own
                                       copies or tensor-core products; its output rows are not written */
+#define TQ_DEVERR_PAGES      0x20u /* tq_plan_pages: a request did not fit the free pages or the token
+                                      buffer, or the queue's state or room was not valid */
 
 /* Decode kernels for the main layout at head_dim 128 (tq_set_decode_path). */
 #define TQ_DECODE_AUTO     0 /* the library chooses per call (default) */
@@ -119,9 +127,16 @@ typedef struct {
   int qjl_m;         /* main: sketch rows m, must equal head_dim; alt: 0 */
   uint64_t seed;     /* table seed; one table set per layer (base seed + layer) */
   int key_format;    /* alt layout, 2-bit keys: TQ_KEY_AFFINE (0, default: uint2, min/max affine codes)
-                        or TQ_KEY_SIGNED (1: int2, signed symmetric mid-rise codes, see below); must
-                        be 0 otherwise */
+                        or TQ_KEY_SIGNED (1: int2, signed symmetric mid-rise codes, see below); dense
+                        layout: TQ_ELEM_F16 (0, default) or TQ_ELEM_BF16 (1); must be 0 otherwise */
 } tq_config;
+
+/* Dense layout: key_bits = value_bits = 16 (default; pages hold the elements as they are) or 8 (pages
+ * hold e4m3 codes with one power-of-two exponent per token, KV head and side).  key_format is the
+ * 16-bit type of the queries, of the stored keys and values handed in, and of 16-bit pages.  Any
+ * num_q_heads / num_kv_heads ratio is accepted; the seed is not used. */
+#define TQ_ELEM_F16 0
+#define TQ_ELEM_BF16 1
 
 /* Key formats of the alternate layout at key_bits 2 (the vllm-metal guide lists int2 and uint2,
  * with the same bytes; the pages give no rule that tells them apart, so this library reads them as):
@@ -151,7 +166,7 @@ typedef struct {
 /* Human-readable name of a status code (static string). */
 const char* tq_status_string(tq_status s);
 
-/* Fill *cfg with the main (key_bits 3 / value_bits 2) or alternate (8 / 3)
+/* Fill *cfg with the main (key_bits 3 / value_bits 2), alternate (8 / 3) or dense (16 / 16)
  * layout defaults: page 16, ring 128, group 32, qjl_m = head_dim (main).
  * key_bits / value_bits may be changed afterwards within the ranges above. */
 tq_status tq_config_init(tq_config* cfg, int layout, int head_dim, int num_q_heads, int num_kv_heads,
@@ -342,6 +357,84 @@ tq_status tq_dequantize_bf16(tq_ctx* ctx, const void* pool, int num_blocks, cons
  * Returns 1 (materialise), 0 (stay compressed) or -1 (negative counts, head_dim or heads <= 0). */
 int tq_should_materialize(int64_t history_tokens, int64_t query_tokens, int head_dim, int num_kv_heads,
                           int64_t max_mib);
+
+/* ------------------------------------------------------------------ page plan and dense pages */
+
+/* Block tables and slot maps of one serving step, from the requests' lengths, in one launch: takes
+ * pages from a queue of free pages for the tokens that each request adds, and gives the pages of
+ * requests that have ended back to it.  Serves every layout; ctx only carries the device error word.
+ *   ctx_len       device int32 [batch]: tokens that request b has cached before the step
+ *   new_len       device int32 [batch]: tokens it adds, 0 or more; negative: the request has ended
+ *   ring_capacity 0: all of a request's L tokens live in pages, ceil(L / 16) of them.
+ *                 128: the newest stay in an exact ring (see tq_append_token) and pages hold
+ *                 the first 128 * ((L - 1) / 128)
+ *   block_table   device int32 [batch][max_blocks], updated in place: entries
+ *                 pages(ctx_len) .. pages(ctx_len + new_len) - 1 of a row are written, the others kept
+ *   queue         device int32 [queue_cap]: ids of free pages, a circular queue; queue_state
+ *                 device int32 [2]: {index of the first free page, number of free pages}
+ *   lengths       out, device int32 [batch]: ctx_len + new_len, or 0 for an ended request
+ *   n_paged, n_ring  out, device int32 [batch], NULL to skip: the tokens of `lengths` in pages and
+ *                 in the ring (n_compressed and n_buf of tq_decode_attention)
+ *   token_start   out, device int32 [batch + 1]: the new tokens of request b are entries
+ *                 token_start[b] .. token_start[b + 1] - 1 of the step's token buffer
+ *   slots         out, device int64 [max_tokens]: block * 16 + position % 16 of each new token,
+ *                 -1 for one that has no page (it is in the ring, or its request was refused)
+ *                 and for entries behind the last token
+ *   positions, rows  out, device int32 [max_tokens], NULL to skip: position and request of each
+ *                 new token, -1 behind the last
+ *   queue_state_out  out, device int32 [2]: the queue after the step
+ * Free pages go to the requests in order, from the queue's front; the pages of ended requests are
+ * appended behind the queue's end in order and are not handed out in the same step.  A request that
+ * finds too few free pages, or whose tokens pass max_tokens, is refused with TQ_DEVERR_PAGES, and
+ * one whose pages pass max_blocks with TQ_DEVERR_POSITION: its lengths entry stays ctx_len (0 if that
+ * is negative), its row and the queue stay as they were, its tokens get slot -1; later requests
+ * that need no page are still served.  A free page id outside [0, num_blocks) becomes
+ * table entry -1 and slots -1 with TQ_DEVERR_BLOCK_ID.  The total of new tokens must be below 2^31.
+ * Outputs must not overlap inputs (block_table and queue, updated in place, apart) or one another. */
+tq_status tq_plan_pages(tq_ctx* ctx, const int32_t* ctx_len, const int32_t* new_len, int batch, int ring_capacity,
+                        int32_t* block_table, int max_blocks, int num_blocks, int32_t* queue, int queue_cap,
+                        const int32_t* queue_state, int32_t* lengths, int32_t* n_paged, int32_t* n_ring,
+                        int32_t* token_start, int64_t* slots, int32_t* positions, int32_t* rows, int max_tokens,
+                        int32_t* queue_state_out, cudaStream_t stream);
+
+/* Write keys and values into the pages of a dense-layout context.
+ *   k, v   device [n_tokens][Hkv][d] of the context's 16-bit type, 16-byte aligned; k_stride and v_stride
+ *          elements apart from token to token (at least Hkv * d, a multiple of 8)
+ *   slots  device int64 [n_tokens]: block * 16 + position % 16 (tq_plan_pages); negative: the token is skipped
+ *   pool   device uint8 [num_blocks][Hkv][tq_page_bytes()], 16-byte aligned
+ * 16-bit pages take the elements unchanged.  8-bit pages take, per token and KV head and for keys and
+ * values apart, e = the least whole number with max|x| <= 448 * 2^e over the finite entries (at least
+ * -120, also for a vector of zeros) and the codes e4m3(x * 2^-e), rounded to nearest even; infinities become
+ * +-448 * 2^e and NaN stays NaN.  A slot outside the pool is skipped with TQ_DEVERR_BLOCK_ID.  Slots
+ * must differ from one another: what a slot named twice holds afterwards is not defined. */
+tq_status tq_paged_store(tq_ctx* ctx, const void* k, const void* v, int64_t k_stride, int64_t v_stride,
+                         const int64_t* slots, int n_tokens, void* pool, int num_blocks, cudaStream_t stream);
+
+/* Workspace bytes of tq_paged_attention for `batch` sequences of any length. */
+tq_status tq_paged_workspace_size(const tq_ctx* ctx, int batch, size_t* bytes);
+
+/* Attention of one new token per sequence over dense-layout pages: for query head h of sequence b,
+ *   out = sum_p softmax_p(scale * q . k_p) v_p over max(0, L - window) <= p < L, L = lengths[b],
+ * the new token itself (stored before the call) being position L - 1.
+ *   q        device [batch][Hq][d] of the context's 16-bit type, 16-byte aligned; q_stride elements
+ *            apart from sequence to sequence (at least Hq * d, a multiple of 8)
+ *   lengths  device int32 [batch]; block_table device int32 [batch][max_blocks]; pool as written by
+ *            tq_paged_store.  Page entries and rows outside the sum are not read into the result,
+ *            whatever they hold
+ *   window   0: all positions; otherwise the newest `window` of them
+ *   scale    0: 1 / sqrt(d); otherwise any finite number
+ *   out      device float32 [batch][Hq][d], 16-byte aligned
+ *   lse      device float32 [batch][Hq] or NULL: ln sum_p exp(scale * q . k_p)
+ *   workspace  device scratch of at least tq_paged_workspace_size(batch) bytes, 256-byte aligned;
+ *            calls that can overlap on the GPU need one each
+ * An empty sequence gets a row of zeros and lse -inf.  A length that is negative or beyond the block
+ * table counts as 0 with TQ_DEVERR_POSITION; a page whose id is outside [0, num_blocks) is left out of
+ * the sums with TQ_DEVERR_BLOCK_ID.  num_blocks * Hkv must be below 2^31.  The current device
+ * must be the context's (TQ_ERR_INVALID_ARG), here and in the two calls above. */
+tq_status tq_paged_attention(tq_ctx* ctx, const void* q, int64_t q_stride, int batch, const void* pool, int num_blocks,
+                             const int32_t* block_table, int max_blocks, const int32_t* lengths, int window,
+                             float scale, float* out, float* lse, void* workspace, size_t ws_bytes,
+                             cudaStream_t stream);
 
 /* ------------------------------------------------------------------ bit packing */
 

@@ -17,10 +17,12 @@ _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libtq.so")
 
 TQ_OK, TQ_ERR_INVALID_ARG, TQ_ERR_UNSUPPORTED, TQ_ERR_WORKSPACE, TQ_ERR_CUDA = range(5)
-TQ_LAYOUT_MAIN, TQ_LAYOUT_ALT = 0, 1
+TQ_LAYOUT_MAIN, TQ_LAYOUT_ALT, TQ_LAYOUT_DENSE = 0, 1, 2
 TQ_DEVERR_BLOCK_ID, TQ_DEVERR_POSITION, TQ_DEVERR_RING, TQ_DEVERR_CHUNKS, TQ_DEVERR_TIMEOUT = 1, 2, 4, 8, 16
+TQ_DEVERR_PAGES = 32
 TQ_DECODE_AUTO, TQ_DECODE_MMA_SYNC, TQ_DECODE_TCGEN05 = 0, 1, 2
 TQ_KEY_AFFINE, TQ_KEY_SIGNED = 0, 1
+TQ_ELEM_F16, TQ_ELEM_BF16 = 0, 1
 
 
 class TQError(RuntimeError):
@@ -86,6 +88,11 @@ _SIGS = {
     "tq_decode_attention_static": (_i, [_vp, _vp, _i, _vp, _i, _vp, _i, _vp, _vp, _vp, _vp, _i, _vp, _vp]),
     "tq_dequantize": (_i, [_vp, _vp, _i, _vp, _i, _vp, _vp, _vp, _vp, _i, _i, _vp, _vp, _vp]),
     "tq_dequantize_bf16": (_i, [_vp, _vp, _i, _vp, _i, _vp, _vp, _vp, _vp, _i, _i, _vp, _vp, _vp]),
+    "tq_plan_pages": (_i, [_vp, _vp, _vp, _i, _i, _vp, _i, _i, _vp, _i, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i,
+                           _vp, _vp]),
+    "tq_paged_store": (_i, [_vp, _vp, _vp, _i64, _i64, _vp, _i, _vp, _i, _vp]),
+    "tq_paged_workspace_size": (_i, [_vp, _i, C.POINTER(_sz)]),
+    "tq_paged_attention": (_i, [_vp, _vp, _i64, _i, _vp, _i, _vp, _i, _vp, _i, C.c_float, _vp, _vp, _vp, _sz, _vp]),
     "tq_should_materialize": (_i, [_i64, _i64, _i, _i, _i64]),
     "tq_pack": (_i, [_vp, _i64, _i, _vp, _vp]),
     "tq_unpack": (_i, [_vp, _i64, _i, _vp, _vp]),
@@ -213,11 +220,11 @@ class Context:
                  centroids=None, signs=None, sketch=None, value_bits=None, key_bits=None, key_format=None):
         self.cfg = tq_config_init(layout, head_dim, num_q_heads, num_kv_heads, seed)
         if value_bits is not None:
-            self.cfg.value_bits = value_bits  # main layout: 2 or 4; alternate layout: 2, 3 or 4
+            self.cfg.value_bits = value_bits  # main layout: 2 or 4; alternate layout: 2, 3 or 4; dense: 16 or 8
         if key_bits is not None:
-            self.cfg.key_bits = key_bits  # main layout: 3, 2 or 4; alternate layout: 8, 5, 4, 2 or 16 (fp16 keys)
+            self.cfg.key_bits = key_bits  # main layout: 3, 2 or 4; alternate layout: 8, 5, 4, 2 or 16 (fp16 keys); dense: 16 or 8
         if key_format is not None:
-            self.cfg.key_format = key_format  # alternate layout, 2-bit keys: TQ_KEY_AFFINE (uint2) or TQ_KEY_SIGNED (int2)
+            self.cfg.key_format = key_format  # alternate layout, 2-bit keys: TQ_KEY_AFFINE (uint2) or TQ_KEY_SIGNED (int2); dense: TQ_ELEM_F16 or TQ_ELEM_BF16
         ptr = C.c_void_p()
         if centroids is None:
             _check(lib.tq_create(C.byref(self.cfg), C.byref(ptr)), "tq_create")
@@ -233,6 +240,9 @@ class Context:
         self.head_dim = head_dim
         self.num_q_heads = num_q_heads
         self.num_kv_heads = num_kv_heads
+        import torch
+
+        self._device = torch.device("cuda", torch.cuda.current_device())  # tq_create used the current device
 
     def close(self):
         if getattr(self, "ptr", None) and self.ptr.value:
@@ -387,6 +397,93 @@ class Context:
                   _dev(n_buf, torch.int32, "n_buf"), bsz, k_out.shape[2],
                   _dev(k_out, k_out.dtype, "k_out"), _dev(v_out, v_out.dtype, "v_out"),
                   _stream(stream)), name)
+
+    # -- page plan and dense pages
+    def _on_device(self, *tensors):
+        """Every tensor (None apart) is on the device that was current when the context was made."""
+        for t in tensors:
+            if t is not None and t.device != self._device:
+                raise ValueError(f"tensors must be on {self._device}, got {t.device}")
+
+    def _elem(self):
+        import torch
+
+        return torch.bfloat16 if self.cfg.key_format == TQ_ELEM_BF16 else torch.float16
+
+    def plan_pages(self, ctx_len, new_len, block_table, queue, queue_state, lengths, token_start, slots, queue_state_out,
+                   num_blocks, positions=None, rows=None, n_paged=None, n_ring=None, ring_capacity=0, stream=None):
+        """tq_plan_pages: block tables, slot maps and the free-page queue of one step.  ctx_len, new_len, lengths,
+        n_paged, n_ring int32 [B]; block_table int32 [B, max_blocks]; queue int32 [cap]; queue_state, queue_state_out
+        int32 [2]; token_start int32 [B + 1]; slots int64 [max_tokens]; positions, rows int32 [max_tokens]."""
+        import torch
+
+        bsz, i32 = ctx_len.numel(), torch.int32
+        self._check_bt(block_table, bsz)
+        if any(t is not None and t.numel() != bsz for t in (new_len, lengths, n_paged, n_ring)):
+            raise ValueError("new_len, lengths, n_paged and n_ring must be [batch]")
+        if queue_state.numel() != 2 or queue_state_out.numel() != 2 or token_start.numel() != bsz + 1:
+            raise ValueError("queue_state and queue_state_out must be [2] and token_start [batch + 1]")
+        n = slots.numel()
+        if any(t is not None and t.numel() != n for t in (positions, rows)):
+            raise ValueError("positions and rows must be [max_tokens], like slots")
+        self._on_device(ctx_len, new_len, block_table, queue, queue_state, lengths, token_start, slots, queue_state_out,
+                        positions, rows, n_paged, n_ring)
+        _check(lib.tq_plan_pages(self.ptr, _dev(ctx_len, i32, "ctx_len"), _dev(new_len, i32, "new_len"), bsz, ring_capacity,
+                                 _dev(block_table, i32, "block_table"), block_table.shape[1], num_blocks,
+                                 _dev(queue, i32, "queue"), queue.numel(), _dev(queue_state, i32, "queue_state"),
+                                 _dev(lengths, i32, "lengths"), _dev(n_paged, i32, "n_paged"), _dev(n_ring, i32, "n_ring"),
+                                 _dev(token_start, i32, "token_start"), _dev(slots, torch.int64, "slots"),
+                                 _dev(positions, i32, "positions"), _dev(rows, i32, "rows"), n,
+                                 _dev(queue_state_out, i32, "queue_state_out"), _stream(stream)), "tq_plan_pages")
+
+    def _rows_of(self, t, heads, name):
+        """Data pointer and row stride of t [n, heads, d]: each row whole, rows any multiple of 8 elements apart."""
+        n, d = t.shape[0], self.head_dim
+        if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != d or t.dtype != self._elem():
+            raise ValueError(f"{name} must be {self._elem()} [n, {heads}, {d}]")
+        if not t.is_cuda:
+            raise ValueError(f"{name} must be a CUDA tensor")
+        if t.stride(2) != 1 or (heads > 1 and t.stride(1) != d):
+            raise ValueError(f"{name}: the heads of a row must be contiguous")
+        return t.data_ptr(), t.stride(0) if n > 1 else heads * d
+
+    def paged_store(self, k, v, slots, pool, stream=None):
+        """tq_paged_store: k, v [n_tokens, Hkv, d] of the context's 16-bit type (rows may be strided) into the pages;
+        slots int64 [n_tokens], negative to skip a token."""
+        import torch
+
+        kp, ks = self._rows_of(k, self.num_kv_heads, "k")
+        vp, vs = self._rows_of(v, self.num_kv_heads, "v")
+        if v.shape[0] != k.shape[0] or slots.numel() != k.shape[0]:
+            raise ValueError("k, v must be [n_tokens, Hkv, d] and slots [n_tokens]")
+        self._check_pool(pool)
+        self._on_device(k, v, slots, pool)
+        _check(lib.tq_paged_store(self.ptr, kp, vp, ks, vs, _dev(slots, torch.int64, "slots"), k.shape[0],
+                                  _dev(pool, torch.uint8, "pool"), pool.shape[0], _stream(stream)), "tq_paged_store")
+
+    def paged_workspace_size(self, batch: int) -> int:
+        n = C.c_size_t()
+        _check(lib.tq_paged_workspace_size(self.ptr, batch, C.byref(n)), "tq_paged_workspace_size")
+        return n.value
+
+    def paged_attention(self, q, pool, block_table, lengths, out, workspace, lse=None, window=0, scale=0.0, stream=None):
+        """tq_paged_attention: q [batch, Hq, d] of the context's 16-bit type (rows may be strided), out fp32
+        [batch, Hq, d], lse fp32 [batch, Hq] or None; window 0 for all positions, scale 0 for 1 / sqrt(d)."""
+        import torch
+
+        bsz = q.shape[0]
+        qp, qs = self._rows_of(q, self.num_q_heads, "q")
+        if out.shape != q.shape or lengths.numel() != bsz or (lse is not None and lse.shape != q.shape[:2]):
+            raise ValueError("out must be [batch, Hq, d], lengths [batch] and lse [batch, Hq]")
+        self._check_pool(pool)
+        self._check_bt(block_table, bsz)
+        self._on_device(q, pool, block_table, lengths, out, workspace, lse)
+        f32, i32 = torch.float32, torch.int32
+        _check(lib.tq_paged_attention(self.ptr, qp, qs, bsz, _dev(pool, torch.uint8, "pool"), pool.shape[0],
+                                      _dev(block_table, i32, "block_table"), block_table.shape[1],
+                                      _dev(lengths, i32, "lengths"), window, scale, _dev(out, f32, "out"),
+                                      _dev(lse, f32, "lse"), _dev(workspace, torch.uint8, "workspace"), workspace.numel(),
+                                      _stream(stream)), "tq_paged_attention")
 
     # -- diagnostics
     def device_errors(self, stream=None) -> int:

@@ -60,6 +60,7 @@ extern "C" tq_status tq_decode_attention_static(tq_ctx* ctx, const void* q, int 
                                                 const int32_t* n_buf, int max_ctx, float* out, cudaStream_t stream) {
   // the argument checks of tq_decode_attention, in its order, before the scratch size
   if (!ctx || batch < 0 || max_blocks < 0 || num_blocks < 0 || max_ctx < 0) return TQ_ERR_INVALID_ARG;
+  if (ctx->cfg.layout == TQ_LAYOUT_DENSE) return TQ_ERR_UNSUPPORTED;
   if (batch == 0) return TQ_OK;
   if (!q || !out || !n_compressed || !block_table || (max_ctx > 0 && !pool)) return TQ_ERR_INVALID_ARG;
   if (n_buf && (!ring_k || !ring_v)) return TQ_ERR_INVALID_ARG;

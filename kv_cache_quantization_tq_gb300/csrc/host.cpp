@@ -199,6 +199,12 @@ tq_status check_config(const tq_config* c) {
   if (!valid_dim(c->head_dim)) return TQ_ERR_UNSUPPORTED;
   if (c->page_size != tq::kPage || c->ring_capacity != tq::kRing || c->group_size != tq::kGroup)
     return TQ_ERR_UNSUPPORTED;
+  if (c->layout == TQ_LAYOUT_DENSE) {
+    if ((c->key_bits != 16 && c->key_bits != 8) || c->value_bits != c->key_bits || c->qjl_m != 0 ||
+        (c->key_format != TQ_ELEM_F16 && c->key_format != TQ_ELEM_BF16))
+      return TQ_ERR_UNSUPPORTED;
+    return TQ_OK;
+  }
   const int n_rep = c->num_q_heads / c->num_kv_heads;
   const int groups = (n_rep + tq::kMaxRep - 1) / tq::kMaxRep;
   if (n_rep % groups) return TQ_ERR_UNSUPPORTED;
@@ -226,7 +232,7 @@ tq_status finish_create(const tq_config* cfg, std::vector<float> cent, std::vect
   ctx->ncent = (int)cent.size();
   const int d = cfg->head_dim;
   ctx->h_centroids = cent;
-  ctx->h_boundaries.resize(cent.size() - 1);
+  ctx->h_boundaries.resize(cent.empty() ? 0 : cent.size() - 1);  // the dense layout has no tables
   for (size_t j = 0; j + 1 < cent.size(); ++j)
     ctx->h_boundaries[j] = (float)(0.5 * ((double)cent[j] + (double)cent[j + 1]));
   // kernel-parameter tables: codebooks of up to 16 entries; wider value codebooks (alternate layout,
@@ -237,9 +243,11 @@ tq_status finish_create(const tq_config* cfg, std::vector<float> cent, std::vect
   ctx->h_sketch = sketch;
   bool ok = cudaGetDevice(&ctx->device) == cudaSuccess;
   ok = ok && cudaDeviceGetAttribute(&ctx->sm_count, cudaDevAttrMultiProcessorCount, ctx->device) == cudaSuccess;
-  ok = ok && cudaMalloc(&ctx->d_signs, sizeof(float) * d) == cudaSuccess;
   ok = ok && cudaMalloc(&ctx->d_err, sizeof(uint32_t)) == cudaSuccess;
-  ok = ok && cudaMemcpy(ctx->d_signs, signs.data(), sizeof(float) * d, cudaMemcpyHostToDevice) == cudaSuccess;
+  if (cfg->layout != TQ_LAYOUT_DENSE) {
+    ok = ok && cudaMalloc(&ctx->d_signs, sizeof(float) * d) == cudaSuccess;
+    ok = ok && cudaMemcpy(ctx->d_signs, signs.data(), sizeof(float) * d, cudaMemcpyHostToDevice) == cudaSuccess;
+  }
   ok = ok && cudaMemset(ctx->d_err, 0, sizeof(uint32_t)) == cudaSuccess;
   if (ok && cfg->layout == TQ_LAYOUT_ALT) {
     // value codebook and its decision boundaries as device tables (up to 256 / 255 floats)
@@ -447,6 +455,10 @@ tq_status tq_config_init(tq_config* cfg, int layout, int head_dim, int num_q_hea
     cfg->key_bits = 3;
     cfg->value_bits = 2;
     cfg->qjl_m = head_dim;
+  } else if (layout == TQ_LAYOUT_DENSE) {
+    cfg->key_bits = 16;
+    cfg->value_bits = 16;
+    cfg->qjl_m = 0;
   } else {
     cfg->key_bits = 8;
     cfg->value_bits = 3;
@@ -471,6 +483,7 @@ tq_status tq_create(const tq_config* cfg, tq_ctx** out) {
   if (!out) return TQ_ERR_INVALID_ARG;
   tq_status st = check_config(cfg);
   if (st != TQ_OK) return st;
+  if (cfg->layout == TQ_LAYOUT_DENSE) return finish_create(cfg, {}, {}, {}, out);
   const int d = cfg->head_dim;
   // main: key_bits - 1 Lloyd-Max bits (one key bit is the QJL sign); alternate: value_bits
   const int bits = cfg->layout == TQ_LAYOUT_MAIN ? cfg->key_bits - 1 : cfg->value_bits;
@@ -488,6 +501,7 @@ tq_status tq_create_with_tables(const tq_config* cfg, const float* centroids, co
   if (!out || !centroids || !signs) return TQ_ERR_INVALID_ARG;
   tq_status st = check_config(cfg);
   if (st != TQ_OK) return st;
+  if (cfg->layout == TQ_LAYOUT_DENSE) return TQ_ERR_UNSUPPORTED;  // no tables to supply
   const int d = cfg->head_dim;
   const int k = 1 << (cfg->layout == TQ_LAYOUT_MAIN ? cfg->key_bits - 1 : cfg->value_bits);
   if (cfg->layout == TQ_LAYOUT_MAIN && !sketch) return TQ_ERR_INVALID_ARG;
@@ -522,6 +536,7 @@ void tq_destroy(tq_ctx* ctx) {
 
 tq_status tq_get_tables(const tq_ctx* ctx, float* centroids, float* boundaries, float* signs, float* sketch) {
   if (!ctx) return TQ_ERR_INVALID_ARG;
+  if (ctx->cfg.layout == TQ_LAYOUT_DENSE) return TQ_ERR_UNSUPPORTED;
   if (centroids) memcpy(centroids, ctx->h_centroids.data(), sizeof(float) * ctx->h_centroids.size());
   if (boundaries) memcpy(boundaries, ctx->h_boundaries.data(), sizeof(float) * ctx->h_boundaries.size());
   if (signs) memcpy(signs, ctx->h_signs.data(), sizeof(float) * ctx->h_signs.size());
@@ -532,9 +547,11 @@ tq_status tq_get_tables(const tq_ctx* ctx, float* centroids, float* boundaries, 
 namespace {
 // main: key_bits key bits, value_bits value bits and one fp16 scale + minimum per group of 32 per
 // coordinate, two fp16 norms; alternate: key_bits-bit key codes + 4 B per block of 32 (or fp16
-// keys alone, key_bits 16), value_bits-bit value indices, fp16 norm
+// keys alone, key_bits 16), value_bits-bit value indices, fp16 norm; dense: the elements and, with
+// 8 bits, two exponent bytes
 size_t record_bytes(const tq_config& c) {
   const size_t d = c.head_dim, vb = c.value_bits, kb = c.key_bits;
+  if (c.layout == TQ_LAYOUT_DENSE) return kb == 16 ? 4 * d : 2 * d + 2;
   return c.layout == TQ_LAYOUT_MAIN ? (kb * d) / 8 + (vb * d) / 8 + d / 8 + 4
                                     : (kb * d) / 8 + (kb == 16 ? 0 : (d / 32) * 4) + (vb * d) / 8 + 2;
 }
@@ -553,6 +570,7 @@ size_t tq_page_bytes(const tq_ctx* ctx) { return tq::kPage * tq_bytes_per_token_
 
 tq_status tq_workspace_size(const tq_ctx* ctx, int batch, int max_ctx, size_t* bytes) {
   if (!ctx || !bytes || batch < 0 || max_ctx < 0) return TQ_ERR_INVALID_ARG;
+  if (ctx->cfg.layout == TQ_LAYOUT_DENSE) return TQ_ERR_UNSUPPORTED;  // tq_paged_workspace_size
   *bytes = tq::decode_plan(ctx, batch, max_ctx).total;
   return TQ_OK;
 }
@@ -564,6 +582,7 @@ tq_status tq_encode_flush(tq_ctx* ctx, const void* k, const void* v, int batch, 
                           int num_blocks, cudaStream_t stream) {
   if (!ctx || batch < 0 || n_tokens < 0 || src_tokens < n_tokens || max_blocks < 0 || num_blocks < 0)
     return TQ_ERR_INVALID_ARG;
+  if (ctx->cfg.layout == TQ_LAYOUT_DENSE) return TQ_ERR_UNSUPPORTED;  // tq_paged_store writes dense pages
   if (n_tokens % tq::kPage) return TQ_ERR_INVALID_ARG;
   if (batch == 0 || n_tokens == 0) return TQ_OK;
   if (!k || !v || !start_pos || !block_table || !pool) return TQ_ERR_INVALID_ARG;
@@ -576,6 +595,7 @@ tq_status tq_append_token(tq_ctx* ctx, const void* k_new, const void* v_new, con
                           void* ring_k, void* ring_v, const int32_t* block_table, int max_blocks, void* pool,
                           int num_blocks, cudaStream_t stream) {
   if (!ctx || batch < 0 || max_blocks < 0 || num_blocks < 0) return TQ_ERR_INVALID_ARG;
+  if (ctx->cfg.layout == TQ_LAYOUT_DENSE) return TQ_ERR_UNSUPPORTED;
   if (batch == 0) return TQ_OK;
   if (!k_new || !v_new || !pos || !ring_k || !ring_v || !block_table || !pool) return TQ_ERR_INVALID_ARG;
   if ((((uintptr_t)ring_k) | ((uintptr_t)ring_v)) & 15) return TQ_ERR_INVALID_ARG;  // 16-byte row copies
@@ -588,6 +608,7 @@ tq_status tq_decode_attention(tq_ctx* ctx, const void* q, int batch, const void*
                               const void* ring_k, const void* ring_v, const int32_t* n_buf, int max_ctx,
                               float* out, void* workspace, size_t ws_bytes, cudaStream_t stream) {
   if (!ctx || batch < 0 || max_blocks < 0 || num_blocks < 0 || max_ctx < 0) return TQ_ERR_INVALID_ARG;
+  if (ctx->cfg.layout == TQ_LAYOUT_DENSE) return TQ_ERR_UNSUPPORTED;  // tq_paged_attention
   if (batch == 0) return TQ_OK;
   if (!q || !out || !n_compressed || !block_table || (max_ctx > 0 && !pool)) return TQ_ERR_INVALID_ARG;
   if (n_buf && (!ring_k || !ring_v)) return TQ_ERR_INVALID_ARG;
@@ -604,6 +625,7 @@ static tq_status dequantize_common(tq_ctx* ctx, const void* pool, int num_blocks
                                    const int32_t* n_buf, int batch, int max_tokens, void* k_out, void* v_out, bool bf16,
                                    cudaStream_t stream) {
   if (!ctx || batch < 0 || max_blocks < 0 || num_blocks < 0 || max_tokens < 0) return TQ_ERR_INVALID_ARG;
+  if (ctx->cfg.layout == TQ_LAYOUT_DENSE) return TQ_ERR_UNSUPPORTED;  // dense pages hold the elements already
   if (batch == 0 || max_tokens == 0) return TQ_OK;
   if (!k_out || !v_out || !n_compressed || !block_table || !pool) return TQ_ERR_INVALID_ARG;
   if (n_buf && (!ring_k || !ring_v)) return TQ_ERR_INVALID_ARG;

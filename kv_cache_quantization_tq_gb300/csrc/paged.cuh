@@ -1,0 +1,67 @@
+// Arguments and launchers of the page plan and the dense-layout page kernels
+// (page_plan.cu, paged_store.cu, paged_attn.cu; entry checks in paged.cpp).
+#pragma once
+
+#include <stdint.h>
+
+#include "tq_internal.h"
+
+namespace tq {
+
+struct PlanArgs {
+  const int32_t* ctx_len;
+  const int32_t* new_len;
+  int batch;
+  int ring;  // 0 or kRing
+  int32_t* block_table;
+  int max_blocks, num_blocks;
+  int32_t* queue;
+  int queue_cap;
+  const int32_t* queue_state;
+  int32_t* lengths;
+  int32_t* n_paged;
+  int32_t* n_ring;
+  int32_t* token_start;
+  int64_t* slots;
+  int32_t* positions;
+  int32_t* rows;
+  int max_tokens;
+  int32_t* queue_state_out;
+  uint32_t* err;
+};
+
+struct StoreArgs {
+  const uint16_t* k;
+  const uint16_t* v;
+  int64_t k_stride, v_stride;  // elements from token to token
+  const int64_t* slots;
+  int n_tokens;
+  uint8_t* pool;
+  int num_blocks;
+  int hkv;
+  uint32_t* err;
+};
+
+struct PagedArgs {
+  const uint16_t* q;
+  int64_t q_stride;  // elements from sequence to sequence
+  int batch;
+  const uint8_t* pool;
+  int num_blocks;
+  const int32_t* block_table;
+  int max_blocks;
+  const int32_t* lengths;
+  int window;
+  float scale;
+  float* out;
+  float* lse;
+  int hq, hkv, n_rep;
+  uint32_t* err;
+};
+
+cudaError_t launch_plan(tq_ctx* ctx, const PlanArgs& a, cudaStream_t s);
+cudaError_t launch_store(tq_ctx* ctx, const StoreArgs& a, cudaStream_t s);
+size_t paged_workspace(const tq_ctx* ctx, int batch);
+cudaError_t launch_paged(tq_ctx* ctx, const PagedArgs& a, void* workspace, cudaStream_t s);
+
+}  // namespace tq
