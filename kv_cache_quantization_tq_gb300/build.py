@@ -22,7 +22,7 @@ ROOT = os.path.dirname(HERE)
 INCLUDE = os.path.join(ROOT, "include")
 
 CU = ["encode.cu", "decode.cu", "decode_tc.cu", "decode_hy.cu", "decode_alt.cu", "decode_static.cu", "dequant.cu", "pack.cu",
-      "page_plan.cu", "paged_store.cu", "paged_attn.cu"]
+      "page_plan.cu", "paged_store.cu", "paged_attn_f16.cu", "paged_attn_bf16.cu", "paged_attn_e4m3.cu"]
 CPP = ["host.cpp", "paged.cpp"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 

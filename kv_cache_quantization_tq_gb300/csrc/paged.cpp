@@ -1,4 +1,5 @@
-// Argument checks of the page plan and of the dense-layout page calls.
+// Argument checks of the page plan and of the dense-layout page calls, the choice of the attention's
+// translation unit and the TMA descriptor of a pool.
 #include <limits.h>
 #include <math.h>
 
@@ -18,6 +19,45 @@ bool on_device(const tq_ctx* ctx) {
 bool aligned16(const void* p) { return (((uintptr_t)p) & 15) == 0; }
 
 }  // namespace
+
+namespace tq {
+
+bool encode_paged_map(const PagedTensorMap& t, CUtensorMap* map) {
+  // the driver's encoder, looked up once (the library is not linked against libcuda)
+  using Encode = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
+                              const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                              CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+  static const Encode encode = [] {
+    void* f = nullptr;
+    cudaDriverEntryPointQueryResult found;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &found) != cudaSuccess ||
+        found != cudaDriverEntryPointSuccess)
+      f = nullptr;
+    return reinterpret_cast<Encode>(f);
+  }();
+  if (!encode) return false;
+  const cuuint64_t dims[3] = {(cuuint64_t)t.d, 2 * kPage, (cuuint64_t)t.tiles};
+  const cuuint64_t strides[2] = {(cuuint64_t)t.d * t.elem, (cuuint64_t)t.tile_bytes};
+  const cuuint32_t box[3] = {(cuuint32_t)(t.row_bytes / t.elem), kPage, 1}, step[3] = {1, 1, 1};
+  return encode(map, t.elem == 1 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_UINT16, 3,
+                const_cast<void*>(t.pool), dims, strides, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                t.row_bytes == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+                CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+size_t paged_workspace(const tq_ctx* ctx, int batch) {
+  const tq_config& c = ctx->cfg;
+  return c.key_bits == 8 ? paged_workspace_e4m3(ctx, batch)
+         : c.key_format == TQ_ELEM_BF16 ? paged_workspace_bf16(ctx, batch) : paged_workspace_f16(ctx, batch);
+}
+
+cudaError_t launch_paged(tq_ctx* ctx, const PagedArgs& a, void* workspace, cudaStream_t s) {
+  const tq_config& c = ctx->cfg;
+  return c.key_bits == 8 ? launch_paged_e4m3(ctx, a, workspace, s)
+         : c.key_format == TQ_ELEM_BF16 ? launch_paged_bf16(ctx, a, workspace, s) : launch_paged_f16(ctx, a, workspace, s);
+}
+
+}  // namespace tq
 
 extern "C" {
 

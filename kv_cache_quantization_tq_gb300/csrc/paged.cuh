@@ -2,6 +2,7 @@
 // (page_plan.cu, paged_store.cu, paged_attn.cu; entry checks in paged.cpp).
 #pragma once
 
+#include <cuda.h>
 #include <stdint.h>
 
 #include "tq_internal.h"
@@ -59,9 +60,27 @@ struct PagedArgs {
   uint32_t* err;
 };
 
+// The pool as a TMA tensor of 16-row boxes: rows of `d` elements of `elem` bytes, 32 rows (keys, then
+// values) per tile, `tiles` tiles `tile_bytes` apart; boxes `row_bytes` wide and swizzled (128 or 64).
+struct PagedTensorMap {
+  const void* pool;
+  int elem, d;
+  int64_t tiles;
+  int tile_bytes, row_bytes;
+};
+bool encode_paged_map(const PagedTensorMap& t, CUtensorMap* map);
+
 cudaError_t launch_plan(tq_ctx* ctx, const PlanArgs& a, cudaStream_t s);
 cudaError_t launch_store(tq_ctx* ctx, const StoreArgs& a, cudaStream_t s);
 size_t paged_workspace(const tq_ctx* ctx, int batch);
 cudaError_t launch_paged(tq_ctx* ctx, const PagedArgs& a, void* workspace, cudaStream_t s);
+
+// one translation unit per element type
+size_t paged_workspace_f16(const tq_ctx* ctx, int batch);
+size_t paged_workspace_bf16(const tq_ctx* ctx, int batch);
+size_t paged_workspace_e4m3(const tq_ctx* ctx, int batch);
+cudaError_t launch_paged_f16(tq_ctx* ctx, const PagedArgs& a, void* workspace, cudaStream_t s);
+cudaError_t launch_paged_bf16(tq_ctx* ctx, const PagedArgs& a, void* workspace, cudaStream_t s);
+cudaError_t launch_paged_e4m3(tq_ctx* ctx, const PagedArgs& a, void* workspace, cudaStream_t s);
 
 }  // namespace tq

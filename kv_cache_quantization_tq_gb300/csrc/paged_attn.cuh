@@ -1,0 +1,966 @@
+// Attention of one new token per sequence over dense-layout pages: kernels, included by one
+// translation unit per element type (paged_attn_f16.cu, paged_attn_bf16.cu, paged_attn_e4m3.cu).
+//
+//   s_p = scale q . k_p,  out = sum_p 2^(s_p log2(e) - m) v_p / sum_p 2^(s_p log2(e) - m)
+//
+// What bounds it: reading the cache once.  A step does 4 d operations per query head for the 4 d bytes (16
+// bits) of a token's key and value, far below what the tensor cores do in that time, so everything here
+// serves one aim: enough bytes in flight on every multiprocessor from the first moment to the last.
+//
+// Work split.  A segment is one (sequence, KV head, group of up to 8 NT query heads); its work is its number
+// of pages.  All segments' pages stand in one line, and T teams get equal pieces of it, whatever the lengths
+// are: a ragged batch and a single long sequence are split alike, in one wave, with no length known on
+// the host.  Cuts that fall within tau pages of a segment's end move there.  A segment that one team holds whole
+// is written out at once; the pieces of a cut one go to the workspace (at most two per team) and the
+// merge kernel joins them.  A team is one CTA (its warps take every NW-th page and are joined in
+// shared memory) when there are few segments, or one warp when there are many short ones.
+//
+// One page (16 tokens) per warp and step, each warp with a ring of S stages that it fills itself by TMA (128-byte
+// swizzle, so that the rows of a plain [16][d] tile are read without bank conflicts) and mbarriers:
+//   S^T = K Q^T   mma.m16n8k16, A = 16 tokens x 16 dims of K (ldmatrix), B = 8 heads of Q in registers
+//   O^T += V^T P^T            A = 16 dims x 16 tokens of V (ldmatrix.trans), B = P^T (movmatrix of S^T's layout)
+// With tokens and dims on the 16-row side, 8 query heads per KV head fill the 8-column side and no row of the
+// products is padding; the accumulators are d / 4 registers.
+//
+// Precision: q and k products are exact and summed in fp32.  Weights are split into 16-bit parts (two fp16
+// parts, 22 bits; three bf16 parts, 24 bits) whose products with V are exact; each page's sum leaves the tensor
+// core and is added to the running sum by an fp32 addition that rounds to nearest (the tensor core cuts, which
+// over thousands of pages would pull the sum towards zero).  The running maximum m is a reference that is only
+// raised when a score passes it by more than 8, so that most pages rescale nothing.  Weights are
+// 2^(s - m + 7) <= 2^15: an fp16 low part then keeps 2^-32 of the largest weight.
+//   e4m3 pages: codes are exact in fp16.  Key exponents scale the fp32 scores.  Value exponents scale the weights
+// relative to the page's largest one, which scales the page's sum when it is added: nothing overflows fp16.
+// bf16 queries are first scaled by a power of two per head into fp16's range (exact down to 2^-31 of the head's
+// largest entry).
+#pragma once
+
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <math_constants.h>
+
+#include "common.cuh"
+#include "paged.cuh"
+
+namespace tq {
+namespace {
+
+enum { kF16 = 0, kBF16 = 1, kE4M3 = 2 };
+
+constexpr float kWeightUp = 7.f;  // weights are 2^(s - m + 7)
+constexpr float kLazy = 8.f;      // the reference is raised when a score passes it by more than this
+
+template <int KIND, int D, int NT>
+struct PagedCfg {
+  static constexpr int ES = KIND == kE4M3 ? 1 : 2;
+  static constexpr int HALF = kPage * D * ES;  // keys or values of a page
+  static constexpr int PAGE = 2 * HALF;
+  static constexpr int EXP = KIND == kE4M3 ? 32 : 0;
+  static constexpr int HEADS = 8 * NT;
+  static constexpr bool QREG = D * NT <= 128;              // query fragments in registers
+  static constexpr int QBYTES = QREG ? 0 : HEADS * D * 2;  // else in shared memory, per warp
+  static constexpr int SLOT = HEADS * (D + 4) * 4 + HEADS * 8;
+  static constexpr int LIMIT = 232448 - 1024;  // 227 KB, less the alignment of the stages
+  static constexpr int fixed(int nw) { return nw * (SLOT + QBYTES) + (nw * 32 + 1) * 8 + 64; }
+  static constexpr int per(int nw) { return nw * (PAGE + EXP + 16); }
+  static constexpr bool fits(int nw) { return fixed(nw) + per(nw) <= LIMIT; }
+  // Warps per CTA: small pages need more of them to keep the bytes in flight
+  static constexpr int NW = PAGE <= 4096 && QREG && fits(16) ? 16 : fits(8) ? 8 : 4;
+  static constexpr int S_FIT = (LIMIT - fixed(NW)) / per(NW);
+  static constexpr int S = S_FIT > 8 ? 8 : S_FIT;
+  static_assert(S >= 1, "one stage per warp fits");
+  static constexpr int THREADS = NW * 32;
+  // dynamic shared memory, from a 1024-byte aligned base
+  static constexpr int OFF_SLOT = NW * S * PAGE;
+  static constexpr int OFF_ML = OFF_SLOT + NW * HEADS * (D + 4) * 4;
+  static constexpr int OFF_Q = OFF_ML + NW * HEADS * 8;
+  static constexpr int OFF_EXP = OFF_Q + NW * QBYTES;
+  static constexpr int OFF_BAR = OFF_EXP + NW * S * EXP;
+  static constexpr int OFF_PRE = OFF_BAR + NW * S * 16;
+  static constexpr int OFF_WARP = OFF_PRE + (THREADS + 1) * 8;
+  static constexpr int SMEM = OFF_WARP + NW * 8 + 1024;
+  static_assert(SMEM <= 232448, "shared memory");
+  static constexpr int SWIZZLE_ROW = D * ES < 128 ? D * ES : 128;  // bytes of a row in one TMA box
+  static constexpr int BOXES = D * ES / SWIZZLE_ROW;               // boxes per half page
+};
+
+// ---------------------------------------------------------------- work split, shared by both kernels
+struct PagedPlan {
+  int teams;       // most teams (CTAs, or warps)
+  int team_warps;  // warps of a team: all of a CTA's, or 1
+  int min_pages;   // a team gets at least about this many pages
+  int tau;         // cuts this near a segment's end move there
+  int groups;      // query-head groups per KV head
+  int scan;        // entries of the scan (threads of a CTA)
+};
+
+struct PagedWork {
+  PagedArgs a;
+  PagedPlan p;
+  int q_bf16;
+  int64_t* pre;   // workspace: scan of the pages, [scan + 1]
+  float* parts;   // workspace: [2 * teams][part]
+};
+
+struct Seq {
+  int len, lo, first, pages;  // length, first position seen, first page, pages seen
+  bool bad;
+};
+__device__ __forceinline__ Seq seq_of(const PagedArgs& a, int b) {
+  Seq s;
+  s.len = a.lengths[b];
+  s.bad = s.len < 0 || s.len > (int64_t)a.max_blocks * kPage;
+  if (s.bad) s.len = 0;
+  s.lo = a.window && s.len > a.window ? s.len - a.window : 0;
+  s.first = s.lo / kPage;
+  s.pages = s.len ? (s.len + kPage - 1) / kPage - s.first : 0;
+  return s;
+}
+
+// Teams in use and the reach of a segment's end, for `work` pages in all.
+struct Split {
+  int64_t work;
+  int teams, tau;
+};
+__device__ __forceinline__ Split split_of(const PagedPlan& p, int64_t work) {
+  Split s;
+  s.work = work;
+  const int64_t t = work / p.min_pages;
+  s.teams = t < 1 ? 1 : t < p.teams ? (int)t : p.teams;
+  const int64_t quarter = work / s.teams / 4;
+  s.tau = quarter < p.tau ? (int)quarter : p.tau;
+  return s;
+}
+
+// ---------------------------------------------------------------- PTX
+__device__ __forceinline__ uint32_t sm_addr(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }
+__device__ __forceinline__ void bar_init(uint32_t bar, uint32_t n) {
+  asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(n) : "memory");
+}
+__device__ __forceinline__ void bar_expect(uint32_t bar, uint32_t bytes) {
+  asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
+}
+// Bounded wait (about a second of %globaltimer); false on expiry.
+__device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity) {
+  uint64_t t0 = 0;
+  for (uint32_t i = 0;; ++i) {
+    uint32_t ok;
+    asm volatile("{ .reg .pred p; mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2; selp.u32 %0, 1, 0, p; }"
+                 : "=r"(ok)
+                 : "r"(bar), "r"(parity)
+                 : "memory");
+    if (ok) return true;
+    if ((i & 63) == 0) {
+      uint64_t now;
+      asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(now));
+      if (i == 0) t0 = now;
+      else if (now - t0 > 1000000000ull) return false;
+    }
+  }
+}
+__device__ __forceinline__ void tma_load(uint32_t dst, const CUtensorMap* map, int x, int y, int z, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cta.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
+      "l"(map), "r"(x), "r"(y), "r"(z), "r"(bar)
+      : "memory");
+}
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
+  asm volatile("cp.async.bulk.shared::cta.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+               "l"(src), "r"(bytes), "r"(bar)
+               : "memory");
+}
+__device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ void ldsm4t(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ uint32_t movmat(uint32_t x) {
+  uint32_t y;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
+}
+template <bool BF>
+__device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  if (BF)
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                 : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+  else
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                 : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+// 2^x; -inf gives +0.
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+// Two e4m3 codes (low byte first) as two fp16.
+__device__ __forceinline__ uint32_t f16_of_e4m3(uint32_t two) {
+  uint32_t r;
+  asm("{ .reg .b16 lo, hi; mov.b32 {lo, hi}, %1; cvt.rn.f16x2.e4m3x2 %0, lo; }" : "=r"(r) : "r"(two));
+  return r;
+}
+__device__ __forceinline__ uint32_t f16_of_e4m3_high(uint32_t four) {
+  uint32_t r;
+  asm("{ .reg .b16 lo, hi; mov.b32 {lo, hi}, %1; cvt.rn.f16x2.e4m3x2 %0, hi; }" : "=r"(r) : "r"(four));
+  return r;
+}
+// 2^e, e held to the normal range.
+__device__ __forceinline__ float power2(int e) { return __int_as_float((max(-126, min(e, 127)) + 127) << 23); }
+
+// 16-bit parts of a pair of fp32 weights: each part rounds what the ones before leave.
+template <bool BF>
+__device__ __forceinline__ uint32_t take_part(float& x, float& y) {
+  if (BF) {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(x, y);
+    const uint32_t u = *reinterpret_cast<const uint32_t*>(&h);
+    x -= __uint_as_float(u << 16);
+    y -= __uint_as_float(u & 0xffff0000u);
+    return u;
+  }
+  const __half2 h = __floats2half2_rn(x, y);
+  const float2 f = __half22float2(h);
+  x -= f.x;
+  y -= f.y;
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+// ---------------------------------------------------------------- scan and walk over the line of pages
+struct Scan {
+  const int64_t* pre;  // pages in front of each entry of `stride` sequences
+  int stride, n;
+  int64_t heads;       // segments per sequence
+};
+
+// The segment that page x of the line belongs to: sequence b, segment hg of it, page p of `s.pages`.
+struct At {
+  int b, hg, p;
+  Seq s;
+};
+__device__ __forceinline__ At locate(const PagedArgs& a, const Scan& sc, int64_t x) {
+  int lo = 0, hi = sc.n - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (sc.pre[mid] <= x) lo = mid;
+    else hi = mid - 1;
+  }
+  At at;
+  int64_t acc = sc.pre[lo];
+  at.b = lo * sc.stride;
+  at.s = seq_of(a, at.b);
+  while (x >= acc + at.s.pages * sc.heads && at.b + 1 < a.batch) {
+    acc += at.s.pages * sc.heads;
+    at.s = seq_of(a, ++at.b);
+  }
+  const int64_t r = x - acc;
+  at.hg = (int)(r / at.s.pages);
+  at.p = (int)(r - (int64_t)at.hg * at.s.pages);
+  return at;
+}
+
+// Cut t of the line, moved to a segment's end within reach.
+__device__ __forceinline__ int64_t cut_of(const PagedArgs& a, const Scan& sc, const Split& sp, int t) {
+  if (t <= 0) return 0;
+  if (t >= sp.teams) return sp.work;
+  const int64_t x = t * sp.work / sp.teams;
+  const At at = locate(a, sc, x);
+  if (at.p <= sp.tau) return x - at.p;
+  if (at.s.pages - at.p <= sp.tau) return x - at.p + at.s.pages;
+  return x;
+}
+
+// A warp's way along its team's piece: portions (the piece's share of one segment), and in a portion the
+// pages p + wt, p + wt + tw, ... of the segment.
+struct Walk {
+  int b, hg, p, take, n;  // segment, first page of the portion, its pages, this warp's number of them
+  Seq s;
+  int64_t left;           // pages of the team's piece from this portion on
+  __device__ __forceinline__ void open(int wt, int tw) {
+    take = left < s.pages - p ? (int)left : s.pages - p;
+    n = take > wt ? (take - wt + tw - 1) / tw : 0;
+  }
+  __device__ __forceinline__ bool next(const PagedArgs& a, int heads, int wt, int tw) {
+    left -= take;
+    if (left <= 0) return false;
+    p = 0;
+    if (++hg == heads) {
+      hg = 0;
+      do {
+        if (++b >= a.batch) return false;
+        s = seq_of(a, b);
+      } while (s.pages == 0);
+    }
+    open(wt, tw);
+    return true;
+  }
+};
+
+// ---------------------------------------------------------------- the kernel
+template <int KIND, int D, int NT>
+__global__ void __launch_bounds__(PagedCfg<KIND, D, NT>::THREADS, 1)
+    paged_kernel(const __grid_constant__ CUtensorMap map, const __grid_constant__ PagedWork w) {
+  using C = PagedCfg<KIND, D, NT>;
+  constexpr bool BF = KIND == kBF16, F8 = KIND == kE4M3;
+  constexpr int NW = C::NW, S = C::S, KS = D / 16;
+  extern __shared__ uint8_t raw[];
+  uint8_t* sm = raw + ((1024 - (sm_addr(raw) & 1023)) & 1023);
+  int64_t* pre = reinterpret_cast<int64_t*>(sm + C::OFF_PRE);
+  const PagedArgs& a = w.a;
+  const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5, g = lane >> 2, t = lane & 3;
+  const int heads = a.hkv * w.p.groups;  // segments per sequence
+  const uint32_t stage0 = sm_addr(sm) + wid * S * C::PAGE, bar0 = sm_addr(sm + C::OFF_BAR) + wid * S * 16;
+  const uint32_t exp0 = sm_addr(sm + C::OFF_EXP) + wid * S * C::EXP;
+
+  asm volatile("griddepcontrol.launch_dependents;");
+  if (lane < 2 * S) bar_init(bar0 + 8 * lane, 1);
+  asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+
+  // ---- scan: pages in front of each entry of `stride` sequences
+  Scan sc;
+  sc.pre = pre;
+  sc.stride = (a.batch + C::THREADS - 1) / C::THREADS;
+  sc.n = (a.batch + sc.stride - 1) / sc.stride;
+  sc.heads = heads;
+  int64_t own = 0;
+  bool bad_len = false;
+  for (int b = tid * sc.stride; b < min((tid + 1) * sc.stride, a.batch); ++b) {
+    const Seq s = seq_of(a, b);
+    bad_len |= s.bad;
+    own += (int64_t)s.pages * heads;
+  }
+  int64_t inc = own;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t up = __shfl_up_sync(kFull, inc, o);
+    if (lane >= o) inc += up;
+  }
+  int64_t* wsum = reinterpret_cast<int64_t*>(sm + C::OFF_WARP);
+  if (lane == 31) wsum[wid] = inc;
+  __syncthreads();
+  int64_t before = 0, work = 0;
+#pragma unroll
+  for (int i = 0; i < NW; ++i) {
+    if (i == wid) before = work;
+    work += wsum[i];
+  }
+  pre[tid] = before + inc - own;
+  if (tid == 0) pre[C::THREADS] = work;
+  if (blockIdx.x == 0) {
+    w.pre[tid] = before + inc - own;
+    if (tid == 0) w.pre[C::THREADS] = work;
+    if (bad_len) flag_error(a.err, TQ_DEVERR_POSITION);
+  }
+  __syncthreads();
+  if (work == 0) return;
+
+  // ---- this team's piece
+  const Split sp = split_of(w.p, work);
+  const int tw = w.p.team_warps, wt = tw == 1 ? 0 : wid;
+  const int team = tw == 1 ? blockIdx.x * NW + wid : blockIdx.x;
+  if (team >= sp.teams) return;
+  const int64_t mine = cut_of(a, sc, sp, team + (lane >> 4));  // both ends at once, half a warp each
+  const int64_t x0 = __shfl_sync(kFull, mine, 0), x1 = __shfl_sync(kFull, mine, 16);
+  if (x0 >= x1) return;
+
+  Walk out, in;  // the portion being computed, and the one being fetched
+  {
+    const At at = locate(a, sc, x0);
+    out.b = at.b;
+    out.hg = at.hg;
+    out.p = at.p;
+    out.s = at.s;
+    out.left = x1 - x0;
+    out.open(wt, tw);
+    in = out;
+  }
+
+  // ---- fetching
+  int in_i = 0, ids = 0, tile = 0;
+  bool in_done = false;
+  uint32_t valid = 0, parity = 0, vparity = 0, issued = 0;  // bit per stage
+  bool bad_id = false, dead = false;
+  // Step to the next page of this warp: its tile in `tile` (-1: a bad id); false when there is none.
+  auto fetch_next = [&]() -> bool {
+    while (!in_done && in_i == in.n) {
+      in_done = !in.next(a, heads, wt, tw);
+      in_i = 0;
+    }
+    if (in_done) return false;
+    if ((in_i & 31) == 0 && in_i + lane < in.n)
+      ids = a.block_table[(int64_t)in.b * a.max_blocks + in.s.first + in.p + wt + (in_i + lane) * tw];
+    const int id = __shfl_sync(kFull, ids, in_i & 31);
+    ++in_i;
+    const bool ok = id >= 0 && id < a.num_blocks;
+    bad_id |= !ok;
+    tile = ok ? id * a.hkv + in.hg / w.p.groups : -1;
+    return true;
+  };
+  auto fetch_half = [&](int st, int side) {  // lane 0
+    const uint32_t bar = bar0 + 16 * st + 8 * side, dst = stage0 + st * C::PAGE + side * C::HALF;
+    bar_expect(bar, C::HALF + (side == 0 ? C::EXP : 0));
+#pragma unroll
+    for (int j = 0; j < C::BOXES; ++j)
+      tma_load(dst + j * (kPage * C::SWIZZLE_ROW), &map, j * (C::SWIZZLE_ROW / C::ES), side * kPage, tile, bar);
+    if (F8 && side == 0)
+      bulk_load(exp0 + st * C::EXP, a.pool + (size_t)tile * (C::PAGE + C::EXP) + C::PAGE, C::EXP, bar);
+  };
+#pragma unroll 1
+  for (int st = 0; st < S; ++st)
+    if (fetch_next()) {
+      issued |= 1u << st;
+      if (tile >= 0) {
+        valid |= 1u << st;
+        if (lane == 0) {
+          fetch_half(st, 0);
+          fetch_half(st, 1);
+        }
+      }
+    }
+
+  // ---- per-lane offsets of the ldmatrix rows (see the swizzle: 16-byte piece c of row r sits at c ^ (r & 7),
+  // or c ^ ((r >> 1) & 3) in 64-byte rows)
+  constexpr bool NARROW = C::SWIZZLE_ROW == 64;
+  auto row_off = [&](int row, int odd) -> uint32_t {  // row's start, with piece `odd` (0 or 1) swizzled
+    const int x = NARROW ? (row >> 1) & 3 : row & 7;
+    return row * C::SWIZZLE_ROW + ((odd ^ x) << 4);
+  };
+  // pieces 2 j and 2 j + 1 of the row: an even piece number is xored in, boxes of 8 pieces are 2048 bytes apart
+  auto piece = [&](uint32_t base, uint32_t off, int j) -> uint32_t {
+    return base + (NARROW ? 0 : (j >> 2) * (kPage * 128)) + (off ^ ((NARROW ? 2 * j : (2 * j & 7)) << 4));
+  };
+  const uint32_t k_off = row_off((lane & 7) + ((lane >> 3) & 1) * 8, lane >> 4);
+  const uint32_t v_off = F8 ? k_off : row_off((lane & 7) + (lane >> 4) * 8, (lane >> 3) & 1);
+
+  uint32_t qf[C::QREG ? NT : 1][C::QREG ? KS : 1][2];
+  uint2* q_sm = reinterpret_cast<uint2*>(sm + C::OFF_Q + wid * C::QBYTES);
+  float o[KS][NT][4], m[NT][2], l[NT][2], qs[NT][2];
+  const float log2e_scale = a.scale * 1.44269504088896340736f;
+  int st = 0;
+
+  // ================================================================ portions
+#pragma unroll 1
+  for (bool more = true; more; more = out.next(a, heads, wt, tw)) {
+    const int kvh = out.hg / w.p.groups, h0 = (out.hg - kvh * w.p.groups) * C::HEADS;
+    const int nh = min(C::HEADS, a.n_rep - h0);
+    const int64_t head0 = (int64_t)kvh * a.n_rep + h0;
+    // ---- queries as B fragments: head g, dims 16 ks + 2 t, + 1 and + 8, + 9 (8-bit pages: 4 t .. 4 t + 3,
+    // the order in which ldmatrix hands out the bytes of a key row)
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      const int h = nt * 8 + g;
+      const uint16_t* qr = a.q + out.b * a.q_stride + (head0 + h) * D;
+      float up = 1.f;
+      if (F8 && w.q_bf16) {
+        uint32_t top = 0;
+        if (h < nh)
+#pragma unroll
+          for (int ks = 0; ks < KS; ++ks) {
+            const uint2 x = *reinterpret_cast<const uint2*>(qr + ks * 16 + 4 * t);
+            top = max(max(top, max(x.x & 0x7fffu, (x.x >> 16) & 0x7fffu)), max(x.y & 0x7fffu, (x.y >> 16) & 0x7fffu));
+          }
+        top = max(top, __shfl_xor_sync(kFull, top, 1));
+        top = max(top, __shfl_xor_sync(kFull, top, 2));
+        // largest entry in [2^14, 2^15); the factor is undone in the score's
+        const int e = (int)(top >> 7) - 127;
+        up = power2(max(-126, min(14 - e, 126)));
+      }
+#pragma unroll
+      for (int ks = 0; ks < KS; ++ks) {
+        uint2 x = make_uint2(0, 0);
+        if (h < nh) {
+          if (F8) x = *reinterpret_cast<const uint2*>(qr + ks * 16 + 4 * t);
+          else {
+            x.x = *reinterpret_cast<const uint32_t*>(qr + ks * 16 + 2 * t);
+            x.y = *reinterpret_cast<const uint32_t*>(qr + ks * 16 + 2 * t + 8);
+          }
+        }
+        if (F8 && w.q_bf16) {
+          const __half2 u = __floats2half2_rn(__uint_as_float(x.x << 16) * up, __uint_as_float(x.x & 0xffff0000u) * up);
+          const __half2 v = __floats2half2_rn(__uint_as_float(x.y << 16) * up, __uint_as_float(x.y & 0xffff0000u) * up);
+          x = make_uint2(*reinterpret_cast<const uint32_t*>(&u), *reinterpret_cast<const uint32_t*>(&v));
+        }
+        if constexpr (C::QREG) {
+          qf[nt][ks][0] = x.x;
+          qf[nt][ks][1] = x.y;
+        } else {
+          q_sm[(nt * KS + ks) * 32 + lane] = x;
+        }
+      }
+      const float down = log2e_scale / up;  // up is a power of two
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        qs[nt][i] = F8 ? __shfl_sync(kFull, down, (2 * t + i) * 4) : log2e_scale;
+        m[nt][i] = -CUDART_INF_F;
+        l[nt][i] = 0.f;
+      }
+    }
+    if constexpr (!C::QREG) __syncwarp();
+#pragma unroll
+    for (int j = 0; j < KS; ++j)
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) o[j][nt][i] = 0.f;
+
+    // ================================================================ pages
+#pragma unroll 1
+    for (int i = 0; i < out.n; ++i, st = st + 1 == S ? 0 : st + 1) {
+      const bool here = valid >> st & 1;
+      const uint32_t kb = stage0 + st * C::PAGE, vb = kb + C::HALF;
+      float s[NT][4];
+      if (here && !dead) dead = !bar_wait(bar0 + 16 * st, parity >> st & 1);
+      if (dead) continue;
+      issued &= ~(1u << st);
+      if (here) parity ^= 1u << st;
+      int exps = 0;
+      if (here) {
+        if (F8) {
+          // lanes 0..15: exponents of the keys, 16..31: of the values
+          asm volatile("ld.shared.s8 %0, [%1];" : "=r"(exps) : "r"(exp0 + st * C::EXP + lane) : "memory");
+        }
+        float s2[NT][4];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int k = 0; k < 4; ++k) s[nt][k] = s2[nt][k] = 0.f;
+        auto score = [&](int ks, const uint32_t(&af)[4], float(&acc)[NT][4]) {
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+            if constexpr (C::QREG) mma<BF>(acc[nt], af, qf[nt][ks][0], qf[nt][ks][1]);
+            else {
+              const uint2 x = q_sm[(nt * KS + ks) * 32 + lane];
+              mma<BF>(acc[nt], af, x.x, x.y);
+            }
+          }
+        };
+        if constexpr (F8) {
+#pragma unroll
+          for (int j = 0; j < KS / 2; ++j) {
+            uint32_t r[4];
+            ldsm4(r, piece(kb, k_off, j));
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+              const uint32_t af[4] = {f16_of_e4m3(r[2 * c]), f16_of_e4m3(r[2 * c + 1]), f16_of_e4m3_high(r[2 * c]),
+                                      f16_of_e4m3_high(r[2 * c + 1])};
+              if (c) score(2 * j + c, af, s2);
+              else score(2 * j + c, af, s);
+            }
+          }
+        } else {
+#pragma unroll
+          for (int ks = 0; ks < KS; ++ks) {
+            uint32_t r[4];
+            ldsm4(r, piece(kb, k_off, ks));
+            if (ks & 1) score(ks, r, s2);
+            else score(ks, r, s);
+          }
+        }
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int k = 0; k < 4; ++k) s[nt][k] += s2[nt][k];
+      }
+      // the keys are read: the stage's next page may come
+      __syncwarp();
+      const bool again = fetch_next();
+      const int next_tile = tile;
+      valid = again && next_tile >= 0 ? valid | 1u << st : valid & ~(1u << st);
+      if (again) issued |= 1u << st;
+      if (again && next_tile >= 0 && lane == 0) fetch_half(st, 0);
+
+      if (here) {
+        // ---- weights
+        const int pg = out.s.first + out.p + wt + i * tw;  // page of the sequence
+        const int t_lo = out.s.lo - pg * kPage, t_hi = out.s.len - pg * kPage;
+        const bool whole = t_lo <= 0 && t_hi >= kPage;
+        const bool ok0 = g >= t_lo && g < t_hi, ok1 = g + 8 >= t_lo && g + 8 < t_hi;
+        if (F8) {
+          const float f0 = power2(__shfl_sync(kFull, exps, g)), f1 = power2(__shfl_sync(kFull, exps, g + 8));
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+            s[nt][0] *= f0;
+            s[nt][1] *= f0;
+            s[nt][2] *= f1;
+            s[nt][3] *= f1;
+          }
+        }
+        bool raise = false;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            s[nt][k] *= qs[nt][k & 1];
+            if (!whole && !(k < 2 ? ok0 : ok1)) s[nt][k] = -CUDART_INF_F;
+            raise |= s[nt][k] > m[nt][k & 1] + kLazy;
+          }
+        if (__any_sync(kFull, raise)) {
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+              float mx = fmaxf(s[nt][k], s[nt][k + 2]);
+#pragma unroll
+              for (int x = 4; x < 32; x <<= 1) mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, x));
+              mx = fmaxf(m[nt][k], mx);
+              const float c = mx == -CUDART_INF_F ? 1.f : ex2(m[nt][k] - mx);
+              m[nt][k] = mx;
+              l[nt][k] *= c;
+#pragma unroll
+              for (int j = 0; j < KS; ++j) {
+                o[j][nt][k] *= c;
+                o[j][nt][k + 2] *= c;
+              }
+            }
+        }
+        float page_up = 1.f, w0 = 1.f, w1 = 1.f;
+        if (F8) {
+          // value exponents of the tokens that count, relative to the largest of them
+          const int tok = lane & 15;
+          const int ev = lane >= 16 && tok >= t_lo && tok < t_hi ? exps : -128;
+          const int top = __reduce_max_sync(kFull, ev);
+          page_up = power2(top);
+          const int e0 = __shfl_sync(kFull, exps, 16 + g), e1 = __shfl_sync(kFull, exps, 24 + g);
+          w0 = ok0 ? power2(e0 - top) : 0.f;
+          w1 = ok1 ? power2(e1 - top) : 0.f;
+        }
+        constexpr int PARTS = BF ? 3 : 2;
+        uint32_t pf[NT][PARTS][2];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          float p[4];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const float ref = m[nt][k & 1] == -CUDART_INF_F ? 0.f : m[nt][k & 1];
+            p[k] = ex2(s[nt][k] - ref + kWeightUp);
+          }
+          l[nt][0] += p[0] + p[2];
+          l[nt][1] += p[1] + p[3];
+          if (F8) {
+            p[0] *= w0;
+            p[1] *= w0;
+            p[2] *= w1;
+            p[3] *= w1;
+          }
+#pragma unroll
+          for (int k = 0; k < PARTS; ++k) {
+            pf[nt][k][0] = movmat(take_part<BF>(p[0], p[1]));
+            pf[nt][k][1] = movmat(take_part<BF>(p[2], p[3]));
+          }
+        }
+        // tokens 2 t, 2 t + 1 and + 8 of the value fragments: rows that do not count are whatever memory held
+        uint32_t keep0 = 0xffffffffu, keep1 = 0xffffffffu;
+        if (!whole) {
+          auto in_range = [&](int tok) { return tok >= t_lo && tok < t_hi; };
+          keep0 = (in_range(2 * t) ? 0xffffu : 0u) | (in_range(2 * t + 1) ? 0xffff0000u : 0u);
+          keep1 = (in_range(2 * t + 8) ? 0xffffu : 0u) | (in_range(2 * t + 9) ? 0xffff0000u : 0u);
+        }
+        dead = !bar_wait(bar0 + 16 * st + 8, vparity >> st & 1);
+        if (!dead) vparity ^= 1u << st;
+        auto add = [&](int j, uint32_t(&af)[4]) {
+          af[0] &= keep0;
+          af[1] &= keep0;
+          af[2] &= keep1;
+          af[3] &= keep1;
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+            float acc[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int k = PARTS - 1; k >= 0; --k) mma<BF>(acc, af, pf[nt][k][0], pf[nt][k][1]);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) o[j][nt][k] = F8 ? fmaf(acc[k], page_up, o[j][nt][k]) : o[j][nt][k] + acc[k];
+          }
+        };
+        if (!dead) {
+          if constexpr (F8) {
+#pragma unroll
+            for (int j = 0; j < KS / 2; ++j) {
+              uint32_t r[4];
+              ldsm4t(r, piece(vb, v_off, j));
+#pragma unroll
+              for (int c = 0; c < 2; ++c) {
+                // bytes (token 2 t: dims 2 g, 2 g + 1; token 2 t + 1: the same) to (dim 2 g | dim 2 g + 1)
+                const uint32_t x = __byte_perm(r[2 * c], 0, 0x3120), y = __byte_perm(r[2 * c + 1], 0, 0x3120);
+                uint32_t af[4] = {f16_of_e4m3(x), f16_of_e4m3_high(x), f16_of_e4m3(y), f16_of_e4m3_high(y)};
+                add(2 * j + c, af);
+              }
+            }
+          } else {
+#pragma unroll
+            for (int j = 0; j < KS; ++j) {
+              uint32_t r[4];
+              ldsm4t(r, piece(vb, v_off, j));
+              add(j, r);
+            }
+          }
+        }
+      }
+      __syncwarp();
+      if (again && next_tile >= 0 && lane == 0) fetch_half(st, 1);
+    }
+
+    // ================================================================ the portion's result
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+#pragma unroll
+        for (int x = 4; x < 32; x <<= 1) l[nt][k] += __shfl_xor_sync(kFull, l[nt][k], x);
+        if (dead) l[nt][k] = CUDART_NAN_F;
+      }
+    // dims of accumulator rows g and g + 8 of tile j
+    auto dim0 = [&](int j) { return F8 ? 16 * j + 2 * g : 16 * j + g; };
+    constexpr int DIM1 = F8 ? 1 : 8;
+    const bool all = out.p == 0 && out.take == out.s.pages;
+    // partials: [heads][D] sums, then [heads] references and [heads] totals; a portion that continues a
+    // segment takes the team's first slot, one that begins a segment the second
+    float* part = w.parts + ((int64_t)team * 2 + (out.p == 0)) * (C::HEADS * (D + 2));
+    if (tw == 1) {
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          const int h = nt * 8 + 2 * t + k;
+          if (h >= nh) continue;
+          const int64_t row = (int64_t)out.b * a.hq + head0 + h;
+          float* dst = all ? a.out + row * D : part + h * D;
+          const float f = all ? (l[nt][k] == 0.f ? 0.f : 1.f / l[nt][k]) : 1.f;
+#pragma unroll
+          for (int j = 0; j < KS; ++j) {
+            dst[dim0(j)] = o[j][nt][k] * f;
+            dst[dim0(j) + DIM1] = o[j][nt][k + 2] * f;
+          }
+          if (g == 0) {
+            if (!all) {
+              part[C::HEADS * D + h] = m[nt][k];
+              part[C::HEADS * (D + 1) + h] = l[nt][k];
+            } else if (a.lse) {
+              a.lse[row] = (m[nt][k] - kWeightUp + log2f(l[nt][k])) * 0.69314718055994530942f;
+            }
+          }
+        }
+    } else {
+      float* slot = reinterpret_cast<float*>(sm + C::OFF_SLOT);
+      float* ml = reinterpret_cast<float*>(sm + C::OFF_ML);
+      const int act = min(NW, out.take);  // warps that had a page
+      if (wid < act) {
+        float* mine_o = slot + wid * C::HEADS * (D + 4);
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            const int h = nt * 8 + 2 * t + k;
+#pragma unroll
+            for (int j = 0; j < KS; ++j) {
+              mine_o[h * (D + 4) + dim0(j)] = o[j][nt][k];
+              mine_o[h * (D + 4) + dim0(j) + DIM1] = o[j][nt][k + 2];
+            }
+            if (g == 0) {
+              ml[(wid * C::HEADS + h) * 2] = m[nt][k];
+              ml[(wid * C::HEADS + h) * 2 + 1] = l[nt][k];
+            }
+          }
+      }
+      __syncthreads();
+      for (int i = tid; i < nh * (D / 4); i += C::THREADS) {
+        const int h = i / (D / 4), d4 = (i - h * (D / 4)) * 4;
+        float M = -CUDART_INF_F;
+        for (int k = 0; k < act; ++k) M = fmaxf(M, ml[(k * C::HEADS + h) * 2]);
+        const float ref = M == -CUDART_INF_F ? 0.f : M;
+        float L = 0.f;
+        float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int k = 0; k < act; ++k) {
+          const float c = ex2(ml[(k * C::HEADS + h) * 2] - ref);
+          L = fmaf(c, ml[(k * C::HEADS + h) * 2 + 1], L);
+          const float4 y = *reinterpret_cast<const float4*>(slot + (k * C::HEADS + h) * (D + 4) + d4);
+          x.x = fmaf(c, y.x, x.x);
+          x.y = fmaf(c, y.y, x.y);
+          x.z = fmaf(c, y.z, x.z);
+          x.w = fmaf(c, y.w, x.w);
+        }
+        if (all) {
+          const int64_t row = (int64_t)out.b * a.hq + head0 + h;
+          const float f = L == 0.f ? 0.f : 1.f / L;
+          *reinterpret_cast<float4*>(a.out + row * D + d4) = make_float4(x.x * f, x.y * f, x.z * f, x.w * f);
+          if (d4 == 0 && a.lse) a.lse[row] = (M - kWeightUp + log2f(L)) * 0.69314718055994530942f;
+        } else {
+          *reinterpret_cast<float4*>(part + h * D + d4) = x;
+          if (d4 == 0) {
+            part[C::HEADS * D + h] = M;
+            part[C::HEADS * (D + 1) + h] = L;
+          }
+        }
+      }
+      __syncthreads();
+    }
+  }
+  if (dead) {
+    // copies still under way end before the CTA does
+    for (int k = 0; k < S; ++k)
+      if ((issued & valid) >> k & 1) {
+        bar_wait(bar0 + 16 * k, parity >> k & 1);
+        bar_wait(bar0 + 16 * k + 8, vparity >> k & 1);
+      }
+    if (lane == 0) flag_error(a.err, TQ_DEVERR_TIMEOUT);
+  }
+  if (bad_id && lane == 0) flag_error(a.err, TQ_DEVERR_BLOCK_ID);
+}
+
+// Joins the portions of the segments that more than one team had, and writes the rows of empty sequences.  One
+// CTA per (segment, share of its heads); a thread per dim.
+template <int D, int HEADS>
+__global__ void __launch_bounds__(128) paged_merge_kernel(const __grid_constant__ PagedWork w) {
+  const PagedArgs& a = w.a;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int heads = a.hkv * w.p.groups;
+  const int64_t seg = blockIdx.x;
+  const int b = (int)(seg / heads), hg = (int)(seg - (int64_t)b * heads);
+  const int kvh = hg / w.p.groups, h0 = (hg - kvh * w.p.groups) * HEADS, nh = min(HEADS, a.n_rep - h0);
+  const int64_t row0 = (int64_t)b * a.hq + (int64_t)kvh * a.n_rep + h0;
+  const Seq s = seq_of(a, b);
+  if (s.pages == 0) {
+    for (int h = blockIdx.y; h < nh; h += gridDim.y) {
+      for (int i = threadIdx.x; i < D; i += 128) a.out[(row0 + h) * D + i] = 0.f;
+      if (threadIdx.x == 0 && a.lse) a.lse[row0 + h] = -CUDART_INF_F;
+    }
+    return;
+  }
+  const int stride = (a.batch + w.p.scan - 1) / w.p.scan, e = b / stride;
+  int64_t first = w.pre[e];
+  for (int i = e * stride; i < b; ++i) first += (int64_t)seq_of(a, i).pages * heads;
+  first += (int64_t)hg * s.pages;
+  const int64_t last = first + s.pages;
+  const Split sp = split_of(w.p, w.pre[w.p.scan]);
+  // cuts floor(t work / teams) that lie more than tau inside the segment
+  const int64_t ta = ((first + sp.tau + 1) * sp.teams + sp.work - 1) / sp.work;
+  const int64_t tb = ((last - sp.tau) * sp.teams + sp.work - 1) / sp.work - 1;
+  if (tb < ta) return;  // one team had it
+  const int n = (int)(tb - ta) + 2;
+  constexpr int PART = HEADS * (D + 2);
+  // portion 0 begins the segment (second slot of team ta - 1), portion k > 0 continues it (first slot of ta + k - 1)
+  auto part = [&](int k) { return w.parts + (k == 0 ? (ta - 1) * 2 + 1 : (ta + k - 1) * 2) * (int64_t)PART; };
+  for (int h = blockIdx.y; h < nh; h += gridDim.y) {
+    float M = -CUDART_INF_F;
+    for (int k = 0; k < n; ++k) M = fmaxf(M, part(k)[HEADS * D + h]);
+    const float ref = M == -CUDART_INF_F ? 0.f : M;
+    float L = 0.f, x[(D + 127) / 128];
+#pragma unroll
+    for (int i = 0; i < (D + 127) / 128; ++i) x[i] = 0.f;
+    for (int k = 0; k < n; ++k) {
+      const float* p = part(k);
+      const float c = ex2(p[HEADS * D + h] - ref);
+      L = fmaf(c, p[HEADS * (D + 1) + h], L);
+#pragma unroll
+      for (int i = 0; i < (D + 127) / 128; ++i)
+        if (D >= 128 || threadIdx.x < D) x[i] = fmaf(c, p[h * D + i * 128 + threadIdx.x], x[i]);
+    }
+    const float f = L == 0.f ? 0.f : 1.f / L;
+#pragma unroll
+    for (int i = 0; i < (D + 127) / 128; ++i)
+      if (D >= 128 || threadIdx.x < D) a.out[(row0 + h) * D + i * 128 + threadIdx.x] = x[i] * f;
+    if (threadIdx.x == 0 && a.lse) a.lse[row0 + h] = (M - kWeightUp + log2f(L)) * 0.69314718055994530942f;
+  }
+}
+
+// ---------------------------------------------------------------- host side
+template <int KIND, int D, int NT>
+PagedPlan plan_of(const tq_ctx* ctx, int batch) {
+  using C = PagedCfg<KIND, D, NT>;
+  PagedPlan p;
+  const int n_rep = ctx->cfg.num_q_heads / ctx->cfg.num_kv_heads;
+  p.groups = (n_rep + C::HEADS - 1) / C::HEADS;
+  const int64_t segments = (int64_t)batch * ctx->cfg.num_kv_heads * p.groups;
+  // Many segments: one warp each, no joining inside the CTA.  Few: the CTA's warps share one.
+  p.team_warps = segments >= 4 * (int64_t)ctx->sm_count ? 1 : C::NW;
+  p.teams = ctx->sm_count * (p.team_warps == 1 ? C::NW : 1);
+  p.min_pages = p.team_warps == 1 ? 2 : C::NW;
+  p.tau = p.team_warps == 1 ? 4 : C::NW;
+  p.scan = C::THREADS;
+  return p;
+}
+
+inline size_t align256(size_t x) { return (x + 255) & ~(size_t)255; }
+
+template <int KIND, int D, int NT>
+size_t workspace_of(const tq_ctx* ctx, int batch) {
+  using C = PagedCfg<KIND, D, NT>;
+  const PagedPlan p = plan_of<KIND, D, NT>(ctx, batch);
+  return align256((C::THREADS + 1) * 8) + (size_t)p.teams * 2 * C::HEADS * (D + 2) * 4;
+}
+
+template <int KIND, int D, int NT>
+cudaError_t launch_one(tq_ctx* ctx, const PagedArgs& a, void* workspace, cudaStream_t s) {
+  using C = PagedCfg<KIND, D, NT>;
+  PagedWork w;
+  w.a = a;
+  w.p = plan_of<KIND, D, NT>(ctx, a.batch);
+  w.q_bf16 = ctx->cfg.key_format == TQ_ELEM_BF16;
+  w.pre = static_cast<int64_t*>(workspace);
+  w.parts = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + align256((C::THREADS + 1) * 8));
+  CUtensorMap map{};
+  if (a.num_blocks > 0) {
+    const PagedTensorMap tm{a.pool, C::ES, D, (int64_t)a.num_blocks * a.hkv, C::PAGE + C::EXP, C::SWIZZLE_ROW};
+    if (!encode_paged_map(tm, &map)) return cudaErrorInvalidValue;
+  }
+  auto kern = paged_kernel<KIND, D, NT>;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+  if (e != cudaSuccess) return e;
+  prof_start(ctx, kProfDecode, s);
+  kern<<<ctx->sm_count, C::THREADS, C::SMEM, s>>>(map, w);
+  e = cudaGetLastError();
+  prof_stop(ctx, kProfDecode, s);
+  if (e != cudaSuccess) return e;
+  ctx->launches++;
+  ctx->decode_kernel = "paged_kernel";
+
+  const int64_t segments = (int64_t)a.batch * a.hkv * w.p.groups;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3((unsigned)segments, segments < 1024 ? (a.n_rep < C::HEADS ? a.n_rep : C::HEADS) : 1);
+  cfg.blockDim = dim3(128);
+  cfg.stream = s;
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  prof_start(ctx, kProfMerge, s);
+  e = cudaLaunchKernelEx(&cfg, paged_merge_kernel<D, C::HEADS>, w);
+  prof_stop(ctx, kProfMerge, s);
+  if (e == cudaSuccess) ctx->launches++;
+  return e;
+}
+
+// Query heads per segment: 8, or 16 when a KV head has more than 8 (d = 512: always 8, for want of registers).
+template <int KIND>
+cudaError_t launch_kind(tq_ctx* ctx, const PagedArgs& a, void* ws, cudaStream_t s) {
+  const bool two = a.n_rep > 8;
+  switch (ctx->cfg.head_dim) {
+    case 64: return two ? launch_one<KIND, 64, 2>(ctx, a, ws, s) : launch_one<KIND, 64, 1>(ctx, a, ws, s);
+    case 128: return two ? launch_one<KIND, 128, 2>(ctx, a, ws, s) : launch_one<KIND, 128, 1>(ctx, a, ws, s);
+    case 256: return two ? launch_one<KIND, 256, 2>(ctx, a, ws, s) : launch_one<KIND, 256, 1>(ctx, a, ws, s);
+    case 512: return launch_one<KIND, 512, 1>(ctx, a, ws, s);
+  }
+  return cudaErrorInvalidValue;
+}
+
+template <int KIND>
+size_t workspace_kind(const tq_ctx* ctx, int batch) {
+  const bool two = ctx->cfg.num_q_heads / ctx->cfg.num_kv_heads > 8;
+  switch (ctx->cfg.head_dim) {
+    case 64: return two ? workspace_of<KIND, 64, 2>(ctx, batch) : workspace_of<KIND, 64, 1>(ctx, batch);
+    case 128: return two ? workspace_of<KIND, 128, 2>(ctx, batch) : workspace_of<KIND, 128, 1>(ctx, batch);
+    case 256: return two ? workspace_of<KIND, 256, 2>(ctx, batch) : workspace_of<KIND, 256, 1>(ctx, batch);
+    case 512: return workspace_of<KIND, 512, 1>(ctx, batch);
+  }
+  return 0;
+}
+
+}  // namespace
+}  // namespace tq
