@@ -242,7 +242,8 @@ class Context:
         self.num_kv_heads = num_kv_heads
         import torch
 
-        self._device = torch.device("cuda", torch.cuda.current_device())  # tq_create used the current device
+        self._device = torch.cuda.current_device()  # the device tq_create used
+        self._page_bytes = self.page_bytes
 
     def close(self):
         if getattr(self, "ptr", None) and self.ptr.value:
@@ -287,8 +288,9 @@ class Context:
     def _check_pool(self, pool):
         if pool is None:
             return
-        if pool.dim() != 3 or pool.shape[1] != self.num_kv_heads or pool.shape[2] != self.page_bytes:
-            raise ValueError(f"pool must be uint8 [num_blocks, {self.num_kv_heads}, {self.page_bytes}]")
+        shape = pool.shape
+        if len(shape) != 3 or shape[1] != self.num_kv_heads or shape[2] != self._page_bytes:
+            raise ValueError(f"pool must be uint8 [num_blocks, {self.num_kv_heads}, {self._page_bytes}]")
 
     def _check_bt(self, bt, batch):
         if bt.dim() != 2 or bt.shape[0] != batch:
@@ -399,16 +401,41 @@ class Context:
                   _stream(stream)), name)
 
     # -- page plan and dense pages
-    def _on_device(self, *tensors):
-        """Every tensor (None apart) is on the device that was current when the context was made."""
-        for t in tensors:
-            if t is not None and t.device != self._device:
-                raise ValueError(f"tensors must be on {self._device}, got {t.device}")
+    def _addr(self, t, dtype, name):
+        """Address of a contiguous tensor of `dtype` on the context's device (None -> NULL)."""
+        if t is None:
+            return None
+        if t.dtype is not dtype:
+            raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+        if t.get_device() != self._device:
+            raise ValueError(f"{name} must be a CUDA tensor on device {self._device}, got {t.device}")
+        if not t.is_contiguous():
+            raise ValueError(f"{name} must be contiguous")
+        return t.data_ptr()
+
+    def _raw_stream(self, stream):
+        if stream is None:
+            import torch
+
+            return torch._C._cuda_getCurrentRawStream(self._device)
+        return _stream(stream)
 
     def _elem(self):
         import torch
 
         return torch.bfloat16 if self.cfg.key_format == TQ_ELEM_BF16 else torch.float16
+
+    def _rows_of(self, t, heads, elem, name):
+        """Address and row stride of t [n, heads, d]: each row whole, rows any multiple of 8 elements apart."""
+        shape, d = t.shape, self.head_dim
+        if len(shape) != 3 or shape[1] != heads or shape[2] != d or t.dtype is not elem:
+            raise ValueError(f"{name} must be {elem} [n, {heads}, {d}]")
+        if t.get_device() != self._device:
+            raise ValueError(f"{name} must be a CUDA tensor on device {self._device}, got {t.device}")
+        row, head, one = t.stride()
+        if one != 1 or (heads > 1 and head != d):
+            raise ValueError(f"{name}: the heads of a row must be contiguous")
+        return t.data_ptr(), row if shape[0] > 1 else heads * d
 
     def plan_pages(self, ctx_len, new_len, block_table, queue, queue_state, lengths, token_start, slots, queue_state_out,
                    num_blocks, positions=None, rows=None, n_paged=None, n_ring=None, ring_capacity=0, stream=None):
@@ -417,49 +444,40 @@ class Context:
         int32 [2]; token_start int32 [B + 1]; slots int64 [max_tokens]; positions, rows int32 [max_tokens]."""
         import torch
 
-        bsz, i32 = ctx_len.numel(), torch.int32
+        bsz, n, i32, addr = ctx_len.numel(), slots.numel(), torch.int32, self._addr
         self._check_bt(block_table, bsz)
-        if any(t is not None and t.numel() != bsz for t in (new_len, lengths, n_paged, n_ring)):
+        if (new_len.numel() != bsz or lengths.numel() != bsz or (n_paged is not None and n_paged.numel() != bsz)
+                or (n_ring is not None and n_ring.numel() != bsz)):
             raise ValueError("new_len, lengths, n_paged and n_ring must be [batch]")
         if queue_state.numel() != 2 or queue_state_out.numel() != 2 or token_start.numel() != bsz + 1:
             raise ValueError("queue_state and queue_state_out must be [2] and token_start [batch + 1]")
-        n = slots.numel()
-        if any(t is not None and t.numel() != n for t in (positions, rows)):
+        if (positions is not None and positions.numel() != n) or (rows is not None and rows.numel() != n):
             raise ValueError("positions and rows must be [max_tokens], like slots")
-        self._on_device(ctx_len, new_len, block_table, queue, queue_state, lengths, token_start, slots, queue_state_out,
-                        positions, rows, n_paged, n_ring)
-        _check(lib.tq_plan_pages(self.ptr, _dev(ctx_len, i32, "ctx_len"), _dev(new_len, i32, "new_len"), bsz, ring_capacity,
-                                 _dev(block_table, i32, "block_table"), block_table.shape[1], num_blocks,
-                                 _dev(queue, i32, "queue"), queue.numel(), _dev(queue_state, i32, "queue_state"),
-                                 _dev(lengths, i32, "lengths"), _dev(n_paged, i32, "n_paged"), _dev(n_ring, i32, "n_ring"),
-                                 _dev(token_start, i32, "token_start"), _dev(slots, torch.int64, "slots"),
-                                 _dev(positions, i32, "positions"), _dev(rows, i32, "rows"), n,
-                                 _dev(queue_state_out, i32, "queue_state_out"), _stream(stream)), "tq_plan_pages")
-
-    def _rows_of(self, t, heads, name):
-        """Data pointer and row stride of t [n, heads, d]: each row whole, rows any multiple of 8 elements apart."""
-        n, d = t.shape[0], self.head_dim
-        if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != d or t.dtype != self._elem():
-            raise ValueError(f"{name} must be {self._elem()} [n, {heads}, {d}]")
-        if not t.is_cuda:
-            raise ValueError(f"{name} must be a CUDA tensor")
-        if t.stride(2) != 1 or (heads > 1 and t.stride(1) != d):
-            raise ValueError(f"{name}: the heads of a row must be contiguous")
-        return t.data_ptr(), t.stride(0) if n > 1 else heads * d
+        st = lib.tq_plan_pages(self.ptr, addr(ctx_len, i32, "ctx_len"), addr(new_len, i32, "new_len"), bsz, ring_capacity,
+                               addr(block_table, i32, "block_table"), block_table.shape[1], num_blocks,
+                               addr(queue, i32, "queue"), queue.numel(), addr(queue_state, i32, "queue_state"),
+                               addr(lengths, i32, "lengths"), addr(n_paged, i32, "n_paged"), addr(n_ring, i32, "n_ring"),
+                               addr(token_start, i32, "token_start"), addr(slots, torch.int64, "slots"),
+                               addr(positions, i32, "positions"), addr(rows, i32, "rows"), n,
+                               addr(queue_state_out, i32, "queue_state_out"), self._raw_stream(stream))
+        if st:
+            raise TQError(st, "tq_plan_pages")
 
     def paged_store(self, k, v, slots, pool, stream=None):
         """tq_paged_store: k, v [n_tokens, Hkv, d] of the context's 16-bit type (rows may be strided) into the pages;
         slots int64 [n_tokens], negative to skip a token."""
         import torch
 
-        kp, ks = self._rows_of(k, self.num_kv_heads, "k")
-        vp, vs = self._rows_of(v, self.num_kv_heads, "v")
-        if v.shape[0] != k.shape[0] or slots.numel() != k.shape[0]:
+        elem, n = self._elem(), k.shape[0]
+        kp, ks = self._rows_of(k, self.num_kv_heads, elem, "k")
+        vp, vs = self._rows_of(v, self.num_kv_heads, elem, "v")
+        if v.shape[0] != n or slots.numel() != n:
             raise ValueError("k, v must be [n_tokens, Hkv, d] and slots [n_tokens]")
         self._check_pool(pool)
-        self._on_device(k, v, slots, pool)
-        _check(lib.tq_paged_store(self.ptr, kp, vp, ks, vs, _dev(slots, torch.int64, "slots"), k.shape[0],
-                                  _dev(pool, torch.uint8, "pool"), pool.shape[0], _stream(stream)), "tq_paged_store")
+        st = lib.tq_paged_store(self.ptr, kp, vp, ks, vs, self._addr(slots, torch.int64, "slots"), n,
+                                self._addr(pool, torch.uint8, "pool"), pool.shape[0], self._raw_stream(stream))
+        if st:
+            raise TQError(st, "tq_paged_store")
 
     def paged_workspace_size(self, batch: int) -> int:
         n = C.c_size_t()
@@ -471,19 +489,18 @@ class Context:
         [batch, Hq, d], lse fp32 [batch, Hq] or None; window 0 for all positions, scale 0 for 1 / sqrt(d)."""
         import torch
 
-        bsz = q.shape[0]
-        qp, qs = self._rows_of(q, self.num_q_heads, "q")
+        qp, qs = self._rows_of(q, self.num_q_heads, self._elem(), "q")
+        bsz, f32, i32, u8, addr = q.shape[0], torch.float32, torch.int32, torch.uint8, self._addr
         if out.shape != q.shape or lengths.numel() != bsz or (lse is not None and lse.shape != q.shape[:2]):
             raise ValueError("out must be [batch, Hq, d], lengths [batch] and lse [batch, Hq]")
         self._check_pool(pool)
         self._check_bt(block_table, bsz)
-        self._on_device(q, pool, block_table, lengths, out, workspace, lse)
-        f32, i32 = torch.float32, torch.int32
-        _check(lib.tq_paged_attention(self.ptr, qp, qs, bsz, _dev(pool, torch.uint8, "pool"), pool.shape[0],
-                                      _dev(block_table, i32, "block_table"), block_table.shape[1],
-                                      _dev(lengths, i32, "lengths"), window, scale, _dev(out, f32, "out"),
-                                      _dev(lse, f32, "lse"), _dev(workspace, torch.uint8, "workspace"), workspace.numel(),
-                                      _stream(stream)), "tq_paged_attention")
+        st = lib.tq_paged_attention(self.ptr, qp, qs, bsz, addr(pool, u8, "pool"), pool.shape[0],
+                                    addr(block_table, i32, "block_table"), block_table.shape[1],
+                                    addr(lengths, i32, "lengths"), window, scale, addr(out, f32, "out"), addr(lse, f32, "lse"),
+                                    addr(workspace, u8, "workspace"), workspace.numel(), self._raw_stream(stream))
+        if st:
+            raise TQError(st, "tq_paged_attention")
 
     # -- diagnostics
     def device_errors(self, stream=None) -> int:

@@ -87,7 +87,8 @@ struct PagedCfg {
 struct PagedPlan {
   int teams;       // most teams (CTAs, or warps)
   int team_warps;  // warps of a team: all of a CTA's, or 1
-  int min_pages;   // a team gets at least about this many pages
+  int lead;        // a segment's work beside its pages, in pages
+  int min_log2;    // a team gets at least about 2^min_log2 of the line
   int tau;         // cuts this near a segment's end move there
   int groups;      // query-head groups per KV head
   int scan;        // entries of the scan (threads of a CTA)
@@ -97,7 +98,7 @@ struct PagedWork {
   PagedArgs a;
   PagedPlan p;
   int q_bf16;
-  int64_t* pre;   // workspace: scan of the pages, [scan + 1]
+  int64_t* pre;   // workspace: scan of the line, [scan + 1]
   float* parts;   // workspace: [2 * teams][part]
 };
 
@@ -115,20 +116,17 @@ __device__ __forceinline__ Seq seq_of(const PagedArgs& a, int b) {
   s.pages = s.len ? (s.len + kPage - 1) / kPage - s.first : 0;
   return s;
 }
+// Length of one segment of the sequence on the line.
+__device__ __forceinline__ int span_of(const PagedPlan& p, const Seq& s) { return s.pages ? s.pages + p.lead : 0; }
 
-// Teams in use and the reach of a segment's end, for `work` pages in all.
-struct Split {
-  int64_t work;
-  int teams, tau;
-};
-__device__ __forceinline__ Split split_of(const PagedPlan& p, int64_t work) {
-  Split s;
-  s.work = work;
-  const int64_t t = work / p.min_pages;
-  s.teams = t < 1 ? 1 : t < p.teams ? (int)t : p.teams;
-  const int64_t quarter = work / s.teams / 4;
-  s.tau = quarter < p.tau ? (int)quarter : p.tau;
-  return s;
+__device__ __forceinline__ int64_t divide(int64_t n, int64_t d) {  // n, d >= 0
+  return ((uint64_t)n | (uint64_t)d) >> 32 ? n / d : (int64_t)((uint32_t)n / (uint32_t)d);
+}
+
+// Teams in use for a line of `work`.
+__device__ __forceinline__ int teams_of(const PagedPlan& p, int64_t work) {
+  const int64_t t = work >> p.min_log2;
+  return t < 1 ? 1 : t < p.teams ? (int)t : p.teams;
 }
 
 // ---------------------------------------------------------------- PTX
@@ -233,72 +231,74 @@ __device__ __forceinline__ uint32_t take_part(float& x, float& y) {
   return *reinterpret_cast<const uint32_t*>(&h);
 }
 
-// ---------------------------------------------------------------- scan and walk over the line of pages
+// ---------------------------------------------------------------- scan and walk over the line
 struct Scan {
-  const int64_t* pre;  // pages in front of each entry of `stride` sequences
+  const int64_t* pre;  // the line in front of each entry of `stride` sequences
   int stride, n;
   int64_t heads;       // segments per sequence
 };
 
-// The segment that page x of the line belongs to: sequence b, segment hg of it, page p of `s.pages`.
+// The segment at point x of the line: sequence b, segment hg of it, at `at` of its `span`.  For a whole warp.
 struct At {
-  int b, hg, p;
+  int b, hg, at, span;
   Seq s;
 };
-__device__ __forceinline__ At locate(const PagedArgs& a, const Scan& sc, int64_t x) {
-  int lo = 0, hi = sc.n - 1;
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) >> 1;
-    if (sc.pre[mid] <= x) lo = mid;
-    else hi = mid - 1;
+__device__ __forceinline__ At locate(const PagedArgs& a, const PagedPlan& p, const Scan& sc, int64_t x, int lane) {
+  int e = -1;  // the last entry that does not begin behind x
+  for (int i = 0; i < sc.n; i += 32) {
+    const int k = __popc(__ballot_sync(kFull, i + lane < sc.n && sc.pre[i + lane] <= x));
+    e += k;
+    if (k < 32) break;
   }
-  At at;
-  int64_t acc = sc.pre[lo];
-  at.b = lo * sc.stride;
-  at.s = seq_of(a, at.b);
-  while (x >= acc + at.s.pages * sc.heads && at.b + 1 < a.batch) {
-    acc += at.s.pages * sc.heads;
-    at.s = seq_of(a, ++at.b);
+  At r;
+  int64_t acc = sc.pre[e];
+  r.b = e * sc.stride;
+  for (;;) {
+    r.s = seq_of(a, r.b);
+    r.span = span_of(p, r.s);
+    if (x < acc + r.span * sc.heads || r.b + 1 >= a.batch) break;
+    acc += r.span * sc.heads;
+    ++r.b;
   }
-  const int64_t r = x - acc;
-  at.hg = (int)(r / at.s.pages);
-  at.p = (int)(r - (int64_t)at.hg * at.s.pages);
-  return at;
+  r.hg = (int)divide(x - acc, r.span);
+  r.at = (int)(x - acc - (int64_t)r.hg * r.span);
+  return r;
 }
 
-// Cut t of the line, moved to a segment's end within reach.
-__device__ __forceinline__ int64_t cut_of(const PagedArgs& a, const Scan& sc, const Split& sp, int t) {
-  if (t <= 0) return 0;
-  if (t >= sp.teams) return sp.work;
-  const int64_t x = t * sp.work / sp.teams;
-  const At at = locate(a, sc, x);
-  if (at.p <= sp.tau) return x - at.p;
-  if (at.s.pages - at.p <= sp.tau) return x - at.p + at.s.pages;
+// Moves a cut at x, which is in segment r, to that segment's end or beginning where it is near.
+__device__ __forceinline__ int64_t settle(const PagedPlan& p, const At& r, int64_t x) {
+  if (r.at <= p.lead + p.tau) return x - r.at;
+  if (r.span - r.at <= p.tau) return x - r.at + r.span;
   return x;
 }
 
 // A warp's way along its team's piece: portions (the piece's share of one segment), and in a portion the
 // pages p + wt, p + wt + tw, ... of the segment.
 struct Walk {
-  int b, hg, p, take, n;  // segment, first page of the portion, its pages, this warp's number of them
+  int b, hg;
+  int at, end, span;  // the portion is at .. end of the segment's span
+  int p, take, n;     // its first page, its pages, this warp's number of them
   Seq s;
-  int64_t left;           // pages of the team's piece from this portion on
-  __device__ __forceinline__ void open(int wt, int tw) {
-    take = left < s.pages - p ? (int)left : s.pages - p;
-    n = take > wt ? (take - wt + tw - 1) / tw : 0;
+  int64_t left;       // what the team has from this portion on
+  __device__ __forceinline__ void open(const PagedPlan& pl, int wt) {
+    end = left < span - at ? at + (int)left : span;
+    p = max(at - pl.lead, 0);
+    take = max(end - pl.lead - p, 0);
+    n = pl.team_warps == 1 ? take : take > wt ? (take - wt + pl.team_warps - 1) / pl.team_warps : 0;
   }
-  __device__ __forceinline__ bool next(const PagedArgs& a, int heads, int wt, int tw) {
-    left -= take;
+  __device__ __forceinline__ bool next(const PagedArgs& a, const PagedPlan& pl, int heads, int wt) {
+    left -= end - at;
     if (left <= 0) return false;
-    p = 0;
+    at = 0;
     if (++hg == heads) {
       hg = 0;
       do {
         if (++b >= a.batch) return false;
         s = seq_of(a, b);
       } while (s.pages == 0);
+      span = span_of(pl, s);
     }
-    open(wt, tw);
+    open(pl, wt);
     return true;
   }
 };
@@ -319,11 +319,14 @@ __global__ void __launch_bounds__(PagedCfg<KIND, D, NT>::THREADS, 1)
   const uint32_t stage0 = sm_addr(sm) + wid * S * C::PAGE, bar0 = sm_addr(sm + C::OFF_BAR) + wid * S * 16;
   const uint32_t exp0 = sm_addr(sm + C::OFF_EXP) + wid * S * C::EXP;
 
+  // what needs no input of the stream comes before the wait for the kernel in front
   asm volatile("griddepcontrol.launch_dependents;");
+  if (tid == 0) asm volatile("prefetch.tensormap [%0];" ::"l"(&map) : "memory");
   if (lane < 2 * S) bar_init(bar0 + 8 * lane, 1);
   asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  asm volatile("griddepcontrol.wait;" ::: "memory");
 
-  // ---- scan: pages in front of each entry of `stride` sequences
+  // ---- scan: the line in front of each entry of `stride` sequences
   Scan sc;
   sc.pre = pre;
   sc.stride = (a.batch + C::THREADS - 1) / C::THREADS;
@@ -334,7 +337,7 @@ __global__ void __launch_bounds__(PagedCfg<KIND, D, NT>::THREADS, 1)
   for (int b = tid * sc.stride; b < min((tid + 1) * sc.stride, a.batch); ++b) {
     const Seq s = seq_of(a, b);
     bad_len |= s.bad;
-    own += (int64_t)s.pages * heads;
+    own += (int64_t)span_of(w.p, s) * heads;
   }
   int64_t inc = own;
 #pragma unroll
@@ -362,23 +365,28 @@ __global__ void __launch_bounds__(PagedCfg<KIND, D, NT>::THREADS, 1)
   if (work == 0) return;
 
   // ---- this team's piece
-  const Split sp = split_of(w.p, work);
-  const int tw = w.p.team_warps, wt = tw == 1 ? 0 : wid;
-  const int team = tw == 1 ? blockIdx.x * NW + wid : blockIdx.x;
-  if (team >= sp.teams) return;
-  const int64_t mine = cut_of(a, sc, sp, team + (lane >> 4));  // both ends at once, half a warp each
-  const int64_t x0 = __shfl_sync(kFull, mine, 0), x1 = __shfl_sync(kFull, mine, 16);
-  if (x0 >= x1) return;
-
+  const int teams = teams_of(w.p, work), tw = w.p.team_warps, wt = tw == 1 ? 0 : wid;
+  const int team = tw == 1 ? wid * gridDim.x + blockIdx.x : blockIdx.x;  // warps: an SM's are apart in the line
+  if (team >= teams) return;
   Walk out, in;  // the portion being computed, and the one being fetched
   {
-    const At at = locate(a, sc, x0);
-    out.b = at.b;
-    out.hg = at.hg;
-    out.p = at.p;
-    out.s = at.s;
+    int64_t x0 = divide((int64_t)team * work, teams), x1 = work;
+    At r = locate(a, w.p, sc, x0, lane);
+    x0 = settle(w.p, r, x0);
+    if (team + 1 < teams) {
+      x1 = divide((int64_t)(team + 1) * work, teams);
+      x1 = settle(w.p, locate(a, w.p, sc, x1, lane), x1);
+    }
+    if (x0 >= x1) return;
+    if (r.at <= w.p.lead + w.p.tau) r.at = 0;
+    else if (r.span - r.at <= w.p.tau) r = locate(a, w.p, sc, x0, lane);  // the next segment
+    out.b = r.b;
+    out.hg = r.hg;
+    out.at = r.at;
+    out.span = r.span;
+    out.s = r.s;
     out.left = x1 - x0;
-    out.open(wt, tw);
+    out.open(w.p, wt);
     in = out;
   }
 
@@ -390,7 +398,7 @@ __global__ void __launch_bounds__(PagedCfg<KIND, D, NT>::THREADS, 1)
   // Step to the next page of this warp: its tile in `tile` (-1: a bad id); false when there is none.
   auto fetch_next = [&]() -> bool {
     while (!in_done && in_i == in.n) {
-      in_done = !in.next(a, heads, wt, tw);
+      in_done = !in.next(a, w.p, heads, wt);
       in_i = 0;
     }
     if (in_done) return false;
@@ -447,7 +455,7 @@ __global__ void __launch_bounds__(PagedCfg<KIND, D, NT>::THREADS, 1)
 
   // ================================================================ portions
 #pragma unroll 1
-  for (bool more = true; more; more = out.next(a, heads, wt, tw)) {
+  for (bool more = true; more; more = out.next(a, w.p, heads, wt)) {
     const int kvh = out.hg / w.p.groups, h0 = (out.hg - kvh * w.p.groups) * C::HEADS;
     const int nh = min(C::HEADS, a.n_rep - h0);
     const int64_t head0 = (int64_t)kvh * a.n_rep + h0;
@@ -718,10 +726,10 @@ __global__ void __launch_bounds__(PagedCfg<KIND, D, NT>::THREADS, 1)
     // dims of accumulator rows g and g + 8 of tile j
     auto dim0 = [&](int j) { return F8 ? 16 * j + 2 * g : 16 * j + g; };
     constexpr int DIM1 = F8 ? 1 : 8;
-    const bool all = out.p == 0 && out.take == out.s.pages;
+    const bool all = out.at == 0 && out.end == out.span;
     // partials: [heads][D] sums, then [heads] references and [heads] totals; a portion that continues a
     // segment takes the team's first slot, one that begins a segment the second
-    float* part = w.parts + ((int64_t)team * 2 + (out.p == 0)) * (C::HEADS * (D + 2));
+    float* part = w.parts + ((int64_t)team * 2 + (out.at == 0)) * (C::HEADS * (D + 2));
     if (tw == 1) {
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
@@ -814,33 +822,39 @@ __global__ void __launch_bounds__(PagedCfg<KIND, D, NT>::THREADS, 1)
 }
 
 // Joins the portions of the segments that more than one team had, and writes the rows of empty sequences.  One
-// CTA per (segment, share of its heads); a thread per dim.
+// CTA per (segment, share of its heads).  Its warps take every fourth portion, a lane D / 32 dims, four
+// portions in flight per warp: a chain of loads from L2 is what this kernel would otherwise wait for.
+constexpr int kMergeWarps = 4;
 template <int D, int HEADS>
-__global__ void __launch_bounds__(128) paged_merge_kernel(const __grid_constant__ PagedWork w) {
+__global__ void __launch_bounds__(kMergeWarps * 32) paged_merge_kernel(const __grid_constant__ PagedWork w) {
+  constexpr int V = D / 32, VL = V < 4 ? V : 4;  // dims of a lane, and of one load
   const PagedArgs& a = w.a;
+  __shared__ float sx[kMergeWarps][D], sl[kMergeWarps], sm_max[kMergeWarps];
+  const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
+  asm volatile("griddepcontrol.launch_dependents;");
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int heads = a.hkv * w.p.groups;
-  const int64_t seg = blockIdx.x;
-  const int b = (int)(seg / heads), hg = (int)(seg - (int64_t)b * heads);
+  const int b = blockIdx.x / (unsigned)heads, hg = blockIdx.x - (unsigned)b * heads;
   const int kvh = hg / w.p.groups, h0 = (hg - kvh * w.p.groups) * HEADS, nh = min(HEADS, a.n_rep - h0);
   const int64_t row0 = (int64_t)b * a.hq + (int64_t)kvh * a.n_rep + h0;
+  const int stride = (a.batch + w.p.scan - 1) / w.p.scan, e = b / stride;
+  int64_t first = w.pre[e];
+  const int64_t work = w.pre[w.p.scan];
   const Seq s = seq_of(a, b);
   if (s.pages == 0) {
     for (int h = blockIdx.y; h < nh; h += gridDim.y) {
-      for (int i = threadIdx.x; i < D; i += 128) a.out[(row0 + h) * D + i] = 0.f;
+      for (int i = threadIdx.x; i < D; i += kMergeWarps * 32) a.out[(row0 + h) * D + i] = 0.f;
       if (threadIdx.x == 0 && a.lse) a.lse[row0 + h] = -CUDART_INF_F;
     }
     return;
   }
-  const int stride = (a.batch + w.p.scan - 1) / w.p.scan, e = b / stride;
-  int64_t first = w.pre[e];
-  for (int i = e * stride; i < b; ++i) first += (int64_t)seq_of(a, i).pages * heads;
-  first += (int64_t)hg * s.pages;
-  const int64_t last = first + s.pages;
-  const Split sp = split_of(w.p, w.pre[w.p.scan]);
-  // cuts floor(t work / teams) that lie more than tau inside the segment
-  const int64_t ta = ((first + sp.tau + 1) * sp.teams + sp.work - 1) / sp.work;
-  const int64_t tb = ((last - sp.tau) * sp.teams + sp.work - 1) / sp.work - 1;
+  const int span = span_of(w.p, s), teams = teams_of(w.p, work);
+  for (int i = e * stride; i < b; ++i) first += (int64_t)span_of(w.p, seq_of(a, i)) * heads;
+  first += (int64_t)hg * span;
+  const int64_t last = first + span;
+  // cuts floor(t work / teams) that stay inside the segment
+  const int64_t ta = divide((first + w.p.lead + w.p.tau + 1) * teams + work - 1, work);
+  const int64_t tb = divide((last - w.p.tau) * teams + work - 1, work) - 1;
   if (tb < ta) return;  // one team had it
   const int n = (int)(tb - ta) + 2;
   constexpr int PART = HEADS * (D + 2);
@@ -848,24 +862,53 @@ __global__ void __launch_bounds__(128) paged_merge_kernel(const __grid_constant_
   auto part = [&](int k) { return w.parts + (k == 0 ? (ta - 1) * 2 + 1 : (ta + k - 1) * 2) * (int64_t)PART; };
   for (int h = blockIdx.y; h < nh; h += gridDim.y) {
     float M = -CUDART_INF_F;
-    for (int k = 0; k < n; ++k) M = fmaxf(M, part(k)[HEADS * D + h]);
-    const float ref = M == -CUDART_INF_F ? 0.f : M;
-    float L = 0.f, x[(D + 127) / 128];
+    for (int k = threadIdx.x; k < n; k += kMergeWarps * 32) M = fmaxf(M, part(k)[HEADS * D + h]);
+    M = warp_max(M);
+    if (lane == 0) sm_max[wid] = M;
+    __syncthreads();
 #pragma unroll
-    for (int i = 0; i < (D + 127) / 128; ++i) x[i] = 0.f;
-    for (int k = 0; k < n; ++k) {
+    for (int i = 0; i < kMergeWarps; ++i) M = fmaxf(M, sm_max[i]);
+    const float ref = M == -CUDART_INF_F ? 0.f : M;
+    float L = 0.f, x[V];
+#pragma unroll
+    for (int i = 0; i < V; ++i) x[i] = 0.f;
+#pragma unroll 4
+    for (int k = wid; k < n; k += kMergeWarps) {
       const float* p = part(k);
       const float c = ex2(p[HEADS * D + h] - ref);
       L = fmaf(c, p[HEADS * (D + 1) + h], L);
 #pragma unroll
-      for (int i = 0; i < (D + 127) / 128; ++i)
-        if (D >= 128 || threadIdx.x < D) x[i] = fmaf(c, p[h * D + i * 128 + threadIdx.x], x[i]);
+      for (int i = 0; i < V; i += VL) {
+        const float* q = p + h * D + (i / VL * 32 + lane) * VL;
+        if constexpr (VL == 2) {
+          const float2 y = *reinterpret_cast<const float2*>(q);
+          x[0] = fmaf(c, y.x, x[0]);
+          x[1] = fmaf(c, y.y, x[1]);
+        } else {
+          const float4 y = *reinterpret_cast<const float4*>(q);
+          x[i] = fmaf(c, y.x, x[i]);
+          x[i + 1] = fmaf(c, y.y, x[i + 1]);
+          x[i + 2] = fmaf(c, y.z, x[i + 2]);
+          x[i + 3] = fmaf(c, y.w, x[i + 3]);
+        }
+      }
     }
-    const float f = L == 0.f ? 0.f : 1.f / L;
 #pragma unroll
-    for (int i = 0; i < (D + 127) / 128; ++i)
-      if (D >= 128 || threadIdx.x < D) a.out[(row0 + h) * D + i * 128 + threadIdx.x] = x[i] * f;
+    for (int i = 0; i < V; ++i) sx[wid][(i / VL * 32 + lane) * VL + i % VL] = x[i];
+    if (lane == 0) sl[wid] = L;
+    __syncthreads();
+    L = 0.f;
+#pragma unroll
+    for (int i = 0; i < kMergeWarps; ++i) L += sl[i];
+    const float f = L == 0.f ? 0.f : 1.f / L;
+    for (int i = threadIdx.x; i < D; i += kMergeWarps * 32) {
+      float y = 0.f;
+#pragma unroll
+      for (int k = 0; k < kMergeWarps; ++k) y += sx[k][i];
+      a.out[(row0 + h) * D + i] = y * f;
+    }
     if (threadIdx.x == 0 && a.lse) a.lse[row0 + h] = (M - kWeightUp + log2f(L)) * 0.69314718055994530942f;
+    if (h + (int)gridDim.y < nh) __syncthreads();
   }
 }
 
@@ -880,8 +923,9 @@ PagedPlan plan_of(const tq_ctx* ctx, int batch) {
   // Many segments: one warp each, no joining inside the CTA.  Few: the CTA's warps share one.
   p.team_warps = segments >= 4 * (int64_t)ctx->sm_count ? 1 : C::NW;
   p.teams = ctx->sm_count * (p.team_warps == 1 ? C::NW : 1);
-  p.min_pages = p.team_warps == 1 ? 2 : C::NW;
-  p.tau = p.team_warps == 1 ? 4 : C::NW;
+  p.lead = p.team_warps == 1 ? 2 : 8;
+  p.min_log2 = p.team_warps == 1 ? 2 : 4;
+  p.tau = 4;
   p.scan = C::THREADS;
   return p;
 }
@@ -912,24 +956,29 @@ cudaError_t launch_one(tq_ctx* ctx, const PagedArgs& a, void* workspace, cudaStr
   auto kern = paged_kernel<KIND, D, NT>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
   if (e != cudaSuccess) return e;
+  // Both launches may begin before the kernel in front of them ends (each waits for it before it reads or
+  // writes memory), which hides their launch and setup.
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.stream = s;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  cfg.gridDim = dim3(ctx->sm_count);
+  cfg.blockDim = dim3(C::THREADS);
+  cfg.dynamicSmemBytes = C::SMEM;
   prof_start(ctx, kProfDecode, s);
-  kern<<<ctx->sm_count, C::THREADS, C::SMEM, s>>>(map, w);
-  e = cudaGetLastError();
+  e = cudaLaunchKernelEx(&cfg, kern, map, w);
   prof_stop(ctx, kProfDecode, s);
   if (e != cudaSuccess) return e;
   ctx->launches++;
   ctx->decode_kernel = "paged_kernel";
 
   const int64_t segments = (int64_t)a.batch * a.hkv * w.p.groups;
-  cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3((unsigned)segments, segments < 1024 ? (a.n_rep < C::HEADS ? a.n_rep : C::HEADS) : 1);
-  cfg.blockDim = dim3(128);
-  cfg.stream = s;
-  cudaLaunchAttribute attr{};
-  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr.val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = &attr;
-  cfg.numAttrs = 1;
+  cfg.blockDim = dim3(kMergeWarps * 32);
+  cfg.dynamicSmemBytes = 0;
   prof_start(ctx, kProfMerge, s);
   e = cudaLaunchKernelEx(&cfg, paged_merge_kernel<D, C::HEADS>, w);
   prof_stop(ctx, kProfMerge, s);

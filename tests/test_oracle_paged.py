@@ -150,7 +150,7 @@ def test_binding_checks_shapes_before_the_library():
     ctx = object.__new__(B.Context)
     ctx.ptr = None
     ctx.cfg = B.tq_config_init(B.TQ_LAYOUT_DENSE, 64, 4, 2)
-    ctx.head_dim, ctx.num_q_heads, ctx.num_kv_heads, ctx._device = 64, 4, 2, torch.device("cuda", 0)
+    ctx.head_dim, ctx.num_q_heads, ctx.num_kv_heads, ctx._device = 64, 4, 2, 0
     i32 = lambda *s: torch.zeros(*s, dtype=torch.int32)  # noqa: E731
     q = torch.zeros(3, 4, 64, dtype=torch.float16)
     with pytest.raises(ValueError, match="CUDA"):
@@ -161,7 +161,7 @@ def test_binding_checks_shapes_before_the_library():
         ctx.paged_store(q, q, torch.zeros(3, dtype=torch.int64), None)
     ok = dict(ctx_len=i32(3), new_len=i32(3), block_table=i32(3, 2), queue=i32(4), queue_state=i32(2), lengths=i32(3),
               token_start=i32(4), slots=torch.zeros(5, dtype=torch.int64), queue_state_out=i32(2), num_blocks=4)
-    with pytest.raises(ValueError, match="tensors must be on"):
+    with pytest.raises(ValueError, match="must be a CUDA tensor"):
         ctx.plan_pages(**ok)
     for name, bad in (("new_len", i32(2)), ("token_start", i32(3)), ("queue_state", i32(1)), ("block_table", i32(2, 2)),
                       ("positions", i32(4)), ("n_ring", i32(4))):
