@@ -68,7 +68,7 @@
  * out of the compression; read by tq_paged_attention):
  *   16-bit tile, 64 d bytes: keys [16][d], then values [16][d], fp16 or bf16;
  *   8-bit tile, 32 d + 32 bytes: key codes [16][d], value codes [16][d] (e4m3), then
- *     int8 exponents of the 16 keys and of the 16 values: entry = code * 2^exponent.
+ *     int8 exponents (-126 .. 126) of the 16 keys and of the 16 values: entry = code * 2^exponent.
  */
 #ifndef TQ_H_
 #define TQ_H_

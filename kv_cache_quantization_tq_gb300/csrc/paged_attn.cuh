@@ -194,6 +194,18 @@ __device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint3
                  : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
                  : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
+// The same with nothing to add to.
+template <bool BF>
+__device__ __forceinline__ void mma_first(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  if (BF)
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+                 : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
+  else
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+                 : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
+}
 // 2^x; -inf gives +0.
 __device__ __forceinline__ float ex2(float x) {
   float y;
@@ -211,8 +223,8 @@ __device__ __forceinline__ uint32_t f16_of_e4m3_high(uint32_t four) {
   asm("{ .reg .b16 lo, hi; mov.b32 {lo, hi}, %1; cvt.rn.f16x2.e4m3x2 %0, hi; }" : "=r"(r) : "r"(four));
   return r;
 }
-// 2^e, e held to the normal range.
-__device__ __forceinline__ float power2(int e) { return __int_as_float((max(-126, min(e, 127)) + 127) << 23); }
+// 2^e for e in [-126, 127]; 0 for -127.
+__device__ __forceinline__ float power2(int e) { return __int_as_float((e + 127) << 23); }
 
 // 16-bit parts of a pair of fp32 weights: each part rounds what the ones before leave.
 template <bool BF>
@@ -391,24 +403,28 @@ __global__ void __launch_bounds__(PagedCfg<KIND, D, NT>::THREADS, 1)
   }
 
   // ---- fetching
-  int in_i = 0, ids = 0, tile = 0;
+  int in_i = 0, tiles = -1, tile = -1;
   bool in_done = false;
   uint32_t valid = 0, parity = 0, vparity = 0, issued = 0;  // bit per stage
   bool bad_id = false, dead = false;
-  // Step to the next page of this warp: its tile in `tile` (-1: a bad id); false when there is none.
+  // Step to the next page of this warp: its tile in `tile` (-1: a bad id); false when there is none.  A
+  // lane looks up every 32nd page's block.
   auto fetch_next = [&]() -> bool {
-    while (!in_done && in_i == in.n) {
-      in_done = !in.next(a, w.p, heads, wt);
-      in_i = 0;
+    if ((in_i & 31) == 0 || in_i == in.n) {
+      while (!in_done && in_i == in.n) {
+        in_done = !in.next(a, w.p, heads, wt);
+        in_i = 0;
+      }
+      if (in_done) return false;
+      tiles = -1;
+      if (in_i + lane < in.n) {
+        const int id = a.block_table[(int64_t)in.b * a.max_blocks + in.s.first + in.p + wt + (in_i + lane) * tw];
+        if (id >= 0 && id < a.num_blocks) tiles = id * a.hkv + in.hg / w.p.groups;
+        else bad_id = true;
+      }
     }
-    if (in_done) return false;
-    if ((in_i & 31) == 0 && in_i + lane < in.n)
-      ids = a.block_table[(int64_t)in.b * a.max_blocks + in.s.first + in.p + wt + (in_i + lane) * tw];
-    const int id = __shfl_sync(kFull, ids, in_i & 31);
+    tile = __shfl_sync(kFull, tiles, in_i & 31);
     ++in_i;
-    const bool ok = id >= 0 && id < a.num_blocks;
-    bad_id |= !ok;
-    tile = ok ? id * a.hkv + in.hg / w.p.groups : -1;
     return true;
   };
   auto fetch_half = [&](int st, int side) {  // lane 0
@@ -449,7 +465,8 @@ __global__ void __launch_bounds__(PagedCfg<KIND, D, NT>::THREADS, 1)
 
   uint32_t qf[C::QREG ? NT : 1][C::QREG ? KS : 1][2];
   uint2* q_sm = reinterpret_cast<uint2*>(sm + C::OFF_Q + wid * C::QBYTES);
-  float o[KS][NT][4], m[NT][2], l[NT][2], qs[NT][2];
+  // m: reference of each of the lane's heads; ref: what is subtracted from its scores, m - 7
+  float o[KS][NT][4], m[NT][2], ref[NT][2], l[NT][2], qs[NT][2];
   const float log2e_scale = a.scale * 1.44269504088896340736f;
   int st = 0;
 
@@ -507,9 +524,12 @@ __global__ void __launch_bounds__(PagedCfg<KIND, D, NT>::THREADS, 1)
       for (int i = 0; i < 2; ++i) {
         qs[nt][i] = F8 ? __shfl_sync(kFull, down, (2 * t + i) * 4) : log2e_scale;
         m[nt][i] = -CUDART_INF_F;
+        ref[nt][i] = 0.f;
         l[nt][i] = 0.f;
       }
     }
+    // pages of the segment that the sequence's end or the window cuts
+    const int cut_first = out.s.lo % kPage ? 0 : -1, cut_last = out.s.len % kPage ? out.s.pages - 1 : -1;
     if constexpr (!C::QREG) __syncwarp();
 #pragma unroll
     for (int j = 0; j < KS; ++j)
@@ -528,25 +548,24 @@ __global__ void __launch_bounds__(PagedCfg<KIND, D, NT>::THREADS, 1)
       if (dead) continue;
       issued &= ~(1u << st);
       if (here) parity ^= 1u << st;
-      int exps = 0;
+      int ek0 = 0, ek1 = 0, ev0 = 0, ev1 = 0;
       if (here) {
-        if (F8) {
-          // lanes 0..15: exponents of the keys, 16..31: of the values
-          asm volatile("ld.shared.s8 %0, [%1];" : "=r"(exps) : "r"(exp0 + st * C::EXP + lane) : "memory");
+        if (F8) {  // exponents of tokens g and g + 8, keys and values
+          const uint32_t ea = exp0 + st * C::EXP + g;
+          asm volatile("ld.shared.s8 %0, [%1];" : "=r"(ek0) : "r"(ea) : "memory");
+          asm volatile("ld.shared.s8 %0, [%1];" : "=r"(ek1) : "r"(ea + 8) : "memory");
+          asm volatile("ld.shared.s8 %0, [%1];" : "=r"(ev0) : "r"(ea + 16) : "memory");
+          asm volatile("ld.shared.s8 %0, [%1];" : "=r"(ev1) : "r"(ea + 24) : "memory");
         }
         float s2[NT][4];
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-          for (int k = 0; k < 4; ++k) s[nt][k] = s2[nt][k] = 0.f;
         auto score = [&](int ks, const uint32_t(&af)[4], float(&acc)[NT][4]) {
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt) {
-            if constexpr (C::QREG) mma<BF>(acc[nt], af, qf[nt][ks][0], qf[nt][ks][1]);
-            else {
-              const uint2 x = q_sm[(nt * KS + ks) * 32 + lane];
-              mma<BF>(acc[nt], af, x.x, x.y);
-            }
+            uint2 x;
+            if constexpr (C::QREG) x = make_uint2(qf[nt][ks][0], qf[nt][ks][1]);
+            else x = q_sm[(nt * KS + ks) * 32 + lane];
+            if (ks < 2) mma_first<BF>(acc[nt], af, x.x, x.y);
+            else mma<BF>(acc[nt], af, x.x, x.y);
           }
         };
         if constexpr (F8) {
@@ -586,12 +605,12 @@ __global__ void __launch_bounds__(PagedCfg<KIND, D, NT>::THREADS, 1)
 
       if (here) {
         // ---- weights
-        const int pg = out.s.first + out.p + wt + i * tw;  // page of the sequence
-        const int t_lo = out.s.lo - pg * kPage, t_hi = out.s.len - pg * kPage;
-        const bool whole = t_lo <= 0 && t_hi >= kPage;
-        const bool ok0 = g >= t_lo && g < t_hi, ok1 = g + 8 >= t_lo && g + 8 < t_hi;
+        const int rel = out.p + wt + i * tw;  // page of the segment
+        const bool whole = rel != cut_first && rel != cut_last;
+        const int t_lo = out.s.lo - (out.s.first + rel) * kPage, t_hi = out.s.len - (out.s.first + rel) * kPage;
+        auto counts = [&](int tok) { return tok >= t_lo && tok < t_hi; };
         if (F8) {
-          const float f0 = power2(__shfl_sync(kFull, exps, g)), f1 = power2(__shfl_sync(kFull, exps, g + 8));
+          const float f0 = power2(ek0), f1 = power2(ek1);
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt) {
             s[nt][0] *= f0;
@@ -604,11 +623,20 @@ __global__ void __launch_bounds__(PagedCfg<KIND, D, NT>::THREADS, 1)
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            s[nt][k] *= qs[nt][k & 1];
-            if (!whole && !(k < 2 ? ok0 : ok1)) s[nt][k] = -CUDART_INF_F;
-            raise |= s[nt][k] > m[nt][k & 1] + kLazy;
-          }
+          for (int k = 0; k < 4; ++k) s[nt][k] *= qs[nt][k & 1];
+        if (!whole) {  // rows that do not count are whatever memory held
+          const bool ok0 = counts(g), ok1 = counts(g + 8);
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int k = 0; k < 4; ++k) s[nt][k] = (k < 2 ? ok0 : ok1) ? s[nt][k] : -CUDART_INF_F;
+          ev0 = ok0 ? ev0 : -127;
+          ev1 = ok1 ? ev1 : -127;
+        }
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int k = 0; k < 4; ++k) raise |= s[nt][k] > m[nt][k & 1] + kLazy;
         if (__any_sync(kFull, raise)) {
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt)
@@ -620,6 +648,7 @@ __global__ void __launch_bounds__(PagedCfg<KIND, D, NT>::THREADS, 1)
               mx = fmaxf(m[nt][k], mx);
               const float c = mx == -CUDART_INF_F ? 1.f : ex2(m[nt][k] - mx);
               m[nt][k] = mx;
+              ref[nt][k] = mx == -CUDART_INF_F ? 0.f : mx - kWeightUp;
               l[nt][k] *= c;
 #pragma unroll
               for (int j = 0; j < KS; ++j) {
@@ -629,15 +658,11 @@ __global__ void __launch_bounds__(PagedCfg<KIND, D, NT>::THREADS, 1)
             }
         }
         float page_up = 1.f, w0 = 1.f, w1 = 1.f;
-        if (F8) {
-          // value exponents of the tokens that count, relative to the largest of them
-          const int tok = lane & 15;
-          const int ev = lane >= 16 && tok >= t_lo && tok < t_hi ? exps : -128;
-          const int top = __reduce_max_sync(kFull, ev);
+        if (F8) {  // value exponents relative to the largest of the page
+          const int top = __reduce_max_sync(kFull, max(ev0, ev1));
           page_up = power2(top);
-          const int e0 = __shfl_sync(kFull, exps, 16 + g), e1 = __shfl_sync(kFull, exps, 24 + g);
-          w0 = ok0 ? power2(e0 - top) : 0.f;
-          w1 = ok1 ? power2(e1 - top) : 0.f;
+          w0 = power2(max(ev0 - top, -127));
+          w1 = power2(max(ev1 - top, -127));
         }
         constexpr int PARTS = BF ? 3 : 2;
         uint32_t pf[NT][PARTS][2];
@@ -645,10 +670,7 @@ __global__ void __launch_bounds__(PagedCfg<KIND, D, NT>::THREADS, 1)
         for (int nt = 0; nt < NT; ++nt) {
           float p[4];
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const float ref = m[nt][k & 1] == -CUDART_INF_F ? 0.f : m[nt][k & 1];
-            p[k] = ex2(s[nt][k] - ref + kWeightUp);
-          }
+          for (int k = 0; k < 4; ++k) p[k] = ex2(s[nt][k] - ref[nt][k & 1]);
           l[nt][0] += p[0] + p[2];
           l[nt][1] += p[1] + p[3];
           if (F8) {
@@ -663,25 +685,26 @@ __global__ void __launch_bounds__(PagedCfg<KIND, D, NT>::THREADS, 1)
             pf[nt][k][1] = movmat(take_part<BF>(p[2], p[3]));
           }
         }
-        // tokens 2 t, 2 t + 1 and + 8 of the value fragments: rows that do not count are whatever memory held
-        uint32_t keep0 = 0xffffffffu, keep1 = 0xffffffffu;
-        if (!whole) {
-          auto in_range = [&](int tok) { return tok >= t_lo && tok < t_hi; };
-          keep0 = (in_range(2 * t) ? 0xffffu : 0u) | (in_range(2 * t + 1) ? 0xffff0000u : 0u);
-          keep1 = (in_range(2 * t + 8) ? 0xffffu : 0u) | (in_range(2 * t + 9) ? 0xffff0000u : 0u);
-        }
         dead = !bar_wait(bar0 + 16 * st + 8, vparity >> st & 1);
         if (!dead) vparity ^= 1u << st;
-        auto add = [&](int j, uint32_t(&af)[4]) {
-          af[0] &= keep0;
-          af[1] &= keep0;
-          af[2] &= keep1;
-          af[3] &= keep1;
+        if (!whole) {
+          // value rows that do not count: a weight of 0 does not remove a NaN
+#pragma unroll
+          for (int k = 0; k < C::HALF / 512; ++k) {
+            const uint32_t off = (k * 32 + lane) * 16;
+            if (!counts((off / C::SWIZZLE_ROW) % kPage))
+              asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(vb + off), "r"(0) : "memory");
+          }
+          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // before the stage's next copy
+          __syncwarp();
+        }
+        auto add = [&](int j, const uint32_t(&af)[4]) {
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt) {
-            float acc[4] = {0.f, 0.f, 0.f, 0.f};
+            float acc[4];
+            mma_first<BF>(acc, af, pf[nt][PARTS - 1][0], pf[nt][PARTS - 1][1]);
 #pragma unroll
-            for (int k = PARTS - 1; k >= 0; --k) mma<BF>(acc, af, pf[nt][k][0], pf[nt][k][1]);
+            for (int k = PARTS - 2; k >= 0; --k) mma<BF>(acc, af, pf[nt][k][0], pf[nt][k][1]);
 #pragma unroll
             for (int k = 0; k < 4; ++k) o[j][nt][k] = F8 ? fmaf(acc[k], page_up, o[j][nt][k]) : o[j][nt][k] + acc[k];
           }
@@ -696,7 +719,7 @@ __global__ void __launch_bounds__(PagedCfg<KIND, D, NT>::THREADS, 1)
               for (int c = 0; c < 2; ++c) {
                 // bytes (token 2 t: dims 2 g, 2 g + 1; token 2 t + 1: the same) to (dim 2 g | dim 2 g + 1)
                 const uint32_t x = __byte_perm(r[2 * c], 0, 0x3120), y = __byte_perm(r[2 * c + 1], 0, 0x3120);
-                uint32_t af[4] = {f16_of_e4m3(x), f16_of_e4m3_high(x), f16_of_e4m3(y), f16_of_e4m3_high(y)};
+                const uint32_t af[4] = {f16_of_e4m3(x), f16_of_e4m3_high(x), f16_of_e4m3(y), f16_of_e4m3_high(y)};
                 add(2 * j + c, af);
               }
             }
@@ -818,7 +841,7 @@ __global__ void __launch_bounds__(PagedCfg<KIND, D, NT>::THREADS, 1)
       }
     if (lane == 0) flag_error(a.err, TQ_DEVERR_TIMEOUT);
   }
-  if (bad_id && lane == 0) flag_error(a.err, TQ_DEVERR_BLOCK_ID);
+  if (bad_id) flag_error(a.err, TQ_DEVERR_BLOCK_ID);
 }
 
 // Joins the portions of the segments that more than one team had, and writes the rows of empty sequences.  One
@@ -923,9 +946,9 @@ PagedPlan plan_of(const tq_ctx* ctx, int batch) {
   // Many segments: one warp each, no joining inside the CTA.  Few: the CTA's warps share one.
   p.team_warps = segments >= 4 * (int64_t)ctx->sm_count ? 1 : C::NW;
   p.teams = ctx->sm_count * (p.team_warps == 1 ? C::NW : 1);
-  p.lead = p.team_warps == 1 ? 2 : 8;
-  p.min_log2 = p.team_warps == 1 ? 2 : 4;
-  p.tau = 4;
+  p.lead = p.team_warps == 1 ? 2 : C::PAGE >= 32768 ? 2 : C::PAGE >= 16384 ? 4 : 8;
+  p.min_log2 = p.team_warps == 1 ? 2 : C::PAGE >= 32768 ? 2 : C::PAGE >= 16384 ? 3 : 4;
+  p.tau = C::PAGE >= 16384 ? 2 : 4;
   p.scan = C::THREADS;
   return p;
 }
