@@ -59,8 +59,9 @@ struct PagedCfg {
   static constexpr bool QREG = D * NT <= 128;              // query fragments in registers
   static constexpr int QBYTES = QREG ? 0 : HEADS * D * 2;  // else in shared memory, per warp
   static constexpr int SLOT = HEADS * (D + 4) * 4 + HEADS * 8;
+  static constexpr bool LENS = D < 512;  // the lengths in shared memory (no room for them at 512)
   static constexpr int LIMIT = 232448 - 1024;  // 227 KB, less the alignment of the stages
-  static constexpr int fixed(int nw) { return nw * (SLOT + QBYTES) + (nw * 32 + 1) * 8 + 64; }
+  static constexpr int fixed(int nw) { return nw * (SLOT + QBYTES) + nw * 32 * (LENS ? 8 : 4) + nw * 4; }
   static constexpr int per(int nw) { return nw * (PAGE + EXP + 16); }
   static constexpr bool fits(int nw) { return fixed(nw) + per(nw) <= LIMIT; }
   // Warps per CTA: small pages need more of them to keep the bytes in flight
@@ -76,8 +77,9 @@ struct PagedCfg {
   static constexpr int OFF_EXP = OFF_Q + NW * QBYTES;
   static constexpr int OFF_BAR = OFF_EXP + NW * S * EXP;
   static constexpr int OFF_PRE = OFF_BAR + NW * S * 16;
-  static constexpr int OFF_WARP = OFF_PRE + (THREADS + 1) * 8;
-  static constexpr int SMEM = OFF_WARP + NW * 8 + 1024;
+  static constexpr int OFF_WARP = OFF_PRE + THREADS * 4;
+  static constexpr int OFF_LEN = OFF_WARP + NW * 4;
+  static constexpr int SMEM = OFF_LEN + (LENS ? THREADS * 4 : 0) + 1024;
   static_assert(SMEM <= 232448, "shared memory");
   static constexpr int SWIZZLE_ROW = D * ES < 128 ? D * ES : 128;  // bytes of a row in one TMA box
   static constexpr int BOXES = D * ES / SWIZZLE_ROW;               // boxes per half page
@@ -87,47 +89,55 @@ struct PagedCfg {
 struct PagedPlan {
   int teams;       // most teams (CTAs, or warps)
   int team_warps;  // warps of a team: all of a CTA's, or 1
-  int lead;        // a segment's work beside its pages, in pages
+  int lead;        // a segment's work beside its pages, in units
+  int unit;        // the line counts 2^unit pages as one, so that it stays below 2^31
   int min_log2;    // a team gets at least about 2^min_log2 of the line
   int tau;         // cuts this near a segment's end move there
   int groups;      // query-head groups per KV head
-  int scan;        // entries of the scan (threads of a CTA)
 };
 
 struct PagedWork {
   PagedArgs a;
   PagedPlan p;
   int q_bf16;
-  int64_t* pre;   // workspace: scan of the line, [scan + 1]
-  float* parts;   // workspace: [2 * teams][part]
+  int2* cuts;    // workspace: per segment {team that has its beginning, pieces beside that}; written where it begins
+  float* parts;  // workspace: [2 * teams][part]
 };
 
 struct Seq {
   int len, lo, first, pages;  // length, first position seen, first page, pages seen
-  bool bad;
 };
-__device__ __forceinline__ Seq seq_of(const PagedArgs& a, int b) {
+__device__ __forceinline__ bool length_ok(const PagedArgs& a, int len) {
+  return len >= 0 && len <= (int64_t)a.max_blocks * kPage;
+}
+__device__ __forceinline__ Seq seq_of(const PagedArgs& a, int len) {
   Seq s;
-  s.len = a.lengths[b];
-  s.bad = s.len < 0 || s.len > (int64_t)a.max_blocks * kPage;
-  if (s.bad) s.len = 0;
+  s.len = length_ok(a, len) ? len : 0;
   s.lo = a.window && s.len > a.window ? s.len - a.window : 0;
   s.first = s.lo / kPage;
   s.pages = s.len ? (s.len + kPage - 1) / kPage - s.first : 0;
   return s;
 }
 // Length of one segment of the sequence on the line.
-__device__ __forceinline__ int span_of(const PagedPlan& p, const Seq& s) { return s.pages ? s.pages + p.lead : 0; }
-
-__device__ __forceinline__ int64_t divide(int64_t n, int64_t d) {  // n, d >= 0
-  return ((uint64_t)n | (uint64_t)d) >> 32 ? n / d : (int64_t)((uint32_t)n / (uint32_t)d);
+__device__ __forceinline__ int span_of(const PagedPlan& p, const Seq& s) {
+  return s.pages ? ((s.pages + (1 << p.unit) - 1) >> p.unit) + p.lead : 0;
 }
 
-// Teams in use for a line of `work`.
-__device__ __forceinline__ int teams_of(const PagedPlan& p, int64_t work) {
-  const int64_t t = work >> p.min_log2;
-  return t < 1 ? 1 : t < p.teams ? (int)t : p.teams;
-}
+// Equal pieces of the line: piece t begins at t base + min(t, rest).
+struct Pieces {
+  unsigned teams, rest, base;
+  __device__ __forceinline__ Pieces(const PagedPlan& p, unsigned work) {
+    teams = min(max(work >> p.min_log2, 1u), (unsigned)p.teams);
+    base = work / teams;
+    rest = work - base * teams;
+  }
+  __device__ __forceinline__ unsigned begin(unsigned t) const { return t * base + min(t, rest); }
+  // the first piece that begins at x or behind it
+  __device__ __forceinline__ unsigned from(unsigned x) const {
+    const unsigned big = rest * (base + 1);
+    return x <= big ? (x + base) / (base + 1) : rest + (x - big + base - 1) / base;
+  }
+};
 
 // ---------------------------------------------------------------- PTX
 __device__ __forceinline__ uint32_t sm_addr(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }
@@ -245,40 +255,48 @@ __device__ __forceinline__ uint32_t take_part(float& x, float& y) {
 
 // ---------------------------------------------------------------- scan and walk over the line
 struct Scan {
-  const int64_t* pre;  // the line in front of each entry of `stride` sequences
+  const unsigned* pre;  // the line in front of each entry of `stride` sequences
+  const int* len;      // the sequences' lengths in shared memory, or NULL
   int stride, n;
-  int64_t heads;       // segments per sequence
+  unsigned heads;      // segments per sequence
+  __device__ __forceinline__ Seq seq(const PagedArgs& a, int b) const {
+    return seq_of(a, len ? len[b] : __ldg(a.lengths + b));
+  }
 };
 
-// The segment at point x of the line: sequence b, segment hg of it, at `at` of its `span`.  For a whole warp.
+// The segment at a point of the line: sequence b, segment hg of it, at `at` of its `span`.
 struct At {
   int b, hg, at, span;
   Seq s;
 };
-__device__ __forceinline__ At locate(const PagedArgs& a, const PagedPlan& p, const Scan& sc, int64_t x, int lane) {
-  int e = -1;  // the last entry that does not begin behind x
+// The segments at x (lanes 0..15) and y (lanes 16..31).  For a whole warp.
+__device__ __forceinline__ At locate(const PagedArgs& a, const PagedPlan& p, const Scan& sc, unsigned x, unsigned y, int lane) {
+  int ex = -1, ey = -1;  // the last entries that do not begin behind x and y
   for (int i = 0; i < sc.n; i += 32) {
-    const int k = __popc(__ballot_sync(kFull, i + lane < sc.n && sc.pre[i + lane] <= x));
-    e += k;
-    if (k < 32) break;
+    const unsigned v = i + lane < sc.n ? sc.pre[i + lane] : 0xffffffffu;
+    ex += __popc(__ballot_sync(kFull, v <= x));
+    const uint32_t m = __ballot_sync(kFull, v <= y);
+    ey += __popc(m);
+    if (m != kFull) break;
   }
+  const int e = lane < 16 ? ex : ey;
   At r;
-  int64_t acc = sc.pre[e];
+  unsigned at = (lane < 16 ? x : y) - sc.pre[e];
   r.b = e * sc.stride;
   for (;;) {
-    r.s = seq_of(a, r.b);
+    r.s = sc.seq(a, r.b);
     r.span = span_of(p, r.s);
-    if (x < acc + r.span * sc.heads || r.b + 1 >= a.batch) break;
-    acc += r.span * sc.heads;
+    if (sc.stride == 1 || at < r.span * sc.heads || r.b + 1 >= a.batch) break;
+    at -= r.span * sc.heads;
     ++r.b;
   }
-  r.hg = (int)divide(x - acc, r.span);
-  r.at = (int)(x - acc - (int64_t)r.hg * r.span);
+  r.hg = at / (unsigned)r.span;
+  r.at = at - r.hg * r.span;
   return r;
 }
 
 // Moves a cut at x, which is in segment r, to that segment's end or beginning where it is near.
-__device__ __forceinline__ int64_t settle(const PagedPlan& p, const At& r, int64_t x) {
+__device__ __forceinline__ unsigned settle(const PagedPlan& p, const At& r, unsigned x) {
   if (r.at <= p.lead + p.tau) return x - r.at;
   if (r.span - r.at <= p.tau) return x - r.at + r.span;
   return x;
@@ -291,22 +309,22 @@ struct Walk {
   int at, end, span;  // the portion is at .. end of the segment's span
   int p, take, n;     // its first page, its pages, this warp's number of them
   Seq s;
-  int64_t left;       // what the team has from this portion on
+  int left;           // what the team has from this portion on
   __device__ __forceinline__ void open(const PagedPlan& pl, int wt) {
-    end = left < span - at ? at + (int)left : span;
-    p = max(at - pl.lead, 0);
-    take = max(end - pl.lead - p, 0);
+    end = min(at + left, span);
+    p = max(at - pl.lead, 0) << pl.unit;
+    take = max(min((end - pl.lead) << pl.unit, s.pages) - p, 0);
     n = pl.team_warps == 1 ? take : take > wt ? (take - wt + pl.team_warps - 1) / pl.team_warps : 0;
   }
-  __device__ __forceinline__ bool next(const PagedArgs& a, const PagedPlan& pl, int heads, int wt) {
+  __device__ __forceinline__ bool next(const PagedArgs& a, const PagedPlan& pl, const Scan& sc, int wt) {
     left -= end - at;
     if (left <= 0) return false;
     at = 0;
-    if (++hg == heads) {
+    if (++hg == (int)sc.heads) {
       hg = 0;
       do {
         if (++b >= a.batch) return false;
-        s = seq_of(a, b);
+        s = sc.seq(a, b);
       } while (s.pages == 0);
       span = span_of(pl, s);
     }
@@ -324,7 +342,7 @@ __global__ void __launch_bounds__(PagedCfg<KIND, D, NT>::THREADS, 1)
   constexpr int NW = C::NW, S = C::S, KS = D / 16;
   extern __shared__ uint8_t raw[];
   uint8_t* sm = raw + ((1024 - (sm_addr(raw) & 1023)) & 1023);
-  int64_t* pre = reinterpret_cast<int64_t*>(sm + C::OFF_PRE);
+  unsigned* pre = reinterpret_cast<unsigned*>(sm + C::OFF_PRE);
   const PagedArgs& a = w.a;
   const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5, g = lane >> 2, t = lane & 3;
   const int heads = a.hkv * w.p.groups;  // segments per sequence
@@ -339,67 +357,67 @@ __global__ void __launch_bounds__(PagedCfg<KIND, D, NT>::THREADS, 1)
   asm volatile("griddepcontrol.wait;" ::: "memory");
 
   // ---- scan: the line in front of each entry of `stride` sequences
+  int* len_sm = reinterpret_cast<int*>(sm + C::OFF_LEN);
   Scan sc;
   sc.pre = pre;
   sc.stride = (a.batch + C::THREADS - 1) / C::THREADS;
-  sc.n = (a.batch + sc.stride - 1) / sc.stride;
+  sc.n = sc.stride == 1 ? a.batch : (a.batch + sc.stride - 1) / sc.stride;
   sc.heads = heads;
-  int64_t own = 0;
+  sc.len = C::LENS && sc.stride == 1 ? len_sm : nullptr;
+  unsigned own = 0;
   bool bad_len = false;
   for (int b = tid * sc.stride; b < min((tid + 1) * sc.stride, a.batch); ++b) {
-    const Seq s = seq_of(a, b);
-    bad_len |= s.bad;
-    own += (int64_t)span_of(w.p, s) * heads;
+    const int len = __ldg(a.lengths + b);
+    if (C::LENS) len_sm[tid] = len;  // used where stride is 1
+    bad_len |= !length_ok(a, len);
+    own += span_of(w.p, seq_of(a, len)) * heads;
   }
-  int64_t inc = own;
+  unsigned inc = own;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const int64_t up = __shfl_up_sync(kFull, inc, o);
+    const unsigned up = __shfl_up_sync(kFull, inc, o);
     if (lane >= o) inc += up;
   }
-  int64_t* wsum = reinterpret_cast<int64_t*>(sm + C::OFF_WARP);
+  unsigned* wsum = reinterpret_cast<unsigned*>(sm + C::OFF_WARP);
   if (lane == 31) wsum[wid] = inc;
   __syncthreads();
-  int64_t before = 0, work = 0;
+  unsigned before = 0, work = 0;
 #pragma unroll
   for (int i = 0; i < NW; ++i) {
     if (i == wid) before = work;
     work += wsum[i];
   }
   pre[tid] = before + inc - own;
-  if (tid == 0) pre[C::THREADS] = work;
-  if (blockIdx.x == 0) {
-    w.pre[tid] = before + inc - own;
-    if (tid == 0) w.pre[C::THREADS] = work;
-    if (bad_len) flag_error(a.err, TQ_DEVERR_POSITION);
-  }
-  __syncthreads();
+  if (blockIdx.x == 0 && bad_len) flag_error(a.err, TQ_DEVERR_POSITION);
   if (work == 0) return;
+  const Pieces pieces(w.p, work);
+  __syncthreads();
 
   // ---- this team's piece
-  const int teams = teams_of(w.p, work), tw = w.p.team_warps, wt = tw == 1 ? 0 : wid;
-  const int team = tw == 1 ? wid * gridDim.x + blockIdx.x : blockIdx.x;  // warps: an SM's are apart in the line
-  if (team >= teams) return;
-  Walk out, in;  // the portion being computed, and the one being fetched
+  const int tw = w.p.team_warps, wt = tw == 1 ? 0 : wid;
+  const unsigned team = tw == 1 ? wid * gridDim.x + blockIdx.x : blockIdx.x;  // warps: an SM's are apart in the line
+  if (team >= pieces.teams) return;
+  Walk out, in;   // the portion being computed, and the one being fetched
+  unsigned x_end;  // where the piece ends
   {
-    int64_t x0 = divide((int64_t)team * work, teams), x1 = work;
-    At r = locate(a, w.p, sc, x0, lane);
-    x0 = settle(w.p, r, x0);
-    if (team + 1 < teams) {
-      x1 = divide((int64_t)(team + 1) * work, teams);
-      x1 = settle(w.p, locate(a, w.p, sc, x1, lane), x1);
-    }
+    unsigned x0 = pieces.begin(team), x1 = pieces.begin(team + 1);
+    At r = locate(a, w.p, sc, x0, min(x1, work - 1), lane);
+    const unsigned x = settle(w.p, r, lane < 16 ? x0 : x1);
+    const int back = __shfl_sync(kFull, r.at, 0), over = __shfl_sync(kFull, r.span, 0) - back;
+    x0 = __shfl_sync(kFull, x, 0);
+    x1 = team + 1 < pieces.teams ? __shfl_sync(kFull, x, 16) : work;
     if (x0 >= x1) return;
-    if (r.at <= w.p.lead + w.p.tau) r.at = 0;
-    else if (r.span - r.at <= w.p.tau) r = locate(a, w.p, sc, x0, lane);  // the next segment
-    out.b = r.b;
-    out.hg = r.hg;
-    out.at = r.at;
-    out.span = r.span;
-    out.s = r.s;
+    if (back > w.p.lead + w.p.tau && over <= w.p.tau) r = locate(a, w.p, sc, x0, x0, lane);  // the next segment
+    out.b = __shfl_sync(kFull, r.b, 0);
+    out.hg = __shfl_sync(kFull, r.hg, 0);
+    out.at = __shfl_sync(kFull, r.at, 0);
+    if (out.at <= w.p.lead + w.p.tau) out.at = 0;
+    out.s = sc.seq(a, out.b);
+    out.span = span_of(w.p, out.s);
     out.left = x1 - x0;
     out.open(w.p, wt);
     in = out;
+    x_end = x1;
   }
 
   // ---- fetching
@@ -412,13 +430,13 @@ __global__ void __launch_bounds__(PagedCfg<KIND, D, NT>::THREADS, 1)
   auto fetch_next = [&]() -> bool {
     if ((in_i & 31) == 0 || in_i == in.n) {
       while (!in_done && in_i == in.n) {
-        in_done = !in.next(a, w.p, heads, wt);
+        in_done = !in.next(a, w.p, sc, wt);
         in_i = 0;
       }
       if (in_done) return false;
       tiles = -1;
       if (in_i + lane < in.n) {
-        const int id = a.block_table[(int64_t)in.b * a.max_blocks + in.s.first + in.p + wt + (in_i + lane) * tw];
+        const int id = __ldg(a.block_table + (int64_t)in.b * a.max_blocks + in.s.first + in.p + wt + (in_i + lane) * tw);
         if (id >= 0 && id < a.num_blocks) tiles = id * a.hkv + in.hg / w.p.groups;
         else bad_id = true;
       }
@@ -472,7 +490,7 @@ __global__ void __launch_bounds__(PagedCfg<KIND, D, NT>::THREADS, 1)
 
   // ================================================================ portions
 #pragma unroll 1
-  for (bool more = true; more; more = out.next(a, w.p, heads, wt)) {
+  for (bool more = true; more; more = out.next(a, w.p, sc, wt)) {
     const int kvh = out.hg / w.p.groups, h0 = (out.hg - kvh * w.p.groups) * C::HEADS;
     const int nh = min(C::HEADS, a.n_rep - h0);
     const int64_t head0 = (int64_t)kvh * a.n_rep + h0;
@@ -481,16 +499,17 @@ __global__ void __launch_bounds__(PagedCfg<KIND, D, NT>::THREADS, 1)
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
       const int h = nt * 8 + g;
-      const uint16_t* qr = a.q + out.b * a.q_stride + (head0 + h) * D;
+      // heads that are none read the first one's row and become zero: loads without a branch go out together
+      const uint16_t* qr = a.q + out.b * a.q_stride + (head0 + (h < nh ? h : 0)) * D;
+      const uint32_t keep = h < nh ? 0xffffffffu : 0u;
       float up = 1.f;
       if (F8 && w.q_bf16) {
         uint32_t top = 0;
-        if (h < nh)
 #pragma unroll
-          for (int ks = 0; ks < KS; ++ks) {
-            const uint2 x = *reinterpret_cast<const uint2*>(qr + ks * 16 + 4 * t);
-            top = max(max(top, max(x.x & 0x7fffu, (x.x >> 16) & 0x7fffu)), max(x.y & 0x7fffu, (x.y >> 16) & 0x7fffu));
-          }
+        for (int ks = 0; ks < KS; ++ks) {
+          const uint2 x = __ldg(reinterpret_cast<const uint2*>(qr + ks * 16 + 4 * t));
+          top = max(max(top, max(x.x & 0x7fffu, (x.x >> 16) & 0x7fffu)), max(x.y & 0x7fffu, (x.y >> 16) & 0x7fffu));
+        }
         top = max(top, __shfl_xor_sync(kFull, top, 1));
         top = max(top, __shfl_xor_sync(kFull, top, 2));
         // largest entry in [2^14, 2^15); the factor is undone in the score's
@@ -499,19 +518,20 @@ __global__ void __launch_bounds__(PagedCfg<KIND, D, NT>::THREADS, 1)
       }
 #pragma unroll
       for (int ks = 0; ks < KS; ++ks) {
-        uint2 x = make_uint2(0, 0);
-        if (h < nh) {
-          if (F8) x = *reinterpret_cast<const uint2*>(qr + ks * 16 + 4 * t);
-          else {
-            x.x = *reinterpret_cast<const uint32_t*>(qr + ks * 16 + 2 * t);
-            x.y = *reinterpret_cast<const uint32_t*>(qr + ks * 16 + 2 * t + 8);
-          }
+        uint2 x;
+        if (F8) {
+          x = __ldg(reinterpret_cast<const uint2*>(qr + ks * 16 + 4 * t));
+        } else {
+          x.x = __ldg(reinterpret_cast<const uint32_t*>(qr + ks * 16 + 2 * t));
+          x.y = __ldg(reinterpret_cast<const uint32_t*>(qr + ks * 16 + 2 * t + 8));
         }
         if (F8 && w.q_bf16) {
           const __half2 u = __floats2half2_rn(__uint_as_float(x.x << 16) * up, __uint_as_float(x.x & 0xffff0000u) * up);
           const __half2 v = __floats2half2_rn(__uint_as_float(x.y << 16) * up, __uint_as_float(x.y & 0xffff0000u) * up);
           x = make_uint2(*reinterpret_cast<const uint32_t*>(&u), *reinterpret_cast<const uint32_t*>(&v));
         }
+        x.x &= keep;
+        x.y &= keep;
         if constexpr (C::QREG) {
           qf[nt][ks][0] = x.x;
           qf[nt][ks][1] = x.y;
@@ -750,6 +770,16 @@ __global__ void __launch_bounds__(PagedCfg<KIND, D, NT>::THREADS, 1)
     auto dim0 = [&](int j) { return F8 ? 16 * j + 2 * g : 16 * j + g; };
     constexpr int DIM1 = F8 ? 1 : 8;
     const bool all = out.at == 0 && out.end == out.span;
+    if (out.at == 0 && lane == 0 && wt == 0) {
+      // cuts inside the segment: pieces that begin more than lead + tau behind its beginning and more
+      // than tau before its end
+      int2 c = make_int2(team, 0);
+      if (!all) {
+        const unsigned first = x_end - out.left, last = first + out.span;
+        c.y = pieces.from(last - w.p.tau) - pieces.from(first + w.p.lead + w.p.tau + 1);
+      }
+      w.cuts[(int64_t)out.b * heads + out.hg] = c;
+    }
     // partials: [heads][D] sums, then [heads] references and [heads] totals; a portion that continues a
     // segment takes the team's first slot, one that begins a segment the second
     float* part = w.parts + ((int64_t)team * 2 + (out.at == 0)) * (C::HEADS * (D + 2));
@@ -803,13 +833,18 @@ __global__ void __launch_bounds__(PagedCfg<KIND, D, NT>::THREADS, 1)
       for (int i = tid; i < nh * (D / 4); i += C::THREADS) {
         const int h = i / (D / 4), d4 = (i - h * (D / 4)) * 4;
         float M = -CUDART_INF_F;
-        for (int k = 0; k < act; ++k) M = fmaxf(M, ml[(k * C::HEADS + h) * 2]);
-        const float ref = M == -CUDART_INF_F ? 0.f : M;
+#pragma unroll
+        for (int k = 0; k < NW; ++k)
+          if (k < act) M = fmaxf(M, ml[(k * C::HEADS + h) * 2]);
+        const float sub = M == -CUDART_INF_F ? 0.f : M;
         float L = 0.f;
         float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-        for (int k = 0; k < act; ++k) {
-          const float c = ex2(ml[(k * C::HEADS + h) * 2] - ref);
-          L = fmaf(c, ml[(k * C::HEADS + h) * 2 + 1], L);
+#pragma unroll
+        for (int k = 0; k < NW; ++k) {
+          if (k >= act) break;
+          const float2 v = *reinterpret_cast<const float2*>(ml + (k * C::HEADS + h) * 2);
+          const float c = ex2(v.x - sub);
+          L = fmaf(c, v.y, L);
           const float4 y = *reinterpret_cast<const float4*>(slot + (k * C::HEADS + h) * (D + 4) + d4);
           x.x = fmaf(c, y.x, x.x);
           x.y = fmaf(c, y.y, x.y);
@@ -844,94 +879,111 @@ __global__ void __launch_bounds__(PagedCfg<KIND, D, NT>::THREADS, 1)
   if (bad_id) flag_error(a.err, TQ_DEVERR_BLOCK_ID);
 }
 
-// Joins the portions of the segments that more than one team had, and writes the rows of empty sequences.  One
-// CTA per (segment, share of its heads).  Its warps take every fourth portion, a lane D / 32 dims, four
-// portions in flight per warp: a chain of loads from L2 is what this kernel would otherwise wait for.
+// Joins the pieces of the segments that more than one team had, and writes the rows of empty sequences.
+// JOIN warps share a (segment, query head): with few segments of many pieces four, one head each; with many of
+// few pieces one warp for all heads of a segment.  A lane has D / 32 dims, four pieces are loaded at a
+// time: what bounds this kernel is the chain of loads from L2, segment -> pieces, and nothing else.
 constexpr int kMergeWarps = 4;
-template <int D, int HEADS>
-__global__ void __launch_bounds__(kMergeWarps * 32) paged_merge_kernel(const __grid_constant__ PagedWork w) {
+template <int D, int HEADS, int JOIN>
+__global__ void __launch_bounds__(kMergeWarps * 32) paged_merge_kernel(const __grid_constant__ PagedWork w, int segments) {
   constexpr int V = D / 32, VL = V < 4 ? V : 4;  // dims of a lane, and of one load
+  constexpr int PART = HEADS * (D + 2);
   const PagedArgs& a = w.a;
-  __shared__ float sx[kMergeWarps][D], sl[kMergeWarps], sm_max[kMergeWarps];
+  __shared__ float sx[JOIN == 1 ? 1 : JOIN][D], sl[JOIN], sm_max[JOIN];
   const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
   asm volatile("griddepcontrol.launch_dependents;");
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int heads = a.hkv * w.p.groups;
-  const int b = blockIdx.x / (unsigned)heads, hg = blockIdx.x - (unsigned)b * heads;
+  const unsigned seg = JOIN == 1 ? blockIdx.x * kMergeWarps + wid : blockIdx.x;
+  if (seg >= (unsigned)segments) return;
+  const unsigned heads = a.hkv * w.p.groups;
+  const int2 cut = w.cuts[seg];
+  const int b = seg / heads, hg = seg - b * heads;
+  const int pages = seq_of(a, a.lengths[b]).pages;
   const int kvh = hg / w.p.groups, h0 = (hg - kvh * w.p.groups) * HEADS, nh = min(HEADS, a.n_rep - h0);
   const int64_t row0 = (int64_t)b * a.hq + (int64_t)kvh * a.n_rep + h0;
-  const int stride = (a.batch + w.p.scan - 1) / w.p.scan, e = b / stride;
-  int64_t first = w.pre[e];
-  const int64_t work = w.pre[w.p.scan];
-  const Seq s = seq_of(a, b);
-  if (s.pages == 0) {
-    for (int h = blockIdx.y; h < nh; h += gridDim.y) {
-      for (int i = threadIdx.x; i < D; i += kMergeWarps * 32) a.out[(row0 + h) * D + i] = 0.f;
-      if (threadIdx.x == 0 && a.lse) a.lse[row0 + h] = -CUDART_INF_F;
-    }
-    return;
-  }
-  const int span = span_of(w.p, s), teams = teams_of(w.p, work);
-  for (int i = e * stride; i < b; ++i) first += (int64_t)span_of(w.p, seq_of(a, i)) * heads;
-  first += (int64_t)hg * span;
-  const int64_t last = first + span;
-  // cuts floor(t work / teams) that stay inside the segment
-  const int64_t ta = divide((first + w.p.lead + w.p.tau + 1) * teams + work - 1, work);
-  const int64_t tb = divide((last - w.p.tau) * teams + work - 1, work) - 1;
-  if (tb < ta) return;  // one team had it
-  const int n = (int)(tb - ta) + 2;
-  constexpr int PART = HEADS * (D + 2);
-  // portion 0 begins the segment (second slot of team ta - 1), portion k > 0 continues it (first slot of ta + k - 1)
-  auto part = [&](int k) { return w.parts + (k == 0 ? (ta - 1) * 2 + 1 : (ta + k - 1) * 2) * (int64_t)PART; };
-  for (int h = blockIdx.y; h < nh; h += gridDim.y) {
-    float M = -CUDART_INF_F;
-    for (int k = threadIdx.x; k < n; k += kMergeWarps * 32) M = fmaxf(M, part(k)[HEADS * D + h]);
-    M = warp_max(M);
-    if (lane == 0) sm_max[wid] = M;
-    __syncthreads();
-#pragma unroll
-    for (int i = 0; i < kMergeWarps; ++i) M = fmaxf(M, sm_max[i]);
-    const float ref = M == -CUDART_INF_F ? 0.f : M;
-    float L = 0.f, x[V];
+  if (pages && cut.y == 0) return;  // one team had it
+  const int n = pages ? cut.y + 1 : 0;
+  // piece 0 is its team's second slot, the others the first slots of the teams behind
+  const float* part0 = w.parts + (int64_t)cut.x * 2 * PART;
+  for (int h = JOIN == 1 ? 0 : blockIdx.y; h < nh; h += JOIN == 1 ? 1 : gridDim.y) {
+    float M = -CUDART_INF_F, L = 0.f, x[V];
 #pragma unroll
     for (int i = 0; i < V; ++i) x[i] = 0.f;
-#pragma unroll 4
-    for (int k = wid; k < n; k += kMergeWarps) {
-      const float* p = part(k);
-      const float c = ex2(p[HEADS * D + h] - ref);
-      L = fmaf(c, p[HEADS * (D + 1) + h], L);
+    for (int k0 = JOIN == 1 ? 0 : wid; k0 < n; k0 += 4 * JOIN) {
+      float m[4], l[4], y[4][V];
 #pragma unroll
-      for (int i = 0; i < V; i += VL) {
-        const float* q = p + h * D + (i / VL * 32 + lane) * VL;
-        if constexpr (VL == 2) {
-          const float2 y = *reinterpret_cast<const float2*>(q);
-          x[0] = fmaf(c, y.x, x[0]);
-          x[1] = fmaf(c, y.y, x[1]);
-        } else {
-          const float4 y = *reinterpret_cast<const float4*>(q);
-          x[i] = fmaf(c, y.x, x[i]);
-          x[i + 1] = fmaf(c, y.y, x[i + 1]);
-          x[i + 2] = fmaf(c, y.z, x[i + 2]);
-          x[i + 3] = fmaf(c, y.w, x[i + 3]);
+      for (int u = 0; u < 4; ++u) {
+        const int k = k0 + u * JOIN;
+        m[u] = -CUDART_INF_F;
+        l[u] = 0.f;
+#pragma unroll
+        for (int i = 0; i < V; ++i) y[u][i] = 0.f;
+        if (k >= n) continue;
+        const float* p = part0 + (k == 0 ? 1 : 2 * k) * (int64_t)PART;
+        m[u] = p[HEADS * D + h];
+        l[u] = p[HEADS * (D + 1) + h];
+#pragma unroll
+        for (int i = 0; i < V; i += VL) {
+          const float* q = p + h * D + (i / VL * 32 + lane) * VL;
+          if constexpr (VL == 2) {
+            const float2 v = *reinterpret_cast<const float2*>(q);
+            y[u][0] = v.x;
+            y[u][1] = v.y;
+          } else {
+            const float4 v = *reinterpret_cast<const float4*>(q);
+            y[u][i] = v.x;
+            y[u][i + 1] = v.y;
+            y[u][i + 2] = v.z;
+            y[u][i + 3] = v.w;
+          }
         }
       }
+      const float top = fmaxf(fmaxf(M, fmaxf(m[0], m[1])), fmaxf(m[2], m[3]));
+      const float sub = top == -CUDART_INF_F ? 0.f : top, c = ex2(M - sub);
+      M = top;
+      L *= c;
+#pragma unroll
+      for (int i = 0; i < V; ++i) x[i] *= c;
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const float f = ex2(m[u] - sub);
+        L = fmaf(f, l[u], L);
+#pragma unroll
+        for (int i = 0; i < V; ++i) x[i] = fmaf(f, y[u][i], x[i]);
+      }
     }
+    if constexpr (JOIN > 1) {
 #pragma unroll
-    for (int i = 0; i < V; ++i) sx[wid][(i / VL * 32 + lane) * VL + i % VL] = x[i];
-    if (lane == 0) sl[wid] = L;
-    __syncthreads();
-    L = 0.f;
+      for (int i = 0; i < V; ++i) sx[wid][(i / VL * 32 + lane) * VL + i % VL] = x[i];
+      if (lane == 0) {
+        sl[wid] = L;
+        sm_max[wid] = M;
+      }
+      __syncthreads();
+      M = fmaxf(fmaxf(sm_max[0], sm_max[1]), fmaxf(sm_max[2], sm_max[3]));
+      const float sub = M == -CUDART_INF_F ? 0.f : M;
+      float c[JOIN];
+      L = 0.f;
 #pragma unroll
-    for (int i = 0; i < kMergeWarps; ++i) L += sl[i];
-    const float f = L == 0.f ? 0.f : 1.f / L;
-    for (int i = threadIdx.x; i < D; i += kMergeWarps * 32) {
-      float y = 0.f;
+      for (int k = 0; k < JOIN; ++k) {
+        c[k] = ex2(sm_max[k] - sub);
+        L = fmaf(c[k], sl[k], L);
+      }
+      const float f = L == 0.f ? 0.f : 1.f / L;
+      for (int i = threadIdx.x; i < D; i += kMergeWarps * 32) {
+        float v = 0.f;
 #pragma unroll
-      for (int k = 0; k < kMergeWarps; ++k) y += sx[k][i];
-      a.out[(row0 + h) * D + i] = y * f;
+        for (int k = 0; k < JOIN; ++k) v = fmaf(c[k], sx[k][i], v);
+        a.out[(row0 + h) * D + i] = v * f;
+      }
+      if (threadIdx.x == 0 && a.lse) a.lse[row0 + h] = L == 0.f ? -CUDART_INF_F : (M - kWeightUp + log2f(L)) * 0.69314718055994530942f;
+      if (h + (int)gridDim.y < nh) __syncthreads();
+    } else {
+      const float f = L == 0.f ? 0.f : 1.f / L;
+#pragma unroll
+      for (int i = 0; i < V; ++i) a.out[(row0 + h) * D + (i / VL * 32 + lane) * VL + i % VL] = x[i] * f;
+      if (lane == 0 && a.lse) a.lse[row0 + h] = L == 0.f ? -CUDART_INF_F : (M - kWeightUp + log2f(L)) * 0.69314718055994530942f;
     }
-    if (threadIdx.x == 0 && a.lse) a.lse[row0 + h] = (M - kWeightUp + log2f(L)) * 0.69314718055994530942f;
-    if (h + (int)gridDim.y < nh) __syncthreads();
   }
 }
 
@@ -949,17 +1001,21 @@ PagedPlan plan_of(const tq_ctx* ctx, int batch) {
   p.lead = p.team_warps == 1 ? 2 : C::PAGE >= 32768 ? 2 : C::PAGE >= 16384 ? 4 : 8;
   p.min_log2 = p.team_warps == 1 ? 2 : C::PAGE >= 32768 ? 2 : C::PAGE >= 16384 ? 3 : 4;
   p.tau = C::PAGE >= 16384 ? 2 : 4;
-  p.scan = C::THREADS;
+  p.unit = 0;
   return p;
 }
 
 inline size_t align256(size_t x) { return (x + 255) & ~(size_t)255; }
 
+// The pieces' slots, then the segments' cuts.
+template <int KIND, int D, int NT>
+size_t parts_bytes(const PagedPlan& p) {
+  return align256((size_t)p.teams * 2 * PagedCfg<KIND, D, NT>::HEADS * (D + 2) * 4);
+}
 template <int KIND, int D, int NT>
 size_t workspace_of(const tq_ctx* ctx, int batch) {
-  using C = PagedCfg<KIND, D, NT>;
   const PagedPlan p = plan_of<KIND, D, NT>(ctx, batch);
-  return align256((C::THREADS + 1) * 8) + (size_t)p.teams * 2 * C::HEADS * (D + 2) * 4;
+  return parts_bytes<KIND, D, NT>(p) + align256((size_t)batch * ctx->cfg.num_kv_heads * p.groups * sizeof(int2));
 }
 
 template <int KIND, int D, int NT>
@@ -969,8 +1025,11 @@ cudaError_t launch_one(tq_ctx* ctx, const PagedArgs& a, void* workspace, cudaStr
   w.a = a;
   w.p = plan_of<KIND, D, NT>(ctx, a.batch);
   w.q_bf16 = ctx->cfg.key_format == TQ_ELEM_BF16;
-  w.pre = static_cast<int64_t*>(workspace);
-  w.parts = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + align256((C::THREADS + 1) * 8));
+  w.parts = static_cast<float*>(workspace);
+  w.cuts = reinterpret_cast<int2*>(static_cast<uint8_t*>(workspace) + parts_bytes<KIND, D, NT>(w.p));
+  const int64_t all = (int64_t)a.batch * a.hkv * w.p.groups;
+  while (all * (((int64_t)a.max_blocks >> w.p.unit) + 1 + w.p.lead) > 0x7fffffff)
+    if (++w.p.unit > 27) return cudaErrorInvalidValue;
   CUtensorMap map{};
   if (a.num_blocks > 0) {
     const PagedTensorMap tm{a.pool, C::ES, D, (int64_t)a.num_blocks * a.hkv, C::PAGE + C::EXP, C::SWIZZLE_ROW};
@@ -998,12 +1057,14 @@ cudaError_t launch_one(tq_ctx* ctx, const PagedArgs& a, void* workspace, cudaStr
   ctx->launches++;
   ctx->decode_kernel = "paged_kernel";
 
-  const int64_t segments = (int64_t)a.batch * a.hkv * w.p.groups;
-  cfg.gridDim = dim3((unsigned)segments, segments < 1024 ? (a.n_rep < C::HEADS ? a.n_rep : C::HEADS) : 1);
+  const int segments = a.batch * a.hkv * w.p.groups;
+  const bool many = w.p.team_warps == 1;
+  cfg.gridDim = many ? dim3((segments + kMergeWarps - 1) / kMergeWarps) : dim3(segments, a.n_rep < C::HEADS ? a.n_rep : C::HEADS);
   cfg.blockDim = dim3(kMergeWarps * 32);
   cfg.dynamicSmemBytes = 0;
   prof_start(ctx, kProfMerge, s);
-  e = cudaLaunchKernelEx(&cfg, paged_merge_kernel<D, C::HEADS>, w);
+  e = many ? cudaLaunchKernelEx(&cfg, paged_merge_kernel<D, C::HEADS, 1>, w, segments)
+           : cudaLaunchKernelEx(&cfg, paged_merge_kernel<D, C::HEADS, kMergeWarps>, w, segments);
   prof_stop(ctx, kProfMerge, s);
   if (e == cudaSuccess) ctx->launches++;
   return e;
