@@ -7,13 +7,15 @@
 // bits) of a token's key and value, far below what the tensor cores do in that time, so everything here
 // serves one aim: enough bytes in flight on every multiprocessor from the first moment to the last.
 //
-// Work split.  A segment is one (sequence, KV head, group of up to 8 NT query heads); its work is its number
-// of pages.  All segments' pages stand in one line, and T teams get equal pieces of it, whatever the lengths
-// are: a ragged batch and a single long sequence are split alike, in one wave, with no length known on
-// the host.  Cuts that fall within tau pages of a segment's end move there.  A segment that one team holds whole
-// is written out at once; the pieces of a cut one go to the workspace (at most two per team) and the
-// merge kernel joins them.  A team is one CTA (its warps take every NW-th page and are joined in
-// shared memory) when there are few segments, or one warp when there are many short ones.
+// Work split.  A segment is one (sequence, KV head, group of up to 8 NT query heads); its work is its
+// number of pages plus `lead` for the queries, the joining and the result.  All segments stand in one line, and
+// T teams get equal pieces of it, whatever the lengths are: a ragged batch and a single long sequence are split
+// alike, in one wave, with no length known on the host.  Cuts that fall within a segment's lead, or within tau pages
+// of its ends, move to the end.  A team is one warp: what a segment costs beside its pages (fetching its queries,
+// joining, writing) is hidden by the CTA's other warps, where a team of all warps would wait for it (measured:
+// 64 sequences of 0.5 to 16K tokens, e4m3, 32 / 8 heads: 3.3 us per segment and CTA).  A segment
+// that one warp holds whole is written out from registers.  The pieces of a cut one are joined in shared memory when
+// the CTA's warps are through, and what crosses CTAs (at most two pieces per CTA) by the merge kernel.
 //
 // One page (16 tokens) per warp and step, each warp with a ring of S stages that it fills itself by TMA (128-byte
 // swizzle, so that the rows of a plain [16][d] tile are read without bank conflicts) and mbarriers:
@@ -58,22 +60,27 @@ struct PagedCfg {
   static constexpr int HEADS = 8 * NT;
   static constexpr bool QREG = D * NT <= 128;              // query fragments in registers
   static constexpr int QBYTES = QREG ? 0 : HEADS * D * 2;  // else in shared memory, per warp
-  static constexpr int SLOT = HEADS * (D + 4) * 4 + HEADS * 8;
+  // A cut segment's sums: [HEADS][PITCH] floats (padded against bank conflicts where there is room) for the piece
+  // that continues one; the piece that begins one is a warp's last, its stages are free to hold it.
+  static constexpr int PITCH = D < 512 && (NT == 1 || D == 64) ? D + 4 : D;
+  static constexpr int SLOT = HEADS * PITCH * 4 + HEADS * 16 + 32;
   static constexpr bool LENS = D < 512;  // the lengths in shared memory (no room for them at 512)
   static constexpr int LIMIT = 232448 - 1024;  // 227 KB, less the alignment of the stages
   static constexpr int fixed(int nw) { return nw * (SLOT + QBYTES) + nw * 32 * (LENS ? 8 : 4) + nw * 4; }
   static constexpr int per(int nw) { return nw * (PAGE + EXP + 16); }
-  static constexpr bool fits(int nw) { return fixed(nw) + per(nw) <= LIMIT; }
-  // Warps per CTA: small pages need more of them to keep the bytes in flight
-  static constexpr int NW = PAGE <= 4096 && QREG && fits(16) ? 16 : fits(8) ? 8 : 4;
-  static constexpr int S_FIT = (LIMIT - fixed(NW)) / per(NW);
+  static constexpr int stages(int nw) { return (LIMIT - fixed(nw)) / per(nw); }
+  // Warps per CTA: small pages need more of them to keep the bytes in flight; two stages per warp before more warps
+  static constexpr int NW = PAGE <= 4096 && QREG && stages(16) >= 2 ? 16 : stages(8) >= 2 ? 8 : 4;
+  static constexpr int S_FIT = stages(NW);
   static constexpr int S = S_FIT > 8 ? 8 : S_FIT;
   static_assert(S >= 1, "one stage per warp fits");
   static constexpr int THREADS = NW * 32;
+  static_assert(HEADS * PITCH * 4 <= S * PAGE, "a warp's stages hold its last piece");
   // dynamic shared memory, from a 1024-byte aligned base
-  static constexpr int OFF_SLOT = NW * S * PAGE;
-  static constexpr int OFF_ML = OFF_SLOT + NW * HEADS * (D + 4) * 4;
-  static constexpr int OFF_Q = OFF_ML + NW * HEADS * 8;
+  static constexpr int OFF_SLOT = NW * S * PAGE;                    // [NW][HEADS][PITCH]
+  static constexpr int OFF_ML = OFF_SLOT + NW * HEADS * PITCH * 4;  // [2][NW][HEADS] references and totals
+  static constexpr int OFF_REC = OFF_ML + NW * HEADS * 16;          // [2][NW] what the pieces are
+  static constexpr int OFF_Q = OFF_REC + NW * 32;
   static constexpr int OFF_EXP = OFF_Q + NW * QBYTES;
   static constexpr int OFF_BAR = OFF_EXP + NW * S * EXP;
   static constexpr int OFF_PRE = OFF_BAR + NW * S * 16;
@@ -87,8 +94,7 @@ struct PagedCfg {
 
 // ---------------------------------------------------------------- work split, shared by both kernels
 struct PagedPlan {
-  int teams;       // most teams (CTAs, or warps)
-  int team_warps;  // warps of a team: all of a CTA's, or 1
+  int teams;       // most teams: the grid's warps
   int lead;        // a segment's work beside its pages, in units
   int unit;        // the line counts 2^unit pages as one, so that it stays below 2^31
   int min_log2;    // a team gets at least about 2^min_log2 of the line
@@ -100,8 +106,8 @@ struct PagedWork {
   PagedArgs a;
   PagedPlan p;
   int q_bf16;
-  int2* cuts;    // workspace: per segment {team that has its beginning, pieces beside that}; written where it begins
-  float* parts;  // workspace: [2 * teams][part]
+  int2* cuts;    // workspace: per segment the first and the last CTA with a piece of it, written by the first
+  float* parts;  // workspace: per CTA the piece that comes from the CTA in front, and the one that goes on behind
 };
 
 struct Seq {
@@ -302,21 +308,19 @@ __device__ __forceinline__ unsigned settle(const PagedPlan& p, const At& r, unsi
   return x;
 }
 
-// A warp's way along its team's piece: portions (the piece's share of one segment), and in a portion the
-// pages p + wt, p + wt + tw, ... of the segment.
+// A warp's way along its piece of the line, by portions: its share of one segment, pages p .. p + take - 1.
 struct Walk {
   int b, hg;
   int at, end, span;  // the portion is at .. end of the segment's span
-  int p, take, n;     // its first page, its pages, this warp's number of them
+  int p, take;        // its first page and its pages
   Seq s;
-  int left;           // what the team has from this portion on
-  __device__ __forceinline__ void open(const PagedPlan& pl, int wt) {
+  int left;           // what the warp has from this portion on
+  __device__ __forceinline__ void open(const PagedPlan& pl) {
     end = min(at + left, span);
     p = max(at - pl.lead, 0) << pl.unit;
     take = max(min((end - pl.lead) << pl.unit, s.pages) - p, 0);
-    n = pl.team_warps == 1 ? take : take > wt ? (take - wt + pl.team_warps - 1) / pl.team_warps : 0;
   }
-  __device__ __forceinline__ bool next(const PagedArgs& a, const PagedPlan& pl, const Scan& sc, int wt) {
+  __device__ __forceinline__ bool next(const PagedArgs& a, const PagedPlan& pl, const Scan& sc) {
     left -= end - at;
     if (left <= 0) return false;
     at = 0;
@@ -328,10 +332,15 @@ struct Walk {
       } while (s.pages == 0);
       span = span_of(pl, s);
     }
-    open(pl, wt);
+    open(pl);
     return true;
   }
 };
+
+// ln of the weights' sum L, which is relative to 2^(M - 7)
+__device__ __forceinline__ float lse_of(float M, float L) {
+  return L == 0.f ? -CUDART_INF_F : (M - kWeightUp + log2f(L)) * 0.69314718055994530942f;
+}
 
 // ---------------------------------------------------------------- the kernel
 template <int KIND, int D, int NT>
@@ -348,11 +357,16 @@ __global__ void __launch_bounds__(PagedCfg<KIND, D, NT>::THREADS, 1)
   const int heads = a.hkv * w.p.groups;  // segments per sequence
   const uint32_t stage0 = sm_addr(sm) + wid * S * C::PAGE, bar0 = sm_addr(sm + C::OFF_BAR) + wid * S * 16;
   const uint32_t exp0 = sm_addr(sm + C::OFF_EXP) + wid * S * C::EXP;
+  float* own_stage = reinterpret_cast<float*>(sm + wid * S * C::PAGE);
+  float* own_slot = reinterpret_cast<float*>(sm + C::OFF_SLOT) + wid * C::HEADS * C::PITCH;
+  float2* ml = reinterpret_cast<float2*>(sm + C::OFF_ML);
+  int4* rec = reinterpret_cast<int4*>(sm + C::OFF_REC);
 
   // what needs no input of the stream comes before the wait for the kernel in front
   asm volatile("griddepcontrol.launch_dependents;");
   if (tid == 0) asm volatile("prefetch.tensormap [%0];" ::"l"(&map) : "memory");
   if (lane < 2 * S) bar_init(bar0 + 8 * lane, 1);
+  if (lane < 2) rec[lane * NW + wid] = make_int4(0, 0, 0, 0);
   asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");
 
@@ -393,56 +407,79 @@ __global__ void __launch_bounds__(PagedCfg<KIND, D, NT>::THREADS, 1)
   const Pieces pieces(w.p, work);
   __syncthreads();
 
-  // ---- this team's piece
-  const int tw = w.p.team_warps, wt = tw == 1 ? 0 : wid;
-  const unsigned team = tw == 1 ? wid * gridDim.x + blockIdx.x : blockIdx.x;  // warps: an SM's are apart in the line
-  if (team >= pieces.teams) return;
-  Walk out, in;   // the portion being computed, and the one being fetched
-  unsigned x_end;  // where the piece ends
-  {
+  if (blockIdx.x * NW >= pieces.teams) return;
+
+  // ---- this warp's piece
+  const unsigned team = blockIdx.x * NW + wid;
+  Walk out{}, in;        // the portion being computed, and the one being fetched
+  unsigned x_end = 0;    // where the piece ends
+  bool busy = team < pieces.teams;
+  if (busy) {
     unsigned x0 = pieces.begin(team), x1 = pieces.begin(team + 1);
     At r = locate(a, w.p, sc, x0, min(x1, work - 1), lane);
     const unsigned x = settle(w.p, r, lane < 16 ? x0 : x1);
     const int back = __shfl_sync(kFull, r.at, 0), over = __shfl_sync(kFull, r.span, 0) - back;
     x0 = __shfl_sync(kFull, x, 0);
-    x1 = team + 1 < pieces.teams ? __shfl_sync(kFull, x, 16) : work;
-    if (x0 >= x1) return;
-    if (back > w.p.lead + w.p.tau && over <= w.p.tau) r = locate(a, w.p, sc, x0, x0, lane);  // the next segment
-    out.b = __shfl_sync(kFull, r.b, 0);
-    out.hg = __shfl_sync(kFull, r.hg, 0);
-    out.at = __shfl_sync(kFull, r.at, 0);
-    if (out.at <= w.p.lead + w.p.tau) out.at = 0;
-    out.s = sc.seq(a, out.b);
-    out.span = span_of(w.p, out.s);
-    out.left = x1 - x0;
-    out.open(w.p, wt);
-    in = out;
-    x_end = x1;
+    x1 = __shfl_sync(kFull, x, 16);
+    if (team + 1 == pieces.teams) x1 = work;
+    busy = x0 < x1;
+    if (busy) {
+      if (back > w.p.lead + w.p.tau && over <= w.p.tau) r = locate(a, w.p, sc, x0, x0, lane);  // the next segment
+      out.b = __shfl_sync(kFull, r.b, 0);
+      out.hg = __shfl_sync(kFull, r.hg, 0);
+      out.at = __shfl_sync(kFull, r.at, 0);
+      if (out.at <= w.p.lead + w.p.tau) out.at = 0;
+      out.s = sc.seq(a, out.b);
+      out.span = span_of(w.p, out.s);
+      out.left = x1 - x0;
+      out.open(w.p);
+      x_end = x1;
+    }
   }
+  in = out;
 
   // ---- fetching
-  int in_i = 0, tiles = -1, tile = -1;
-  bool in_done = false;
+  // Block ids are looked up by batches of up to 32 pages (one per lane), a batch ahead, and the queries of a new
+  // portion are brought to L1 then: with every stage in flight a load waits its turn for microseconds.
+  int in_i = 0, next_n = 0, next_id = -1, next_kvh = 0;
+  int cur_i = 0, cur_n = 0, tiles = -1, tile = -1;
+  bool in_done = !busy;
   uint32_t valid = 0, parity = 0, vparity = 0, issued = 0;  // bit per stage
   bool bad_id = false, dead = false;
-  // Step to the next page of this warp: its tile in `tile` (-1: a bad id); false when there is none.  A
-  // lane looks up every 32nd page's block.
-  auto fetch_next = [&]() -> bool {
-    if ((in_i & 31) == 0 || in_i == in.n) {
-      while (!in_done && in_i == in.n) {
-        in_done = !in.next(a, w.p, sc, wt);
-        in_i = 0;
-      }
-      if (in_done) return false;
-      tiles = -1;
-      if (in_i + lane < in.n) {
-        const int id = __ldg(a.block_table + (int64_t)in.b * a.max_blocks + in.s.first + in.p + wt + (in_i + lane) * tw);
-        if (id >= 0 && id < a.num_blocks) tiles = id * a.hkv + in.hg / w.p.groups;
-        else bad_id = true;
-      }
+  auto enter = [&]() {
+    in_i = 0;
+    next_kvh = in.hg / w.p.groups;
+    const int h0 = (in.hg - next_kvh * w.p.groups) * C::HEADS;
+    const char* q = reinterpret_cast<const char*>(a.q + in.b * a.q_stride + ((int64_t)next_kvh * a.n_rep + h0) * D);
+    for (int off = lane * 128; off < min(C::HEADS, a.n_rep - h0) * D * 2; off += 32 * 128)
+      asm volatile("prefetch.global.L1 [%0];" ::"l"(q + off));
+  };
+  auto load_batch = [&]() {
+    while (!in_done && in_i == in.take) {
+      in_done = !in.next(a, w.p, sc);
+      if (!in_done) enter();
     }
-    tile = __shfl_sync(kFull, tiles, in_i & 31);
-    ++in_i;
+    next_n = in_done ? 0 : min(in.take - in_i, 32);
+    if (lane < next_n) next_id = __ldg(a.block_table + (int64_t)in.b * a.max_blocks + in.s.first + in.p + in_i + lane);
+    in_i += next_n;
+  };
+  if (busy) {
+    enter();
+    load_batch();
+  }
+  // Step to the next page of this warp: its tile in `tile` (-1: a bad id); false when there is none.
+  auto fetch_next = [&]() -> bool {
+    if (cur_i == cur_n) {
+      if (next_n == 0) return false;
+      cur_n = next_n;
+      cur_i = 0;
+      const bool ok = next_id >= 0 && next_id < a.num_blocks;
+      bad_id |= lane < cur_n && !ok;
+      tiles = ok ? next_id * a.hkv + next_kvh : -1;
+      load_batch();
+    }
+    tile = __shfl_sync(kFull, tiles, cur_i);
+    ++cur_i;
     return true;
   };
   auto fetch_half = [&](int st, int side) {  // lane 0
@@ -490,7 +527,7 @@ __global__ void __launch_bounds__(PagedCfg<KIND, D, NT>::THREADS, 1)
 
   // ================================================================ portions
 #pragma unroll 1
-  for (bool more = true; more; more = out.next(a, w.p, sc, wt)) {
+  for (bool more = busy; more; more = out.next(a, w.p, sc)) {
     const int kvh = out.hg / w.p.groups, h0 = (out.hg - kvh * w.p.groups) * C::HEADS;
     const int nh = min(C::HEADS, a.n_rep - h0);
     const int64_t head0 = (int64_t)kvh * a.n_rep + h0;
@@ -505,7 +542,7 @@ __global__ void __launch_bounds__(PagedCfg<KIND, D, NT>::THREADS, 1)
       float up = 1.f;
       if (F8 && w.q_bf16) {
         uint32_t top = 0;
-#pragma unroll
+#pragma unroll 8
         for (int ks = 0; ks < KS; ++ks) {
           const uint2 x = __ldg(reinterpret_cast<const uint2*>(qr + ks * 16 + 4 * t));
           top = max(max(top, max(x.x & 0x7fffu, (x.x >> 16) & 0x7fffu)), max(x.y & 0x7fffu, (x.y >> 16) & 0x7fffu));
@@ -516,7 +553,8 @@ __global__ void __launch_bounds__(PagedCfg<KIND, D, NT>::THREADS, 1)
         const int e = (int)(top >> 7) - 127;
         up = power2(max(-126, min(14 - e, 126)));
       }
-#pragma unroll
+      // rolled where it can be: code that runs once costs its fetch, not its execution
+#pragma unroll(C::QREG ? KS : 8)
       for (int ks = 0; ks < KS; ++ks) {
         uint2 x;
         if (F8) {
@@ -560,7 +598,7 @@ __global__ void __launch_bounds__(PagedCfg<KIND, D, NT>::THREADS, 1)
 
     // ================================================================ pages
 #pragma unroll 1
-    for (int i = 0; i < out.n; ++i, st = st + 1 == S ? 0 : st + 1) {
+    for (int i = 0; i < out.take; ++i, st = st + 1 == S ? 0 : st + 1) {
       const bool here = valid >> st & 1;
       const uint32_t kb = stage0 + st * C::PAGE, vb = kb + C::HALF;
       float s[NT][4];
@@ -625,7 +663,7 @@ __global__ void __launch_bounds__(PagedCfg<KIND, D, NT>::THREADS, 1)
 
       if (here) {
         // ---- weights
-        const int rel = out.p + wt + i * tw;  // page of the segment
+        const int rel = out.p + i;  // page of the segment
         const bool whole = rel != cut_first && rel != cut_last;
         const int t_lo = out.s.lo - (out.s.first + rel) * kPage, t_hi = out.s.len - (out.s.first + rel) * kPage;
         auto counts = [&](int tok) { return tok >= t_lo && tok < t_hi; };
@@ -766,106 +804,33 @@ __global__ void __launch_bounds__(PagedCfg<KIND, D, NT>::THREADS, 1)
         for (int x = 4; x < 32; x <<= 1) l[nt][k] += __shfl_xor_sync(kFull, l[nt][k], x);
         if (dead) l[nt][k] = CUDART_NAN_F;
       }
-    // dims of accumulator rows g and g + 8 of tile j
-    auto dim0 = [&](int j) { return F8 ? 16 * j + 2 * g : 16 * j + g; };
-    constexpr int DIM1 = F8 ? 1 : 8;
-    const bool all = out.at == 0 && out.end == out.span;
-    if (out.at == 0 && lane == 0 && wt == 0) {
-      // cuts inside the segment: pieces that begin more than lead + tau behind its beginning and more
-      // than tau before its end
-      int2 c = make_int2(team, 0);
-      if (!all) {
-        const unsigned first = x_end - out.left, last = first + out.span;
-        c.y = pieces.from(last - w.p.tau) - pieces.from(first + w.p.lead + w.p.tau + 1);
-      }
-      w.cuts[(int64_t)out.b * heads + out.hg] = c;
-    }
-    // partials: [heads][D] sums, then [heads] references and [heads] totals; a portion that continues a
-    // segment takes the team's first slot, one that begins a segment the second
-    float* part = w.parts + ((int64_t)team * 2 + (out.at == 0)) * (C::HEADS * (D + 2));
-    if (tw == 1) {
+    // The rows: to the outputs when the warp had the whole segment, else to its slot of shared memory.
+    const bool begins = out.at == 0, all = begins && out.end == out.span;
+    if (all && lane == 0) w.cuts[(int64_t)out.b * heads + out.hg] = make_int2(0, 0);
+    const int64_t row = (int64_t)out.b * a.hq + head0;
+    float* dst = all ? a.out + row * D : begins ? own_stage : own_slot;
+    const int pitch = all ? D : C::PITCH;
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
+    for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          const int h = nt * 8 + 2 * t + k;
-          if (h >= nh) continue;
-          const int64_t row = (int64_t)out.b * a.hq + head0 + h;
-          float* dst = all ? a.out + row * D : part + h * D;
-          const float f = all ? (l[nt][k] == 0.f ? 0.f : 1.f / l[nt][k]) : 1.f;
+      for (int k = 0; k < 2; ++k) {
+        const int h = nt * 8 + 2 * t + k;
+        if (h >= nh) continue;
+        float* p = dst + h * pitch + (F8 ? 2 * g : g);  // accumulator rows g and g + 8 of tile j
+        const float f = all ? (l[nt][k] == 0.f ? 0.f : 1.f / l[nt][k]) : 1.f;
 #pragma unroll
-          for (int j = 0; j < KS; ++j) {
-            dst[dim0(j)] = o[j][nt][k] * f;
-            dst[dim0(j) + DIM1] = o[j][nt][k + 2] * f;
-          }
-          if (g == 0) {
-            if (!all) {
-              part[C::HEADS * D + h] = m[nt][k];
-              part[C::HEADS * (D + 1) + h] = l[nt][k];
-            } else if (a.lse) {
-              a.lse[row] = (m[nt][k] - kWeightUp + log2f(l[nt][k])) * 0.69314718055994530942f;
-            }
-          }
+        for (int j = 0; j < KS; ++j) {
+          p[16 * j] = o[j][nt][k] * f;
+          p[16 * j + (F8 ? 1 : 8)] = o[j][nt][k + 2] * f;
         }
-    } else {
-      float* slot = reinterpret_cast<float*>(sm + C::OFF_SLOT);
-      float* ml = reinterpret_cast<float*>(sm + C::OFF_ML);
-      const int act = min(NW, out.take);  // warps that had a page
-      if (wid < act) {
-        float* mine_o = slot + wid * C::HEADS * (D + 4);
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-          for (int k = 0; k < 2; ++k) {
-            const int h = nt * 8 + 2 * t + k;
-#pragma unroll
-            for (int j = 0; j < KS; ++j) {
-              mine_o[h * (D + 4) + dim0(j)] = o[j][nt][k];
-              mine_o[h * (D + 4) + dim0(j) + DIM1] = o[j][nt][k + 2];
-            }
-            if (g == 0) {
-              ml[(wid * C::HEADS + h) * 2] = m[nt][k];
-              ml[(wid * C::HEADS + h) * 2 + 1] = l[nt][k];
-            }
-          }
-      }
-      __syncthreads();
-      for (int i = tid; i < nh * (D / 4); i += C::THREADS) {
-        const int h = i / (D / 4), d4 = (i - h * (D / 4)) * 4;
-        float M = -CUDART_INF_F;
-#pragma unroll
-        for (int k = 0; k < NW; ++k)
-          if (k < act) M = fmaxf(M, ml[(k * C::HEADS + h) * 2]);
-        const float sub = M == -CUDART_INF_F ? 0.f : M;
-        float L = 0.f;
-        float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-        for (int k = 0; k < NW; ++k) {
-          if (k >= act) break;
-          const float2 v = *reinterpret_cast<const float2*>(ml + (k * C::HEADS + h) * 2);
-          const float c = ex2(v.x - sub);
-          L = fmaf(c, v.y, L);
-          const float4 y = *reinterpret_cast<const float4*>(slot + (k * C::HEADS + h) * (D + 4) + d4);
-          x.x = fmaf(c, y.x, x.x);
-          x.y = fmaf(c, y.y, x.y);
-          x.z = fmaf(c, y.z, x.z);
-          x.w = fmaf(c, y.w, x.w);
-        }
-        if (all) {
-          const int64_t row = (int64_t)out.b * a.hq + head0 + h;
-          const float f = L == 0.f ? 0.f : 1.f / L;
-          *reinterpret_cast<float4*>(a.out + row * D + d4) = make_float4(x.x * f, x.y * f, x.z * f, x.w * f);
-          if (d4 == 0 && a.lse) a.lse[row] = (M - kWeightUp + log2f(L)) * 0.69314718055994530942f;
-        } else {
-          *reinterpret_cast<float4*>(part + h * D + d4) = x;
-          if (d4 == 0) {
-            part[C::HEADS * D + h] = M;
-            part[C::HEADS * (D + 1) + h] = L;
-          }
+        if (g == 0) {
+          if (!all) ml[(begins * NW + wid) * C::HEADS + h] = make_float2(m[nt][k], l[nt][k]);
+          else if (a.lse) a.lse[row + h] = lse_of(m[nt][k], l[nt][k]);
         }
       }
-      __syncthreads();
-    }
+    // sequence, segment, whether it ends here, and where it ends on the line
+    if (!all && lane == 0)
+      rec[begins * NW + wid] = make_int4(out.b, out.hg, 1 + (out.end == out.span), x_end - out.left - out.at + out.span);
   }
   if (dead) {
     // copies still under way end before the CTA does
@@ -877,6 +842,91 @@ __global__ void __launch_bounds__(PagedCfg<KIND, D, NT>::THREADS, 1)
     if (lane == 0) flag_error(a.err, TQ_DEVERR_TIMEOUT);
   }
   if (bad_id) flag_error(a.err, TQ_DEVERR_BLOCK_ID);
+
+  // ================================================================ the CTA's cut segments
+  // A run: the piece that begins a segment (or the first warp's, if it continues one) and the pieces of
+  // the next warps that continue it.  A warp per (run, head).
+  __syncthreads();
+  const int4 r0 = lane < NW ? rec[lane] : make_int4(0, 0, 0, 0), r1 = lane < NW ? rec[NW + lane] : make_int4(0, 0, 0, 0);
+  const uint32_t goes_on = __ballot_sync(kFull, r0.z != 0), stops = __ballot_sync(kFull, r0.z == 2);
+  const uint32_t begun = __ballot_sync(kFull, r1.z != 0);
+  const int runs = __popc(begun) + (goes_on & 1), per_run = min(C::HEADS, a.n_rep);
+#pragma unroll 1
+  for (int it = wid; it < runs * per_run; it += NW) {
+    const int run = it / per_run, h = it - run * per_run;
+    // the run's first warp, and whether it begins the segment
+    const bool kind = !(run == 0 && (goes_on & 1));
+    const int lead = kind ? __fns(begun, 0, run + 1 - (int)(goes_on & 1)) : 0;
+    const int seq = __shfl_sync(kFull, kind ? r1.x : r0.x, lead), hg = __shfl_sync(kFull, kind ? r1.y : r0.y, lead);
+    const int ends_at = __shfl_sync(kFull, r1.w, lead);
+    // the warps behind it that continue: as long as there are such, up to one that ends it
+    const uint32_t on = lead < 31 ? goes_on >> (lead + 1) : 0, off = lead < 31 ? stops >> (lead + 1) : 0;
+    int more = __ffs(~on) - 1;
+    bool ends = !kind && (stops & 1);
+    if (ends) more = 0;
+    else if (off && __ffs(off) <= more) {
+      more = __ffs(off);
+      ends = true;
+    }
+    const int kvh = hg / w.p.groups, h0 = (hg - kvh * w.p.groups) * C::HEADS;
+    if (h >= a.n_rep - h0) continue;
+    // lane k: reference and total of warp k's piece
+    const bool part_of = lane >= lead && lane <= lead + more;
+    const float2 v = part_of ? ml[((lane == lead && kind) * NW + lane) * C::HEADS + h] : make_float2(-CUDART_INF_F, 0.f);
+    const float M = warp_max(v.x);
+    const float c = ex2(v.x - (M == -CUDART_INF_F ? 0.f : M));
+    const float L = warp_sum(c * v.y);
+    constexpr int V = D / 32, VL = V < 4 ? V : 4;
+    float x[V];
+#pragma unroll
+    for (int i = 0; i < V; ++i) x[i] = 0.f;
+    const float* p = (kind ? reinterpret_cast<const float*>(sm + lead * S * C::PAGE)
+                           : reinterpret_cast<const float*>(sm + C::OFF_SLOT)) + h * C::PITCH;
+#pragma unroll 4
+    for (int k = 0; k <= more; ++k) {
+      const float f = __shfl_sync(kFull, c, lead + k);
+#pragma unroll
+      for (int i = 0; i < V; i += VL) {
+        const float* q = p + (i / VL * 32 + lane) * VL;
+        if constexpr (VL == 2) {
+          const float2 y = *reinterpret_cast<const float2*>(q);
+          x[0] = fmaf(f, y.x, x[0]);
+          x[1] = fmaf(f, y.y, x[1]);
+        } else {
+          const float4 y = *reinterpret_cast<const float4*>(q);
+          x[i] = fmaf(f, y.x, x[i]);
+          x[i + 1] = fmaf(f, y.y, x[i + 1]);
+          x[i + 2] = fmaf(f, y.z, x[i + 2]);
+          x[i + 3] = fmaf(f, y.w, x[i + 3]);
+        }
+      }
+      p = reinterpret_cast<const float*>(sm + C::OFF_SLOT) + ((lead + k + 1) * C::HEADS + h) * C::PITCH;
+    }
+    // a whole segment goes to the outputs; else the CTA's slot of its kind: [HEADS][D] sums, then references
+    // and totals
+    const bool all = kind && ends;
+    const int64_t row = (int64_t)seq * a.hq + (int64_t)kvh * a.n_rep + h0 + h;
+    float* part = w.parts + ((int64_t)blockIdx.x * 2 + kind) * (C::HEADS * (D + 2));
+    float* dst = all ? a.out + row * D : part + h * D;
+    const float f = all ? (L == 0.f ? 0.f : 1.f / L) : 1.f;
+#pragma unroll
+    for (int i = 0; i < V; i += VL) {
+      float* q = dst + (i / VL * 32 + lane) * VL;
+      if constexpr (VL == 2) *reinterpret_cast<float2*>(q) = make_float2(x[0] * f, x[1] * f);
+      else *reinterpret_cast<float4*>(q) = make_float4(x[i] * f, x[i + 1] * f, x[i + 2] * f, x[i + 3] * f);
+    }
+    if (lane == 0) {
+      if (!all) {
+        part[C::HEADS * D + h] = M;
+        part[C::HEADS * (D + 1) + h] = L;
+      } else if (a.lse) {
+        a.lse[row] = lse_of(M, L);
+      }
+      // the last CTA with a piece of it: the one with the last cut more than tau before its end
+      if (kind && h == 0)
+        w.cuts[(int64_t)seq * heads + hg] = make_int2(blockIdx.x, ends ? blockIdx.x : (pieces.from(ends_at - w.p.tau) - 1) / NW);
+    }
+  }
 }
 
 // Joins the pieces of the segments that more than one team had, and writes the rows of empty sequences.
@@ -901,9 +951,9 @@ __global__ void __launch_bounds__(kMergeWarps * 32) paged_merge_kernel(const __g
   const int pages = seq_of(a, a.lengths[b]).pages;
   const int kvh = hg / w.p.groups, h0 = (hg - kvh * w.p.groups) * HEADS, nh = min(HEADS, a.n_rep - h0);
   const int64_t row0 = (int64_t)b * a.hq + (int64_t)kvh * a.n_rep + h0;
-  if (pages && cut.y == 0) return;  // one team had it
-  const int n = pages ? cut.y + 1 : 0;
-  // piece 0 is its team's second slot, the others the first slots of the teams behind
+  const int n = pages ? cut.y - cut.x + 1 : 0;  // CTAs that had pieces of it
+  if (n == 1) return;
+  // the first CTA's second slot, the first slots of those behind
   const float* part0 = w.parts + (int64_t)cut.x * 2 * PART;
   for (int h = JOIN == 1 ? 0 : blockIdx.y; h < nh; h += JOIN == 1 ? 1 : gridDim.y) {
     float M = -CUDART_INF_F, L = 0.f, x[V];
@@ -976,13 +1026,13 @@ __global__ void __launch_bounds__(kMergeWarps * 32) paged_merge_kernel(const __g
         for (int k = 0; k < JOIN; ++k) v = fmaf(c[k], sx[k][i], v);
         a.out[(row0 + h) * D + i] = v * f;
       }
-      if (threadIdx.x == 0 && a.lse) a.lse[row0 + h] = L == 0.f ? -CUDART_INF_F : (M - kWeightUp + log2f(L)) * 0.69314718055994530942f;
+      if (threadIdx.x == 0 && a.lse) a.lse[row0 + h] = lse_of(M, L);
       if (h + (int)gridDim.y < nh) __syncthreads();
     } else {
       const float f = L == 0.f ? 0.f : 1.f / L;
 #pragma unroll
       for (int i = 0; i < V; ++i) a.out[(row0 + h) * D + (i / VL * 32 + lane) * VL + i % VL] = x[i] * f;
-      if (lane == 0 && a.lse) a.lse[row0 + h] = L == 0.f ? -CUDART_INF_F : (M - kWeightUp + log2f(L)) * 0.69314718055994530942f;
+      if (lane == 0 && a.lse) a.lse[row0 + h] = lse_of(M, L);
     }
   }
 }
@@ -994,23 +1044,21 @@ PagedPlan plan_of(const tq_ctx* ctx, int batch) {
   PagedPlan p;
   const int n_rep = ctx->cfg.num_q_heads / ctx->cfg.num_kv_heads;
   p.groups = (n_rep + C::HEADS - 1) / C::HEADS;
-  const int64_t segments = (int64_t)batch * ctx->cfg.num_kv_heads * p.groups;
-  // Many segments: one warp each, no joining inside the CTA.  Few: the CTA's warps share one.
-  p.team_warps = segments >= 4 * (int64_t)ctx->sm_count ? 1 : C::NW;
-  p.teams = ctx->sm_count * (p.team_warps == 1 ? C::NW : 1);
-  p.lead = p.team_warps == 1 ? 2 : C::PAGE >= 32768 ? 2 : C::PAGE >= 16384 ? 4 : 8;
-  p.min_log2 = p.team_warps == 1 ? 2 : C::PAGE >= 32768 ? 2 : C::PAGE >= 16384 ? 3 : 4;
-  p.tau = C::PAGE >= 16384 ? 2 : 4;
+  p.teams = ctx->sm_count * C::NW;
+  p.lead = 2;
+  p.min_log2 = 1;
+  p.tau = 1;
   p.unit = 0;
   return p;
 }
 
 inline size_t align256(size_t x) { return (x + 255) & ~(size_t)255; }
 
-// The pieces' slots, then the segments' cuts.
+// The CTAs' slots, then the segments' cuts.
 template <int KIND, int D, int NT>
 size_t parts_bytes(const PagedPlan& p) {
-  return align256((size_t)p.teams * 2 * PagedCfg<KIND, D, NT>::HEADS * (D + 2) * 4);
+  using C = PagedCfg<KIND, D, NT>;
+  return align256((size_t)(p.teams / C::NW) * 2 * C::HEADS * (D + 2) * 4);
 }
 template <int KIND, int D, int NT>
 size_t workspace_of(const tq_ctx* ctx, int batch) {
@@ -1058,7 +1106,7 @@ cudaError_t launch_one(tq_ctx* ctx, const PagedArgs& a, void* workspace, cudaStr
   ctx->decode_kernel = "paged_kernel";
 
   const int segments = a.batch * a.hkv * w.p.groups;
-  const bool many = w.p.team_warps == 1;
+  const bool many = segments >= 4 * ctx->sm_count;
   cfg.gridDim = many ? dim3((segments + kMergeWarps - 1) / kMergeWarps) : dim3(segments, a.n_rep < C::HEADS ? a.n_rep : C::HEADS);
   cfg.blockDim = dim3(kMergeWarps * 32);
   cfg.dynamicSmemBytes = 0;
