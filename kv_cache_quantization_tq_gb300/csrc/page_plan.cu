@@ -7,9 +7,13 @@
 // What bounds it: launch latency and a chain of dependent loads (lengths, then queue, then the
 // stores); the data are a few bytes per request and 16 per token.  So nothing is handed from CTA
 // to CTA: every CTA scans all lengths itself (one entry of `stride` requests per thread, at most 1024
-// entries) and then writes its own share of the rows, pages and tokens, finding the request
-// of an item by bisection in the scan.  A second launch for the scan, or CTAs that wait for one
-// another, would cost more than the repeated reads (8 bytes per request, from L2).
+// entries, kept in shared memory) and then writes its own share of the rows, pages and tokens, finding the
+// request of an item by bisection in the scan.  A second launch for the scan, or CTAs that wait for one
+// another, would cost more than the repeated reads (8 bytes per request, from L2).  A thread has one token while
+// the grid has threads enough (the shortest chain), four with a shared search beyond that (fewer instructions).
+//
+// Sums are held at 2^31 - 1: every page handed out and every token written lies below that, so a held sum only
+// says "behind everything", whatever the lengths on the device are.
 #include "common.cuh"
 #include "paged.cuh"
 
@@ -17,236 +21,271 @@ namespace tq {
 namespace {
 
 constexpr int kPlanThreads = 1024;
+constexpr unsigned kHold = 0x7fffffffu;
+
+__device__ __forceinline__ unsigned add_held(unsigned x, unsigned y) { return min(x + y, kHold); }
 
 struct Req {
-  int64_t ctx, add;    // tokens held and added
-  int64_t old, need;   // pages held and wanted
-  int64_t back;        // pages given back
+  int ctx;             // tokens held
+  unsigned add;        // tokens added
+  unsigned old, need;  // pages held and wanted
+  unsigned back;       // pages given back
   bool ended, sound;   // sound: non-negative length, pages within the row
 };
 
-__device__ __forceinline__ int64_t pages_of(int64_t tokens, int ring) {
-  if (ring) return tokens > 0 ? (tokens - 1) / kRing * (kRing / kPage) : 0;
+__device__ __forceinline__ unsigned pages_of(unsigned tokens, int ring) {
+  if (ring) return tokens ? (tokens - 1) / kRing * (kRing / kPage) : 0;
   return (tokens + kPage - 1) / kPage;
 }
 
-__device__ __forceinline__ Req request(const PlanArgs& a, int b) {
+__device__ __forceinline__ Req request(const PlanArgs& a, int ctx, int add) {
   Req r;
-  r.ctx = a.ctx_len[b];
-  const int64_t n = a.new_len[b];
-  r.ended = n < 0;
-  r.add = n < 0 ? 0 : n;
-  r.old = r.ctx < 0 ? 0 : pages_of(r.ctx, a.ring);
-  const int64_t all = pages_of(r.ctx + r.add, a.ring);
-  r.sound = r.ctx >= 0 && all <= a.max_blocks && r.ctx + r.add <= 0x7fffffff;
+  r.ctx = ctx;
+  r.ended = add < 0;
+  r.add = add < 0 ? 0 : add;
+  r.old = ctx < 0 ? 0 : pages_of(ctx, a.ring);
+  const unsigned total = (unsigned)ctx + r.add;
+  const unsigned all = pages_of(total, a.ring);
+  r.sound = ctx >= 0 && total <= kHold && all <= (unsigned)a.max_blocks;
   r.need = r.sound && !r.ended ? all - r.old : 0;
   r.back = r.sound && r.ended ? r.old : 0;
   return r;
 }
 
 struct Sums {
-  int64_t tok, need, back;
+  unsigned tok, need, back;
   __device__ __forceinline__ Sums& operator+=(const Sums& o) {
-    tok += o.tok;
-    need += o.need;
-    back += o.back;
+    tok = add_held(tok, o.tok);
+    need = add_held(need, o.need);
+    back = add_held(back, o.back);
     return *this;
   }
+  __device__ __forceinline__ Sums& operator+=(const Req& r) { return *this += Sums{r.add, r.need, r.back}; }
 };
 
+__device__ __forceinline__ Sums of_lane(const Sums& s, int lane) {
+  return Sums{__shfl_sync(kFull, s.tok, lane), __shfl_sync(kFull, s.need, lane), __shfl_sync(kFull, s.back, lane)};
+}
+// Inclusive sums over the lanes.
+__device__ __forceinline__ Sums scan_warp(Sums s, int lane) {
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const Sums up{__shfl_up_sync(kFull, s.tok, o), __shfl_up_sync(kFull, s.need, o), __shfl_up_sync(kFull, s.back, o)};
+    if (lane >= o) s += up;
+  }
+  return s;
+}
+
 struct PlanSmem {
-  int64_t tok[kPlanThreads + 1], need[kPlanThreads + 1], back[kPlanThreads + 1];  // exclusive sums per entry
+  unsigned tok[kPlanThreads], need[kPlanThreads], back[kPlanThreads];  // sums in front of each entry
+  int ctx[kPlanThreads], add[kPlanThreads];                           // the requests, where stride is 1
   Sums warp[32];
-  int64_t taken[32];
+  unsigned taken[32];
 };
 
 // Free pages the step may hand out, and where they start; a state that is not one counts as empty.
 struct Queue {
-  int head;
-  int64_t count;
+  unsigned head, count;
   bool sound;
 };
-__device__ __forceinline__ Queue queue_of(const PlanArgs& a) {
-  Queue q;
-  q.head = a.queue_state[0];
-  q.count = a.queue_state[1];
-  q.sound = q.count >= 0 && q.count <= a.queue_cap && q.head >= 0 && (q.head < a.queue_cap || a.queue_cap == 0);
-  if (!q.sound) {
-    q.head = 0;
-    q.count = 0;
-  }
-  return q;
+
+// A request is served when it is sound, its tokens fit the buffer and its pages the queue.  `at` are the sums in
+// front of it; they grow with b, so the pages of the served requests are the first ones of the queue
+// without a gap.
+__device__ __forceinline__ bool served(const PlanArgs& a, const Queue& q, const Req& r, const Sums& at) {
+  return r.sound && (r.add == 0 || at.tok + r.add <= (unsigned)a.max_tokens) && (r.need == 0 || at.need + r.need <= q.count);
 }
 
-// A request is served when it is sound, its tokens fit the buffer and its pages the queue.  tok and need
-// are the sums in front of it; both sums grow with b, so the pages of the served requests are
-// the first ones of the queue without a gap.
-__device__ __forceinline__ bool served(const PlanArgs& a, const Queue& q, const Req& r, int64_t tok, int64_t need) {
-  return r.sound && (r.add == 0 || tok + r.add <= a.max_tokens) && (r.need == 0 || need + r.need <= q.count);
-}
-
-__device__ __forceinline__ int64_t wrap(int64_t i, int cap) { return i >= cap ? i - cap : i; }
+__device__ __forceinline__ unsigned wrap(unsigned i, unsigned cap) { return i >= cap ? i - cap : i; }
 
 // A free page by its place in the queue; -1 for an id that is not a block.
-__device__ __forceinline__ int free_page(const PlanArgs& a, const Queue& q, int64_t k) {
+__device__ __forceinline__ int free_page(const PlanArgs& a, const Queue& q, unsigned k) {
   const int id = a.queue[wrap(q.head + k, a.queue_cap)];
   return id >= 0 && id < a.num_blocks ? id : -1;
 }
 
-// Last entry whose sum in front is <= x (sums ascend; n >= 1).
-__device__ __forceinline__ int entry_of(const int64_t* sum, int n, int64_t x) {
-  int lo = 0, hi = n - 1;
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) >> 1;
-    if (sum[mid] <= x) lo = mid;
-    else hi = mid - 1;
-  }
-  return lo;
-}
-
-__global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanArgs a) {
+template <int T>  // tokens of a thread
+__global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanArgs a, const int vec) {
   __shared__ PlanSmem sm;
   const int tid = threadIdx.x, nt = blockDim.x, lane = tid & 31, wid = tid >> 5;
-  const int stride = (a.batch + nt - 1) / nt;                       // requests per entry
-  const int ne = stride ? (a.batch + stride - 1) / stride : 0;      // entries
-  const Queue q = queue_of(a);
-  uint32_t flags = q.sound ? 0u : TQ_DEVERR_PAGES;
+  const int stride = (a.batch + nt - 1) / nt;                   // requests per entry
+  const int ne = stride ? (a.batch + stride - 1) / stride : 0;  // entries
+  asm volatile("griddepcontrol.launch_dependents;");
+  asm volatile("griddepcontrol.wait;" ::: "memory");
 
   // ---- scan of the entries' sums
+  const int q_head = a.queue_state[0], q_count = a.queue_state[1];
   Sums own{0, 0, 0};
   const int b0 = tid < ne ? tid * stride : a.batch, b1 = min(b0 + stride, a.batch);
   for (int b = b0; b < b1; ++b) {
-    const Req r = request(a, b);
-    own += Sums{r.add, r.need, r.back};
+    sm.ctx[tid] = a.ctx_len[b];
+    sm.add[tid] = a.new_len[b];
+    own += request(a, sm.ctx[tid], sm.add[tid]);
   }
-  Sums inc = own;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const Sums up{__shfl_up_sync(kFull, inc.tok, o), __shfl_up_sync(kFull, inc.need, o),
-                  __shfl_up_sync(kFull, inc.back, o)};
-    if (lane >= o) inc += up;
-  }
+  Queue q;
+  q.sound = q_count >= 0 && q_count <= a.queue_cap && q_head >= 0 && (q_head < a.queue_cap || a.queue_cap == 0);
+  q.head = q.sound ? q_head : 0;
+  q.count = q.sound ? q_count : 0;
+  const Sums inc = scan_warp(own, lane);
   if (lane == 31) sm.warp[wid] = inc;
   __syncthreads();
-  Sums before{0, 0, 0}, total{0, 0, 0};
-  for (int w = 0; w < nt / 32; ++w) {
-    if (w == wid) before = total;
-    total += sm.warp[w];
-  }
-  before += Sums{inc.tok - own.tok, inc.need - own.need, inc.back - own.back};
+  const Sums warps = scan_warp(lane < nt / 32 ? sm.warp[lane] : Sums{0, 0, 0}, lane), total = of_lane(warps, 31);
+  // in front of this thread: the warps before, and the lanes before (held sums cannot be subtracted)
+  Sums before = of_lane(warps, max(wid - 1, 0));
+  if (wid == 0) before = Sums{0, 0, 0};
+  const Sums lanes = of_lane(inc, max(lane - 1, 0));
+  if (lane) before += lanes;
   sm.tok[tid] = before.tok;
   sm.need[tid] = before.need;
   sm.back[tid] = before.back;
   __syncthreads();
+  auto get = [&](int b) {
+    return stride == 1 ? request(a, sm.ctx[b], sm.add[b]) : request(a, a.ctx_len[b], a.new_len[b]);
+  };
+  // The request that item x of the given sums belongs to (x is below their total) and the sums in front of it.
+  auto find = [&](const unsigned* sum, unsigned x, unsigned Sums::*which, unsigned Req::*size, Sums& at, Req& r) {
+    int lo = 0, hi = ne - 1;  // the last entry that does not begin behind x
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (sum[mid] <= x) lo = mid;
+      else hi = mid - 1;
+    }
+    at = Sums{sm.tok[lo], sm.need[lo], sm.back[lo]};
+    int b = lo * stride;
+    r = get(b);
+    while (x >= at.*which + r.*size && b + 1 < a.batch) {
+      at += r;
+      r = get(++b);
+    }
+    return b;
+  };
 
   // ---- per-request outputs: this CTA's share of the entries (CTA 0 looks at all for the flags and the queue)
   const int per = (ne + gridDim.x - 1) / gridDim.x;
-  const bool mine = tid / max(per, 1) == (int)blockIdx.x && tid < ne;
-  int64_t taken = 0;
+  const bool mine = tid < ne && tid >= per * (int)blockIdx.x && tid < per * ((int)blockIdx.x + 1);
+  uint32_t flags = q.sound ? 0u : TQ_DEVERR_PAGES;
+  unsigned taken = 0;
   if (mine || blockIdx.x == 0) {
     Sums at = before;
     for (int b = b0; b < b1; ++b) {
-      const Req r = request(a, b);
-      const bool ok = served(a, q, r, at.tok, at.need);
+      const Req r = get(b);
+      const bool ok = served(a, q, r, at);
       if (ok && r.need) taken = at.need + r.need;
       if (!r.sound) flags |= TQ_DEVERR_POSITION;
       else if (!ok) flags |= TQ_DEVERR_PAGES;
       if (mine) {
-        const int64_t len = r.ended ? 0 : ok ? r.ctx + r.add : r.ctx < 0 ? 0 : r.ctx;
-        const int64_t paged = a.ring ? (len > 0 ? (len - 1) / kRing * kRing : 0) : len;
-        a.lengths[b] = (int)len;
-        if (a.n_paged) a.n_paged[b] = (int)paged;
-        if (a.n_ring) a.n_ring[b] = (int)(len - paged);
-        a.token_start[b] = (int)at.tok;
+        const int len = r.ended ? 0 : ok ? r.ctx + (int)r.add : max(r.ctx, 0);
+        const int paged = a.ring ? max(len - 1, 0) / kRing * kRing : len;
+        a.lengths[b] = len;
+        if (a.n_paged) a.n_paged[b] = paged;
+        if (a.n_ring) a.n_ring[b] = len - paged;
+        a.token_start[b] = at.tok;
       }
-      at += Sums{r.add, r.need, r.back};
+      at += r;
     }
   }
+  // pages given back beyond the queue's room cannot be stored: they are dropped and flagged
+  const unsigned room = q.sound ? a.queue_cap - q.count : 0, kept = min(total.back, room);
   if (blockIdx.x == 0) {
-    for (int o = 16; o; o >>= 1) taken = max(taken, __shfl_xor_sync(kFull, taken, o));
+    taken = __reduce_max_sync(kFull, taken);
     if (lane == 0) sm.taken[wid] = taken;
     __syncthreads();
     if (tid == 0) {
       for (int w = 1; w < nt / 32; ++w) taken = max(taken, sm.taken[w]);
-      // pages given back beyond the queue's room cannot be stored: they are dropped and flagged
-      const int64_t room = q.sound ? a.queue_cap - q.count : 0;
-      const int64_t kept = total.back < room ? total.back : room;
       if (kept < total.back) flags |= TQ_DEVERR_PAGES;
-      a.token_start[a.batch] = (int)total.tok;
-      a.queue_state_out[0] = q.sound ? (a.queue_cap ? (int)wrap(q.head + taken, a.queue_cap) : 0) : a.queue_state[0];
-      a.queue_state_out[1] = q.sound ? (int)(q.count - taken + kept) : a.queue_state[1];
+      a.token_start[a.batch] = total.tok;
+      a.queue_state_out[0] = q.sound ? (a.queue_cap ? wrap(q.head + taken, a.queue_cap) : 0) : q_head;
+      a.queue_state_out[1] = q.sound ? q.count - taken + kept : q_count;
     }
     if (flags) flag_error(a.err, flags);
   }
 
-  // ---- new table entries
-  const int64_t gt = (int64_t)blockIdx.x * nt + tid, gn = (int64_t)gridDim.x * nt;
+  // tokens from the first thread on, pages from the last: in a small step different warps have them
+  const unsigned gn = gridDim.x * nt, gt = blockIdx.x * nt + tid, rt = gn - 1 - gt;
   bool bad = false;
-  const int64_t want = total.need < q.count ? total.need : q.count;  // no later page can be handed out
-  for (int64_t j = gt; j < want; j += gn) {
-    const int e = entry_of(sm.need, ne, j);
-    Sums at{sm.tok[e], sm.need[e], 0};
-    int b = e * stride;
-    Req r = request(a, b);
-    while (j >= at.need + r.need) {
-      at += Sums{r.add, r.need, 0};
-      r = request(a, ++b);
-    }
-    if (!served(a, q, r, at.tok, at.need)) continue;
+
+  // ---- new table entries (pages beyond the queue's count go to nobody)
+  for (uint64_t j = rt; j < min(total.need, q.count); j += gn) {
+    Sums at;
+    Req r;
+    const int b = find(sm.need, j, &Sums::need, &Req::need, at, r);
+    if (!served(a, q, r, at)) continue;
     const int id = free_page(a, q, j);
     bad |= id < 0;
-    a.block_table[(int64_t)b * a.max_blocks + r.old + (j - at.need)] = id;
+    a.block_table[(int64_t)b * a.max_blocks + r.old + ((unsigned)j - at.need)] = id;
   }
 
   // ---- pages given back, behind the queue's end
-  const int64_t room = q.sound ? a.queue_cap - q.count : 0;
-  const int64_t kept = total.back < room ? total.back : room;
-  for (int64_t j = gt; j < kept; j += gn) {
-    const int e = entry_of(sm.back, ne, j);
-    int64_t at = sm.back[e];
-    int b = e * stride;
-    Req r = request(a, b);
-    while (j >= at + r.back) {
-      at += r.back;
-      r = request(a, ++b);
-    }
-    a.queue[wrap(wrap(q.head + q.count, a.queue_cap) + j, a.queue_cap)] =
-        a.block_table[(int64_t)b * a.max_blocks + (j - at)];
+  for (uint64_t j = rt; j < kept; j += gn) {
+    Sums at;
+    Req r;
+    const int b = find(sm.back, j, &Sums::back, &Req::back, at, r);
+    a.queue[wrap(wrap(q.head + q.count, a.queue_cap) + (unsigned)j, a.queue_cap)] =
+        a.block_table[(int64_t)b * a.max_blocks + ((unsigned)j - at.back)];
   }
 
   // ---- tokens
-  for (int64_t i = gt; i < a.max_tokens; i += gn) {
-    int64_t slot = -1;
-    int pos = -1, row = -1;
-    if (i < total.tok) {
-      const int e = entry_of(sm.tok, ne, i);
-      Sums at{sm.tok[e], sm.need[e], 0};
-      int b = e * stride;
-      Req r = request(a, b);
-      while (i >= at.tok + r.add) {
-        at += Sums{r.add, r.need, 0};
-        r = request(a, ++b);
+  for (uint64_t i0 = (uint64_t)T * gt; i0 < (unsigned)a.max_tokens; i0 += (uint64_t)T * gn) {
+    int64_t slot[T];
+    int pos[T], row[T];
+    Sums at{0, 0, 0};
+    Req r;
+    int b = -1, id = -1;
+    unsigned page = 0xffffffffu;  // the page of request b that id is
+    bool ok = false;
+    unsigned paged = 0;
+    auto open = [&]() {
+      ok = served(a, q, r, at);
+      const unsigned len = r.ctx + r.add;
+      paged = a.ring ? (len - 1) / kRing * kRing : len;  // len > 0: a token is at hand
+      page = 0xffffffffu;
+    };
+#pragma unroll
+    for (int k = 0; k < T; ++k) {
+      const unsigned i = (unsigned)i0 + k;
+      slot[k] = -1;
+      pos[k] = row[k] = -1;
+      if (i >= total.tok) continue;
+      if (b < 0) {
+        b = find(sm.tok, i, &Sums::tok, &Req::add, at, r);
+        open();
+      } else if (i >= at.tok + r.add) {
+        do {
+          at += r;
+          r = get(++b);
+        } while (i >= at.tok + r.add && b + 1 < a.batch);
+        open();
       }
-      const int64_t p = r.ctx + (i - at.tok);
-      pos = r.ctx < 0 || p > 0x7fffffff ? -1 : (int)p;
-      row = b;
-      const int64_t len = r.ctx + r.add;
-      if (served(a, q, r, at.tok, at.need) && (!a.ring || p < (len - 1) / kRing * kRing)) {
-        const int64_t pg = p / kPage;
-        int id;
-        if (pg < r.old) {
-          id = a.block_table[(int64_t)b * a.max_blocks + pg];
+      const unsigned p = (unsigned)r.ctx + (i - at.tok);
+      pos[k] = r.ctx < 0 || p > kHold ? -1 : (int)p;
+      row[k] = b;
+      if (!ok || p >= paged) continue;
+      if (p / kPage != page) {
+        page = p / kPage;
+        if (page < r.old) {
+          id = a.block_table[(int64_t)b * a.max_blocks + page];
           if (id < 0 || id >= a.num_blocks) id = -1;
         } else {
-          id = free_page(a, q, at.need + (pg - r.old));
+          id = free_page(a, q, at.need + (page - r.old));
         }
-        if (id >= 0) slot = (int64_t)id * kPage + p % kPage;
-        else bad = true;
+      }
+      if (id >= 0) slot[k] = (int64_t)id * kPage + p % kPage;
+      else bad = true;
+    }
+    if (T == 4 && vec && i0 + 4 <= (unsigned)a.max_tokens) {
+      reinterpret_cast<longlong2*>(a.slots + i0)[0] = make_longlong2(slot[0], slot[T > 1]);
+      reinterpret_cast<longlong2*>(a.slots + i0)[1] = make_longlong2(slot[T > 2 ? 2 : 0], slot[T - 1]);
+      if (a.positions) *reinterpret_cast<int4*>(a.positions + i0) = make_int4(pos[0], pos[T > 1], pos[T > 2 ? 2 : 0], pos[T - 1]);
+      if (a.rows) *reinterpret_cast<int4*>(a.rows + i0) = make_int4(row[0], row[T > 1], row[T > 2 ? 2 : 0], row[T - 1]);
+    } else {
+#pragma unroll
+      for (int k = 0; k < T; ++k) {
+        if (i0 + k >= (unsigned)a.max_tokens) break;
+        a.slots[i0 + k] = slot[k];
+        if (a.positions) a.positions[i0 + k] = pos[k];
+        if (a.rows) a.rows[i0 + k] = row[k];
       }
     }
-    a.slots[i] = slot;
-    if (a.positions) a.positions[i] = pos;
-    if (a.rows) a.rows[i] = row;
   }
   if (bad) flag_error(a.err, TQ_DEVERR_BLOCK_ID);
 }
@@ -255,13 +294,15 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanArgs a) {
 
 cudaError_t launch_plan(tq_ctx* ctx, const PlanArgs& a, cudaStream_t s) {
   // one CTA for a decode step; more when tokens (or rows, whose pages may be many) ask for them
-  const int threads = a.batch <= 256 ? 256 : kPlanThreads;
-  const int64_t work = ((int64_t)a.max_tokens + threads - 1) / threads;
+  const int threads = a.batch <= 128 ? 128 : a.batch <= 256 ? 256 : kPlanThreads;
+  const int64_t most = 2ll * ctx->sm_count * (kPlanThreads / threads);
+  const int tokens = a.max_tokens <= most * threads ? 1 : 4;
+  const int64_t work = ((int64_t)a.max_tokens + tokens * threads - 1) / (tokens * threads);
   int64_t grid = work > (a.batch + 63) / 64 ? work : (a.batch + 63) / 64;
   if (grid < 1) grid = 1;
-  if (grid > ctx->sm_count) grid = ctx->sm_count;
-  plan_kernel<<<(int)grid, threads, 0, s>>>(a);
-  const cudaError_t e = cudaGetLastError();
+  if (grid > most) grid = most;
+  const int vec = ((((uintptr_t)a.slots) | ((uintptr_t)a.positions) | ((uintptr_t)a.rows)) & 15) == 0;
+  const cudaError_t e = launch_early(tokens == 1 ? plan_kernel<1> : plan_kernel<4>, dim3((unsigned)grid), dim3(threads), 0, s, a, vec);
   if (e == cudaSuccess) ctx->launches++;
   return e;
 }

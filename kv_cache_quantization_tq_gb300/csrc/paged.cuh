@@ -70,6 +70,24 @@ struct PagedTensorMap {
 };
 bool encode_paged_map(const PagedTensorMap& t, CUtensorMap* map);
 
+// A launch that may begin before the kernel in front of it ends.  The kernel says griddepcontrol.wait before
+// it touches memory, and griddepcontrol.launch_dependents for the next such launch; what that hides is
+// the launch itself.
+template <typename... Params, typename... Values>
+cudaError_t launch_early(void (*kernel)(Params...), dim3 grid, dim3 block, size_t smem, cudaStream_t s, Values... values) {
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = grid;
+  cfg.blockDim = block;
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, static_cast<Params>(values)...);
+}
+
 cudaError_t launch_plan(tq_ctx* ctx, const PlanArgs& a, cudaStream_t s);
 cudaError_t launch_store(tq_ctx* ctx, const StoreArgs& a, cudaStream_t s);
 size_t paged_workspace(const tq_ctx* ctx, int batch);

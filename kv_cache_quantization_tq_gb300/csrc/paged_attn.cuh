@@ -1046,7 +1046,7 @@ PagedPlan plan_of(const tq_ctx* ctx, int batch) {
   p.groups = (n_rep + C::HEADS - 1) / C::HEADS;
   p.teams = ctx->sm_count * C::NW;
   p.lead = 2;
-  p.min_log2 = 1;
+  p.min_log2 = 0;
   p.tau = 1;
   p.unit = 0;
   return p;
@@ -1086,20 +1086,8 @@ cudaError_t launch_one(tq_ctx* ctx, const PagedArgs& a, void* workspace, cudaStr
   auto kern = paged_kernel<KIND, D, NT>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
   if (e != cudaSuccess) return e;
-  // Both launches may begin before the kernel in front of them ends (each waits for it before it reads or
-  // writes memory), which hides their launch and setup.
-  cudaLaunchAttribute attr{};
-  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr.val.programmaticStreamSerializationAllowed = 1;
-  cudaLaunchConfig_t cfg{};
-  cfg.stream = s;
-  cfg.attrs = &attr;
-  cfg.numAttrs = 1;
-  cfg.gridDim = dim3(ctx->sm_count);
-  cfg.blockDim = dim3(C::THREADS);
-  cfg.dynamicSmemBytes = C::SMEM;
   prof_start(ctx, kProfDecode, s);
-  e = cudaLaunchKernelEx(&cfg, kern, map, w);
+  e = launch_early(kern, dim3(ctx->sm_count), dim3(C::THREADS), C::SMEM, s, map, w);
   prof_stop(ctx, kProfDecode, s);
   if (e != cudaSuccess) return e;
   ctx->launches++;
@@ -1107,12 +1095,11 @@ cudaError_t launch_one(tq_ctx* ctx, const PagedArgs& a, void* workspace, cudaStr
 
   const int segments = a.batch * a.hkv * w.p.groups;
   const bool many = segments >= 4 * ctx->sm_count;
-  cfg.gridDim = many ? dim3((segments + kMergeWarps - 1) / kMergeWarps) : dim3(segments, a.n_rep < C::HEADS ? a.n_rep : C::HEADS);
-  cfg.blockDim = dim3(kMergeWarps * 32);
-  cfg.dynamicSmemBytes = 0;
+  const dim3 block(kMergeWarps * 32);
   prof_start(ctx, kProfMerge, s);
-  e = many ? cudaLaunchKernelEx(&cfg, paged_merge_kernel<D, C::HEADS, 1>, w, segments)
-           : cudaLaunchKernelEx(&cfg, paged_merge_kernel<D, C::HEADS, kMergeWarps>, w, segments);
+  e = many ? launch_early(paged_merge_kernel<D, C::HEADS, 1>, dim3((segments + kMergeWarps - 1) / kMergeWarps), block, 0, s, w, segments)
+           : launch_early(paged_merge_kernel<D, C::HEADS, kMergeWarps>, dim3(segments, a.n_rep < C::HEADS ? a.n_rep : C::HEADS), block, 0,
+                          s, w, segments);
   prof_stop(ctx, kProfMerge, s);
   if (e == cudaSuccess) ctx->launches++;
   return e;
