@@ -263,7 +263,7 @@ __device__ __forceinline__ uint32_t take_part(float& x, float& y) {
 struct Scan {
   const unsigned* pre;  // the line in front of each entry of `stride` sequences
   const int* len;      // the sequences' lengths in shared memory, or NULL
-  int stride, n;
+  int stride;
   unsigned heads;      // segments per sequence
   __device__ __forceinline__ Seq seq(const PagedArgs& a, int b) const {
     return seq_of(a, len ? len[b] : __ldg(a.lengths + b));
@@ -275,16 +275,14 @@ struct At {
   int b, hg, at, span;
   Seq s;
 };
-// The segments at x (lanes 0..15) and y (lanes 16..31).  For a whole warp.
-__device__ __forceinline__ At locate(const PagedArgs& a, const PagedPlan& p, const Scan& sc, unsigned x, unsigned y, int lane) {
-  int ex = -1, ey = -1;  // the last entries that do not begin behind x and y
-  for (int i = 0; i < sc.n; i += 32) {
-    const unsigned v = i + lane < sc.n ? sc.pre[i + lane] : 0xffffffffu;
-    ex += __popc(__ballot_sync(kFull, v <= x));
-    const uint32_t m = __ballot_sync(kFull, v <= y);
-    ey += __popc(m);
-    if (m != kFull) break;
-  }
+// The segments at x (lanes 0..15) and y (lanes 16..31); front: the line in front of the scan's entries 32 lane.  For
+// a whole warp.
+__device__ __forceinline__ At locate(const PagedArgs& a, const PagedPlan& p, const Scan& sc, unsigned front, unsigned x, unsigned y,
+                                     int lane) {
+  // the last entries that do not begin behind x and y: first their block of 32, then in it
+  const int bx = (__popc(__ballot_sync(kFull, front <= x)) - 1) * 32, by = (__popc(__ballot_sync(kFull, front <= y)) - 1) * 32;
+  const int ex = bx + __popc(__ballot_sync(kFull, sc.pre[bx + lane] <= x)) - 1;
+  const int ey = by + __popc(__ballot_sync(kFull, sc.pre[by + lane] <= y)) - 1;
   const int e = lane < 16 ? ex : ey;
   At r;
   unsigned at = (lane < 16 ? x : y) - sc.pre[e];
@@ -375,7 +373,6 @@ __global__ void __launch_bounds__(PagedCfg<KIND, D, NT>::THREADS, 1)
   Scan sc;
   sc.pre = pre;
   sc.stride = (a.batch + C::THREADS - 1) / C::THREADS;
-  sc.n = sc.stride == 1 ? a.batch : (a.batch + sc.stride - 1) / sc.stride;
   sc.heads = heads;
   sc.len = C::LENS && sc.stride == 1 ? len_sm : nullptr;
   unsigned own = 0;
@@ -395,13 +392,17 @@ __global__ void __launch_bounds__(PagedCfg<KIND, D, NT>::THREADS, 1)
   unsigned* wsum = reinterpret_cast<unsigned*>(sm + C::OFF_WARP);
   if (lane == 31) wsum[wid] = inc;
   __syncthreads();
-  unsigned before = 0, work = 0;
+  unsigned front = lane < NW ? wsum[lane] : 0, work;
 #pragma unroll
-  for (int i = 0; i < NW; ++i) {
-    if (i == wid) before = work;
-    work += wsum[i];
+  for (int o = 1; o < NW; o <<= 1) {
+    const unsigned up = __shfl_up_sync(kFull, front, o);
+    if (lane >= o) front += up;
   }
-  pre[tid] = before + inc - own;
+  work = __shfl_sync(kFull, front, NW - 1);
+  front = __shfl_up_sync(kFull, front, 1);  // the line in front of warp `lane`'s entries
+  if (lane == 0) front = 0;
+  if (lane >= NW) front = 0xffffffffu;
+  pre[tid] = __shfl_sync(kFull, front, wid) + inc - own;
   if (blockIdx.x == 0 && bad_len) flag_error(a.err, TQ_DEVERR_POSITION);
   if (work == 0) return;
   const Pieces pieces(w.p, work);
@@ -416,7 +417,7 @@ __global__ void __launch_bounds__(PagedCfg<KIND, D, NT>::THREADS, 1)
   bool busy = team < pieces.teams;
   if (busy) {
     unsigned x0 = pieces.begin(team), x1 = pieces.begin(team + 1);
-    At r = locate(a, w.p, sc, x0, min(x1, work - 1), lane);
+    At r = locate(a, w.p, sc, front, x0, min(x1, work - 1), lane);
     const unsigned x = settle(w.p, r, lane < 16 ? x0 : x1);
     const int back = __shfl_sync(kFull, r.at, 0), over = __shfl_sync(kFull, r.span, 0) - back;
     x0 = __shfl_sync(kFull, x, 0);
@@ -424,7 +425,7 @@ __global__ void __launch_bounds__(PagedCfg<KIND, D, NT>::THREADS, 1)
     if (team + 1 == pieces.teams) x1 = work;
     busy = x0 < x1;
     if (busy) {
-      if (back > w.p.lead + w.p.tau && over <= w.p.tau) r = locate(a, w.p, sc, x0, x0, lane);  // the next segment
+      if (back > w.p.lead + w.p.tau && over <= w.p.tau) r = locate(a, w.p, sc, front, x0, x0, lane);  // the next segment
       out.b = __shfl_sync(kFull, r.b, 0);
       out.hg = __shfl_sync(kFull, r.hg, 0);
       out.at = __shfl_sync(kFull, r.at, 0);
@@ -491,19 +492,6 @@ __global__ void __launch_bounds__(PagedCfg<KIND, D, NT>::THREADS, 1)
     if (F8 && side == 0)
       bulk_load(exp0 + st * C::EXP, a.pool + (size_t)tile * (C::PAGE + C::EXP) + C::PAGE, C::EXP, bar);
   };
-#pragma unroll 1
-  for (int st = 0; st < S; ++st)
-    if (fetch_next()) {
-      issued |= 1u << st;
-      if (tile >= 0) {
-        valid |= 1u << st;
-        if (lane == 0) {
-          fetch_half(st, 0);
-          fetch_half(st, 1);
-        }
-      }
-    }
-
   // ---- per-lane offsets of the ldmatrix rows (see the swizzle: 16-byte piece c of row r sits at c ^ (r & 7),
   // or c ^ ((r >> 1) & 3) in 64-byte rows)
   constexpr bool NARROW = C::SWIZZLE_ROW == 64;
@@ -524,6 +512,7 @@ __global__ void __launch_bounds__(PagedCfg<KIND, D, NT>::THREADS, 1)
   float o[KS][NT][4], m[NT][2], ref[NT][2], l[NT][2], qs[NT][2];
   const float log2e_scale = a.scale * 1.44269504088896340736f;
   int st = 0;
+  bool first = true;
 
   // ================================================================ portions
 #pragma unroll 1
@@ -589,6 +578,21 @@ __global__ void __launch_bounds__(PagedCfg<KIND, D, NT>::THREADS, 1)
     // pages of the segment that the sequence's end or the window cuts
     const int cut_first = out.s.lo % kPage ? 0 : -1, cut_last = out.s.len % kPage ? out.s.pages - 1 : -1;
     if constexpr (!C::QREG) __syncwarp();
+    if (first) {  // the first pages, behind the queries on the way to memory: behind them those would wait
+      first = false;
+#pragma unroll 1
+      for (int st = 0; st < S; ++st)
+        if (fetch_next()) {
+          issued |= 1u << st;
+          if (tile >= 0) {
+            valid |= 1u << st;
+            if (lane == 0) {
+              fetch_half(st, 0);
+              fetch_half(st, 1);
+            }
+          }
+        }
+    }
 #pragma unroll
     for (int j = 0; j < KS; ++j)
 #pragma unroll
