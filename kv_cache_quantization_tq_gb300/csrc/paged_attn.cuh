@@ -492,6 +492,22 @@ __global__ void __launch_bounds__(PagedCfg<KIND, D, NT>::THREADS, 1)
     if (F8 && side == 0)
       bulk_load(exp0 + st * C::EXP, a.pool + (size_t)tile * (C::PAGE + C::EXP) + C::PAGE, C::EXP, bar);
   };
+  auto fill = [&]() {
+#pragma unroll 1
+    for (int st = 0; st < S; ++st)
+      if (fetch_next()) {
+        issued |= 1u << st;
+        if (tile >= 0) {
+          valid |= 1u << st;
+          if (lane == 0) {
+            fetch_half(st, 0);
+            fetch_half(st, 1);
+          }
+        }
+      }
+  };
+  if (F8) fill();
+
   // ---- per-lane offsets of the ldmatrix rows (see the swizzle: 16-byte piece c of row r sits at c ^ (r & 7),
   // or c ^ ((r >> 1) & 3) in 64-byte rows)
   constexpr bool NARROW = C::SWIZZLE_ROW == 64;
@@ -578,20 +594,11 @@ __global__ void __launch_bounds__(PagedCfg<KIND, D, NT>::THREADS, 1)
     // pages of the segment that the sequence's end or the window cuts
     const int cut_first = out.s.lo % kPage ? 0 : -1, cut_last = out.s.len % kPage ? out.s.pages - 1 : -1;
     if constexpr (!C::QREG) __syncwarp();
-    if (first) {  // the first pages, behind the queries on the way to memory: behind them those would wait
+    // The first pages, behind the queries on the way to memory: queries behind them would wait.  (8-bit pages: before
+    // the loop; here it cost the loop's code 4%, 64 ragged sequences 176 against 169 us.)
+    if (!F8 && first) {
       first = false;
-#pragma unroll 1
-      for (int st = 0; st < S; ++st)
-        if (fetch_next()) {
-          issued |= 1u << st;
-          if (tile >= 0) {
-            valid |= 1u << st;
-            if (lane == 0) {
-              fetch_half(st, 0);
-              fetch_half(st, 1);
-            }
-          }
-        }
+      fill();
     }
 #pragma unroll
     for (int j = 0; j < KS; ++j)
@@ -877,9 +884,9 @@ __global__ void __launch_bounds__(PagedCfg<KIND, D, NT>::THREADS, 1)
     // lane k: reference and total of warp k's piece
     const bool part_of = lane >= lead && lane <= lead + more;
     const float2 v = part_of ? ml[((lane == lead && kind) * NW + lane) * C::HEADS + h] : make_float2(-CUDART_INF_F, 0.f);
-    const float M = warp_max(v.x);
-    const float c = ex2(v.x - (M == -CUDART_INF_F ? 0.f : M));
-    const float L = warp_sum(c * v.y);
+    float M, L = 0.f;
+    asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(M) : "f"(v.x));
+    const float c = ex2(v.x - (M == -CUDART_INF_F ? 0.f : M)), cl = c * v.y;
     constexpr int V = D / 32, VL = V < 4 ? V : 4;
     float x[V];
 #pragma unroll
@@ -889,6 +896,7 @@ __global__ void __launch_bounds__(PagedCfg<KIND, D, NT>::THREADS, 1)
 #pragma unroll 4
     for (int k = 0; k <= more; ++k) {
       const float f = __shfl_sync(kFull, c, lead + k);
+      L += __shfl_sync(kFull, cl, lead + k);
 #pragma unroll
       for (int i = 0; i < V; i += VL) {
         const float* q = p + (i / VL * 32 + lane) * VL;
@@ -934,16 +942,17 @@ __global__ void __launch_bounds__(PagedCfg<KIND, D, NT>::THREADS, 1)
 }
 
 // Joins the pieces of the segments that more than one team had, and writes the rows of empty sequences.
-// JOIN warps share a (segment, query head): with few segments of many pieces four, one head each; with many of
-// few pieces one warp for all heads of a segment.  A lane has D / 32 dims, four pieces are loaded at a
-// time: what bounds this kernel is the chain of loads from L2, segment -> pieces, and nothing else.
+// JOIN warps share a (segment, query head): with few segments of many pieces all of a CTA's, a CTA per head; with
+// many of few pieces one warp for all heads of a segment.  A lane has D / 32 dims, four pieces are loaded
+// at a time: what bounds this kernel is the chain of loads from L2, segment -> pieces, and nothing else.
 constexpr int kMergeWarps = 4;
 template <int D, int HEADS, int JOIN>
-__global__ void __launch_bounds__(kMergeWarps * 32) paged_merge_kernel(const __grid_constant__ PagedWork w, int segments) {
+__global__ void __launch_bounds__((JOIN == 1 ? kMergeWarps : JOIN) * 32) paged_merge_kernel(const __grid_constant__ PagedWork w, int segments) {
   constexpr int V = D / 32, VL = V < 4 ? V : 4;  // dims of a lane, and of one load
   constexpr int PART = HEADS * (D + 2);
   const PagedArgs& a = w.a;
-  __shared__ float sx[JOIN == 1 ? 1 : JOIN][D], sl[JOIN], sm_max[JOIN];
+  __shared__ __align__(16) float sx[JOIN == 1 ? 1 : JOIN][D];
+  __shared__ float sl[JOIN], sm_max[JOIN];
   const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
   asm volatile("griddepcontrol.launch_dependents;");
   asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -1014,7 +1023,9 @@ __global__ void __launch_bounds__(kMergeWarps * 32) paged_merge_kernel(const __g
         sm_max[wid] = M;
       }
       __syncthreads();
-      M = fmaxf(fmaxf(sm_max[0], sm_max[1]), fmaxf(sm_max[2], sm_max[3]));
+      M = sm_max[0];
+#pragma unroll
+      for (int k = 1; k < JOIN; ++k) M = fmaxf(M, sm_max[k]);
       const float sub = M == -CUDART_INF_F ? 0.f : M;
       float c[JOIN];
       L = 0.f;
@@ -1024,7 +1035,7 @@ __global__ void __launch_bounds__(kMergeWarps * 32) paged_merge_kernel(const __g
         L = fmaf(c[k], sl[k], L);
       }
       const float f = L == 0.f ? 0.f : 1.f / L;
-      for (int i = threadIdx.x; i < D; i += kMergeWarps * 32) {
+      for (int i = threadIdx.x; i < D; i += JOIN * 32) {
         float v = 0.f;
 #pragma unroll
         for (int k = 0; k < JOIN; ++k) v = fmaf(c[k], sx[k][i], v);
@@ -1078,10 +1089,17 @@ cudaError_t launch_one(tq_ctx* ctx, const PagedArgs& a, void* workspace, cudaStr
   w.p = plan_of<KIND, D, NT>(ctx, a.batch);
   w.q_bf16 = ctx->cfg.key_format == TQ_ELEM_BF16;
   w.parts = static_cast<float*>(workspace);
-  w.cuts = reinterpret_cast<int2*>(static_cast<uint8_t*>(workspace) + parts_bytes<KIND, D, NT>(w.p));
+  w.cuts = reinterpret_cast<int2*>(static_cast<uint8_t*>(workspace) + parts_bytes<KIND, D, NT>(w.p));  // for all CTAs
+  // The longest line these arguments allow: the unit keeps it below 2^31, and a short one gets no more CTAs than
+  // it has use for.
   const int64_t all = (int64_t)a.batch * a.hkv * w.p.groups;
-  while (all * (((int64_t)a.max_blocks >> w.p.unit) + 1 + w.p.lead) > 0x7fffffff)
+  int64_t pages = a.max_blocks;
+  if (a.window && pages > ((int64_t)a.window + 2 * kPage - 2) / kPage) pages = ((int64_t)a.window + 2 * kPage - 2) / kPage;
+  while (all * ((pages >> w.p.unit) + 1 + w.p.lead) > 0x7fffffff)
     if (++w.p.unit > 27) return cudaErrorInvalidValue;
+  const int64_t line = all * ((pages >> w.p.unit) + 1 + w.p.lead), want = (line + C::NW - 1) / C::NW;
+  const int ctas = want < ctx->sm_count ? (int)want : ctx->sm_count;
+  w.p.teams = ctas * C::NW;
   CUtensorMap map{};
   if (a.num_blocks > 0) {
     const PagedTensorMap tm{a.pool, C::ES, D, (int64_t)a.num_blocks * a.hkv, C::PAGE + C::EXP, C::SWIZZLE_ROW};
@@ -1091,7 +1109,7 @@ cudaError_t launch_one(tq_ctx* ctx, const PagedArgs& a, void* workspace, cudaStr
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
   if (e != cudaSuccess) return e;
   prof_start(ctx, kProfDecode, s);
-  e = launch_early(kern, dim3(ctx->sm_count), dim3(C::THREADS), C::SMEM, s, map, w);
+  e = launch_early(kern, dim3(ctas), dim3(C::THREADS), C::SMEM, s, map, w);
   prof_stop(ctx, kProfDecode, s);
   if (e != cudaSuccess) return e;
   ctx->launches++;
@@ -1099,11 +1117,15 @@ cudaError_t launch_one(tq_ctx* ctx, const PagedArgs& a, void* workspace, cudaStr
 
   const int segments = a.batch * a.hkv * w.p.groups;
   const bool many = segments >= 4 * ctx->sm_count;
-  const dim3 block(kMergeWarps * 32);
+  const dim3 each(segments, a.n_rep < C::HEADS ? a.n_rep : C::HEADS);  // a CTA per (segment, head)
   prof_start(ctx, kProfMerge, s);
-  e = many ? launch_early(paged_merge_kernel<D, C::HEADS, 1>, dim3((segments + kMergeWarps - 1) / kMergeWarps), block, 0, s, w, segments)
-           : launch_early(paged_merge_kernel<D, C::HEADS, kMergeWarps>, dim3(segments, a.n_rep < C::HEADS ? a.n_rep : C::HEADS), block, 0,
-                          s, w, segments);
+  if (many)
+    e = launch_early(paged_merge_kernel<D, C::HEADS, 1>, dim3((segments + kMergeWarps - 1) / kMergeWarps), dim3(kMergeWarps * 32), 0, s, w,
+                     segments);
+  else if (24 * segments > ctx->sm_count)
+    e = launch_early(paged_merge_kernel<D, C::HEADS, kMergeWarps>, each, dim3(kMergeWarps * 32), 0, s, w, segments);
+  else  // up to all CTAs' pieces in one segment (2 segments of 2900 pages, 76 pieces each: 5 us with 4 warps)
+    e = launch_early(paged_merge_kernel<D, C::HEADS, 16>, each, dim3(16 * 32), 0, s, w, segments);
   prof_stop(ctx, kProfMerge, s);
   if (e == cudaSuccess) ctx->launches++;
   return e;
