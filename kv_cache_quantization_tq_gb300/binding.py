@@ -244,6 +244,10 @@ class Context:
 
         self._device = torch.cuda.current_device()  # the device tq_create used
         self._page_bytes = self.page_bytes
+        # what the dense-layout calls look up on every call
+        self._raw = torch._C._cuda_getCurrentRawStream
+        self._types = (torch.int32, torch.int64, torch.float32, torch.uint8)
+        self._elem = torch.bfloat16 if self.cfg.key_format == TQ_ELEM_BF16 else torch.float16
 
     def close(self):
         if getattr(self, "ptr", None) and self.ptr.value:
@@ -413,18 +417,6 @@ class Context:
             raise ValueError(f"{name} must be contiguous")
         return t.data_ptr()
 
-    def _raw_stream(self, stream):
-        if stream is None:
-            import torch
-
-            return torch._C._cuda_getCurrentRawStream(self._device)
-        return _stream(stream)
-
-    def _elem(self):
-        import torch
-
-        return torch.bfloat16 if self.cfg.key_format == TQ_ELEM_BF16 else torch.float16
-
     def _rows_of(self, t, heads, elem, name):
         """Address and row stride of t [n, heads, d]: each row whole, rows any multiple of 8 elements apart."""
         shape, d = t.shape, self.head_dim
@@ -442,9 +434,8 @@ class Context:
         """tq_plan_pages: block tables, slot maps and the free-page queue of one step.  ctx_len, new_len, lengths,
         n_paged, n_ring int32 [B]; block_table int32 [B, max_blocks]; queue int32 [cap]; queue_state, queue_state_out
         int32 [2]; token_start int32 [B + 1]; slots int64 [max_tokens]; positions, rows int32 [max_tokens]."""
-        import torch
-
-        bsz, n, i32, addr = ctx_len.numel(), slots.numel(), torch.int32, self._addr
+        bsz, n, addr = ctx_len.numel(), slots.numel(), self._addr
+        i32, i64, _, _ = self._types
         self._check_bt(block_table, bsz)
         if (new_len.numel() != bsz or lengths.numel() != bsz or (n_paged is not None and n_paged.numel() != bsz)
                 or (n_ring is not None and n_ring.numel() != bsz)):
@@ -457,25 +448,24 @@ class Context:
                                addr(block_table, i32, "block_table"), block_table.shape[1], num_blocks,
                                addr(queue, i32, "queue"), queue.numel(), addr(queue_state, i32, "queue_state"),
                                addr(lengths, i32, "lengths"), addr(n_paged, i32, "n_paged"), addr(n_ring, i32, "n_ring"),
-                               addr(token_start, i32, "token_start"), addr(slots, torch.int64, "slots"),
+                               addr(token_start, i32, "token_start"), addr(slots, i64, "slots"),
                                addr(positions, i32, "positions"), addr(rows, i32, "rows"), n,
-                               addr(queue_state_out, i32, "queue_state_out"), self._raw_stream(stream))
+                               addr(queue_state_out, i32, "queue_state_out"), self._raw(self._device) if stream is None else _stream(stream))
         if st:
             raise TQError(st, "tq_plan_pages")
 
     def paged_store(self, k, v, slots, pool, stream=None):
         """tq_paged_store: k, v [n_tokens, Hkv, d] of the context's 16-bit type (rows may be strided) into the pages;
         slots int64 [n_tokens], negative to skip a token."""
-        import torch
-
-        elem, n = self._elem(), k.shape[0]
+        elem, n = self._elem, k.shape[0]
+        _, i64, _, u8 = self._types
         kp, ks = self._rows_of(k, self.num_kv_heads, elem, "k")
         vp, vs = self._rows_of(v, self.num_kv_heads, elem, "v")
         if v.shape[0] != n or slots.numel() != n:
             raise ValueError("k, v must be [n_tokens, Hkv, d] and slots [n_tokens]")
         self._check_pool(pool)
-        st = lib.tq_paged_store(self.ptr, kp, vp, ks, vs, self._addr(slots, torch.int64, "slots"), n,
-                                self._addr(pool, torch.uint8, "pool"), pool.shape[0], self._raw_stream(stream))
+        st = lib.tq_paged_store(self.ptr, kp, vp, ks, vs, self._addr(slots, i64, "slots"), n,
+                                self._addr(pool, u8, "pool"), pool.shape[0], self._raw(self._device) if stream is None else _stream(stream))
         if st:
             raise TQError(st, "tq_paged_store")
 
@@ -487,10 +477,9 @@ class Context:
     def paged_attention(self, q, pool, block_table, lengths, out, workspace, lse=None, window=0, scale=0.0, stream=None):
         """tq_paged_attention: q [batch, Hq, d] of the context's 16-bit type (rows may be strided), out fp32
         [batch, Hq, d], lse fp32 [batch, Hq] or None; window 0 for all positions, scale 0 for 1 / sqrt(d)."""
-        import torch
-
-        qp, qs = self._rows_of(q, self.num_q_heads, self._elem(), "q")
-        bsz, f32, i32, u8, addr = q.shape[0], torch.float32, torch.int32, torch.uint8, self._addr
+        qp, qs = self._rows_of(q, self.num_q_heads, self._elem, "q")
+        bsz, addr = q.shape[0], self._addr
+        i32, _, f32, u8 = self._types
         if out.shape != q.shape or lengths.numel() != bsz or (lse is not None and lse.shape != q.shape[:2]):
             raise ValueError("out must be [batch, Hq, d], lengths [batch] and lse [batch, Hq]")
         self._check_pool(pool)
@@ -498,7 +487,7 @@ class Context:
         st = lib.tq_paged_attention(self.ptr, qp, qs, bsz, addr(pool, u8, "pool"), pool.shape[0],
                                     addr(block_table, i32, "block_table"), block_table.shape[1],
                                     addr(lengths, i32, "lengths"), window, scale, addr(out, f32, "out"), addr(lse, f32, "lse"),
-                                    addr(workspace, u8, "workspace"), workspace.numel(), self._raw_stream(stream))
+                                    addr(workspace, u8, "workspace"), workspace.numel(), self._raw(self._device) if stream is None else _stream(stream))
         if st:
             raise TQError(st, "tq_paged_attention")
 

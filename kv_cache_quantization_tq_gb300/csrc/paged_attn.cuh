@@ -299,6 +299,9 @@ __device__ __forceinline__ At locate(const PagedArgs& a, const PagedPlan& p, con
   return r;
 }
 
+// The KV head of a segment.
+__device__ __forceinline__ int kv_head(const PagedPlan& p, int hg) { return p.groups == 1 ? hg : hg / p.groups; }
+
 // Moves a cut at x, which is in segment r, to that segment's end or beginning where it is near.
 __device__ __forceinline__ unsigned settle(const PagedPlan& p, const At& r, unsigned x) {
   if (r.at <= p.lead + p.tau) return x - r.at;
@@ -449,7 +452,7 @@ __global__ void __launch_bounds__(PagedCfg<KIND, D, NT>::THREADS, 1)
   bool bad_id = false, dead = false;
   auto enter = [&]() {
     in_i = 0;
-    next_kvh = in.hg / w.p.groups;
+    next_kvh = kv_head(w.p, in.hg);
     const int h0 = (in.hg - next_kvh * w.p.groups) * C::HEADS;
     const char* q = reinterpret_cast<const char*>(a.q + in.b * a.q_stride + ((int64_t)next_kvh * a.n_rep + h0) * D);
     for (int off = lane * 128; off < min(C::HEADS, a.n_rep - h0) * D * 2; off += 32 * 128)
@@ -533,7 +536,7 @@ __global__ void __launch_bounds__(PagedCfg<KIND, D, NT>::THREADS, 1)
   // ================================================================ portions
 #pragma unroll 1
   for (bool more = busy; more; more = out.next(a, w.p, sc)) {
-    const int kvh = out.hg / w.p.groups, h0 = (out.hg - kvh * w.p.groups) * C::HEADS;
+    const int kvh = kv_head(w.p, out.hg), h0 = (out.hg - kvh * w.p.groups) * C::HEADS;
     const int nh = min(C::HEADS, a.n_rep - h0);
     const int64_t head0 = (int64_t)kvh * a.n_rep + h0;
     // ---- queries as B fragments: head g, dims 16 ks + 2 t, + 1 and + 8, + 9 (8-bit pages: 4 t .. 4 t + 3,
@@ -867,7 +870,9 @@ __global__ void __launch_bounds__(PagedCfg<KIND, D, NT>::THREADS, 1)
     const int run = it / per_run, h = it - run * per_run;
     // the run's first warp, and whether it begins the segment
     const bool kind = !(run == 0 && (goes_on & 1));
-    const int lead = kind ? __fns(begun, 0, run + 1 - (int)(goes_on & 1)) : 0;
+    uint32_t left = begun;
+    for (int k = goes_on & 1; k < run; ++k) left &= left - 1;
+    const int lead = kind ? __ffs(left) - 1 : 0;
     const int seq = __shfl_sync(kFull, kind ? r1.x : r0.x, lead), hg = __shfl_sync(kFull, kind ? r1.y : r0.y, lead);
     const int ends_at = __shfl_sync(kFull, r1.w, lead);
     // the warps behind it that continue: as long as there are such, up to one that ends it
@@ -879,7 +884,7 @@ __global__ void __launch_bounds__(PagedCfg<KIND, D, NT>::THREADS, 1)
       more = __ffs(off);
       ends = true;
     }
-    const int kvh = hg / w.p.groups, h0 = (hg - kvh * w.p.groups) * C::HEADS;
+    const int kvh = kv_head(w.p, hg), h0 = (hg - kvh * w.p.groups) * C::HEADS;
     if (h >= a.n_rep - h0) continue;
     // lane k: reference and total of warp k's piece
     const bool part_of = lane >= lead && lane <= lead + more;
@@ -962,7 +967,7 @@ __global__ void __launch_bounds__((JOIN == 1 ? kMergeWarps : JOIN) * 32) paged_m
   const int2 cut = w.cuts[seg];
   const int b = seg / heads, hg = seg - b * heads;
   const int pages = seq_of(a, a.lengths[b]).pages;
-  const int kvh = hg / w.p.groups, h0 = (hg - kvh * w.p.groups) * HEADS, nh = min(HEADS, a.n_rep - h0);
+  const int kvh = kv_head(w.p, hg), h0 = (hg - kvh * w.p.groups) * HEADS, nh = min(HEADS, a.n_rep - h0);
   const int64_t row0 = (int64_t)b * a.hq + (int64_t)kvh * a.n_rep + h0;
   const int n = pages ? cut.y - cut.x + 1 : 0;  // CTAs that had pieces of it
   if (n == 1) return;

@@ -151,6 +151,7 @@ def test_binding_checks_shapes_before_the_library():
     ctx.ptr = None
     ctx.cfg = B.tq_config_init(B.TQ_LAYOUT_DENSE, 64, 4, 2)
     ctx.head_dim, ctx.num_q_heads, ctx.num_kv_heads, ctx._device = 64, 4, 2, 0
+    ctx._elem, ctx._types = torch.float16, (torch.int32, torch.int64, torch.float32, torch.uint8)
     i32 = lambda *s: torch.zeros(*s, dtype=torch.int32)  # noqa: E731
     q = torch.zeros(3, 4, 64, dtype=torch.float16)
     with pytest.raises(ValueError, match="CUDA"):
