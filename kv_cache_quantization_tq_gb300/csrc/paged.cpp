@@ -38,7 +38,7 @@ bool encode_paged_map(const PagedTensorMap& t, CUtensorMap* map) {
   if (!encode) return false;
   const cuuint64_t dims[3] = {(cuuint64_t)t.d, 2 * kPage, (cuuint64_t)t.tiles};
   const cuuint64_t strides[2] = {(cuuint64_t)t.d * t.elem, (cuuint64_t)t.tile_bytes};
-  const cuuint32_t box[3] = {(cuuint32_t)(t.row_bytes / t.elem), kPage, 1}, step[3] = {1, 1, 1};
+  const cuuint32_t box[3] = {(cuuint32_t)(t.row_bytes / t.elem), (cuuint32_t)t.box_rows, 1}, step[3] = {1, 1, 1};
   return encode(map, t.elem == 1 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_UINT16, 3,
                 const_cast<void*>(t.pool), dims, strides, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
                 t.row_bytes == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,

@@ -60,19 +60,20 @@ struct PagedArgs {
   uint32_t* err;
 };
 
-// The pool as a TMA tensor of 16-row boxes: rows of `d` elements of `elem` bytes, 32 rows (keys, then
-// values) per tile, `tiles` tiles `tile_bytes` apart; boxes `row_bytes` wide and swizzled (128 or 64).
+// The pool as a TMA tensor: rows of `d` elements of `elem` bytes, 32 rows (keys, then values) per tile,
+// `tiles` tiles `tile_bytes` apart; boxes of `box_rows` rows, `row_bytes` wide and swizzled (128 or 64).
 struct PagedTensorMap {
   const void* pool;
   int elem, d;
   int64_t tiles;
-  int tile_bytes, row_bytes;
+  int tile_bytes, row_bytes, box_rows;
 };
 bool encode_paged_map(const PagedTensorMap& t, CUtensorMap* map);
 
 // A launch that may begin before the kernel in front of it ends.  The kernel says griddepcontrol.wait before
 // it touches memory, and griddepcontrol.launch_dependents for the next such launch; what that hides is
-// the launch itself.
+// the launch itself.  Inputs are read by ordinary loads: the kernel in front may write them while this one
+// is resident, so they are not constant for its lifetime (no __ldg).
 template <typename... Params, typename... Values>
 cudaError_t launch_early(void (*kernel)(Params...), dim3 grid, dim3 block, size_t smem, cudaStream_t s, Values... values) {
   cudaLaunchAttribute attr{};

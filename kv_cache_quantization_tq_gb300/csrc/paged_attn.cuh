@@ -69,8 +69,11 @@ struct PagedCfg {
   static constexpr int fixed(int nw) { return nw * (SLOT + QBYTES) + nw * 32 * (LENS ? 8 : 4) + nw * 4; }
   static constexpr int per(int nw) { return nw * (PAGE + EXP + 16); }
   static constexpr int stages(int nw) { return (LIMIT - fixed(nw)) / per(nw); }
-  // Warps per CTA: small pages need more of them to keep the bytes in flight; two stages per warp before more warps
-  static constexpr int NW = PAGE <= 4096 && QREG && stages(16) >= 2 ? 16 : stages(8) >= 2 ? 8 : 4;
+  static constexpr int MIN_S = (HEADS * PITCH * 4 + PAGE - 1) / PAGE;  // a warp's stages hold its last piece
+  static constexpr bool fits(int nw, int s) { return stages(nw) >= (s > MIN_S ? s : MIN_S); }
+  // Warps per CTA: as many as fit, each with its stages.  With 16-bit pages of d = 128, 12 warps of one stage beat 8 of
+  // two (8 x 32K: 87.1 against 89.0 us; 16 ragged sequences: 622 against 645) and 16 of one (88.3, 625).
+  static constexpr int NW = PAGE <= 4096 && QREG && fits(16, 2) ? 16 : fits(12, 1) ? 12 : fits(8, 1) ? 8 : fits(6, 1) ? 6 : 4;
   static constexpr int S_FIT = stages(NW);
   static constexpr int S = S_FIT > 8 ? 8 : S_FIT;
   static_assert(S >= 1, "one stage per warp fits");
@@ -89,7 +92,13 @@ struct PagedCfg {
   static constexpr int SMEM = OFF_LEN + (LENS ? THREADS * 4 : 0) + 1024;
   static_assert(SMEM <= 232448, "shared memory");
   static constexpr int SWIZZLE_ROW = D * ES < 128 ? D * ES : 128;  // bytes of a row in one TMA box
-  static constexpr int BOXES = D * ES / SWIZZLE_ROW;               // boxes per half page
+  static constexpr int BOXES = D * ES / SWIZZLE_ROW;               // boxes side by side in a page
+  // With one stage keys and values are copied apart, so that the next keys come while the values are used; with more
+  // a page is one copy and one wait (fewer instructions: e4m3 at d = 64 54 against 64 us, at d = 512 65 against 69).
+  // Two stages of 4 KB e4m3 pages are too little for that: 64 ragged sequences 180 us, against 172 apart.
+  static constexpr bool APART = S == 1 || (KIND == kE4M3 && PAGE == 4096 && S == 2);
+  static constexpr int BOX_ROWS = APART ? kPage : 2 * kPage;
+  static constexpr int BOX = BOX_ROWS * SWIZZLE_ROW;
 };
 
 // ---------------------------------------------------------------- work split, shared by both kernels
@@ -266,7 +275,7 @@ struct Scan {
   int stride;
   unsigned heads;      // segments per sequence
   __device__ __forceinline__ Seq seq(const PagedArgs& a, int b) const {
-    return seq_of(a, len ? len[b] : __ldg(a.lengths + b));
+    return seq_of(a, len ? len[b] : a.lengths[b]);
   }
 };
 
@@ -365,7 +374,7 @@ __global__ void __launch_bounds__(PagedCfg<KIND, D, NT>::THREADS, 1)
 
   // what needs no input of the stream comes before the wait for the kernel in front
   asm volatile("griddepcontrol.launch_dependents;");
-  if (tid == 0) asm volatile("prefetch.tensormap [%0];" ::"l"(&map) : "memory");
+  if (tid == 0 && a.num_blocks > 0) asm volatile("prefetch.tensormap [%0];" ::"l"(&map) : "memory");
   if (lane < 2 * S) bar_init(bar0 + 8 * lane, 1);
   if (lane < 2) rec[lane * NW + wid] = make_int4(0, 0, 0, 0);
   asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -381,7 +390,7 @@ __global__ void __launch_bounds__(PagedCfg<KIND, D, NT>::THREADS, 1)
   unsigned own = 0;
   bool bad_len = false;
   for (int b = tid * sc.stride; b < min((tid + 1) * sc.stride, a.batch); ++b) {
-    const int len = __ldg(a.lengths + b);
+    const int len = a.lengths[b];
     if (C::LENS) len_sm[tid] = len;  // used where stride is 1
     bad_len |= !length_ok(a, len);
     own += span_of(w.p, seq_of(a, len)) * heads;
@@ -448,7 +457,7 @@ __global__ void __launch_bounds__(PagedCfg<KIND, D, NT>::THREADS, 1)
   int in_i = 0, next_n = 0, next_id = -1, next_kvh = 0;
   int cur_i = 0, cur_n = 0, tiles = -1, tile = -1;
   bool in_done = !busy;
-  uint32_t valid = 0, parity = 0, vparity = 0, issued = 0;  // bit per stage
+  uint32_t valid = 0, parity = 0, vparity = 0;  // bit per stage: a page is there or on its way; phases of the barriers
   bool bad_id = false, dead = false;
   auto enter = [&]() {
     in_i = 0;
@@ -464,7 +473,7 @@ __global__ void __launch_bounds__(PagedCfg<KIND, D, NT>::THREADS, 1)
       if (!in_done) enter();
     }
     next_n = in_done ? 0 : min(in.take - in_i, 32);
-    if (lane < next_n) next_id = __ldg(a.block_table + (int64_t)in.b * a.max_blocks + in.s.first + in.p + in_i + lane);
+    if (lane < next_n) next_id = a.block_table[(int64_t)in.b * a.max_blocks + in.s.first + in.p + in_i + lane];
     in_i += next_n;
   };
   if (busy) {
@@ -486,26 +495,24 @@ __global__ void __launch_bounds__(PagedCfg<KIND, D, NT>::THREADS, 1)
     ++cur_i;
     return true;
   };
-  auto fetch_half = [&](int st, int side) {  // lane 0
+  // Lane 0 starts the copies of a page's keys (side 0) or values (1), or of the whole page (side 0).
+  auto fetch = [&](int st, int side) {
     const uint32_t bar = bar0 + 16 * st + 8 * side, dst = stage0 + st * C::PAGE + side * C::HALF;
-    bar_expect(bar, C::HALF + (side == 0 ? C::EXP : 0));
+    bar_expect(bar, (C::APART ? C::HALF : C::PAGE) + (side == 0 ? C::EXP : 0));
 #pragma unroll
     for (int j = 0; j < C::BOXES; ++j)
-      tma_load(dst + j * (kPage * C::SWIZZLE_ROW), &map, j * (C::SWIZZLE_ROW / C::ES), side * kPage, tile, bar);
+      tma_load(dst + j * C::BOX, &map, j * (C::SWIZZLE_ROW / C::ES), side * kPage, tile, bar);
     if (F8 && side == 0)
       bulk_load(exp0 + st * C::EXP, a.pool + (size_t)tile * (C::PAGE + C::EXP) + C::PAGE, C::EXP, bar);
   };
   auto fill = [&]() {
 #pragma unroll 1
     for (int st = 0; st < S; ++st)
-      if (fetch_next()) {
-        issued |= 1u << st;
-        if (tile >= 0) {
-          valid |= 1u << st;
-          if (lane == 0) {
-            fetch_half(st, 0);
-            fetch_half(st, 1);
-          }
+      if (fetch_next() && tile >= 0) {
+        valid |= 1u << st;
+        if (lane == 0) {
+          fetch(st, 0);
+          if (C::APART) fetch(st, 1);
         }
       }
   };
@@ -518,9 +525,9 @@ __global__ void __launch_bounds__(PagedCfg<KIND, D, NT>::THREADS, 1)
     const int x = NARROW ? (row >> 1) & 3 : row & 7;
     return row * C::SWIZZLE_ROW + ((odd ^ x) << 4);
   };
-  // pieces 2 j and 2 j + 1 of the row: an even piece number is xored in, boxes of 8 pieces are 2048 bytes apart
+  // pieces 2 j and 2 j + 1 of the row: an even piece number is xored in, boxes hold 8 pieces of each row
   auto piece = [&](uint32_t base, uint32_t off, int j) -> uint32_t {
-    return base + (NARROW ? 0 : (j >> 2) * (kPage * 128)) + (off ^ ((NARROW ? 2 * j : (2 * j & 7)) << 4));
+    return base + (NARROW ? 0 : (j >> 2) * C::BOX) + (off ^ ((NARROW ? 2 * j : (2 * j & 7)) << 4));
   };
   const uint32_t k_off = row_off((lane & 7) + ((lane >> 3) & 1) * 8, lane >> 4);
   const uint32_t v_off = F8 ? k_off : row_off((lane & 7) + (lane >> 4) * 8, (lane >> 3) & 1);
@@ -552,7 +559,7 @@ __global__ void __launch_bounds__(PagedCfg<KIND, D, NT>::THREADS, 1)
         uint32_t top = 0;
 #pragma unroll 8
         for (int ks = 0; ks < KS; ++ks) {
-          const uint2 x = __ldg(reinterpret_cast<const uint2*>(qr + ks * 16 + 4 * t));
+          const uint2 x = *reinterpret_cast<const uint2*>(qr + ks * 16 + 4 * t);
           top = max(max(top, max(x.x & 0x7fffu, (x.x >> 16) & 0x7fffu)), max(x.y & 0x7fffu, (x.y >> 16) & 0x7fffu));
         }
         top = max(top, __shfl_xor_sync(kFull, top, 1));
@@ -566,10 +573,10 @@ __global__ void __launch_bounds__(PagedCfg<KIND, D, NT>::THREADS, 1)
       for (int ks = 0; ks < KS; ++ks) {
         uint2 x;
         if (F8) {
-          x = __ldg(reinterpret_cast<const uint2*>(qr + ks * 16 + 4 * t));
+          x = *reinterpret_cast<const uint2*>(qr + ks * 16 + 4 * t);
         } else {
-          x.x = __ldg(reinterpret_cast<const uint32_t*>(qr + ks * 16 + 2 * t));
-          x.y = __ldg(reinterpret_cast<const uint32_t*>(qr + ks * 16 + 2 * t + 8));
+          x.x = *reinterpret_cast<const uint32_t*>(qr + ks * 16 + 2 * t);
+          x.y = *reinterpret_cast<const uint32_t*>(qr + ks * 16 + 2 * t + 8);
         }
         if (F8 && w.q_bf16) {
           const __half2 u = __floats2half2_rn(__uint_as_float(x.x << 16) * up, __uint_as_float(x.x & 0xffff0000u) * up);
@@ -614,11 +621,10 @@ __global__ void __launch_bounds__(PagedCfg<KIND, D, NT>::THREADS, 1)
 #pragma unroll 1
     for (int i = 0; i < out.take; ++i, st = st + 1 == S ? 0 : st + 1) {
       const bool here = valid >> st & 1;
-      const uint32_t kb = stage0 + st * C::PAGE, vb = kb + C::HALF;
+      const uint32_t kb = stage0 + st * C::PAGE, vb = kb + (C::APART ? C::HALF : kPage * C::SWIZZLE_ROW);
       float s[NT][4];
       if (here && !dead) dead = !bar_wait(bar0 + 16 * st, parity >> st & 1);
       if (dead) continue;
-      issued &= ~(1u << st);
       if (here) parity ^= 1u << st;
       int ek0 = 0, ek1 = 0, ev0 = 0, ev1 = 0;
       if (here) {
@@ -667,13 +673,14 @@ __global__ void __launch_bounds__(PagedCfg<KIND, D, NT>::THREADS, 1)
 #pragma unroll
           for (int k = 0; k < 4; ++k) s[nt][k] += s2[nt][k];
       }
-      // the keys are read: the stage's next page may come
-      __syncwarp();
-      const bool again = fetch_next();
-      const int next_tile = tile;
-      valid = again && next_tile >= 0 ? valid | 1u << st : valid & ~(1u << st);
-      if (again) issued |= 1u << st;
-      if (again && next_tile >= 0 && lane == 0) fetch_half(st, 0);
+      bool again = false;
+      auto next_page = [&]() {
+        __syncwarp();  // every lane has read what the copy replaces
+        again = fetch_next() && tile >= 0;
+        valid = again ? valid | 1u << st : valid & ~(1u << st);
+        if (again && lane == 0) fetch(st, 0);
+      };
+      if (C::APART) next_page();  // the keys are read
 
       if (here) {
         // ---- weights
@@ -757,15 +764,19 @@ __global__ void __launch_bounds__(PagedCfg<KIND, D, NT>::THREADS, 1)
             pf[nt][k][1] = movmat(take_part<BF>(p[2], p[3]));
           }
         }
-        dead = !bar_wait(bar0 + 16 * st + 8, vparity >> st & 1);
-        if (!dead) vparity ^= 1u << st;
+        if (C::APART) {
+          dead = !bar_wait(bar0 + 16 * st + 8, vparity >> st & 1);
+          if (!dead) vparity ^= 1u << st;
+        }
         if (!whole) {
           // value rows that do not count: a weight of 0 does not remove a NaN
 #pragma unroll
           for (int k = 0; k < C::HALF / 512; ++k) {
-            const uint32_t off = (k * 32 + lane) * 16;
-            if (!counts((off / C::SWIZZLE_ROW) % kPage))
-              asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(vb + off), "r"(0) : "memory");
+            const uint32_t row = (k * 32 + lane) * 16 / C::SWIZZLE_ROW, col = (k * 32 + lane) * 16 % C::SWIZZLE_ROW;
+            if (!counts(row % kPage))
+              asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(vb + row / kPage * C::BOX + row % kPage * C::SWIZZLE_ROW + col),
+                           "r"(0)
+                           : "memory");
           }
           asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // before the stage's next copy
           __syncwarp();
@@ -805,8 +816,12 @@ __global__ void __launch_bounds__(PagedCfg<KIND, D, NT>::THREADS, 1)
           }
         }
       }
-      __syncwarp();
-      if (again && next_tile >= 0 && lane == 0) fetch_half(st, 1);
+      if (C::APART) {
+        __syncwarp();
+        if (again && lane == 0) fetch(st, 1);
+      } else {
+        next_page();
+      }
     }
 
     // ================================================================ the portion's result
@@ -849,9 +864,9 @@ __global__ void __launch_bounds__(PagedCfg<KIND, D, NT>::THREADS, 1)
   if (dead) {
     // copies still under way end before the CTA does
     for (int k = 0; k < S; ++k)
-      if ((issued & valid) >> k & 1) {
+      if (valid >> k & 1) {
         bar_wait(bar0 + 16 * k, parity >> k & 1);
-        bar_wait(bar0 + 16 * k + 8, vparity >> k & 1);
+        if (C::APART) bar_wait(bar0 + 16 * k + 8, vparity >> k & 1);
       }
     if (lane == 0) flag_error(a.err, TQ_DEVERR_TIMEOUT);
   }
@@ -1107,7 +1122,7 @@ cudaError_t launch_one(tq_ctx* ctx, const PagedArgs& a, void* workspace, cudaStr
   w.p.teams = ctas * C::NW;
   CUtensorMap map{};
   if (a.num_blocks > 0) {
-    const PagedTensorMap tm{a.pool, C::ES, D, (int64_t)a.num_blocks * a.hkv, C::PAGE + C::EXP, C::SWIZZLE_ROW};
+    const PagedTensorMap tm{a.pool, C::ES, D, (int64_t)a.num_blocks * a.hkv, C::PAGE + C::EXP, C::SWIZZLE_ROW, C::BOX_ROWS};
     if (!encode_paged_map(tm, &map)) return cudaErrorInvalidValue;
   }
   auto kern = paged_kernel<KIND, D, NT>;

@@ -67,7 +67,7 @@ __device__ __forceinline__ Share share_of(const StoreArgs& a, const Divisor& row
   Share p{nullptr, nullptr, 0, 0};
   const uint32_t row = u / L, tok = rows(row);  // a token's key heads, then its value heads
   if (tok >= (uint32_t)a.n_tokens) return p;
-  const int64_t slot = __ldg(a.slots + tok);
+  const int64_t slot = a.slots[tok];
   if (slot < 0) return p;
   if (slot >= (int64_t)a.num_blocks * kPage) {
     bad = true;
@@ -97,8 +97,8 @@ __global__ void __launch_bounds__(kStoreThreads) store_kernel(const StoreArgs a,
     p[k] = share_of<D, FP8>(a, rows, (blockIdx.x * N + k) * kStoreThreads + threadIdx.x, bad);
     x[k][0] = x[k][1] = make_uint4(0, 0, 0, 0);
     if (p[k].tile) {
-      x[k][0] = __ldg(p[k].src);
-      x[k][1] = __ldg(p[k].src + 1);
+      x[k][0] = p[k].src[0];
+      x[k][1] = p[k].src[1];
     }
   }
 #pragma unroll
