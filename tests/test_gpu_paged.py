@@ -316,6 +316,15 @@ def test_attention_in_a_graph_and_on_another_stream():
         check(e, o, l)
 
 
+def test_attention_line_beyond_31_bits():
+    """A block table so long that the work line of all pages it allows counts two pages as one."""
+    hkv, d, maxb = 64, 64, 2_200_000
+    e = make_case(59, [3000 - 177 * i for i in range(16)], hkv, hkv, d, 16, False, max_blocks=maxb)
+    assert 16 * hkv * maxb > 2 ** 31
+    check(e, *attend(e))
+    check(e, *attend(e, window=70), window=70)
+
+
 def test_page_offsets_beyond_32_bits():
     """Pages behind the first 4 GiB of the pool."""
     d, hkv = 512, 2
@@ -379,6 +388,41 @@ def test_plan_steps(batch, most, maxb, nb, max_tokens, ring):
         new[rng.random(batch) < 0.08] = -1
         r = check_plan(ctx, lens, new, table, queue, state, nb, max_tokens, ring)
         table, queue, state, lens = r["block_table"], r["queue"], r["queue_state"], r["lengths"]
+
+
+@pytest.mark.parametrize("skew", [0, 1])
+def test_plan_large_prefill(skew):
+    """More tokens than the grid has threads, the token buffers 16-byte aligned and not."""
+    ctx = dense(64, 1, 1)
+    ctx_len, new = np.array([5, 0, 700, 31], np.int32), np.array([200001, 3, -1, 199990], np.int32)
+    nb, maxb, cap, n = 30000, 13000, 30000, 400003
+    held = np.full((4, maxb), -1, np.int32)
+    held[0, 0], held[2, :44], held[3, :2] = 29000, np.arange(29001, 29045), [29100, 29101]
+    queue, state = np.arange(cap, dtype=np.int32) % 28000, np.array([3000, 26000], np.int32)
+    ref = paged.plan(ctx_len, new, held, queue, state, nb, n)
+    dev = lambda x: torch.from_numpy(x.copy()).cuda()  # noqa: E731
+    at = lambda dt: torch.full((n + skew,), 77, dtype=dt, device="cuda")[skew:]  # noqa: E731
+    r = dict(block_table=dev(held), queue=dev(queue), lengths=torch.zeros(4, dtype=torch.int32, device="cuda"),
+             token_start=torch.zeros(5, dtype=torch.int32, device="cuda"), slots=at(torch.int64), positions=at(torch.int32),
+             rows=at(torch.int32), queue_state=torch.zeros(2, dtype=torch.int32, device="cuda"))
+    ctx.plan_pages(dev(ctx_len), dev(new), r["block_table"], r["queue"], dev(state), r["lengths"], r["token_start"], r["slots"],
+                   r["queue_state"], num_blocks=nb, positions=r["positions"], rows=r["rows"])
+    assert ctx.device_errors() == ref["flags"]
+    for name, t in r.items():
+        assert np.array_equal(t.cpu().numpy(), ref[name]), name
+
+
+def test_plan_sums_beyond_31_bits():
+    """Lengths whose sums pass 2^31: what lies behind is refused, what lies in front is served."""
+    ctx = dense(64, 1, 1)
+    big = 2 ** 31 - 1
+    check_plan(ctx, [0, 0, 0, 4], [20, 10 ** 9, 10 ** 9, 3], np.full((4, 4), 2, np.int32), np.arange(8), [0, 8], 10, 50, 0)
+    r = run_plan(ctx, [0, 0, 0, 0], [20, big, big, big], np.full((4, 4), 2, np.int32), np.arange(8), [0, 8], 10, 50, 0)
+    assert r["lengths"].tolist() == [20, 0, 0, 0] and r["slots"][:20].tolist() == list(range(20)) and (r["slots"][20:] == -1).all()
+    assert ctx.device_errors() == paged.ERR_POSITION
+    # pages of rows that are all sound: 6 x 2^27 / 16 ... more than the queue has, more than 2^31 tokens in all
+    lens = run_plan(ctx, [0] * 5, [2 ** 29] * 5, np.zeros((5, 1), np.int32), np.arange(8), [0, 8], 10, 50, 0)["lengths"]
+    assert lens.tolist() == [0] * 5 and ctx.device_errors() == paged.ERR_POSITION
 
 
 def test_plan_refusals_and_bad_values():
@@ -473,6 +517,56 @@ def test_a_run_of_steps(bits, bf16):
         check(e, *attend(e))
         live = np.concatenate([table[b, :-(-int(lens[b]) // 16)] for b in range(bsz)])
         assert len(np.unique(live)) == len(live)
+
+
+@pytest.mark.parametrize("bits,bf16", FORMS)
+def test_captured_decode_steps(bits, bf16):
+    """Two decode steps (plan, store, attend; lengths and queue state handed from one to the other and back) in one
+    graph, replayed without a synchronisation between its kernels, against the pages as they then stand."""
+    d, hq, hkv, bsz, nb, maxb = 64, 6, 3, 5, 60, 10
+    gen = torch.Generator().manual_seed(67)
+    ctx, dt = dense(d, hq, hkv, bits, bf16), elem(bf16)
+    i32 = lambda *x: torch.tensor(x, dtype=torch.int32, device="cuda")  # noqa: E731
+    pool = torch.full((nb, hkv, ctx.page_bytes), 0xFF, dtype=torch.uint8, device="cuda")
+    table = torch.full((bsz, maxb), -1, dtype=torch.int32, device="cuda")
+    queue, states = torch.randperm(nb, generator=gen).int().cuda(), [i32(7, nb), i32(0, 0)]
+    # the two lengths share a line of memory, as slices of one buffer do
+    both = torch.zeros(2 * bsz, dtype=torch.int32, device="cuda")
+    lens, new = [both[:bsz], both[bsz:]], torch.ones(bsz, dtype=torch.int32, device="cuda")
+    starts, slots = torch.zeros(bsz + 1, dtype=torch.int32, device="cuda"), torch.zeros(bsz, dtype=torch.int64, device="cuda")
+    kv = [torch.zeros(bsz, 2 * hkv * d, dtype=dt, device="cuda") for _ in range(2)]
+    q = [torch.zeros(bsz, hq, d, dtype=dt, device="cuda") for _ in range(2)]
+    out = [torch.zeros(bsz, hq, d, device="cuda") for _ in range(2)]
+    lse = [torch.zeros(bsz, hq, device="cuda") for _ in range(2)]
+    ws = torch.full((ctx.paged_workspace_size(bsz),), 0xFF, dtype=torch.uint8, device="cuda")
+    snap = torch.zeros_like(pool)
+
+    def step(i):
+        ctx.plan_pages(lens[i], new, table, queue, states[i], lens[1 - i], starts, slots, states[1 - i], num_blocks=nb)
+        k, v = kv[i][:, :hkv * d].view(bsz, hkv, d), kv[i][:, hkv * d:].view(bsz, hkv, d)
+        ctx.paged_store(k, v, slots, pool)
+        ctx.paged_attention(q[i], pool, table, lens[1 - i], out[i], ws, lse=lse[i])
+
+    warm = torch.zeros_like(pool)  # the first calls outside the capture, on a pool of their own
+    ctx.paged_attention(q[0], warm, table, lens[0], out[0], ws)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        step(0)
+        snap.copy_(pool)
+        step(1)
+    host = 0
+    for _ in range(24):
+        for t in kv + q:
+            t.copy_(torch.randn(t.shape, generator=gen).to(dt))
+        g.replay()
+        torch.cuda.synchronize()
+        assert ctx.device_errors() == 0
+        for i, pages in ((0, snap), (1, pool)):
+            host += 1
+            e = dict(ctx=ctx, q=q[i].cpu(), pool=pages, bt=table.cpu().numpy(), lengths=np.full(bsz, host, np.int32), d=d, bits=bits, bf16=bf16)
+            check(e, out[i], lse[i])
+    assert states[0].tolist() == [(7 + bsz * 3) % nb, nb - bsz * 3] and lens[0].tolist() == [48] * bsz
 
 
 def test_plan_feeds_the_compressed_cache():
