@@ -405,17 +405,22 @@ class Context:
                   _stream(stream)), name)
 
     # -- page plan and dense pages
-    def _addr(self, t, dtype, name):
-        """Address of a contiguous tensor of `dtype` on the context's device (None -> NULL)."""
-        if t is None:
-            return None
-        if t.dtype is not dtype:
-            raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
-        if t.get_device() != self._device:
-            raise ValueError(f"{name} must be a CUDA tensor on device {self._device}, got {t.device}")
-        if not t.is_contiguous():
-            raise ValueError(f"{name} must be contiguous")
-        return t.data_ptr()
+    def _addrs(self, dtype, names, *tensors):
+        """Addresses of contiguous tensors of `dtype` on the context's device (None -> NULL)."""
+        dev, out = self._device, []
+        for t in tensors:
+            if t is None:
+                out.append(None)
+            elif t.dtype is dtype and t.get_device() == dev and t.is_contiguous():
+                out.append(t.data_ptr())
+            else:
+                name = names.split()[len(out)]
+                if t.dtype is not dtype:
+                    raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+                if t.get_device() != dev:
+                    raise ValueError(f"{name} must be a CUDA tensor on device {dev}, got {t.device}")
+                raise ValueError(f"{name} must be contiguous")
+        return out
 
     def _rows_of(self, t, heads, elem, name):
         """Address and row stride of t [n, heads, d]: each row whole, rows any multiple of 8 elements apart."""
@@ -434,7 +439,7 @@ class Context:
         """tq_plan_pages: block tables, slot maps and the free-page queue of one step.  ctx_len, new_len, lengths,
         n_paged, n_ring int32 [B]; block_table int32 [B, max_blocks]; queue int32 [cap]; queue_state, queue_state_out
         int32 [2]; token_start int32 [B + 1]; slots int64 [max_tokens]; positions, rows int32 [max_tokens]."""
-        bsz, n, addr = ctx_len.numel(), slots.numel(), self._addr
+        bsz, n = ctx_len.numel(), slots.numel()
         i32, i64, _, _ = self._types
         self._check_bt(block_table, bsz)
         if (new_len.numel() != bsz or lengths.numel() != bsz or (n_paged is not None and n_paged.numel() != bsz)
@@ -444,13 +449,13 @@ class Context:
             raise ValueError("queue_state and queue_state_out must be [2] and token_start [batch + 1]")
         if (positions is not None and positions.numel() != n) or (rows is not None and rows.numel() != n):
             raise ValueError("positions and rows must be [max_tokens], like slots")
-        st = lib.tq_plan_pages(self.ptr, addr(ctx_len, i32, "ctx_len"), addr(new_len, i32, "new_len"), bsz, ring_capacity,
-                               addr(block_table, i32, "block_table"), block_table.shape[1], num_blocks,
-                               addr(queue, i32, "queue"), queue.numel(), addr(queue_state, i32, "queue_state"),
-                               addr(lengths, i32, "lengths"), addr(n_paged, i32, "n_paged"), addr(n_ring, i32, "n_ring"),
-                               addr(token_start, i32, "token_start"), addr(slots, i64, "slots"),
-                               addr(positions, i32, "positions"), addr(rows, i32, "rows"), n,
-                               addr(queue_state_out, i32, "queue_state_out"), self._raw(self._device) if stream is None else _stream(stream))
+        (a_ctx, a_new, a_table, a_queue, a_state, a_len, a_paged, a_ring, a_start, a_pos, a_rows, a_out) = self._addrs(
+            i32, "ctx_len new_len block_table queue queue_state lengths n_paged n_ring token_start positions rows queue_state_out",
+            ctx_len, new_len, block_table, queue, queue_state, lengths, n_paged, n_ring, token_start, positions, rows, queue_state_out)
+        a_slots, = self._addrs(i64, "slots", slots)
+        st = lib.tq_plan_pages(self.ptr, a_ctx, a_new, bsz, ring_capacity, a_table, block_table.shape[1], num_blocks, a_queue,
+                               queue.numel(), a_state, a_len, a_paged, a_ring, a_start, a_slots, a_pos, a_rows, n, a_out,
+                               self._raw(self._device) if stream is None else _stream(stream))
         if st:
             raise TQError(st, "tq_plan_pages")
 
@@ -464,8 +469,10 @@ class Context:
         if v.shape[0] != n or slots.numel() != n:
             raise ValueError("k, v must be [n_tokens, Hkv, d] and slots [n_tokens]")
         self._check_pool(pool)
-        st = lib.tq_paged_store(self.ptr, kp, vp, ks, vs, self._addr(slots, i64, "slots"), n,
-                                self._addr(pool, u8, "pool"), pool.shape[0], self._raw(self._device) if stream is None else _stream(stream))
+        a_slots, = self._addrs(i64, "slots", slots)
+        a_pool, = self._addrs(u8, "pool", pool)
+        st = lib.tq_paged_store(self.ptr, kp, vp, ks, vs, a_slots, n, a_pool, pool.shape[0],
+                                self._raw(self._device) if stream is None else _stream(stream))
         if st:
             raise TQError(st, "tq_paged_store")
 
@@ -478,16 +485,18 @@ class Context:
         """tq_paged_attention: q [batch, Hq, d] of the context's 16-bit type (rows may be strided), out fp32
         [batch, Hq, d], lse fp32 [batch, Hq] or None; window 0 for all positions, scale 0 for 1 / sqrt(d)."""
         qp, qs = self._rows_of(q, self.num_q_heads, self._elem, "q")
-        bsz, addr = q.shape[0], self._addr
+        bsz = q.shape[0]
         i32, _, f32, u8 = self._types
         if out.shape != q.shape or lengths.numel() != bsz or (lse is not None and lse.shape != q.shape[:2]):
             raise ValueError("out must be [batch, Hq, d], lengths [batch] and lse [batch, Hq]")
         self._check_pool(pool)
         self._check_bt(block_table, bsz)
-        st = lib.tq_paged_attention(self.ptr, qp, qs, bsz, addr(pool, u8, "pool"), pool.shape[0],
-                                    addr(block_table, i32, "block_table"), block_table.shape[1],
-                                    addr(lengths, i32, "lengths"), window, scale, addr(out, f32, "out"), addr(lse, f32, "lse"),
-                                    addr(workspace, u8, "workspace"), workspace.numel(), self._raw(self._device) if stream is None else _stream(stream))
+        a_pool, a_ws = self._addrs(u8, "pool workspace", pool, workspace)
+        a_table, a_len = self._addrs(i32, "block_table lengths", block_table, lengths)
+        a_out, a_lse = self._addrs(f32, "out lse", out, lse)
+        st = lib.tq_paged_attention(self.ptr, qp, qs, bsz, a_pool, pool.shape[0], a_table, block_table.shape[1], a_len, window, scale,
+                                    a_out, a_lse, a_ws, workspace.numel(),
+                                    self._raw(self._device) if stream is None else _stream(stream))
         if st:
             raise TQError(st, "tq_paged_attention")
 
