@@ -21,6 +21,7 @@
 // swizzle, so that the rows of a plain [16][d] tile are read without bank conflicts) and mbarriers:
 //   S^T = K Q^T   mma.m16n8k16, A = 16 tokens x 16 dims of K (ldmatrix), B = 8 heads of Q in registers
 //   O^T += V^T P^T            A = 16 dims x 16 tokens of V (ldmatrix.trans), B = P^T (movmatrix of S^T's layout)
+// (8-bit pages: bytes are transposed by ldmatrix.m16n16.b8, its rows ordered as the weights' fragments want them.)
 // With tokens and dims on the 16-row side, 8 query heads per KV head fill the 8-column side and no row of the
 // products is padding; the accumulators are d / 4 registers.
 //
@@ -62,21 +63,24 @@ struct PagedCfg {
   static constexpr int QBYTES = QREG ? 0 : HEADS * D * 2;  // else in shared memory, per warp
   // A cut segment's sums: [HEADS][PITCH] floats (padded against bank conflicts where there is room) for the piece
   // that continues one; the piece that begins one is a warp's last, its stages are free to hold it.
-  static constexpr int PITCH = D < 512 && (NT == 1 || D == 64) ? D + 4 : D;
+  static constexpr int PITCH = D < 512 && (NT == 1 || D == 64) && !(KIND == kE4M3 && D == 128) ? D + 4 : D;
   static constexpr int SLOT = HEADS * PITCH * 4 + HEADS * 16 + 32;
   static constexpr bool LENS = D < 512;  // the lengths in shared memory (no room for them at 512)
   static constexpr int LIMIT = 232448 - 1024;  // 227 KB, less the alignment of the stages
-  static constexpr int fixed(int nw) { return nw * (SLOT + QBYTES) + nw * 32 * (LENS ? 8 : 4) + nw * 4; }
+  static constexpr int fixed(int nw) { return nw * (SLOT + QBYTES) + nw * 32 * (LENS ? 8 : 4) + nw * 4 + (nw == 16 ? nw * 48 : 0); }
   static constexpr int per(int nw) { return nw * (PAGE + EXP + 16); }
   static constexpr int stages(int nw) { return (LIMIT - fixed(nw)) / per(nw); }
   static constexpr int MIN_S = (HEADS * PITCH * 4 + PAGE - 1) / PAGE;  // a warp's stages hold its last piece
   static constexpr bool fits(int nw, int s) { return stages(nw) >= (s > MIN_S ? s : MIN_S); }
-  // Warps per CTA: as many as fit, each with its stages.  With 16-bit pages of d = 128, 12 warps of one stage beat 8 of
-  // two (8 x 32K: 87.1 against 89.0 us; 16 ragged sequences: 622 against 645) and 16 of one (88.3, 625).
-  static constexpr int NW = PAGE <= 4096 && QREG && fits(16, 2) ? 16 : fits(12, 1) ? 12 : fits(8, 1) ? 8 : fits(6, 1) ? 6 : 4;
-  static constexpr int S_FIT = stages(NW);
-  static constexpr int S = S_FIT > 8 ? 8 : S_FIT;
-  static_assert(S >= 1, "one stage per warp fits");
+  // Warps per CTA: as many as fit.  Stages: what keeps about 96 KB (e4m3) or 128 KB per multiprocessor on the way.  More
+  // is not better: with every queue full the multiprocessors farther from memory fall behind and the last of
+  // them ends late.  16-bit pages of d = 128, 8 x 32K and 16 ragged sequences: 12 warps x 1 stage 87.1 and 622 us,
+  // 8 x 2 89.0 and 645, 16 x 1 88.3 and 625.  e4m3 pages of d = 128, 64 ragged sequences: 16 x 1 169 us, 16 x 2 181.
+  static constexpr int NW = PAGE <= 4096 && QREG && fits(16, 1) ? 16 : fits(12, 1) ? 12 : fits(8, 1) ? 8 : fits(6, 1) ? 6 : 4;
+  static constexpr int S_WANT = (KIND == kE4M3 ? 96 : 128) * 1024 / (NW * PAGE);
+  static constexpr int S_LEAST = S_WANT > MIN_S ? S_WANT : MIN_S;
+  static constexpr int S = S_LEAST < stages(NW) ? S_LEAST : stages(NW);
+  static_assert(S >= 1 && S <= 8, "one stage per warp fits");
   static constexpr int THREADS = NW * 32;
   static_assert(HEADS * PITCH * 4 <= S * PAGE, "a warp's stages hold its last piece");
   // dynamic shared memory, from a 1024-byte aligned base
@@ -89,14 +93,16 @@ struct PagedCfg {
   static constexpr int OFF_PRE = OFF_BAR + NW * S * 16;
   static constexpr int OFF_WARP = OFF_PRE + THREADS * 4;
   static constexpr int OFF_LEN = OFF_WARP + NW * 4;
-  static constexpr int SMEM = OFF_LEN + (LENS ? THREADS * 4 : 0) + 1024;
+  // with 16 warps (128 registers a thread) the way of the fetches is kept here between batches
+  static constexpr bool PARK = NW == 16;
+  static constexpr int OFF_WALK = (OFF_LEN + (LENS ? THREADS * 4 : 0) + 15) / 16 * 16;
+  static constexpr int SMEM = OFF_WALK + (PARK ? NW * 48 : 0) + 1024;
   static_assert(SMEM <= 232448, "shared memory");
   static constexpr int SWIZZLE_ROW = D * ES < 128 ? D * ES : 128;  // bytes of a row in one TMA box
   static constexpr int BOXES = D * ES / SWIZZLE_ROW;               // boxes side by side in a page
   // With one stage keys and values are copied apart, so that the next keys come while the values are used; with more
   // a page is one copy and one wait (fewer instructions: e4m3 at d = 64 54 against 64 us, at d = 512 65 against 69).
-  // Two stages of 4 KB e4m3 pages are too little for that: 64 ragged sequences 180 us, against 172 apart.
-  static constexpr bool APART = S == 1 || (KIND == kE4M3 && PAGE == 4096 && S == 2);
+  static constexpr bool APART = S == 1;
   static constexpr int BOX_ROWS = APART ? kPage : 2 * kPage;
   static constexpr int BOX = BOX_ROWS * SWIZZLE_ROW;
 };
@@ -199,6 +205,13 @@ __device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr) {
 }
 __device__ __forceinline__ void ldsm4t(uint32_t (&r)[4], uint32_t addr) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+// Two 16 x 16 tiles of bytes, transposed: rows g and g + 8 of the first, then of the second, bytes 4 t .. 4 t + 3.
+__device__ __forceinline__ void ldsm2t8(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m16n16.x2.trans.shared.b8 {%0,%1,%2,%3}, [%4];"
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
                : "r"(addr)
                : "memory");
@@ -319,7 +332,7 @@ __device__ __forceinline__ unsigned settle(const PagedPlan& p, const At& r, unsi
 }
 
 // A warp's way along its piece of the line, by portions: its share of one segment, pages p .. p + take - 1.
-struct Walk {
+struct __align__(16) Walk {
   int b, hg;
   int at, end, span;  // the portion is at .. end of the segment's span
   int p, take;        // its first page and its pages
@@ -424,7 +437,7 @@ __global__ void __launch_bounds__(PagedCfg<KIND, D, NT>::THREADS, 1)
 
   // ---- this warp's piece
   const unsigned team = blockIdx.x * NW + wid;
-  Walk out{}, in;        // the portion being computed, and the one being fetched
+  Walk out{}, in_reg;    // the portion being computed, and the one being fetched
   unsigned x_end = 0;    // where the piece ends
   bool busy = team < pieces.teams;
   if (busy) {
@@ -449,7 +462,6 @@ __global__ void __launch_bounds__(PagedCfg<KIND, D, NT>::THREADS, 1)
       x_end = x1;
     }
   }
-  in = out;
 
   // ---- fetching
   // Block ids are looked up by batches of up to 32 pages (one per lane), a batch ahead, and the queries of a new
@@ -459,7 +471,8 @@ __global__ void __launch_bounds__(PagedCfg<KIND, D, NT>::THREADS, 1)
   bool in_done = !busy;
   uint32_t valid = 0, parity = 0, vparity = 0;  // bit per stage: a page is there or on its way; phases of the barriers
   bool bad_id = false, dead = false;
-  auto enter = [&]() {
+  Walk* parked = reinterpret_cast<Walk*>(sm + C::OFF_WALK) + wid;
+  auto enter = [&](const Walk& in) {
     in_i = 0;
     next_kvh = kv_head(w.p, in.hg);
     const int h0 = (in.hg - next_kvh * w.p.groups) * C::HEADS;
@@ -468,16 +481,33 @@ __global__ void __launch_bounds__(PagedCfg<KIND, D, NT>::THREADS, 1)
       asm volatile("prefetch.global.L1 [%0];" ::"l"(q + off));
   };
   auto load_batch = [&]() {
+    Walk in;
+    if constexpr (C::PARK) in = *parked;
+    else in = in_reg;
+    const bool moves = !in_done && in_i == in.take;
     while (!in_done && in_i == in.take) {
       in_done = !in.next(a, w.p, sc);
-      if (!in_done) enter();
+      if (!in_done) enter(in);
+    }
+    if constexpr (C::PARK) {
+      __syncwarp();
+      if (moves && lane == 0) *parked = in;
+      __syncwarp();
+    } else {
+      in_reg = in;
     }
     next_n = in_done ? 0 : min(in.take - in_i, 32);
     if (lane < next_n) next_id = a.block_table[(int64_t)in.b * a.max_blocks + in.s.first + in.p + in_i + lane];
     in_i += next_n;
   };
   if (busy) {
-    enter();
+    if constexpr (C::PARK) {
+      if (lane == 0) *parked = out;
+      __syncwarp();
+    } else {
+      in_reg = out;
+    }
+    enter(out);
     load_batch();
   }
   // Step to the next page of this warp: its tile in `tile` (-1: a bad id); false when there is none.
@@ -530,7 +560,9 @@ __global__ void __launch_bounds__(PagedCfg<KIND, D, NT>::THREADS, 1)
     return base + (NARROW ? 0 : (j >> 2) * C::BOX) + (off ^ ((NARROW ? 2 * j : (2 * j & 7)) << 4));
   };
   const uint32_t k_off = row_off((lane & 7) + ((lane >> 3) & 1) * 8, lane >> 4);
-  const uint32_t v_off = F8 ? k_off : row_off((lane & 7) + (lane >> 4) * 8, (lane >> 3) & 1);
+  // 8-bit values: bytes 4 t .. 4 t + 3 of a transposed row are to be tokens 2 t, 2 t + 1, 2 t + 8, 2 t + 9
+  const uint32_t v_off = F8 ? row_off(2 * ((lane & 15) >> 2) + (lane & 1) + (lane & 2) * 4, lane >> 4)
+                            : row_off((lane & 7) + (lane >> 4) * 8, (lane >> 3) & 1);
 
   uint32_t qf[C::QREG ? NT : 1][C::QREG ? KS : 1][2];
   uint2* q_sm = reinterpret_cast<uint2*>(sm + C::OFF_Q + wid * C::QBYTES);
@@ -797,13 +829,11 @@ __global__ void __launch_bounds__(PagedCfg<KIND, D, NT>::THREADS, 1)
 #pragma unroll
             for (int j = 0; j < KS / 2; ++j) {
               uint32_t r[4];
-              ldsm4t(r, piece(vb, v_off, j));
+              ldsm2t8(r, piece(vb, v_off, j));
 #pragma unroll
               for (int c = 0; c < 2; ++c) {
-                // bytes 0, 1: dims 2 g, 2 g + 1 of token 2 t, 2, 3: of token 2 t + 1; a row is a dim's two tokens
-                const uint32_t x = r[2 * c], y = r[2 * c + 1];
-                const uint32_t af[4] = {f16_of_e4m3(__byte_perm(x, 0, 0x20)), f16_of_e4m3(__byte_perm(x, 0, 0x31)),
-                                        f16_of_e4m3(__byte_perm(y, 0, 0x20)), f16_of_e4m3(__byte_perm(y, 0, 0x31))};
+                const uint32_t af[4] = {f16_of_e4m3(r[2 * c]), f16_of_e4m3(r[2 * c + 1]), f16_of_e4m3_high(r[2 * c]),
+                                        f16_of_e4m3_high(r[2 * c + 1])};
                 add(2 * j + c, af);
               }
             }
@@ -846,12 +876,12 @@ __global__ void __launch_bounds__(PagedCfg<KIND, D, NT>::THREADS, 1)
       for (int k = 0; k < 2; ++k) {
         const int h = nt * 8 + 2 * t + k;
         if (h >= nh) continue;
-        float* p = dst + h * pitch + (F8 ? 2 * g : g);  // accumulator rows g and g + 8 of tile j
+        float* p = dst + h * pitch + g;  // accumulator rows g and g + 8 of tile j
         const float f = all ? (l[nt][k] == 0.f ? 0.f : 1.f / l[nt][k]) : 1.f;
 #pragma unroll
         for (int j = 0; j < KS; ++j) {
           p[16 * j] = o[j][nt][k] * f;
-          p[16 * j + (F8 ? 1 : 8)] = o[j][nt][k + 2] * f;
+          p[16 * j + 8] = o[j][nt][k + 2] * f;
         }
         if (g == 0) {
           if (!all) ml[(begins * NW + wid) * C::HEADS + h] = make_float2(m[nt][k], l[nt][k]);
