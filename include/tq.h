@@ -15,6 +15,10 @@
  *  - alternate layout: keys per-block affine 8-bit without rotation, values
  *    Walsh-Hadamard + 3-bit Lloyd-Max with an fp16 norm (vllm-metal
  *    TurboQuant guide, "quantisation principle" table);
+ *  - dense pages (16-bit or e4m3 elements) beside the compressed caches: a page
+ *    plan of a serving step, the store of new tokens, and attention of one
+ *    new token per sequence (tq_plan_pages, tq_paged_store, tq_paged_attention;
+ *    these have no counterpart in the source pages);
  *  - decode attention: softmax(q k^T / sqrt(d)) v over the compressed tokens
  *    plus an exact fp16 buffer of the newest <= 128 tokens (turboquant-bench,
  *    "buffer strategy"; turboquant vLLM guide, section 5.1 ring buffer and
@@ -427,7 +431,7 @@ tq_status tq_paged_workspace_size(const tq_ctx* ctx, int batch, size_t* bytes);
  *   lse      device float32 [batch][Hq] or NULL: ln sum_p exp(scale * q . k_p)
  *   workspace  device scratch of at least tq_paged_workspace_size(batch) bytes, 256-byte aligned;
  *            calls that can overlap on the GPU need one each
- * An empty sequence gets a row of zeros and lse -inf.  A length that is negative or beyond the block
+ * An empty sequence, or one whose scores are all -inf, gets a row of zeros and lse -inf.  A length that is negative or beyond the block
  * table counts as 0 with TQ_DEVERR_POSITION; a page whose id is outside [0, num_blocks) is left out of
  * the sums with TQ_DEVERR_BLOCK_ID.  num_blocks * Hkv must be below 2^31.  The current device
  * must be the context's (TQ_ERR_INVALID_ARG), here and in the two calls above. */
