@@ -433,7 +433,9 @@ tq_status tq_paged_workspace_size(const tq_ctx* ctx, int batch, size_t* bytes);
  *            calls that can overlap on the GPU need one each
  * An empty sequence, or one whose scores are all -inf, gets a row of zeros and lse -inf.  A length that is negative or beyond the block
  * table counts as 0 with TQ_DEVERR_POSITION; a page whose id is outside [0, num_blocks) is left out of
- * the sums with TQ_DEVERR_BLOCK_ID.  num_blocks * Hkv must be below 2^31.  The current device
+ * the sums with TQ_DEVERR_BLOCK_ID.  A warp that gives up waiting for its copies (about a second) sets
+ * TQ_DEVERR_TIMEOUT, and the rows it has a part in become NaN.  A NaN or an infinity in a row that counts makes
+ * what depends on it NaN (weights are multiplied in parts).  num_blocks * Hkv must be below 2^31.  The current device
  * must be the context's (TQ_ERR_INVALID_ARG), here and in the two calls above. */
 tq_status tq_paged_attention(tq_ctx* ctx, const void* q, int64_t q_stride, int batch, const void* pool, int num_blocks,
                              const int32_t* block_table, int max_blocks, const int32_t* lengths, int window,

@@ -449,6 +449,8 @@ class Context:
             raise ValueError("queue_state and queue_state_out must be [2] and token_start [batch + 1]")
         if (positions is not None and positions.numel() != n) or (rows is not None and rows.numel() != n):
             raise ValueError("positions and rows must be [max_tokens], like slots")
+        if not 0 <= num_blocks < 2 ** 31:
+            raise ValueError("num_blocks must be a count below 2^31")
         (a_ctx, a_new, a_table, a_queue, a_state, a_len, a_paged, a_ring, a_start, a_pos, a_rows, a_out) = self._addrs(
             i32, "ctx_len new_len block_table queue queue_state lengths n_paged n_ring token_start positions rows queue_state_out",
             ctx_len, new_len, block_table, queue, queue_state, lengths, n_paged, n_ring, token_start, positions, rows, queue_state_out)
@@ -489,6 +491,8 @@ class Context:
         i32, _, f32, u8 = self._types
         if out.shape != q.shape or lengths.numel() != bsz or (lse is not None and lse.shape != q.shape[:2]):
             raise ValueError("out must be [batch, Hq, d], lengths [batch] and lse [batch, Hq]")
+        if not 0 <= window < 2 ** 31:
+            raise ValueError("window must be 0 or a count below 2^31")
         self._check_pool(pool)
         self._check_bt(block_table, bsz)
         a_pool, a_ws = self._addrs(u8, "pool workspace", pool, workspace)

@@ -263,6 +263,22 @@ def test_attention_bad_device_values_are_flagged():
     check(e, *attend(e), flags=paged.ERR_BLOCK_ID | paged.ERR_POSITION)
 
 
+def test_attention_of_a_pool_without_blocks():
+    ctx = dense(64, 4, 2)
+    pool = torch.empty(0, 2, ctx.page_bytes, dtype=torch.uint8, device="cuda")
+    e = dict(ctx=ctx, q=torch.randn(2, 4, 64).half(), pool=pool, bt=np.zeros((2, 2), np.int32), lengths=np.array([0, 20], np.int32),
+             d=64, bits=16, bf16=False)
+    check(e, *attend(e), flags=paged.ERR_BLOCK_ID)
+
+
+def test_attention_refuses_counts_beyond_31_bits():
+    e = make_case(42, [5], 4, 2, 64, 16, False)
+    for window in (-1, 2 ** 31, 2 ** 32 + 5):
+        with pytest.raises(ValueError):
+            attend(e, window=window)
+    check(e, *attend(e, window=2 ** 31 - 1), window=2 ** 31 - 1)
+
+
 def test_attention_shared_pages_and_repeated_calls():
     """Two sequences that name the same pages; the same call ten times gives the same bits."""
     e = make_case(43, [400, 400, 333], 8, 2, 128, 16, True)

@@ -165,6 +165,6 @@ def test_binding_checks_shapes_before_the_library():
     with pytest.raises(ValueError, match="must be a CUDA tensor"):
         ctx.plan_pages(**ok)
     for name, bad in (("new_len", i32(2)), ("token_start", i32(3)), ("queue_state", i32(1)), ("block_table", i32(2, 2)),
-                      ("positions", i32(4)), ("n_ring", i32(4))):
+                      ("positions", i32(4)), ("n_ring", i32(4)), ("num_blocks", 2 ** 32 + 4), ("num_blocks", -1)):
         with pytest.raises(ValueError):
             ctx.plan_pages(**{**ok, name: bad})
