@@ -28,7 +28,7 @@
 // Precision: q and k products are exact and summed in fp32.  Weights are split into 16-bit parts (two fp16
 // parts, 22 bits; three bf16 parts, 24 bits) whose products with V are exact; each page's sum leaves the tensor
 // core and is added to the running sum by an fp32 addition that rounds to nearest (the tensor core cuts, which
-// over thousands of pages would pull the sum towards zero).  The running maximum m is a reference that is only
+// over thousands of pages would pull the sum towards zero); the weights' total is a compensated sum.  The running maximum m is a reference that is only
 // raised when a score passes it by more than 8, so that most pages rescale nothing.  Weights are
 // 2^(s - m + 7) <= 2^15: an fp16 low part then keeps 2^-32 of the largest weight.
 //   e4m3 pages: codes are exact in fp16.  Key exponents scale the fp32 scores.  Value exponents scale the weights
@@ -104,6 +104,10 @@ struct PagedCfg {
   // With one stage keys and values are copied apart, so that the next keys come while the values are used; with more
   // a page is one copy and one wait (fewer instructions: e4m3 at d = 64 54 against 64 us, at d = 512 65 against 69).
   static constexpr bool APART = S == 1;
+  // The weights' total grows by every page: its rounding is the largest error of a long sequence (16 ragged sequences up
+  // to 128K tokens: 1.2e-6 of the result, 4.2e-7 with what is lost kept; the same time).  8-bit pages with 16
+  // heads or d = 512 have no registers left for it (76 against 81 us at d = 64, 65 against 68 at 512).
+  static constexpr bool KEEP_LOST = KIND != kE4M3 || (NT == 1 && D < 512);
   static constexpr int BOX_ROWS = APART ? kPage : 2 * kPage;
   static constexpr int BOX = BOX_ROWS * SWIZZLE_ROW;
 };
@@ -565,7 +569,7 @@ __global__ void __launch_bounds__(PagedCfg<KIND, D, NT>::THREADS, 1)
   uint32_t qf[C::QREG ? NT : 1][C::QREG ? KS : 1][2];
   uint2* q_sm = reinterpret_cast<uint2*>(sm + C::OFF_Q + wid * C::QBYTES);
   // m: reference of each of the lane's heads; ref: what is subtracted from its scores, m - 7
-  float o[KS][NT][4], m[NT][2], ref[NT][2], l[NT][2], qs[NT][2];
+  float o[KS][NT][4], m[NT][2], ref[NT][2], l[NT][2], lost[NT][2], qs[NT][2];
   const float log2e_scale = a.scale * 1.44269504088896340736f;
   int st = 0;
 
@@ -627,7 +631,7 @@ __global__ void __launch_bounds__(PagedCfg<KIND, D, NT>::THREADS, 1)
         qs[nt][i] = F8 ? __shfl_sync(kFull, down, (2 * t + i) * 4) : log2e_scale;
         m[nt][i] = -CUDART_INF_F;
         ref[nt][i] = 0.f;
-        l[nt][i] = 0.f;
+        l[nt][i] = lost[nt][i] = 0.f;
       }
     }
     // pages of the segment that the sequence's end or the window cuts
@@ -752,6 +756,7 @@ __global__ void __launch_bounds__(PagedCfg<KIND, D, NT>::THREADS, 1)
               m[nt][k] = mx;
               ref[nt][k] = mx == -CUDART_INF_F ? 0.f : mx - kWeightUp;
               l[nt][k] *= c;
+              if (C::KEEP_LOST) lost[nt][k] *= c;
 #pragma unroll
               for (int j = 0; j < KS; ++j) {
                 o[j][nt][k] *= c;
@@ -773,8 +778,16 @@ __global__ void __launch_bounds__(PagedCfg<KIND, D, NT>::THREADS, 1)
           float p[4];
 #pragma unroll
           for (int k = 0; k < 4; ++k) p[k] = ex2(s[nt][k] - ref[nt][k & 1]);
-          l[nt][0] += p[0] + p[2];
-          l[nt][1] += p[1] + p[3];
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            if constexpr (C::KEEP_LOST) {  // what an addition loses is kept for the next one (Kahan's sum)
+              const float y = p[k] + p[k + 2] - lost[nt][k], sum = l[nt][k] + y;
+              lost[nt][k] = sum - l[nt][k] - y;
+              l[nt][k] = sum;
+            } else {
+              l[nt][k] += p[k] + p[k + 2];
+            }
+          }
           if (F8) {
             p[0] *= w0;
             p[1] *= w0;
