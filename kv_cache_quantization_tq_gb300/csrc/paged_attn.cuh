@@ -25,16 +25,26 @@
 // With tokens and dims on the 16-row side, 8 query heads per KV head fill the 8-column side and no row of the
 // products is padding; the accumulators are d / 4 registers.
 //
-// Precision: q and k products are exact and summed in fp32.  Weights are split into 16-bit parts (two fp16
-// parts, 22 bits; three bf16 parts, 24 bits) whose products with V are exact; each page's sum leaves the tensor
-// core and is added to the running sum by an fp32 addition that rounds to nearest (the tensor core cuts, which
-// over thousands of pages would pull the sum towards zero); the weights' total is a compensated sum.  The running maximum m is a reference that is only
-// raised when a score passes it by more than 8, so that most pages rescale nothing.  Weights are
-// 2^(s - m + 7) <= 2^15: an fp16 low part then keeps 2^-32 of the largest weight.
-//   e4m3 pages: codes are exact in fp16.  Key exponents scale the fp32 scores.  Value exponents scale the weights
-// relative to the page's largest one, which scales the page's sum when it is added: nothing overflows fp16.
-// bf16 queries are first scaled by a power of two per head into fp16's range (exact down to 2^-31 of the head's
-// largest entry).
+// Precision: q and k products are exact and summed in fp32.  A weight is split into parts whose products with V are
+// exact.  Each page's sum leaves the tensor core and is added to the running sum by an fp32 addition that rounds to
+// nearest (the tensor core cuts, which over thousands of pages would pull the sum towards zero); the weights' total is a
+// compensated sum.  The running maximum m is a whole number that is only raised when a score passes it by more
+// than 8, so that most pages rescale nothing, and then by a power of two.  Weights of the total are 2^(s - m) <= 2^8, those
+// of the values 2^-8 times that, at most 1: a sum of values overflows where the number of tokens times the largest
+// value does.
+//   16-bit pages: three bf16 parts (24 bits) beside bf16 values, two tf32 parts (22 bits) beside fp16 values, which are
+// exact in tf32.  Both have the exponents of fp32: a part of a small weight is as good as one of a large one, so
+// it does not matter what a token's values are worth beside its neighbours'.  (Two fp16 parts end at 2^-25, and a token
+// of small weight and large values then loses its bits.)  Two fp16 parts take the same time: 16 ragged sequences
+// 624 us, tf32 parts 622.
+//   e4m3 pages: codes are exact in fp16, and tf32 parts would cost their widening (64 ragged sequences 186 against
+// 173 us), so the weights have two fp16 parts.  Key exponents scale the fp32 scores, value exponents the weights.  As the
+// exponent is the size of a token's values, weight and exponent together say what the token is worth in the result: a
+// second reference per head, a power of two, holds the largest of these below 2^15 and, when it is set, at 2^12.  What
+// the parts leave out is 2^-37 of the largest token's share.
+//   bf16 queries on e4m3 pages are scaled by a power of two per head into fp16's range (exact down to 2^-31 of the
+// head's largest entry); half of its inverse comes before a key's exponent and half behind it, so that large
+// keys with small queries do not overflow on the way.
 #pragma once
 
 #include <cuda.h>
@@ -49,8 +59,12 @@ namespace {
 
 enum { kF16 = 0, kBF16 = 1, kE4M3 = 2 };
 
-constexpr float kWeightUp = 7.f;  // weights are 2^(s - m + 7)
-constexpr float kLazy = 8.f;      // the reference is raised when a score passes it by more than this
+constexpr float kLazy = 8.f;                     // the reference is raised when a score passes it by more than this
+constexpr float kDown = 1.f / 256, kUp = 256.f;  // values are summed with weights of at most 1: 2^-kLazy, and back
+constexpr float kNone = -3.402823466e38f;        // m before the first score
+// e4m3 pages: the values' reference is set so that the largest product is in [2^12, 2^13), and lowered when one
+// passes 2^15; it begins at 2^100 and stays within 2^-113 and 2^100
+constexpr int kValueAt = 12, kValueMost = 15, kValueTop = 100, kValueLeast = -113;
 
 template <int KIND, int D, int NT>
 struct PagedCfg {
@@ -76,7 +90,8 @@ struct PagedCfg {
   // is not better: with every queue full the multiprocessors farther from memory fall behind and the last of
   // them ends late.  16-bit pages of d = 128, 8 x 32K and 16 ragged sequences: 12 warps x 1 stage 87.1 and 622 us,
   // 8 x 2 89.0 and 645, 16 x 1 88.3 and 625.  e4m3 pages of d = 128, 64 ragged sequences: 16 x 1 169 us, 16 x 2 181.
-  static constexpr int NW = PAGE <= 4096 && QREG && fits(16, 1) ? 16 : fits(12, 1) ? 12 : fits(8, 1) ? 8 : fits(6, 1) ? 6 : 4;
+  // (e4m3 at d = 64 with 16 query heads has no registers for 16 warps: 16 92.1 us, 12 87.2.)
+  static constexpr int NW = PAGE <= 4096 && QREG && (NT == 1 || KIND != kE4M3) && fits(16, 1) ? 16 : fits(12, 1) ? 12 : fits(8, 1) ? 8 : fits(6, 1) ? 6 : 4;
   static constexpr int S_WANT = (KIND == kE4M3 ? 96 : 128) * 1024 / (NW * PAGE);
   static constexpr int S_LEAST = S_WANT > MIN_S ? S_WANT : MIN_S;
   static constexpr int S = S_LEAST < stages(NW) ? S_LEAST : stages(NW);
@@ -93,8 +108,7 @@ struct PagedCfg {
   static constexpr int OFF_PRE = OFF_BAR + NW * S * 16;
   static constexpr int OFF_WARP = OFF_PRE + THREADS * 4;
   static constexpr int OFF_LEN = OFF_WARP + NW * 4;
-  // with 16 warps (128 registers a thread) the way of the fetches is kept here between batches (e4m3 at d = 64, 16
-  // query heads: 76.3 against 81.5 us; the others the same)
+  // with 16 warps (128 registers a thread) the way of the fetches is kept here between batches
   static constexpr bool PARK = NW == 16;
   static constexpr int OFF_WALK = (OFF_LEN + (LENS ? THREADS * 4 : 0) + 15) / 16 * 16;
   static constexpr int SMEM = OFF_WALK + (PARK ? NW * 48 : 0) + 1024;
@@ -249,6 +263,23 @@ __device__ __forceinline__ void mma_first(float (&d)[4], const uint32_t (&a)[4],
                  : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
                  : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
 }
+// d += A B, A 16 dims x 8 tokens and B 8 tokens x 8 heads of tf32.
+__device__ __forceinline__ void mma_tf32(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile("mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+               : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+               : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void mma_tf32_first(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile("mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+               : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+               : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
+}
+// Two fp16 as the fp32 they are, which tf32 (10 fraction bits, 8 exponent bits) holds.
+__device__ __forceinline__ void widen(uint32_t two, uint32_t& lo, uint32_t& hi) {
+  const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&two));
+  lo = __float_as_uint(f.x);
+  hi = __float_as_uint(f.y);
+}
 // 2^x; -inf gives +0.
 __device__ __forceinline__ float ex2(float x) {
   float y;
@@ -269,6 +300,9 @@ __device__ __forceinline__ uint32_t f16_of_e4m3_high(uint32_t four) {
 // 2^e for e in [-126, 127]; 0 for -127.
 __device__ __forceinline__ float power2(int e) { return __int_as_float((e + 127) << 23); }
 
+// The exponent of a positive normal number, as of 2^e (of an infinity 128).
+__device__ __forceinline__ int exponent_in(float x) { return (__float_as_int(x) >> 23) - 127; }
+
 // 16-bit parts of a pair of fp32 weights: each part rounds what the ones before leave.
 template <bool BF>
 __device__ __forceinline__ uint32_t take_part(float& x, float& y) {
@@ -284,6 +318,19 @@ __device__ __forceinline__ uint32_t take_part(float& x, float& y) {
   x -= f.x;
   y -= f.y;
   return *reinterpret_cast<const uint32_t*>(&h);
+}
+// Weights of 8 tokens (row g) and heads 2 t, 2 t + 1 handed over as those of head g and tokens 2 t, 2 t + 1: the fp32
+// words by their 16-bit halves.
+__device__ __forceinline__ void turn(float& x, float& y) {
+  const uint32_t a = __float_as_uint(x), b = __float_as_uint(y);
+  const uint32_t h = movmat(__byte_perm(a, b, 0x7632)), l = movmat(__byte_perm(a, b, 0x5410));
+  x = __uint_as_float(__byte_perm(l, h, 0x5410));
+  y = __uint_as_float(__byte_perm(l, h, 0x7632));
+}
+// tf32 parts of an fp32 weight: the first 11 bits cut off (a NaN stays one), and what is left rounded to 11.
+__device__ __forceinline__ void tf32_parts(float x, uint32_t& high, uint32_t& low) {
+  high = __float_as_uint(x) & 0xffffe000u;
+  low = (__float_as_uint(x - __uint_as_float(high)) + 0x1000u) & 0xffffe000u;
 }
 
 // ---------------------------------------------------------------- scan and walk over the line
@@ -365,10 +412,12 @@ struct __align__(16) Walk {
   }
 };
 
-// ln of the weights' sum L, which is relative to 2^(M - 7)
+// ln of the weights' sum L, which is relative to 2^M
 __device__ __forceinline__ float lse_of(float M, float L) {
-  return L == 0.f ? -CUDART_INF_F : (M - kWeightUp + log2f(L)) * 0.69314718055994530942f;
+  return L == 0.f ? -CUDART_INF_F : (M + log2f(L)) * 0.69314718055994530942f;
 }
+// What turns the values' sum into the result.
+__device__ __forceinline__ float inverse_of(float L) { return L == 0.f ? 0.f : kUp / L; }
 
 // ---------------------------------------------------------------- the kernel
 template <int KIND, int D, int NT>
@@ -568,8 +617,10 @@ __global__ void __launch_bounds__(PagedCfg<KIND, D, NT>::THREADS, 1)
 
   uint32_t qf[C::QREG ? NT : 1][C::QREG ? KS : 1][2];
   uint2* q_sm = reinterpret_cast<uint2*>(sm + C::OFF_Q + wid * C::QBYTES);
-  // m: reference of each of the lane's heads; ref: what is subtracted from its scores, m - 7
-  float o[KS][NT][4], m[NT][2], ref[NT][2], l[NT][2], lost[NT][2], qs[NT][2];
+  // m: reference of each of the lane's heads; qs: the score's factor.  8-bit pages: qh the part of that factor that
+  // comes before the key's exponent, vr the values' reference (o is the sum times it), most what a score's place under
+  // m and a value's exponent may come to together before vr is lowered
+  float o[KS][NT][4], m[NT][2], l[NT][2], lost[NT][2], qs[NT][2], qh[NT][2], vr[NT][2], most[NT][2];
   const float log2e_scale = a.scale * 1.44269504088896340736f;
   int st = 0;
 
@@ -587,7 +638,7 @@ __global__ void __launch_bounds__(PagedCfg<KIND, D, NT>::THREADS, 1)
       // heads that are none read the first one's row and become zero: loads without a branch go out together
       const uint16_t* qr = a.q + out.b * a.q_stride + (head0 + (h < nh ? h : 0)) * D;
       const uint32_t keep = h < nh ? 0xffffffffu : 0u;
-      float up = 1.f;
+      int e_up = 0;
       if (F8 && w.q_bf16) {
         uint32_t top = 0;
 #pragma unroll 8
@@ -599,8 +650,9 @@ __global__ void __launch_bounds__(PagedCfg<KIND, D, NT>::THREADS, 1)
         top = max(top, __shfl_xor_sync(kFull, top, 2));
         // largest entry in [2^14, 2^15); the factor is undone in the score's
         const int e = (int)(top >> 7) - 127;
-        up = power2(max(-126, min(14 - e, 126)));
+        e_up = max(-126, min(14 - e, 126));
       }
+      const float up = power2(e_up);
       // rolled where it can be: code that runs once costs its fetch, not its execution
 #pragma unroll(C::QREG ? KS : 8)
       for (int ks = 0; ks < KS; ++ks) {
@@ -625,12 +677,18 @@ __global__ void __launch_bounds__(PagedCfg<KIND, D, NT>::THREADS, 1)
           q_sm[(nt * KS + ks) * 32 + lane] = x;
         }
       }
-      const float down = log2e_scale / up;  // up is a power of two
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        qs[nt][i] = F8 ? __shfl_sync(kFull, down, (2 * t + i) * 4) : log2e_scale;
-        m[nt][i] = -CUDART_INF_F;
-        ref[nt][i] = 0.f;
+        if (F8) {
+          const int e = __shfl_sync(kFull, e_up, (2 * t + i) * 4);
+          qh[nt][i] = power2(-(e >> 1));
+          qs[nt][i] = log2e_scale * power2((e >> 1) - e);
+        } else {
+          qs[nt][i] = log2e_scale;
+        }
+        m[nt][i] = kNone;
+        vr[nt][i] = power2(kValueTop);
+        most[nt][i] = kValueMost + kLazy - kValueTop;
         l[nt][i] = lost[nt][i] = 0.f;
       }
     }
@@ -718,12 +776,9 @@ __global__ void __launch_bounds__(PagedCfg<KIND, D, NT>::THREADS, 1)
         if (F8) {
           const float f0 = power2(ek0), f1 = power2(ek1);
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt) {
-            s[nt][0] *= f0;
-            s[nt][1] *= f0;
-            s[nt][2] *= f1;
-            s[nt][3] *= f1;
-          }
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int k = 0; k < 4; ++k) s[nt][k] = s[nt][k] * qh[nt][k & 1] * (k < 2 ? f0 : f1);
         }
         bool raise = false;
 #pragma unroll
@@ -739,11 +794,17 @@ __global__ void __launch_bounds__(PagedCfg<KIND, D, NT>::THREADS, 1)
           ev0 = ok0 ? ev0 : -127;
           ev1 = ok1 ? ev1 : -127;
         }
+        const float fe0 = (float)ev0, fe1 = (float)ev1;
+        float p[NT][4];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-          for (int k = 0; k < 4; ++k) raise |= s[nt][k] > m[nt][k & 1] + kLazy;
-        if (__any_sync(kFull, raise)) {
+          for (int k = 0; k < 4; ++k) {
+            p[nt][k] = s[nt][k] - m[nt][k & 1];
+            raise |= p[nt][k] > kLazy;
+            if (F8) raise |= p[nt][k] + (k < 2 ? fe0 : fe1) > most[nt][k & 1];
+          }
+        if (__any_sync(kFull, raise)) {  // all heads' references are set anew: fewer pages come here
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -751,53 +812,69 @@ __global__ void __launch_bounds__(PagedCfg<KIND, D, NT>::THREADS, 1)
               float mx = fmaxf(s[nt][k], s[nt][k + 2]);
 #pragma unroll
               for (int x = 4; x < 32; x <<= 1) mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, x));
-              mx = fmaxf(m[nt][k], mx);
-              const float c = mx == -CUDART_INF_F ? 1.f : ex2(m[nt][k] - mx);
+              mx = fmaxf(m[nt][k], ceilf(mx));
+              const float up = mx - m[nt][k], c = ex2(-up);
               m[nt][k] = mx;
-              ref[nt][k] = mx == -CUDART_INF_F ? 0.f : mx - kWeightUp;
               l[nt][k] *= c;
               if (C::KEEP_LOST) lost[nt][k] *= c;
+              p[nt][k] = s[nt][k] - mx;
+              p[nt][k + 2] = s[nt][k + 2] - mx;
+              float co = c;
+              if (F8) {  // the values' reference follows, and their sum takes what it does not
+                float top = fmaxf(fmaxf(p[nt][k] + fe0, p[nt][k + 2] + fe1), -1000.f);
+#pragma unroll
+                for (int x = 4; x < 32; x <<= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, x));
+                const int e = kValueMost + (int)kLazy - (int)most[nt][k], by = (int)fminf(up, 1000.f);
+                const int e1 = max(min(min(e + by, kValueTop), kValueAt + (int)kLazy - (int)floorf(top)), kValueLeast);
+                most[nt][k] = (float)(kValueMost + (int)kLazy - e1);
+                vr[nt][k] = power2(e1);
+                co = power2(max(e1 - e - by, -127));
+              }
 #pragma unroll
               for (int j = 0; j < KS; ++j) {
-                o[j][nt][k] *= c;
-                o[j][nt][k + 2] *= c;
+                o[j][nt][k] *= co;
+                o[j][nt][k + 2] *= co;
               }
             }
         }
-        float page_up = 1.f, w0 = 1.f, w1 = 1.f;
-        if (F8) {  // value exponents relative to the largest of the page
-          const int top = __reduce_max_sync(kFull, max(ev0, ev1));
-          page_up = power2(top);
-          w0 = power2(max(ev0 - top, -127));
-          w1 = power2(max(ev1 - top, -127));
-        }
-        constexpr int PARTS = BF ? 3 : 2;
-        uint32_t pf[NT][PARTS][2];
+        // what a token's weight at its values has besides: 2^-8, and on 8-bit pages their exponent
+        const float w0 = F8 ? power2(ev0) * kDown : kDown, w1 = F8 ? power2(ev1) * kDown : kDown;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
-          float p[4];
 #pragma unroll
-          for (int k = 0; k < 4; ++k) p[k] = ex2(s[nt][k] - ref[nt][k & 1]);
+          for (int k = 0; k < 4; ++k) p[nt][k] = ex2(p[nt][k]);
 #pragma unroll
           for (int k = 0; k < 2; ++k) {
             if constexpr (C::KEEP_LOST) {  // what an addition loses is kept for the next one (Kahan's sum)
-              const float y = p[k] + p[k + 2] - lost[nt][k], sum = l[nt][k] + y;
+              const float y = p[nt][k] + p[nt][k + 2] - lost[nt][k], sum = l[nt][k] + y;
               lost[nt][k] = sum - l[nt][k] - y;
               l[nt][k] = sum;
             } else {
-              l[nt][k] += p[k] + p[k + 2];
+              l[nt][k] += p[nt][k] + p[nt][k + 2];
             }
           }
-          if (F8) {
-            p[0] *= w0;
-            p[1] *= w0;
-            p[2] *= w1;
-            p[3] *= w1;
-          }
 #pragma unroll
-          for (int k = 0; k < PARTS; ++k) {
-            pf[nt][k][0] = movmat(take_part<BF>(p[0], p[1]));
-            pf[nt][k][1] = movmat(take_part<BF>(p[2], p[3]));
+          for (int k = 0; k < 4; ++k) {
+            p[nt][k] *= k < 2 ? w0 : w1;
+            if (F8) p[nt][k] *= vr[nt][k & 1];
+          }
+        }
+        constexpr int PARTS = BF ? 3 : 2;
+        // 16-bit parts of tokens 0 .. 7 and 8 .. 15, or tf32 parts of tokens 2 t, 2 t + 1, 2 t + 8, 2 t + 9
+        uint32_t pf[KIND == kF16 ? 1 : NT][PARTS][2], wh[KIND == kF16 ? NT : 1][4], wl[KIND == kF16 ? NT : 1][4];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          if constexpr (KIND == kF16) {
+            turn(p[nt][0], p[nt][1]);
+            turn(p[nt][2], p[nt][3]);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) tf32_parts(p[nt][k], wh[nt][k], wl[nt][k]);
+          } else {
+#pragma unroll
+            for (int k = 0; k < PARTS; ++k) {
+              pf[nt][k][0] = movmat(take_part<BF>(p[nt][0], p[nt][1]));
+              pf[nt][k][1] = movmat(take_part<BF>(p[nt][2], p[nt][3]));
+            }
           }
         }
         if (C::APART) {
@@ -818,14 +895,27 @@ __global__ void __launch_bounds__(PagedCfg<KIND, D, NT>::THREADS, 1)
           __syncwarp();
         }
         auto add = [&](int j, const uint32_t(&af)[4]) {
+          // af: dims g, g + 8 of tokens 2 t, 2 t + 1 (first two), 2 t + 8, 2 t + 9; a product of 8 tokens takes a
+          // pair's first token as number t and its second as number t + 4
+          uint32_t va[2][4];
+          if constexpr (KIND == kF16)
+#pragma unroll
+            for (int k = 0; k < 4; ++k) widen(af[k], va[k >> 1][k & 1], va[k >> 1][(k & 1) + 2]);
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt) {
             float acc[4];
-            mma_first<BF>(acc, af, pf[nt][PARTS - 1][0], pf[nt][PARTS - 1][1]);
+            if constexpr (KIND != kF16) {
+              mma_first<BF>(acc, af, pf[nt][PARTS - 1][0], pf[nt][PARTS - 1][1]);
 #pragma unroll
-            for (int k = PARTS - 2; k >= 0; --k) mma<BF>(acc, af, pf[nt][k][0], pf[nt][k][1]);
+              for (int k = PARTS - 2; k >= 0; --k) mma<BF>(acc, af, pf[nt][k][0], pf[nt][k][1]);
+            } else {
+              mma_tf32_first(acc, va[0], wl[nt][0], wl[nt][1]);
+              mma_tf32(acc, va[1], wl[nt][2], wl[nt][3]);
+              mma_tf32(acc, va[0], wh[nt][0], wh[nt][1]);
+              mma_tf32(acc, va[1], wh[nt][2], wh[nt][3]);
+            }
 #pragma unroll
-            for (int k = 0; k < 4; ++k) o[j][nt][k] = F8 ? fmaf(acc[k], page_up, o[j][nt][k]) : o[j][nt][k] + acc[k];
+            for (int k = 0; k < 4; ++k) o[j][nt][k] += acc[k];
           }
         };
         if (!dead) {
@@ -881,7 +971,7 @@ __global__ void __launch_bounds__(PagedCfg<KIND, D, NT>::THREADS, 1)
         const int h = nt * 8 + 2 * t + k;
         if (h >= nh) continue;
         float* p = dst + h * pitch + g;  // accumulator rows g and g + 8 of tile j
-        const float f = all ? (l[nt][k] == 0.f ? 0.f : 1.f / l[nt][k]) : 1.f;
+        const float f = (all ? inverse_of(l[nt][k]) : 1.f) * (F8 ? power2(-exponent_in(vr[nt][k])) : 1.f);
 #pragma unroll
         for (int j = 0; j < KS; ++j) {
           p[16 * j] = o[j][nt][k] * f;
@@ -975,7 +1065,7 @@ __global__ void __launch_bounds__(PagedCfg<KIND, D, NT>::THREADS, 1)
     const int64_t row = (int64_t)seq * a.hq + (int64_t)kvh * a.n_rep + h0 + h;
     float* part = w.parts + ((int64_t)blockIdx.x * 2 + kind) * (C::HEADS * (D + 2));
     float* dst = all ? a.out + row * D : part + h * D;
-    const float f = all ? (L == 0.f ? 0.f : 1.f / L) : 1.f;
+    const float f = all ? inverse_of(L) : 1.f;
 #pragma unroll
     for (int i = 0; i < V; i += VL) {
       float* q = dst + (i / VL * 32 + lane) * VL;
@@ -1089,7 +1179,7 @@ __global__ void __launch_bounds__((JOIN == 1 ? kMergeWarps : JOIN) * 32) paged_m
         c[k] = ex2(sm_max[k] - sub);
         L = fmaf(c[k], sl[k], L);
       }
-      const float f = L == 0.f ? 0.f : 1.f / L;
+      const float f = inverse_of(L);
       for (int i = threadIdx.x; i < D; i += JOIN * 32) {
         float v = 0.f;
 #pragma unroll
@@ -1099,7 +1189,7 @@ __global__ void __launch_bounds__((JOIN == 1 ? kMergeWarps : JOIN) * 32) paged_m
       if (threadIdx.x == 0 && a.lse) a.lse[row0 + h] = lse_of(M, L);
       if (h + (int)gridDim.y < nh) __syncthreads();
     } else {
-      const float f = L == 0.f ? 0.f : 1.f / L;
+      const float f = inverse_of(L);
 #pragma unroll
       for (int i = 0; i < V; ++i) a.out[(row0 + h) * D + (i / VL * 32 + lane) * VL + i % VL] = x[i] * f;
       if (lane == 0 && a.lse) a.lse[row0 + h] = lse_of(M, L);
