@@ -433,7 +433,7 @@ tq_status tq_paged_workspace_size(const tq_ctx* ctx, int batch, size_t* bytes);
  *            calls that can overlap on the GPU need one each
  * An empty sequence, or one whose scores are all -inf, gets a row of zeros and lse -inf.  A length that is negative or beyond the block
  * table counts as 0 with TQ_DEVERR_POSITION; a page whose id is outside [0, num_blocks) is left out of
- * the sums with TQ_DEVERR_BLOCK_ID.  A warp that gives up waiting for its copies (about a second) sets
+ * the sums with TQ_DEVERR_BLOCK_ID.  A warp that gives up waiting for its copies (tq_set_wait_limit) sets
  * TQ_DEVERR_TIMEOUT, and the rows it has a part in become NaN.  A NaN or an infinity in a row that counts makes
  * what depends on it NaN (weights are multiplied in parts).  Sums are held in 32 bits: they overflow where the
  * number of positions times the largest |value| passes 2^127, and weights or values below about 2^-100 (of a row's largest
@@ -444,6 +444,11 @@ tq_status tq_paged_attention(tq_ctx* ctx, const void* q, int64_t q_stride, int b
                              const int32_t* block_table, int max_blocks, const int32_t* lengths, int window,
                              float scale, float* out, float* lse, void* workspace, size_t ws_bytes,
                              cudaStream_t stream);
+
+/* How long later tq_paged_attention calls (and graphs captured later) wait for a copy of their own before they give
+ * up with TQ_DEVERR_TIMEOUT; 10^9 nanoseconds unless set.  Meant for tests of that path: with 0 a warp's first
+ * copy is waited for as usual and the next one counts as late.  Host only. */
+tq_status tq_set_wait_limit(tq_ctx* ctx, uint32_t nanoseconds);
 
 /* ------------------------------------------------------------------ bit packing */
 

@@ -93,6 +93,7 @@ _SIGS = {
     "tq_paged_store": (_i, [_vp, _vp, _vp, _i64, _i64, _vp, _i, _vp, _i, _vp]),
     "tq_paged_workspace_size": (_i, [_vp, _i, C.POINTER(_sz)]),
     "tq_paged_attention": (_i, [_vp, _vp, _i64, _i, _vp, _i, _vp, _i, _vp, _i, C.c_float, _vp, _vp, _vp, _sz, _vp]),
+    "tq_set_wait_limit": (_i, [_vp, C.c_uint32]),
     "tq_should_materialize": (_i, [_i64, _i64, _i, _i, _i64]),
     "tq_pack": (_i, [_vp, _i64, _i, _vp, _vp]),
     "tq_unpack": (_i, [_vp, _i64, _i, _vp, _vp]),
@@ -277,6 +278,12 @@ class Context:
     def set_decode_path(self, path: int):
         """TQ_DECODE_AUTO, TQ_DECODE_MMA_SYNC or TQ_DECODE_TCGEN05 (main layout, head_dim 128)."""
         _check(lib.tq_set_decode_path(self.ptr, path), "tq_set_decode_path")
+
+    def set_wait_limit(self, nanoseconds: int):
+        """How long paged_attention waits for a copy before it gives up with TQ_DEVERR_TIMEOUT (10^9 unless set)."""
+        if not 0 <= nanoseconds < 2 ** 32:
+            raise ValueError("nanoseconds must be below 2^32")
+        _check(lib.tq_set_wait_limit(self.ptr, nanoseconds), "tq_set_wait_limit")
 
     def get_tables(self):
         k = 1 << (self.cfg.key_bits - 1 if self.layout == TQ_LAYOUT_MAIN else self.cfg.value_bits)

@@ -130,6 +130,12 @@ tq_status tq_paged_workspace_size(const tq_ctx* ctx, int batch, size_t* bytes) {
   return TQ_OK;
 }
 
+tq_status tq_set_wait_limit(tq_ctx* ctx, uint32_t nanoseconds) {
+  if (!ctx) return TQ_ERR_INVALID_ARG;
+  ctx->wait_limit = nanoseconds;
+  return TQ_OK;
+}
+
 tq_status tq_paged_attention(tq_ctx* ctx, const void* q, int64_t q_stride, int batch, const void* pool, int num_blocks,
                              const int32_t* block_table, int max_blocks, const int32_t* lengths, int window,
                              float scale, float* out, float* lse, void* workspace, size_t ws_bytes,

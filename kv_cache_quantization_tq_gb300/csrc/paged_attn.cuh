@@ -134,6 +134,7 @@ struct PagedPlan {
   int min_log2;    // a team gets at least about 2^min_log2 of the line
   int tau;         // cuts this near a segment's end move there
   int groups;      // query-head groups per KV head
+  uint32_t wait_limit;  // nanoseconds that a warp waits for a copy
 };
 
 struct PagedWork {
@@ -187,8 +188,10 @@ __device__ __forceinline__ void bar_init(uint32_t bar, uint32_t n) {
 __device__ __forceinline__ void bar_expect(uint32_t bar, uint32_t bytes) {
   asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
 }
-// Bounded wait (about a second of %globaltimer); false on expiry.
-__device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity) {
+// Bounded wait, `limit` nanoseconds of %globaltimer (0: none, and no look either); false on expiry.  Lanes poll each for
+// itself, so near the limit their answers can differ.
+__device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity, uint32_t limit) {
+  if (limit == 0) return false;
   uint64_t t0 = 0;
   for (uint32_t i = 0;; ++i) {
     uint32_t ok;
@@ -201,10 +204,12 @@ __device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity) {
       uint64_t now;
       asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(now));
       if (i == 0) t0 = now;
-      else if (now - t0 > 1000000000ull) return false;
+      else if (now - t0 > limit) return false;
     }
   }
 }
+constexpr uint32_t kLate = 0x80000000u;        // in a lane's word of barrier phases: it has given up waiting
+constexpr uint32_t kDrainLimit = 1000000000u;  // for the copies under way when a lane has given up
 __device__ __forceinline__ void tma_load(uint32_t dst, const CUtensorMap* map, int x, int y, int z, uint32_t bar) {
   asm volatile(
       "cp.async.bulk.tensor.3d.shared::cta.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
@@ -524,7 +529,10 @@ __global__ void __launch_bounds__(PagedCfg<KIND, D, NT>::THREADS, 1)
   int cur_i = 0, cur_n = 0, tiles = -1, tile = -1;
   bool in_done = !busy;
   uint32_t valid = 0, parity = 0, vparity = 0;  // bit per stage: a page is there or on its way; phases of the barriers
-  bool bad_id = false, dead = false;
+  bool bad_id = false;
+  // A lane whose wait runs out is late (kLate in `parity`): it waits for nothing more, and lane 0 then starts no more
+  // copies, but it goes on with the warp, which computes with whatever the stages hold: lanes near the limit can differ,
+  // and everything here is written for whole warps.  At the end of a portion one late lane makes the warp's rows NaN.
   Walk* parked = reinterpret_cast<Walk*>(sm + C::OFF_WALK) + wid;
   auto enter = [&](const Walk& in) {
     in_i = 0;
@@ -588,6 +596,16 @@ __global__ void __launch_bounds__(PagedCfg<KIND, D, NT>::THREADS, 1)
       tma_load(dst + j * C::BOX, &map, j * (C::SWIZZLE_ROW / C::ES), side * kPage, tile, bar);
     if (F8 && side == 0)
       bulk_load(exp0 + st * C::EXP, a.pool + (size_t)tile * (C::PAGE + C::EXP) + C::PAGE, C::EXP, bar);
+  };
+  // Before a late lane goes on, the copies that are on their way come to their end (lane 0 starts them): a phase of each
+  // barrier at most is open, the keys' of the stages in `valid`, the values' of those in `values`.
+  auto give_up = [&](uint32_t values) {
+    parity |= kLate;
+#pragma unroll 1
+    for (int k = 0; k < S; ++k) {
+      if (valid >> k & 1) bar_wait(bar0 + 16 * k, parity >> k & 1, kDrainLimit);
+      if (C::APART && (values >> k & 1)) bar_wait(bar0 + 16 * k + 8, vparity >> k & 1, kDrainLimit);
+    }
   };
 #pragma unroll 1
   for (int st = 0; st < S; ++st)
@@ -708,9 +726,11 @@ __global__ void __launch_bounds__(PagedCfg<KIND, D, NT>::THREADS, 1)
       const bool here = valid >> st & 1;
       const uint32_t kb = stage0 + st * C::PAGE, vb = kb + (C::APART ? C::HALF : kPage * C::SWIZZLE_ROW);
       float s[NT][4];
-      if (here && !dead) dead = !bar_wait(bar0 + 16 * st, parity >> st & 1);
-      if (dead) continue;
-      if (here) parity ^= 1u << st;
+      if (here) {  // with a limit of 0 the first copy is waited for
+        const uint32_t limit = w.p.wait_limit || parity ? w.p.wait_limit : kDrainLimit;
+        if ((parity & kLate) == 0 && !bar_wait(bar0 + 16 * st, parity >> st & 1, limit)) give_up(valid);
+        parity ^= 1u << st;
+      }
       int ek0 = 0, ek1 = 0, ev0 = 0, ev1 = 0;
       if (here) {
         if (F8) {  // exponents of tokens g and g + 8, keys and values
@@ -763,7 +783,7 @@ __global__ void __launch_bounds__(PagedCfg<KIND, D, NT>::THREADS, 1)
         __syncwarp();  // every lane has read what the copy replaces
         again = fetch_next() && tile >= 0;
         valid = again ? valid | 1u << st : valid & ~(1u << st);
-        if (again && lane == 0) fetch(st, 0);
+        if (again && (parity & kLate) == 0 && lane == 0) fetch(st, 0);
       };
       if (C::APART) next_page();  // the keys are read
 
@@ -878,8 +898,8 @@ __global__ void __launch_bounds__(PagedCfg<KIND, D, NT>::THREADS, 1)
           }
         }
         if (C::APART) {
-          dead = !bar_wait(bar0 + 16 * st + 8, vparity >> st & 1);
-          if (!dead) vparity ^= 1u << st;
+          if ((parity & kLate) == 0 && !bar_wait(bar0 + 16 * st + 8, vparity >> st & 1, w.p.wait_limit)) give_up(valid | 1u << st);
+          vparity ^= 1u << st;
         }
         if (!whole) {
           // value rows that do not count: a weight of 0 does not remove a NaN
@@ -918,38 +938,37 @@ __global__ void __launch_bounds__(PagedCfg<KIND, D, NT>::THREADS, 1)
             for (int k = 0; k < 4; ++k) o[j][nt][k] += acc[k];
           }
         };
-        if (!dead) {
-          if constexpr (F8) {
+        if constexpr (F8) {
 #pragma unroll
-            for (int j = 0; j < KS / 2; ++j) {
-              uint32_t r[4];
-              ldsm2t8(r, piece(vb, v_off, j));
+          for (int j = 0; j < KS / 2; ++j) {
+            uint32_t r[4];
+            ldsm2t8(r, piece(vb, v_off, j));
 #pragma unroll
-              for (int c = 0; c < 2; ++c) {
-                const uint32_t af[4] = {f16_of_e4m3(r[2 * c]), f16_of_e4m3(r[2 * c + 1]), f16_of_e4m3_high(r[2 * c]),
-                                        f16_of_e4m3_high(r[2 * c + 1])};
-                add(2 * j + c, af);
-              }
+            for (int c = 0; c < 2; ++c) {
+              const uint32_t af[4] = {f16_of_e4m3(r[2 * c]), f16_of_e4m3(r[2 * c + 1]), f16_of_e4m3_high(r[2 * c]),
+                                      f16_of_e4m3_high(r[2 * c + 1])};
+              add(2 * j + c, af);
             }
-          } else {
+          }
+        } else {
 #pragma unroll
-            for (int j = 0; j < KS; ++j) {
-              uint32_t r[4];
-              ldsm4t(r, piece(vb, v_off, j));
-              add(j, r);
-            }
+          for (int j = 0; j < KS; ++j) {
+            uint32_t r[4];
+            ldsm4t(r, piece(vb, v_off, j));
+            add(j, r);
           }
         }
       }
       if (C::APART) {
         __syncwarp();
-        if (again && lane == 0) fetch(st, 1);
+        if (again && (parity & kLate) == 0 && lane == 0) fetch(st, 1);
       } else {
         next_page();
       }
     }
 
     // ================================================================ the portion's result
+    const bool dead = __any_sync(kFull, (parity & kLate) != 0);
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -986,15 +1005,7 @@ __global__ void __launch_bounds__(PagedCfg<KIND, D, NT>::THREADS, 1)
     if (!all && lane == 0)
       rec[begins * NW + wid] = make_int4(out.b, out.hg, 1 + (out.end == out.span), x_end - out.left - out.at + out.span);
   }
-  if (dead) {
-    // copies still under way end before the CTA does
-    for (int k = 0; k < S; ++k)
-      if (valid >> k & 1) {
-        bar_wait(bar0 + 16 * k, parity >> k & 1);
-        if (C::APART) bar_wait(bar0 + 16 * k + 8, vparity >> k & 1);
-      }
-    if (lane == 0) flag_error(a.err, TQ_DEVERR_TIMEOUT);
-  }
+  if (parity & kLate) flag_error(a.err, TQ_DEVERR_TIMEOUT);
   if (bad_id) flag_error(a.err, TQ_DEVERR_BLOCK_ID);
 
   // ================================================================ the CTA's cut segments
@@ -1213,6 +1224,7 @@ PagedPlan plan_of(const tq_ctx* ctx, int batch) {
   p.min_log2 = 0;
   p.tau = 1;
   p.unit = 0;
+  p.wait_limit = ctx->wait_limit;
   return p;
 }
 

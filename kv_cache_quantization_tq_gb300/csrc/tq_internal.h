@@ -56,6 +56,7 @@ struct tq_ctx {
   uint32_t* d_err = nullptr;    // device error word
   int64_t launches = 0;
   int decode_path = 0;          // TQ_DECODE_AUTO / _MMA_SYNC / _TCGEN05
+  uint32_t wait_limit = 1000000000u;  // nanoseconds that tq_paged_attention waits for its copies
   const char* decode_kernel = nullptr;  // kernel of the last decode call (profiling reports)
   bool profiling = false;
   tq::ProfileKind prof[3];      // 0 decode, 1 encode, 2 merge
