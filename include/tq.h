@@ -393,7 +393,8 @@ int tq_should_materialize(int64_t history_tokens, int64_t query_tokens, int head
  * one whose pages pass max_blocks with TQ_DEVERR_POSITION: its lengths entry stays ctx_len (0 if that
  * is negative), its row and the queue stay as they were, its tokens get slot -1; later requests
  * that need no page are still served.  A free page id outside [0, num_blocks) becomes
- * table entry -1 and slots -1 with TQ_DEVERR_BLOCK_ID.  The total of new tokens must be below 2^31.
+ * table entry -1 and slots -1 with TQ_DEVERR_BLOCK_ID; a table entry outside it that an ended request gives back is
+ * flagged in the same way and stands in the queue as a free page that is none, until the caller takes it out.  The total of new tokens must be below 2^31.
  * Outputs must not overlap inputs (block_table and queue, updated in place, apart) or one another. */
 tq_status tq_plan_pages(tq_ctx* ctx, const int32_t* ctx_len, const int32_t* new_len, int batch, int ring_capacity,
                         int32_t* block_table, int max_blocks, int num_blocks, int32_t* queue, int queue_cap,

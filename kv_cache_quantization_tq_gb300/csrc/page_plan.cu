@@ -220,8 +220,9 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanArgs a, co
     Sums at;
     Req r;
     const int b = find(sm.back, j, &Sums::back, &Req::back, at, r);
-    a.queue[wrap(wrap(q.head + q.count, a.queue_cap) + (unsigned)j, a.queue_cap)] =
-        a.block_table[(int64_t)b * a.max_blocks + ((unsigned)j - at.back)];
+    const int id = a.block_table[(int64_t)b * a.max_blocks + ((unsigned)j - at.back)];
+    bad |= id < 0 || id >= a.num_blocks;  // leaving it out would move every page behind it: a scan over all pages
+    a.queue[wrap(wrap(q.head + q.count, a.queue_cap) + (unsigned)j, a.queue_cap)] = id;
   }
 
   // ---- tokens

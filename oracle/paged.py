@@ -180,6 +180,8 @@ def plan(ctx_len, new_len, block_table, queue, queue_state, num_blocks, max_toke
             for j in range(old):
                 if back < room:
                     q_out[(head + count + back) % cap] = block_table[b, j]
+                    if not 0 <= block_table[b, j] < num_blocks:
+                        flags |= ERR_BLOCK_ID
                     back += 1
                 else:
                     flags |= ERR_PAGES
