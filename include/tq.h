@@ -226,6 +226,9 @@ size_t tq_bytes_per_token_head(const tq_ctx* ctx);
 /* Bytes of one tile (one page of one KV head) = 16 * tq_bytes_per_token_head. */
 size_t tq_page_bytes(const tq_ctx* ctx);
 
+/* The CUDA device the context was made on (-1 for NULL). */
+int tq_ctx_device(const tq_ctx* ctx);
+
 /* Workspace bytes tq_decode_attention needs for `batch` sequences whose
  * compressed lengths are all <= max_ctx tokens (for the decode path selected
  * when it is called: query the size again after tq_set_decode_path). */

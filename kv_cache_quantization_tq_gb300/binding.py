@@ -81,6 +81,7 @@ _SIGS = {
     "tq_generate_tables": (_i, [_u64, _i, _i, _vp, _vp]),
     "tq_bytes_per_token_head": (_sz, [_vp]),
     "tq_page_bytes": (_sz, [_vp]),
+    "tq_ctx_device": (_i, [_vp]),
     "tq_workspace_size": (_i, [_vp, _i, _i, C.POINTER(_sz)]),
     "tq_encode_flush": (_i, [_vp, _vp, _vp, _i, _i, _i, _vp, _vp, _i, _vp, _i, _vp]),
     "tq_append_token": (_i, [_vp, _vp, _vp, _vp, _i, _vp, _vp, _vp, _i, _vp, _i, _vp]),
@@ -241,14 +242,8 @@ class Context:
         self.head_dim = head_dim
         self.num_q_heads = num_q_heads
         self.num_kv_heads = num_kv_heads
-        import torch
-
-        self._device = torch.cuda.current_device()  # the device tq_create used
+        self._device = lib.tq_ctx_device(ptr)
         self._page_bytes = self.page_bytes
-        # what the dense-layout calls look up on every call
-        self._raw = torch._C._cuda_getCurrentRawStream
-        self._types = (torch.int32, torch.int64, torch.float32, torch.uint8)
-        self._elem = torch.bfloat16 if self.cfg.key_format == TQ_ELEM_BF16 else torch.float16
 
     def close(self):
         if getattr(self, "ptr", None) and self.ptr.value:
@@ -412,6 +407,17 @@ class Context:
                   _stream(stream)), name)
 
     # -- page plan and dense pages
+    _types = None
+
+    def _look_up(self):
+        """What these calls need of torch, kept after the first of them: a context is made without it."""
+        import torch
+
+        self._raw = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (lambda dev: torch.cuda.current_stream(dev).cuda_stream)
+        self._elem = torch.bfloat16 if self.cfg.key_format == TQ_ELEM_BF16 else torch.float16
+        self._types = (torch.int32, torch.int64, torch.float32, torch.uint8)
+        return self._types
+
     def _addrs(self, dtype, names, *tensors):
         """Addresses of contiguous tensors of `dtype` on the context's device (None -> NULL)."""
         dev, out = self._device, []
@@ -447,7 +453,7 @@ class Context:
         n_paged, n_ring int32 [B]; block_table int32 [B, max_blocks]; queue int32 [cap]; queue_state, queue_state_out
         int32 [2]; token_start int32 [B + 1]; slots int64 [max_tokens]; positions, rows int32 [max_tokens]."""
         bsz, n = ctx_len.numel(), slots.numel()
-        i32, i64, _, _ = self._types
+        i32, i64, _, _ = self._types or self._look_up()
         self._check_bt(block_table, bsz)
         if (new_len.numel() != bsz or lengths.numel() != bsz or (n_paged is not None and n_paged.numel() != bsz)
                 or (n_ring is not None and n_ring.numel() != bsz)):
@@ -471,8 +477,8 @@ class Context:
     def paged_store(self, k, v, slots, pool, stream=None):
         """tq_paged_store: k, v [n_tokens, Hkv, d] of the context's 16-bit type (rows may be strided) into the pages;
         slots int64 [n_tokens], negative to skip a token."""
+        _, i64, _, u8 = self._types or self._look_up()
         elem, n = self._elem, k.shape[0]
-        _, i64, _, u8 = self._types
         kp, ks = self._rows_of(k, self.num_kv_heads, elem, "k")
         vp, vs = self._rows_of(v, self.num_kv_heads, elem, "v")
         if v.shape[0] != n or slots.numel() != n:
@@ -493,9 +499,9 @@ class Context:
     def paged_attention(self, q, pool, block_table, lengths, out, workspace, lse=None, window=0, scale=0.0, stream=None):
         """tq_paged_attention: q [batch, Hq, d] of the context's 16-bit type (rows may be strided), out fp32
         [batch, Hq, d], lse fp32 [batch, Hq] or None; window 0 for all positions, scale 0 for 1 / sqrt(d)."""
+        i32, _, f32, u8 = self._types or self._look_up()
         qp, qs = self._rows_of(q, self.num_q_heads, self._elem, "q")
         bsz = q.shape[0]
-        i32, _, f32, u8 = self._types
         if out.shape != q.shape or lengths.numel() != bsz or (lse is not None and lse.shape != q.shape[:2]):
             raise ValueError("out must be [batch, Hq, d], lengths [batch] and lse [batch, Hq]")
         if not 0 <= window < 2 ** 31:

@@ -566,6 +566,8 @@ tq_status tq_config_check(const tq_config* cfg, size_t* bytes_per_token_head) {
 
 size_t tq_bytes_per_token_head(const tq_ctx* ctx) { return ctx ? record_bytes(ctx->cfg) : 0; }
 
+int tq_ctx_device(const tq_ctx* ctx) { return ctx ? ctx->device : -1; }
+
 size_t tq_page_bytes(const tq_ctx* ctx) { return tq::kPage * tq_bytes_per_token_head(ctx); }
 
 tq_status tq_workspace_size(const tq_ctx* ctx, int batch, int max_ctx, size_t* bytes) {
