@@ -106,7 +106,7 @@ tq_status tq_paged_store(tq_ctx* ctx, const void* k, const void* v, int64_t k_st
   if (ctx->cfg.layout != TQ_LAYOUT_DENSE) return TQ_ERR_UNSUPPORTED;
   if (n_tokens == 0) return TQ_OK;
   const int64_t row = (int64_t)ctx->cfg.num_kv_heads * ctx->cfg.head_dim;
-  if (!k || !v || !slots || !pool || !aligned16(k) || !aligned16(v) || !aligned16(pool)) return TQ_ERR_INVALID_ARG;
+  if (!k || !v || !slots || (num_blocks > 0 && !pool) || !aligned16(k) || !aligned16(v) || !aligned16(pool)) return TQ_ERR_INVALID_ARG;
   if (k_stride < row || v_stride < row || (k_stride | v_stride) & 7) return TQ_ERR_INVALID_ARG;
   if (!on_device(ctx)) return TQ_ERR_INVALID_ARG;
   tq::StoreArgs a;
