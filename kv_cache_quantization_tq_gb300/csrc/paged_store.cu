@@ -4,8 +4,9 @@
 // What bounds it: memory traffic, each element read once and written once.  A thread moves 32 bytes of a row
 // (16 elements: one 16-byte store of codes); the d / 16 lanes of a row are neighbours, so that a vector's
 // largest entry is found by shuffles within a warp for every d.  Rows go token by token; by tiles (16 tokens of a
-// head, neighbours in the pool) measured the same.  32768 tokens x 8 heads x 128, bf16: 41.5 us as 16-bit
-// copies (6.5 TB/s, 95% of a plain copy), 34.3 us as e4m3 (5.9 TB/s, bound by its conversions' issue slots).
+// head, neighbours in the pool) measured the same.  32768 tokens x 8 heads x 128, bf16: 41.1 us as 16-bit
+// copies (6.5 TB/s, 96% of a plain copy), 33.3 us as e4m3 (6.1 TB/s, 89%, with the ALU pipe 67% and the issue slots 66%
+// taken: the conversions and packed maxima beside the memory, neither of them alone).
 //
 // The exponent of a vector is e = min { e : max|x| <= 448 2^e }, read off the float bits of max|x|: with
 // max|x| = m 2^x, 1 <= m < 2, it is x - 8 for m <= 1.75 and x - 7 otherwise (448 = 1.75 2^8).  A power of two
