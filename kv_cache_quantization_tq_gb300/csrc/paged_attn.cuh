@@ -8,9 +8,9 @@
 // serves one aim: enough bytes in flight on every multiprocessor from the first moment to the last.
 //
 // Work split.  A segment is one (sequence, KV head, group of up to 8 NT query heads); its work is its
-// number of pages plus `lead` for the queries, the joining and the result.  All segments stand in one line, and
+// number of pages plus kLead for the queries, the joining and the result.  All segments stand in one line, and
 // T teams get equal pieces of it, whatever the lengths are: a ragged batch and a single long sequence are split
-// alike, in one wave, with no length known on the host.  Cuts that fall within a segment's lead, or within tau pages
+// alike, in one wave, with no length known on the host.  Cuts that fall within a segment's lead, or within kTau pages
 // of its ends, move to the end.  A team is one warp: what a segment costs beside its pages (fetching its queries,
 // joining, writing) is hidden by the CTA's other warps, where a team of all warps would wait for it (measured:
 // 64 sequences of 0.5 to 16K tokens, e4m3, 32 / 8 heads: 3.3 us per segment and CTA).  A segment
@@ -86,10 +86,13 @@ struct PagedCfg {
   static constexpr int stages(int nw) { return (LIMIT - fixed(nw)) / per(nw); }
   static constexpr int MIN_S = (HEADS * PITCH * 4 + PAGE - 1) / PAGE;  // a warp's stages hold its last piece
   static constexpr bool fits(int nw, int s) { return stages(nw) >= (s > MIN_S ? s : MIN_S); }
-  // Warps per CTA: as many as fit.  Stages: what keeps about 96 KB (e4m3) or 128 KB per multiprocessor on the way.  More
+  // Warps per CTA: as many as fit.  Stages: as many whole ones as stay within 96 KB (e4m3) or 128 KB per multiprocessor,
+  // which rounds down.  On the way, with up to 8 heads a segment and with 16: 16-bit pages 128 and 128 KB at d = 64, 96
+  // and 64 at 128 and 256, 128 at 512; e4m3 pages 96 and 96 at d = 64, 64 and 96 at 128, 96 and 96 at 256, 64 at 512.  More
   // is not better: with every queue full the multiprocessors farther from memory fall behind and the last of
-  // them ends late.  16-bit pages of d = 128, 8 x 32K and 16 ragged sequences: 12 warps x 1 stage 87.1 and 622 us,
-  // 8 x 2 89.0 and 645, 16 x 1 88.3 and 625.  e4m3 pages of d = 128, 64 ragged sequences: 16 x 1 169 us, 16 x 2 181.
+  // them ends late.  16-bit pages of d = 128, 8 x 32K and 16 ragged sequences: 12 warps x 1 stage (96 KB) 85.8 and 622 us,
+  // 8 x 2 (128 KB) 87.0 and 634, 16 x 1 (128 KB) 88.7 and 644.  e4m3 pages of d = 128, 64 ragged sequences: 16 x 1 (64 KB)
+  // 173 us, 16 x 2 (128 KB) 181.
   // (e4m3 at d = 64 with 16 query heads has no registers for 16 warps: 16 92.1 us, 12 87.2.)
   static constexpr int NW = PAGE <= 4096 && QREG && (NT == 1 || KIND != kE4M3) && fits(16, 1) ? 16 : fits(12, 1) ? 12 : fits(8, 1) ? 8 : fits(6, 1) ? 6 : 4;
   static constexpr int S_WANT = (KIND == kE4M3 ? 96 : 128) * 1024 / (NW * PAGE);
@@ -115,24 +118,28 @@ struct PagedCfg {
   static_assert(SMEM <= 232448, "shared memory");
   static constexpr int SWIZZLE_ROW = D * ES < 128 ? D * ES : 128;  // bytes of a row in one TMA box
   static constexpr int BOXES = D * ES / SWIZZLE_ROW;               // boxes side by side in a page
-  // With one stage keys and values are copied apart, so that the next keys come while the values are used; with more
-  // a page is one copy and one wait (fewer instructions: e4m3 at d = 64 54 against 64 us, at d = 512 65 against 69).
+  // With one stage keys and values are copied apart, so that the next keys come while the values are used (e4m3 at d = 512
+  // 68.6 against 79.9 us); with more a page is one copy and one wait (fewer instructions: e4m3 at d = 64 55.9 against 64.9).
   static constexpr bool APART = S == 1;
   // The weights' total grows by every page: its rounding is the largest error of a long sequence (16 ragged sequences up
   // to 128K tokens: 1.2e-6 of the result, 4.2e-7 with what is lost kept; the same time).  8-bit pages with 16
-  // heads or d = 512 have no registers left for it (76 against 81 us at d = 64, 65 against 68 at 512).
+  // heads or d = 512 go without (with it 87.5 against 85.6 us at d = 64, 74.1 against 72.9 at 128, 71.9 against 68.6 at 512).
   static constexpr bool KEEP_LOST = KIND != kE4M3 || (NT == 1 && D < 512);
   static constexpr int BOX_ROWS = APART ? kPage : 2 * kPage;
   static constexpr int BOX = BOX_ROWS * SWIZZLE_ROW;
 };
 
 // ---------------------------------------------------------------- work split, shared by both kernels
+// A segment's queries, joining and result cost a warp about two pages' time: kLead units of the line beside its pages (2: 256
+// short sequences 29.6 us, 64 ragged e4m3 173.2; 0: 36.0 and 174.8; 4: 30.2 and 174.0).  Pieces go down to one unit:
+// more warps shorten a small call's chain (1 x 1K 10.0 us, from two units on 10.5).  Cuts within kTau pages of a
+// segment's ends move there, which saves pieces of one page; more cost balance (4: 256 short 32.4, sliding window at d
+// 256 31.1 against 28.7).
+constexpr int kLead = 2, kTau = 1;
+
 struct PagedPlan {
   int teams;       // most teams: the grid's warps
-  int lead;        // a segment's work beside its pages, in units
   int unit;        // the line counts 2^unit pages as one, so that it stays below 2^31
-  int min_log2;    // a team gets at least about 2^min_log2 of the line
-  int tau;         // cuts this near a segment's end move there
   int groups;      // query-head groups per KV head
   uint32_t wait_limit;  // nanoseconds that a warp waits for a copy
 };
@@ -161,14 +168,14 @@ __device__ __forceinline__ Seq seq_of(const PagedArgs& a, int len) {
 }
 // Length of one segment of the sequence on the line.
 __device__ __forceinline__ int span_of(const PagedPlan& p, const Seq& s) {
-  return s.pages ? ((s.pages + (1 << p.unit) - 1) >> p.unit) + p.lead : 0;
+  return s.pages ? ((s.pages + (1 << p.unit) - 1) >> p.unit) + kLead : 0;
 }
 
 // Equal pieces of the line: piece t begins at t base + min(t, rest).
 struct Pieces {
   unsigned teams, rest, base;
   __device__ __forceinline__ Pieces(const PagedPlan& p, unsigned work) {
-    teams = min(max(work >> p.min_log2, 1u), (unsigned)p.teams);
+    teams = min(max(work, 1u), (unsigned)p.teams);
     base = work / teams;
     rest = work - base * teams;
   }
@@ -383,8 +390,8 @@ __device__ __forceinline__ int kv_head(const PagedPlan& p, int hg) { return p.gr
 
 // Moves a cut at x, which is in segment r, to that segment's end or beginning where it is near.
 __device__ __forceinline__ unsigned settle(const PagedPlan& p, const At& r, unsigned x) {
-  if (r.at <= p.lead + p.tau) return x - r.at;
-  if (r.span - r.at <= p.tau) return x - r.at + r.span;
+  if (r.at <= kLead + kTau) return x - r.at;
+  if (r.span - r.at <= kTau) return x - r.at + r.span;
   return x;
 }
 
@@ -397,8 +404,8 @@ struct __align__(16) Walk {
   int left;           // what the warp has from this portion on
   __device__ __forceinline__ void open(const PagedPlan& pl) {
     end = min(at + left, span);
-    p = max(at - pl.lead, 0) << pl.unit;
-    take = max(min((end - pl.lead) << pl.unit, s.pages) - p, 0);
+    p = max(at - kLead, 0) << pl.unit;
+    take = max(min((end - kLead) << pl.unit, s.pages) - p, 0);
   }
   __device__ __forceinline__ bool next(const PagedArgs& a, const PagedPlan& pl, const Scan& sc) {
     left -= end - at;
@@ -509,11 +516,11 @@ __global__ void __launch_bounds__(PagedCfg<KIND, D, NT>::THREADS, 1)
     if (team + 1 == pieces.teams) x1 = work;
     busy = x0 < x1;
     if (busy) {
-      if (back > w.p.lead + w.p.tau && over <= w.p.tau) r = locate(a, w.p, sc, front, x0, x0, lane);  // the next segment
+      if (back > kLead + kTau && over <= kTau) r = locate(a, w.p, sc, front, x0, x0, lane);  // the next segment
       out.b = __shfl_sync(kFull, r.b, 0);
       out.hg = __shfl_sync(kFull, r.hg, 0);
       out.at = __shfl_sync(kFull, r.at, 0);
-      if (out.at <= w.p.lead + w.p.tau) out.at = 0;
+      if (out.at <= kLead + kTau) out.at = 0;
       out.s = sc.seq(a, out.b);
       out.span = span_of(w.p, out.s);
       out.left = x1 - x0;
@@ -1092,7 +1099,7 @@ __global__ void __launch_bounds__(PagedCfg<KIND, D, NT>::THREADS, 1)
       }
       // the last CTA with a piece of it: the one with the last cut more than tau before its end
       if (kind && h == 0)
-        w.cuts[(int64_t)seq * heads + hg] = make_int2(blockIdx.x, ends ? blockIdx.x : (pieces.from(ends_at - w.p.tau) - 1) / NW);
+        w.cuts[(int64_t)seq * heads + hg] = make_int2(blockIdx.x, ends ? blockIdx.x : (pieces.from(ends_at - kTau) - 1) / NW);
     }
   }
 }
@@ -1210,19 +1217,12 @@ __global__ void __launch_bounds__((JOIN == 1 ? kMergeWarps : JOIN) * 32) paged_m
 
 // ---------------------------------------------------------------- host side
 template <int KIND, int D, int NT>
-PagedPlan plan_of(const tq_ctx* ctx, int batch) {
+PagedPlan plan_of(const tq_ctx* ctx) {
   using C = PagedCfg<KIND, D, NT>;
   PagedPlan p;
   const int n_rep = ctx->cfg.num_q_heads / ctx->cfg.num_kv_heads;
   p.groups = (n_rep + C::HEADS - 1) / C::HEADS;
   p.teams = ctx->sm_count * C::NW;
-  // A segment's queries, joining and result cost a warp about two pages' time (4: 64 ragged sequences 185.3 against
-  // 184.0 us, 0: 256 short ones 38 against 30).  Pieces go down to one unit: more warps shorten a small call's chain
-  // (1 x 1K 8.6 us, from two units on 9.1).  Moving cuts by one page at a segment's ends saves pieces of one page;
-  // four cost balance (sliding window at d 256 33.4 against 30.4).
-  p.lead = 2;
-  p.min_log2 = 0;
-  p.tau = 1;
   p.unit = 0;
   p.wait_limit = ctx->wait_limit;
   return p;
@@ -1238,7 +1238,7 @@ size_t parts_bytes(const PagedPlan& p) {
 }
 template <int KIND, int D, int NT>
 size_t workspace_of(const tq_ctx* ctx, int batch) {
-  const PagedPlan p = plan_of<KIND, D, NT>(ctx, batch);
+  const PagedPlan p = plan_of<KIND, D, NT>(ctx);
   return parts_bytes<KIND, D, NT>(p) + align256((size_t)batch * ctx->cfg.num_kv_heads * p.groups * sizeof(int2));
 }
 
@@ -1247,7 +1247,7 @@ cudaError_t launch_one(tq_ctx* ctx, const PagedArgs& a, void* workspace, cudaStr
   using C = PagedCfg<KIND, D, NT>;
   PagedWork w;
   w.a = a;
-  w.p = plan_of<KIND, D, NT>(ctx, a.batch);
+  w.p = plan_of<KIND, D, NT>(ctx);
   w.q_bf16 = ctx->cfg.key_format == TQ_ELEM_BF16;
   w.parts = static_cast<float*>(workspace);
   w.cuts = reinterpret_cast<int2*>(static_cast<uint8_t*>(workspace) + parts_bytes<KIND, D, NT>(w.p));  // for all CTAs
@@ -1256,9 +1256,9 @@ cudaError_t launch_one(tq_ctx* ctx, const PagedArgs& a, void* workspace, cudaStr
   const int64_t all = (int64_t)a.batch * a.hkv * w.p.groups;
   int64_t pages = a.max_blocks;
   if (a.window && pages > ((int64_t)a.window + 2 * kPage - 2) / kPage) pages = ((int64_t)a.window + 2 * kPage - 2) / kPage;
-  while (all * ((pages >> w.p.unit) + 1 + w.p.lead) > 0x7fffffff)
+  while (all * ((pages >> w.p.unit) + 1 + kLead) > 0x7fffffff)
     if (++w.p.unit > 27) return cudaErrorInvalidValue;
-  const int64_t line = all * ((pages >> w.p.unit) + 1 + w.p.lead), want = (line + C::NW - 1) / C::NW;
+  const int64_t line = all * ((pages >> w.p.unit) + 1 + kLead), want = (line + C::NW - 1) / C::NW;
   const int ctas = want < ctx->sm_count ? (int)want : ctx->sm_count;
   w.p.teams = ctas * C::NW;
   CUtensorMap map{};
