@@ -440,8 +440,8 @@ tq_status tq_paged_workspace_size(const tq_ctx* ctx, int batch, size_t* bytes);
  * the sums with TQ_DEVERR_BLOCK_ID.  A warp that gives up waiting for its copies (tq_set_wait_limit) sets
  * TQ_DEVERR_TIMEOUT, and the rows it has a part in become NaN.  A NaN or an infinity in a row that counts makes
  * what depends on it NaN (weights are multiplied in parts).  Sums are held in 32 bits: they overflow where the
- * number of positions times the largest |value| passes 2^127, and weights or values below about 2^-100 (of a row's largest
- * weight; of 1) count with fewer bits or not at all.  On 8-bit pages a position counts to within 2^-36 of the
+ * number of positions times the largest |value| passes 2^127, and weights below about 2^-100 of a row's largest and values
+ * whose vector is below about 2^-100 (8-bit pages: 2^-78) count with fewer bits or not at all.  On 8-bit pages a position counts to within 2^-36 of the
  * row's largest weight times |value|, and a bf16 query entry to within 2^-39 of its head's largest.  num_blocks * Hkv must be below 2^31.  The current device
  * must be the context's (TQ_ERR_INVALID_ARG), here and in the two calls above. */
 tq_status tq_paged_attention(tq_ctx* ctx, const void* q, int64_t q_stride, int batch, const void* pool, int num_blocks,

@@ -86,6 +86,16 @@ def test_values_near_the_largest(bits, hq, d):
     check(e, *attend(e))
 
 
+@pytest.mark.parametrize("bits,size_log2", [(16, (-100, -98)), (8, (-78, -76))])
+@pytest.mark.parametrize("hq,d", [(4, 64), (16, 128), (2, 512)])
+def test_values_near_the_smallest(bits, size_log2, hq, d):
+    """bf16 values down to where the range that is kept ends."""
+    lengths = [100, 17, 1]
+    e = make_case(d, lengths, hq, 1, d, bits, True)
+    fill(e, *single_term(d, lengths, hq, 1, d, torch.bfloat16, -12, size_log2, heavy=False))
+    check(e, *attend(e))
+
+
 @pytest.mark.parametrize("power", [-118, -90, 90, 118])
 def test_queries_against_keys_of_the_opposite_size(power):
     """8-bit pages: bf16 queries times 2^power, keys times 2^-power (8-bit keys go down to about 2^-120)."""
