@@ -604,12 +604,12 @@ __global__ void __launch_bounds__(PagedCfg<KIND, D, NT>::THREADS, 1)
     if (F8 && side == 0)
       bulk_load(exp0 + st * C::EXP, a.pool + (size_t)tile * (C::PAGE + C::EXP) + C::PAGE, C::EXP, bar);
   };
-  // Before a late lane goes on, the copies that are on their way come to their end (lane 0 starts them): a phase of each
-  // barrier at most is open, the keys' of the stages in `valid`, the values' of those in `values`.
+  // Before a late lane 0 goes on, the copies that it has on their way come to their end: a phase of each barrier at most is
+  // open, the keys' of the stages in `valid`, the values' of those in `values`.  The other lanes started none.
   auto give_up = [&](uint32_t values) {
     parity |= kLate;
 #pragma unroll 1
-    for (int k = 0; k < S; ++k) {
+    for (int k = 0; k < S && lane == 0; ++k) {
       if (valid >> k & 1) bar_wait(bar0 + 16 * k, parity >> k & 1, kDrainLimit);
       if (C::APART && (values >> k & 1)) bar_wait(bar0 + 16 * k + 8, vparity >> k & 1, kDrainLimit);
     }
