@@ -15,10 +15,11 @@
  *  - alternate layout: keys per-block affine 8-bit without rotation, values
  *    Walsh-Hadamard + 3-bit Lloyd-Max with an fp16 norm (vllm-metal
  *    TurboQuant guide, "quantisation principle" table);
- *  - dense pages (16-bit or e4m3 elements) beside the compressed caches: a page
- *    plan of a serving step, the store of new tokens, and attention of one
- *    new token per sequence (tq_plan_pages, tq_paged_store, tq_paged_attention;
- *    these have no counterpart in the source pages);
+ *  - dense pages (16-bit, e4m3 or e2m1 elements) beside the compressed caches: a page
+ *    plan of a serving step, the store of new tokens, attention of one
+ *    new token per sequence, and the eviction of tokens by their share of
+ *    attention (tq_plan_pages, tq_paged_store, tq_paged_attention, tq_paged_weights,
+ *    tq_paged_evict; these have no counterpart in the source pages);
  *  - decode attention: softmax(q k^T / sqrt(d)) v over the compressed tokens
  *    plus an exact fp16 buffer of the newest <= 128 tokens (turboquant-bench,
  *    "buffer strategy"; turboquant vLLM guide, section 5.1 ring buffer and
@@ -68,11 +69,14 @@
  *     fp16 keys (32 d bytes) and there is no KSM.  VI is a dense vb-bit
  *     stream per token, 2 vb d bytes.  tq_config_check gives the size.
  *
- * Dense layout (uncompressed or 8-bit float pages, for the layers a model keeps
+ * Dense layout (uncompressed, 8-bit or 4-bit float pages, for the layers a model keeps
  * out of the compression; read by tq_paged_attention):
  *   16-bit tile, 64 d bytes: keys [16][d], then values [16][d], fp16 or bf16;
  *   8-bit tile, 32 d + 32 bytes: key codes [16][d], value codes [16][d] (e4m3), then
  *     int8 exponents (-126 .. 126) of the 16 keys and of the 16 values: entry = code * 2^exponent.
+ *   4-bit tile, 18 d + 32 bytes: key codes [16][d / 2], value codes [16][d / 2] (e2m1, entry 2 i in the low half of byte i),
+ *     key scales [16][d / 16], value scales [16][d / 16] (e4m3, not negative, one for 16 entries), then
+ *     int8 exponents (-126 .. 126) of keys and values: entry = code * scale * 2^exponent.
  */
 #ifndef TQ_H_
 #define TQ_H_
@@ -135,8 +139,9 @@ typedef struct {
                         layout: TQ_ELEM_F16 (0, default) or TQ_ELEM_BF16 (1); must be 0 otherwise */
 } tq_config;
 
-/* Dense layout: key_bits = value_bits = 16 (default; pages hold the elements as they are) or 8 (pages
- * hold e4m3 codes with one power-of-two exponent per token, KV head and side).  key_format is the
+/* Dense layout: key_bits = value_bits = 16 (default; pages hold the elements as they are), 8 (pages
+ * hold e4m3 codes with one power-of-two exponent per token, KV head and side) or 4 (e2m1 codes with an e4m3
+ * scale per 16 entries beside such an exponent).  key_format is the
  * 16-bit type of the queries, of the stored keys and values handed in, and of 16-bit pages.  Any
  * num_q_heads / num_kv_heads ratio is accepted; the seed is not used. */
 #define TQ_ELEM_F16 0
@@ -413,7 +418,10 @@ tq_status tq_plan_pages(tq_ctx* ctx, const int32_t* ctx_len, const int32_t* new_
  * 16-bit pages take the elements unchanged.  8-bit pages take, per token and KV head and for keys and
  * values apart, e = the least whole number with max|x| <= 448 * 2^e over the finite entries (at least
  * -120, also for a vector of zeros) and the codes e4m3(x * 2^-e), rounded to nearest even; infinities become
- * +-448 * 2^e and NaN stays NaN.  A slot outside the pool is skipped with TQ_DEVERR_BLOCK_ID.  Slots
+ * +-448 * 2^e and NaN stays NaN.  4-bit pages take e = the least whole number with max|x| <= 2688 * 2^e (at least -120),
+ * for every 16 entries the scale s = e4m3(max|x| * 2^-e / 6), and the codes e2m1(x * 2^-e / s), all rounded to nearest even
+ * (magnitudes 0, 0.5, 1, 1.5, 2, 3, 4, 6; s = 0: codes of zero with the entries' signs).  16 entries with an infinity have s = 448 and the
+ * infinity becomes +-6 * 448 * 2^e; 16 entries with a NaN are all NaN (s is NaN).  A slot outside the pool is skipped with TQ_DEVERR_BLOCK_ID.  Slots
  * must differ from one another: what a slot named twice holds afterwards is not defined. */
 tq_status tq_paged_store(tq_ctx* ctx, const void* k, const void* v, int64_t k_stride, int64_t v_stride,
                          const int64_t* slots, int n_tokens, void* pool, int num_blocks, cudaStream_t stream);
@@ -449,7 +457,62 @@ tq_status tq_paged_attention(tq_ctx* ctx, const void* q, int64_t q_stride, int b
                              float scale, float* out, float* lse, void* workspace, size_t ws_bytes,
                              cudaStream_t stream);
 
-/* How long later tq_paged_attention calls (and graphs captured later) wait for a copy of their own before they give
+/* tq_paged_attention with other scores: z = scale * q . k_p, then with cap > 0 z = cap * tanh(z / cap), then with slopes (device
+ * float32 [Hq], NULL: none) z += slopes[h] * (p - (L - 1)), which is 0 at the new token.  out and lse are those of z.  cap 0 and
+ * no slopes: tq_paged_attention.  cap: 0, or in [2^-60, 2^60].  p counts the sequence's slots: behind tq_paged_evict the
+ * distance (and the window) is one in the tokens that are left. */
+tq_status tq_paged_attention_scored(tq_ctx* ctx, const void* q, int64_t q_stride, int batch, const void* pool, int num_blocks,
+                                    const int32_t* block_table, int max_blocks, const int32_t* lengths, int window,
+                                    float scale, float cap, const float* slopes, float* out, float* lse, void* workspace,
+                                    size_t ws_bytes, cudaStream_t stream);
+
+/* The attention weights of one new token per sequence, added up per cached token and KV head:
+ *   weights_out[b][kvh][p] = decay * weights[b][kvh][p] + sum over the query heads h of kvh of exp(z_hp - lse[b][h])
+ * for p < lengths[b], z as in tq_paged_attention_scored (0 for p in front of the window); entries from lengths[b] on are left as
+ * they were.  Reads the keys alone.  Arguments as there, and
+ *   lse          device float32 [batch][Hq], what the attention call gave (-inf: the row's weights are 0)
+ *   weights      device float32 [batch][Hkv][weights_stride], NULL for zeros; weights_out: likewise, the same array or one
+ *                that does not overlap it
+ *   decay        any finite number
+ * A length beyond weights_stride or the block table, or negative, counts as 0 with TQ_DEVERR_POSITION; tokens of a page whose
+ * id is outside [0, num_blocks) get no weight, with TQ_DEVERR_BLOCK_ID; after TQ_DEVERR_TIMEOUT the sums of the tokens
+ * concerned are NaN.  Needs no workspace. */
+tq_status tq_paged_weights(tq_ctx* ctx, const void* q, int64_t q_stride, int batch, const void* pool, int num_blocks,
+                           const int32_t* block_table, int max_blocks, const int32_t* lengths, int window, float scale,
+                           float cap, const float* slopes, const float* lse, const float* weights, float decay,
+                           float* weights_out, int64_t weights_stride, cudaStream_t stream);
+
+/* Keeps the tokens of a dense cache that had the most attention and moves them together.  Per sequence b and KV head, with
+ * L = lengths[b] and K = min(keep[b], L) (0 if keep is negative): the newest min(recent, K) tokens stay, of the oldest as many of `sinks`
+ * as still fit, and of those between them the ones with the largest weights (the older of equal ones; NaN counts as the
+ * largest, -0 as 0) until there are K.  They keep their order and become slots 0 .. K - 1 of the sequence; a token that stays where it was
+ * is not written.
+ *   weights      device float32 [batch][Hkv][weights_stride] (tq_paged_weights); weights_stride at most 2^30
+ *   pool, block_table  as for tq_paged_attention; the pool is changed in place, so no page may belong to two sequences
+ *   lengths, keep      device int32 [batch]
+ *   weights_out  as weights, another array: entries 0 .. K - 1 are those of the kept tokens, K .. L - 1 become 0
+ *   lengths_out  device int32 [batch]: K
+ *   kept         device int32 [batch][Hkv][weights_stride]: entries 0 .. K - 1 are the slots that the tokens come from
+ * Slots K .. L - 1 of the pages are no longer defined.  A length that is negative, or beyond the block table or weights_stride,
+ * counts as 0 with TQ_DEVERR_POSITION; a token is not moved from or to a page whose id is outside [0, num_blocks)
+ * (TQ_DEVERR_BLOCK_ID).  batch * Hkv must be below 2^28.  Calls that share pages, and the calls that read them, must be ordered. */
+tq_status tq_paged_evict(tq_ctx* ctx, const float* weights, int64_t weights_stride, int batch, void* pool, int num_blocks,
+                         const int32_t* block_table, int max_blocks, const int32_t* lengths, const int32_t* keep, int sinks,
+                         int recent, float* weights_out, int32_t* lengths_out, int32_t* kept, cudaStream_t stream);
+
+/* Gives pages that hold no token any more back to the queue of free pages (tq_plan_pages): of each request the table's entries
+ * ceil(new_lengths / 16) .. ceil(lengths / 16) - 1, request by request, behind the queue's end.  The table keeps its entries.  All layers
+ * that share the table must have been shortened first.
+ *   lengths, new_lengths  device int32 [batch]; block_table device int32 [batch][max_blocks]
+ *   queue, queue_state, queue_state_out  as for tq_plan_pages; queue_state_out is another array than queue_state
+ * A request with new_lengths negative or beyond lengths, or with lengths beyond the table, gives nothing back, with
+ * TQ_DEVERR_POSITION.  Pages that find no room in the queue are lost, and a queue state that is not valid stays as it is, with
+ * TQ_DEVERR_PAGES; an entry outside [0, num_blocks) is flagged (TQ_DEVERR_BLOCK_ID) and stands in the queue as it is. */
+tq_status tq_release_pages(tq_ctx* ctx, const int32_t* lengths, const int32_t* new_lengths, int batch,
+                           const int32_t* block_table, int max_blocks, int num_blocks, int32_t* queue, int queue_cap,
+                           const int32_t* queue_state, int32_t* queue_state_out, cudaStream_t stream);
+
+/* How long later tq_paged_attention, _scored and tq_paged_weights calls (and graphs captured later) wait for a copy of their own before they give
  * up with TQ_DEVERR_TIMEOUT; 10^9 nanoseconds unless set.  Meant for tests of that path: with 0 a warp's first
  * copy is waited for as usual and the next one counts as late.  Host only. */
 tq_status tq_set_wait_limit(tq_ctx* ctx, uint32_t nanoseconds);

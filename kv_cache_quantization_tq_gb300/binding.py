@@ -94,6 +94,12 @@ _SIGS = {
     "tq_paged_store": (_i, [_vp, _vp, _vp, _i64, _i64, _vp, _i, _vp, _i, _vp]),
     "tq_paged_workspace_size": (_i, [_vp, _i, C.POINTER(_sz)]),
     "tq_paged_attention": (_i, [_vp, _vp, _i64, _i, _vp, _i, _vp, _i, _vp, _i, C.c_float, _vp, _vp, _vp, _sz, _vp]),
+    "tq_paged_attention_scored": (_i, [_vp, _vp, _i64, _i, _vp, _i, _vp, _i, _vp, _i, C.c_float, C.c_float, _vp, _vp, _vp, _vp, _sz,
+                                       _vp]),
+    "tq_paged_weights": (_i, [_vp, _vp, _i64, _i, _vp, _i, _vp, _i, _vp, _i, C.c_float, C.c_float, _vp, _vp, _vp, C.c_float, _vp,
+                              _i64, _vp]),
+    "tq_paged_evict": (_i, [_vp, _vp, _i64, _i, _vp, _i, _vp, _i, _vp, _vp, _i, _i, _vp, _vp, _vp, _vp]),
+    "tq_release_pages": (_i, [_vp, _vp, _vp, _i, _vp, _i, _i, _vp, _i, _vp, _vp, _vp]),
     "tq_set_wait_limit": (_i, [_vp, C.c_uint32]),
     "tq_should_materialize": (_i, [_i64, _i64, _i, _i, _i64]),
     "tq_pack": (_i, [_vp, _i64, _i, _vp, _vp]),
@@ -222,9 +228,9 @@ class Context:
                  centroids=None, signs=None, sketch=None, value_bits=None, key_bits=None, key_format=None):
         self.cfg = tq_config_init(layout, head_dim, num_q_heads, num_kv_heads, seed)
         if value_bits is not None:
-            self.cfg.value_bits = value_bits  # main layout: 2 or 4; alternate layout: 2, 3 or 4; dense: 16 or 8
+            self.cfg.value_bits = value_bits  # main layout: 2 or 4; alternate layout: 2, 3 or 4; dense: 16, 8 or 4
         if key_bits is not None:
-            self.cfg.key_bits = key_bits  # main layout: 3, 2 or 4; alternate layout: 8, 5, 4, 2 or 16 (fp16 keys); dense: 16 or 8
+            self.cfg.key_bits = key_bits  # main layout: 3, 2 or 4; alternate layout: 8, 5, 4, 2 or 16 (fp16 keys); dense: 16, 8 or 4
         if key_format is not None:
             self.cfg.key_format = key_format  # alternate layout, 2-bit keys: TQ_KEY_AFFINE (uint2) or TQ_KEY_SIGNED (int2); dense: TQ_ELEM_F16 or TQ_ELEM_BF16
         ptr = C.c_void_p()
@@ -496,9 +502,11 @@ class Context:
         _check(lib.tq_paged_workspace_size(self.ptr, batch, C.byref(n)), "tq_paged_workspace_size")
         return n.value
 
-    def paged_attention(self, q, pool, block_table, lengths, out, workspace, lse=None, window=0, scale=0.0, stream=None):
+    def paged_attention(self, q, pool, block_table, lengths, out, workspace, lse=None, window=0, scale=0.0, stream=None,
+                        cap=0.0, slopes=None):
         """tq_paged_attention: q [batch, Hq, d] of the context's 16-bit type (rows may be strided), out fp32
-        [batch, Hq, d], lse fp32 [batch, Hq] or None; window 0 for all positions, scale 0 for 1 / sqrt(d)."""
+        [batch, Hq, d], lse fp32 [batch, Hq] or None; window 0 for all positions, scale 0 for 1 / sqrt(d).  With cap or
+        slopes (fp32 [Hq]) tq_paged_attention_scored: scores cap * tanh(score / cap) + slope * (position - newest position)."""
         i32, _, f32, u8 = self._types or self._look_up()
         qp, qs = self._rows_of(q, self.num_q_heads, self._elem, "q")
         bsz = q.shape[0]
@@ -506,16 +514,99 @@ class Context:
             raise ValueError("out must be [batch, Hq, d], lengths [batch] and lse [batch, Hq]")
         if not 0 <= window < 2 ** 31:
             raise ValueError("window must be 0 or a count below 2^31")
+        if slopes is not None and slopes.numel() != self.num_q_heads:
+            raise ValueError("slopes must be [Hq]")
         self._check_pool(pool)
         self._check_bt(block_table, bsz)
         a_pool, a_ws = self._addrs(u8, "pool workspace", pool, workspace)
         a_table, a_len = self._addrs(i32, "block_table lengths", block_table, lengths)
-        a_out, a_lse = self._addrs(f32, "out lse", out, lse)
-        st = lib.tq_paged_attention(self.ptr, qp, qs, bsz, a_pool, pool.shape[0], a_table, block_table.shape[1], a_len, window, scale,
-                                    a_out, a_lse, a_ws, workspace.numel(),
-                                    self._raw(self._device) if stream is None else _stream(stream))
+        a_out, a_lse, a_slopes = self._addrs(f32, "out lse slopes", out, lse, slopes)
+        stream = self._raw(self._device) if stream is None else _stream(stream)
+        if cap or slopes is not None:
+            st, name = lib.tq_paged_attention_scored(self.ptr, qp, qs, bsz, a_pool, pool.shape[0], a_table, block_table.shape[1], a_len,
+                                                     window, scale, cap, a_slopes, a_out, a_lse, a_ws, workspace.numel(),
+                                                     stream), "tq_paged_attention_scored"
+        else:
+            st, name = lib.tq_paged_attention(self.ptr, qp, qs, bsz, a_pool, pool.shape[0], a_table, block_table.shape[1], a_len, window,
+                                              scale, a_out, a_lse, a_ws, workspace.numel(), stream), "tq_paged_attention"
         if st:
-            raise TQError(st, "tq_paged_attention")
+            raise TQError(st, name)
+
+    def paged_weights(self, q, pool, block_table, lengths, lse, weights_out, weights=None, decay=1.0, window=0, scale=0.0, cap=0.0,
+                      slopes=None, stream=None):
+        """tq_paged_weights: weights_out = decay * weights + the attention weights of q per cached token and KV head; weights and
+        weights_out fp32 [batch, Hkv, n] (the same tensor, or two; weights None for zeros), lse fp32 [batch, Hq] as
+        paged_attention gives it with the same window, scale, cap and slopes."""
+        i32, _, f32, u8 = self._types or self._look_up()
+        qp, qs = self._rows_of(q, self.num_q_heads, self._elem, "q")
+        bsz = q.shape[0]
+        if lengths.numel() != bsz or lse.shape != q.shape[:2]:
+            raise ValueError("lengths must be [batch] and lse [batch, Hq]")
+        self._check_weights(weights_out, bsz, "weights_out")
+        if weights is not None and weights.shape != weights_out.shape:
+            raise ValueError("weights must be of the shape of weights_out")
+        if not 0 <= window < 2 ** 31:
+            raise ValueError("window must be 0 or a count below 2^31")
+        if slopes is not None and slopes.numel() != self.num_q_heads:
+            raise ValueError("slopes must be [Hq]")
+        self._check_pool(pool)
+        self._check_bt(block_table, bsz)
+        a_pool, = self._addrs(u8, "pool", pool)
+        a_table, a_len = self._addrs(i32, "block_table lengths", block_table, lengths)
+        a_lse, a_in, a_out, a_slopes = self._addrs(f32, "lse weights weights_out slopes", lse, weights, weights_out, slopes)
+        st = lib.tq_paged_weights(self.ptr, qp, qs, bsz, a_pool, pool.shape[0], a_table, block_table.shape[1], a_len, window, scale, cap,
+                                  a_slopes, a_lse, a_in, decay, a_out, weights_out.shape[2],
+                                  self._raw(self._device) if stream is None else _stream(stream))
+        if st:
+            raise TQError(st, "tq_paged_weights")
+
+    def _check_weights(self, t, batch, name):
+        if len(t.shape) != 3 or t.shape[0] != batch or t.shape[1] != self.num_kv_heads:
+            raise ValueError(f"{name} must be [batch, {self.num_kv_heads}, n]")
+
+    def paged_evict(self, weights, pool, block_table, lengths, keep, weights_out, lengths_out, kept, sinks=0, recent=0, stream=None):
+        """tq_paged_evict: the keep[b] tokens with the largest weights (and the newest `recent`, the oldest `sinks`) move to
+        the front of each sequence and KV head, in place; weights, weights_out fp32 and kept int32 [batch, Hkv, n], keep and
+        lengths_out int32 [batch]."""
+        i32, _, f32, u8 = self._types or self._look_up()
+        bsz = lengths.numel()
+        if keep.numel() != bsz or lengths_out.numel() != bsz:
+            raise ValueError("keep and lengths_out must be [batch]")
+        self._check_weights(weights, bsz, "weights")
+        if weights_out.shape != weights.shape or kept.shape != weights.shape:
+            raise ValueError("weights_out and kept must be of the shape of weights")
+        if not (0 <= sinks < 2 ** 31 and 0 <= recent < 2 ** 31):
+            raise ValueError("sinks and recent must be counts below 2^31")
+        self._check_pool(pool)
+        self._check_bt(block_table, bsz)
+        a_pool, = self._addrs(u8, "pool", pool)
+        a_w, a_wo = self._addrs(f32, "weights weights_out", weights, weights_out)
+        a_table, a_len, a_keep, a_lo, a_kept = self._addrs(i32, "block_table lengths keep lengths_out kept", block_table, lengths, keep,
+                                                           lengths_out, kept)
+        st = lib.tq_paged_evict(self.ptr, a_w, weights.shape[2], bsz, a_pool, pool.shape[0], a_table, block_table.shape[1], a_len, a_keep,
+                                sinks, recent, a_wo, a_lo, a_kept, self._raw(self._device) if stream is None else _stream(stream))
+        if st:
+            raise TQError(st, "tq_paged_evict")
+
+    def release_pages(self, lengths, new_lengths, block_table, queue, queue_state, queue_state_out, num_blocks, stream=None):
+        """tq_release_pages: the pages of slots new_lengths .. lengths - 1 that hold nothing else go to the end of the queue of
+        free pages (of plan_pages)."""
+        i32, _, _, _ = self._types or self._look_up()
+        bsz = lengths.numel()
+        if new_lengths.numel() != bsz:
+            raise ValueError("new_lengths must be [batch]")
+        if queue_state.numel() != 2 or queue_state_out.numel() != 2:
+            raise ValueError("queue_state and queue_state_out must be [2]")
+        if not 0 <= num_blocks < 2 ** 31:
+            raise ValueError("num_blocks must be a count below 2^31")
+        self._check_bt(block_table, bsz)
+        a_len, a_new, a_table, a_queue, a_state, a_out = self._addrs(
+            i32, "lengths new_lengths block_table queue queue_state queue_state_out", lengths, new_lengths, block_table, queue,
+            queue_state, queue_state_out)
+        st = lib.tq_release_pages(self.ptr, a_len, a_new, bsz, a_table, block_table.shape[1], num_blocks, a_queue, queue.numel(),
+                                  a_state, a_out, self._raw(self._device) if stream is None else _stream(stream))
+        if st:
+            raise TQError(st, "tq_release_pages")
 
     # -- diagnostics
     def device_errors(self, stream=None) -> int:

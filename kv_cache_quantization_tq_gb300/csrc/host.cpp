@@ -200,7 +200,7 @@ tq_status check_config(const tq_config* c) {
   if (c->page_size != tq::kPage || c->ring_capacity != tq::kRing || c->group_size != tq::kGroup)
     return TQ_ERR_UNSUPPORTED;
   if (c->layout == TQ_LAYOUT_DENSE) {
-    if ((c->key_bits != 16 && c->key_bits != 8) || c->value_bits != c->key_bits || c->qjl_m != 0 ||
+    if ((c->key_bits != 16 && c->key_bits != 8 && c->key_bits != 4) || c->value_bits != c->key_bits || c->qjl_m != 0 ||
         (c->key_format != TQ_ELEM_F16 && c->key_format != TQ_ELEM_BF16))
       return TQ_ERR_UNSUPPORTED;
     return TQ_OK;
@@ -547,11 +547,11 @@ tq_status tq_get_tables(const tq_ctx* ctx, float* centroids, float* boundaries, 
 namespace {
 // main: key_bits key bits, value_bits value bits and one fp16 scale + minimum per group of 32 per
 // coordinate, two fp16 norms; alternate: key_bits-bit key codes + 4 B per block of 32 (or fp16
-// keys alone, key_bits 16), value_bits-bit value indices, fp16 norm; dense: the elements and, with
-// 8 bits, two exponent bytes
+// keys alone, key_bits 16), value_bits-bit value indices, fp16 norm; dense: the elements, with
+// 8 and 4 bits two exponent bytes, with 4 bits a byte per 16 elements
 size_t record_bytes(const tq_config& c) {
   const size_t d = c.head_dim, vb = c.value_bits, kb = c.key_bits;
-  if (c.layout == TQ_LAYOUT_DENSE) return kb == 16 ? 4 * d : 2 * d + 2;
+  if (c.layout == TQ_LAYOUT_DENSE) return kb == 16 ? 4 * d : kb == 8 ? 2 * d + 2 : d + d / 8 + 2;
   return c.layout == TQ_LAYOUT_MAIN ? (kb * d) / 8 + (vb * d) / 8 + d / 8 + 4
                                     : (kb * d) / 8 + (kb == 16 ? 0 : (d / 32) * 4) + (vb * d) / 8 + 2;
 }

@@ -18,6 +18,41 @@ bool on_device(const tq_ctx* ctx) {
 
 bool aligned16(const void* p) { return (((uintptr_t)p) & 15) == 0; }
 
+// Checks that attention and weight sums share, and the arguments they share.
+tq_status paged_args(tq_ctx* ctx, const void* q, int64_t q_stride, int batch, const void* pool, int num_blocks,
+                            const int32_t* block_table, int max_blocks, const int32_t* lengths, int window, float scale,
+                            float cap, const float* slopes, tq::PagedArgs& a, tq::ScoreArgs& sc) {
+  const tq_config& c = ctx->cfg;
+  if (scale == 0.f) scale = (float)(1.0 / sqrt((double)c.head_dim));
+  // far caps would leave scale / cap, or the tanh, without bits
+  if (!isfinite(scale) || !(cap == 0.f || (cap >= 0x1p-60f && cap <= 0x1p60f && isfinite(scale / cap)))) return TQ_ERR_INVALID_ARG;
+  if (batch == 0) return TQ_OK;
+  if (!q || !lengths || (max_blocks > 0 && !block_table) || (num_blocks > 0 && !pool)) return TQ_ERR_INVALID_ARG;
+  if (!aligned16(q) || !aligned16(pool) || (q_stride & 7) || q_stride < (int64_t)c.num_q_heads * c.head_dim)
+    return TQ_ERR_INVALID_ARG;
+  if (max_blocks > INT_MAX / tq::kPage || (int64_t)num_blocks * c.num_kv_heads > INT_MAX) return TQ_ERR_INVALID_ARG;
+  a.q = static_cast<const uint16_t*>(q);
+  a.q_stride = q_stride;
+  a.batch = batch;
+  a.pool = static_cast<const uint8_t*>(pool);
+  a.num_blocks = num_blocks;
+  a.block_table = block_table;
+  a.max_blocks = max_blocks;
+  a.max_len = (int64_t)max_blocks * tq::kPage;
+  a.lengths = lengths;
+  a.window = window;
+  a.scale = scale;
+  a.out = nullptr;
+  a.lse = nullptr;
+  a.hq = c.num_q_heads;
+  a.hkv = c.num_kv_heads;
+  a.n_rep = c.num_q_heads / c.num_kv_heads;
+  a.err = ctx->d_err;
+  sc.cap = cap;
+  sc.slopes = slopes;
+  return TQ_OK;
+}
+
 }  // namespace
 
 namespace tq {
@@ -41,20 +76,44 @@ bool encode_paged_map(const PagedTensorMap& t, CUtensorMap* map) {
   const cuuint32_t box[3] = {(cuuint32_t)(t.row_bytes / t.elem), (cuuint32_t)t.box_rows, 1}, step[3] = {1, 1, 1};
   return encode(map, t.elem == 1 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_UINT16, 3,
                 const_cast<void*>(t.pool), dims, strides, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                t.row_bytes == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+                t.row_bytes == 128  ? CU_TENSOR_MAP_SWIZZLE_128B
+                : t.row_bytes == 64 ? CU_TENSOR_MAP_SWIZZLE_64B
+                                    : CU_TENSOR_MAP_SWIZZLE_NONE,
                 CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 size_t paged_workspace(const tq_ctx* ctx, int batch) {
   const tq_config& c = ctx->cfg;
-  return c.key_bits == 8 ? paged_workspace_e4m3(ctx, batch)
+  return c.key_bits == 4 ? paged_workspace_e2m1(ctx, batch)
+         : c.key_bits == 8 ? paged_workspace_e4m3(ctx, batch)
          : c.key_format == TQ_ELEM_BF16 ? paged_workspace_bf16(ctx, batch) : paged_workspace_f16(ctx, batch);
 }
 
-cudaError_t launch_paged(tq_ctx* ctx, const PagedArgs& a, void* workspace, cudaStream_t s) {
+cudaError_t launch_paged(tq_ctx* ctx, const PagedArgs& a, const ScoreArgs& sc, void* workspace, cudaStream_t s) {
   const tq_config& c = ctx->cfg;
-  return c.key_bits == 8 ? launch_paged_e4m3(ctx, a, workspace, s)
-         : c.key_format == TQ_ELEM_BF16 ? launch_paged_bf16(ctx, a, workspace, s) : launch_paged_f16(ctx, a, workspace, s);
+  const bool bf = c.key_format == TQ_ELEM_BF16;
+  if (sc.cap > 0.f || sc.slopes)
+    return c.key_bits == 4   ? launch_scored_e2m1(ctx, a, sc, workspace, s)
+           : c.key_bits == 8 ? launch_scored_e4m3(ctx, a, sc, workspace, s)
+           : bf              ? launch_scored_bf16(ctx, a, sc, workspace, s)
+                             : launch_scored_f16(ctx, a, sc, workspace, s);
+  return c.key_bits == 4   ? launch_paged_e2m1(ctx, a, workspace, s)
+         : c.key_bits == 8 ? launch_paged_e4m3(ctx, a, workspace, s)
+         : bf              ? launch_paged_bf16(ctx, a, workspace, s)
+                           : launch_paged_f16(ctx, a, workspace, s);
+}
+
+cudaError_t launch_weights(tq_ctx* ctx, const PagedArgs& a, const ScoreArgs& sc, const WeightArgs& w, cudaStream_t s) {
+  const tq_config& c = ctx->cfg;
+  // entries in front of the window are only faded: nothing to do where that changes nothing
+  if (a.window > 0 && !(w.in == w.out && w.decay == 1.f)) {
+    const cudaError_t e = launch_fade(ctx, a, w, s);
+    if (e != cudaSuccess) return e;
+  }
+  return c.key_bits == 4                    ? launch_weights_e2m1(ctx, a, sc, w, s)
+         : c.key_bits == 8                  ? launch_weights_e4m3(ctx, a, sc, w, s)
+         : c.key_format == TQ_ELEM_BF16     ? launch_weights_bf16(ctx, a, sc, w, s)
+                                            : launch_weights_f16(ctx, a, sc, w, s);
 }
 
 }  // namespace tq
@@ -136,42 +195,107 @@ tq_status tq_set_wait_limit(tq_ctx* ctx, uint32_t nanoseconds) {
   return TQ_OK;
 }
 
+tq_status tq_paged_attention_scored(tq_ctx* ctx, const void* q, int64_t q_stride, int batch, const void* pool, int num_blocks,
+                                    const int32_t* block_table, int max_blocks, const int32_t* lengths, int window,
+                                    float scale, float cap, const float* slopes, float* out, float* lse, void* workspace,
+                                    size_t ws_bytes, cudaStream_t stream) {
+  if (!ctx || batch < 0 || num_blocks < 0 || max_blocks < 0 || window < 0) return TQ_ERR_INVALID_ARG;
+  if (ctx->cfg.layout != TQ_LAYOUT_DENSE) return TQ_ERR_UNSUPPORTED;
+  tq::PagedArgs a;
+  tq::ScoreArgs sc;
+  const tq_status st = paged_args(ctx, q, q_stride, batch, pool, num_blocks, block_table, max_blocks, lengths, window, scale, cap,
+                                  slopes, a, sc);
+  if (st != TQ_OK || batch == 0) return st;
+  if (!out || !aligned16(out)) return TQ_ERR_INVALID_ARG;
+  if (!workspace || ws_bytes < tq::paged_workspace(ctx, batch)) return TQ_ERR_WORKSPACE;
+  if (((uintptr_t)workspace) & 255) return TQ_ERR_INVALID_ARG;
+  if (!on_device(ctx)) return TQ_ERR_INVALID_ARG;
+  a.out = out;
+  a.lse = lse;
+  return cuda_status(tq::launch_paged(ctx, a, sc, workspace, stream));
+}
+
 tq_status tq_paged_attention(tq_ctx* ctx, const void* q, int64_t q_stride, int batch, const void* pool, int num_blocks,
                              const int32_t* block_table, int max_blocks, const int32_t* lengths, int window,
                              float scale, float* out, float* lse, void* workspace, size_t ws_bytes,
                              cudaStream_t stream) {
-  if (!ctx || batch < 0 || num_blocks < 0 || max_blocks < 0 || window < 0) return TQ_ERR_INVALID_ARG;
+  return tq_paged_attention_scored(ctx, q, q_stride, batch, pool, num_blocks, block_table, max_blocks, lengths, window, scale, 0.f,
+                                   nullptr, out, lse, workspace, ws_bytes, stream);
+}
+
+tq_status tq_paged_weights(tq_ctx* ctx, const void* q, int64_t q_stride, int batch, const void* pool, int num_blocks,
+                           const int32_t* block_table, int max_blocks, const int32_t* lengths, int window, float scale,
+                           float cap, const float* slopes, const float* lse, const float* weights, float decay,
+                           float* weights_out, int64_t weights_stride, cudaStream_t stream) {
+  if (!ctx || batch < 0 || num_blocks < 0 || max_blocks < 0 || window < 0 || weights_stride < 0) return TQ_ERR_INVALID_ARG;
   if (ctx->cfg.layout != TQ_LAYOUT_DENSE) return TQ_ERR_UNSUPPORTED;
-  if (!isfinite(scale)) return TQ_ERR_INVALID_ARG;
-  if (batch == 0) return TQ_OK;
-  const tq_config& c = ctx->cfg;
-  if (!q || !out || !lengths || (max_blocks > 0 && !block_table) || (num_blocks > 0 && !pool))
-    return TQ_ERR_INVALID_ARG;
-  if (!aligned16(q) || !aligned16(out) || !aligned16(pool) || (q_stride & 7) ||
-      q_stride < (int64_t)c.num_q_heads * c.head_dim)
-    return TQ_ERR_INVALID_ARG;
-  if (max_blocks > INT_MAX / tq::kPage || (int64_t)num_blocks * c.num_kv_heads > INT_MAX) return TQ_ERR_INVALID_ARG;
-  if (!workspace || ws_bytes < tq::paged_workspace(ctx, batch)) return TQ_ERR_WORKSPACE;
-  if (((uintptr_t)workspace) & 255) return TQ_ERR_INVALID_ARG;
-  if (!on_device(ctx)) return TQ_ERR_INVALID_ARG;
+  if (!isfinite(decay)) return TQ_ERR_INVALID_ARG;
   tq::PagedArgs a;
-  a.q = static_cast<const uint16_t*>(q);
-  a.q_stride = q_stride;
+  tq::ScoreArgs sc;
+  const tq_status st = paged_args(ctx, q, q_stride, batch, pool, num_blocks, block_table, max_blocks, lengths, window, scale, cap,
+                                  slopes, a, sc);
+  if (st != TQ_OK || batch == 0) return st;
+  if (!lse || (weights_stride > 0 && !weights_out)) return TQ_ERR_INVALID_ARG;
+  if (!on_device(ctx)) return TQ_ERR_INVALID_ARG;
+  if (a.max_len > weights_stride) a.max_len = weights_stride;
+  const tq::WeightArgs w{lse, weights, weights_out, weights_stride, decay};
+  return cuda_status(tq::launch_weights(ctx, a, sc, w, stream));
+}
+
+tq_status tq_paged_evict(tq_ctx* ctx, const float* weights, int64_t weights_stride, int batch, void* pool, int num_blocks,
+                         const int32_t* block_table, int max_blocks, const int32_t* lengths, const int32_t* keep, int sinks,
+                         int recent, float* weights_out, int32_t* lengths_out, int32_t* kept, cudaStream_t stream) {
+  if (!ctx || batch < 0 || num_blocks < 0 || max_blocks < 0 || sinks < 0 || recent < 0 || weights_stride < 0)
+    return TQ_ERR_INVALID_ARG;
+  if (ctx->cfg.layout != TQ_LAYOUT_DENSE) return TQ_ERR_UNSUPPORTED;
+  if (batch == 0) return TQ_OK;
+  if (!lengths || !keep || !lengths_out || lengths_out == keep || lengths_out == lengths) return TQ_ERR_INVALID_ARG;
+  if ((max_blocks > 0 && !block_table) || (num_blocks > 0 && !pool) || !aligned16(pool)) return TQ_ERR_INVALID_ARG;
+  if (weights_stride > 0 && (!weights || !weights_out || !kept || weights == weights_out)) return TQ_ERR_INVALID_ARG;
+  if (weights_stride > (1 << 30) || max_blocks > INT_MAX / tq::kPage) return TQ_ERR_INVALID_ARG;
+  if ((int64_t)batch * ctx->cfg.num_kv_heads > INT_MAX / 8) return TQ_ERR_INVALID_ARG;  // the grid, in clusters of up to 8
+  if (!on_device(ctx)) return TQ_ERR_INVALID_ARG;
+  tq::EvictArgs a;
+  a.weights = weights;
+  a.stride = weights_stride;
   a.batch = batch;
-  a.pool = static_cast<const uint8_t*>(pool);
+  a.hkv = ctx->cfg.num_kv_heads;
+  a.pool = static_cast<uint8_t*>(pool);
   a.num_blocks = num_blocks;
   a.block_table = block_table;
   a.max_blocks = max_blocks;
   a.lengths = lengths;
-  a.window = window;
-  a.scale = scale == 0.f ? (float)(1.0 / sqrt((double)c.head_dim)) : scale;
-  a.out = out;
-  a.lse = lse;
-  a.hq = c.num_q_heads;
-  a.hkv = c.num_kv_heads;
-  a.n_rep = c.num_q_heads / c.num_kv_heads;
+  a.keep = keep;
+  a.sinks = sinks;
+  a.recent = recent;
+  a.weights_out = weights_out;
+  a.lengths_out = lengths_out;
+  a.kept = kept;
   a.err = ctx->d_err;
-  return cuda_status(tq::launch_paged(ctx, a, workspace, stream));
+  return cuda_status(tq::launch_evict(ctx, a, stream));
+}
+
+tq_status tq_release_pages(tq_ctx* ctx, const int32_t* lengths, const int32_t* new_lengths, int batch,
+                           const int32_t* block_table, int max_blocks, int num_blocks, int32_t* queue, int queue_cap,
+                           const int32_t* queue_state, int32_t* queue_state_out, cudaStream_t stream) {
+  if (!ctx || batch < 0 || max_blocks < 0 || num_blocks < 0 || queue_cap < 0) return TQ_ERR_INVALID_ARG;
+  if (max_blocks > INT_MAX / tq::kPage) return TQ_ERR_INVALID_ARG;
+  if (!queue_state || !queue_state_out || queue_state == queue_state_out || (queue_cap > 0 && !queue)) return TQ_ERR_INVALID_ARG;
+  if (batch > 0 && (!lengths || !new_lengths || (max_blocks > 0 && !block_table))) return TQ_ERR_INVALID_ARG;
+  if (!on_device(ctx)) return TQ_ERR_INVALID_ARG;
+  tq::ReleaseArgs a;
+  a.lengths = lengths;
+  a.new_lengths = new_lengths;
+  a.batch = batch;
+  a.block_table = block_table;
+  a.max_blocks = max_blocks;
+  a.num_blocks = num_blocks;
+  a.queue = queue;
+  a.queue_cap = queue_cap;
+  a.queue_state = queue_state;
+  a.queue_state_out = queue_state_out;
+  a.err = ctx->d_err;
+  return cuda_status(tq::launch_release(ctx, a, stream));
 }
 
 }  // extern "C"

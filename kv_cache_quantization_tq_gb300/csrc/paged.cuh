@@ -51,6 +51,7 @@ struct PagedArgs {
   int num_blocks;
   const int32_t* block_table;
   int max_blocks;
+  int64_t max_len;  // most tokens of a sequence
   const int32_t* lengths;
   int window;
   float scale;
@@ -60,8 +61,52 @@ struct PagedArgs {
   uint32_t* err;
 };
 
+// What happens to scores between the product and the softmax.
+struct ScoreArgs {
+  float cap = 0.f;                // 0: none
+  const float* slopes = nullptr;  // NULL: none
+};
+
+struct WeightArgs {
+  const float* lse;
+  const float* in;  // NULL: zeros
+  float* out;
+  int64_t stride;  // entries per (sequence, KV head)
+  float decay;
+};
+
+struct EvictArgs {
+  const float* weights;
+  int64_t stride;  // entries per (sequence, KV head) of weights, weights_out and kept
+  int batch, hkv;
+  uint8_t* pool;
+  int num_blocks;
+  const int32_t* block_table;
+  int max_blocks;
+  const int32_t* lengths;
+  const int32_t* keep;
+  int sinks, recent;
+  float* weights_out;
+  int32_t* lengths_out;
+  int32_t* kept;
+  uint32_t* err;
+};
+
+struct ReleaseArgs {
+  const int32_t* lengths;
+  const int32_t* new_lengths;
+  int batch;
+  const int32_t* block_table;
+  int max_blocks, num_blocks;
+  int32_t* queue;
+  int queue_cap;
+  const int32_t* queue_state;
+  int32_t* queue_state_out;
+  uint32_t* err;
+};
+
 // The pool as a TMA tensor: rows of `d` elements of `elem` bytes, 32 rows (keys, then values) per tile,
-// `tiles` tiles `tile_bytes` apart; boxes of `box_rows` rows, `row_bytes` wide and swizzled (128 or 64).
+// `tiles` tiles `tile_bytes` apart; boxes of `box_rows` rows, `row_bytes` wide and swizzled (128 or 64) or not (32).
 struct PagedTensorMap {
   const void* pool;
   int elem, d;
@@ -92,14 +137,29 @@ cudaError_t launch_early(void (*kernel)(Params...), dim3 grid, dim3 block, size_
 cudaError_t launch_plan(tq_ctx* ctx, const PlanArgs& a, cudaStream_t s);
 cudaError_t launch_store(tq_ctx* ctx, const StoreArgs& a, cudaStream_t s);
 size_t paged_workspace(const tq_ctx* ctx, int batch);
-cudaError_t launch_paged(tq_ctx* ctx, const PagedArgs& a, void* workspace, cudaStream_t s);
+// sc without cap and slopes: the plain form
+cudaError_t launch_paged(tq_ctx* ctx, const PagedArgs& a, const ScoreArgs& sc, void* workspace, cudaStream_t s);
+cudaError_t launch_weights(tq_ctx* ctx, const PagedArgs& a, const ScoreArgs& sc, const WeightArgs& w, cudaStream_t s);
+cudaError_t launch_fade(tq_ctx* ctx, const PagedArgs& a, const WeightArgs& w, cudaStream_t s);
+cudaError_t launch_evict(tq_ctx* ctx, const EvictArgs& a, cudaStream_t s);
+cudaError_t launch_release(tq_ctx* ctx, const ReleaseArgs& a, cudaStream_t s);
 
-// one translation unit per element type
+// one translation unit per element type and kind of call
 size_t paged_workspace_f16(const tq_ctx* ctx, int batch);
 size_t paged_workspace_bf16(const tq_ctx* ctx, int batch);
 size_t paged_workspace_e4m3(const tq_ctx* ctx, int batch);
+size_t paged_workspace_e2m1(const tq_ctx* ctx, int batch);
 cudaError_t launch_paged_f16(tq_ctx* ctx, const PagedArgs& a, void* workspace, cudaStream_t s);
 cudaError_t launch_paged_bf16(tq_ctx* ctx, const PagedArgs& a, void* workspace, cudaStream_t s);
 cudaError_t launch_paged_e4m3(tq_ctx* ctx, const PagedArgs& a, void* workspace, cudaStream_t s);
+cudaError_t launch_paged_e2m1(tq_ctx* ctx, const PagedArgs& a, void* workspace, cudaStream_t s);
+cudaError_t launch_scored_f16(tq_ctx* ctx, const PagedArgs& a, const ScoreArgs& sc, void* workspace, cudaStream_t s);
+cudaError_t launch_scored_bf16(tq_ctx* ctx, const PagedArgs& a, const ScoreArgs& sc, void* workspace, cudaStream_t s);
+cudaError_t launch_scored_e4m3(tq_ctx* ctx, const PagedArgs& a, const ScoreArgs& sc, void* workspace, cudaStream_t s);
+cudaError_t launch_scored_e2m1(tq_ctx* ctx, const PagedArgs& a, const ScoreArgs& sc, void* workspace, cudaStream_t s);
+cudaError_t launch_weights_f16(tq_ctx* ctx, const PagedArgs& a, const ScoreArgs& sc, const WeightArgs& w, cudaStream_t s);
+cudaError_t launch_weights_bf16(tq_ctx* ctx, const PagedArgs& a, const ScoreArgs& sc, const WeightArgs& w, cudaStream_t s);
+cudaError_t launch_weights_e4m3(tq_ctx* ctx, const PagedArgs& a, const ScoreArgs& sc, const WeightArgs& w, cudaStream_t s);
+cudaError_t launch_weights_e2m1(tq_ctx* ctx, const PagedArgs& a, const ScoreArgs& sc, const WeightArgs& w, cudaStream_t s);
 
 }  // namespace tq

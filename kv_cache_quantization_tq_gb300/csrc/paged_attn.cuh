@@ -57,7 +57,8 @@
 namespace tq {
 namespace {
 
-enum { kF16 = 0, kBF16 = 1, kE4M3 = 2 };
+enum { kF16 = 0, kBF16 = 1, kE4M3 = 2, kE2M1 = 3 };
+enum { kAttend = 0, kScored = 1, kWeights = 2 };  // scored: capped and biased; weights: no values, the weights themselves
 
 constexpr float kLazy = 8.f;                     // the reference is raised when a score passes it by more than this
 constexpr float kDown = 1.f / 256, kUp = 256.f;  // values are summed with weights of at most 1: 2^-kLazy, and back
@@ -66,25 +67,33 @@ constexpr float kNone = -3.402823466e38f;        // m before the first score
 // passes 2^15; it begins at 2^100 and stays within 2^-113 and 2^100
 constexpr int kValueAt = 12, kValueMost = 15, kValueTop = 100, kValueLeast = -113;
 
-template <int KIND, int D, int NT>
+template <int KIND, int D, int NT, int MODE>
 struct PagedCfg {
-  static constexpr int ES = KIND == kE4M3 ? 1 : 2;
-  static constexpr int HALF = kPage * D * ES;  // keys or values of a page
-  static constexpr int PAGE = 2 * HALF;
-  static constexpr int EXP = KIND == kE4M3 ? 32 : 0;
+  static constexpr int ES = KIND == kE4M3 || KIND == kE2M1 ? 1 : 2;  // bytes that TMA counts as one
+  static constexpr int ROW = KIND == kE2M1 ? D / 2 : D * ES;
+  static constexpr int HALF = kPage * ROW;  // keys or values of a page
+  static constexpr bool KEYS = MODE == kWeights;  // keys alone
+  static constexpr int PAGE = (KEYS ? 1 : 2) * HALF;
+  // What stands behind them in a tile: 4-bit pages' scales of the keys, of the values; the exponents of both.  Of that a stage has
+  // EXP bytes, the exponents from AT_EXP on.
+  static constexpr int SCALES = KIND == kE2M1 ? D : 0;
+  static constexpr int TAIL = ES == 1 ? 2 * SCALES + 32 : 0, TILE = 2 * HALF + TAIL;
+  static constexpr int AT_EXP = (KEYS ? 1 : 2) * SCALES;
+  static constexpr int EXP = ES == 1 ? AT_EXP + (KEYS ? 16 : 32) : 0;
   static constexpr int HEADS = 8 * NT;
   static constexpr bool QREG = D * NT <= 128;              // query fragments in registers
   static constexpr int QBYTES = QREG ? 0 : HEADS * D * 2;  // else in shared memory, per warp
   // A cut segment's sums: [HEADS][PITCH] floats (padded against bank conflicts where there is room) for the piece
   // that continues one; the piece that begins one is a warp's last, its stages are free to hold it.
   static constexpr int PITCH = D < 512 && (NT == 1 || D == 64) && !(KIND == kE4M3 && D == 128) ? D + 4 : D;
-  static constexpr int SLOT = HEADS * PITCH * 4 + HEADS * 16 + 32;
+  static constexpr int SUMS = KEYS ? 0 : HEADS * PITCH * 4;
+  static constexpr int SLOT = KEYS ? 0 : SUMS + HEADS * 16 + 32;
   static constexpr bool LENS = D < 512;  // the lengths in shared memory (no room for them at 512)
   static constexpr int LIMIT = 232448 - 1024;  // 227 KB, less the alignment of the stages
   static constexpr int fixed(int nw) { return nw * (SLOT + QBYTES) + nw * 32 * (LENS ? 8 : 4) + nw * 4 + (nw == 16 ? nw * 48 : 0); }
   static constexpr int per(int nw) { return nw * (PAGE + EXP + 16); }
   static constexpr int stages(int nw) { return (LIMIT - fixed(nw)) / per(nw); }
-  static constexpr int MIN_S = (HEADS * PITCH * 4 + PAGE - 1) / PAGE;  // a warp's stages hold its last piece
+  static constexpr int MIN_S = KEYS ? 1 : (SUMS + PAGE - 1) / PAGE;  // a warp's stages hold its last piece
   static constexpr bool fits(int nw, int s) { return stages(nw) >= (s > MIN_S ? s : MIN_S); }
   // Warps per CTA: as many as fit.  Stages: as many whole ones as stay within 96 KB (e4m3) or 128 KB per multiprocessor,
   // which rounds down.  On the way, with up to 8 heads a segment and with 16: 16-bit pages 128 and 128 KB at d = 64, 96
@@ -94,18 +103,18 @@ struct PagedCfg {
   // 8 x 2 (128 KB) 87.0 and 634, 16 x 1 (128 KB) 88.7 and 644.  e4m3 pages of d = 128, 64 ragged sequences: 16 x 1 (64 KB)
   // 173 us, 16 x 2 (128 KB) 181.
   // (e4m3 at d = 64 with 16 query heads has no registers for 16 warps: 16 92.1 us, 12 87.2.)
-  static constexpr int NW = PAGE <= 4096 && QREG && (NT == 1 || KIND != kE4M3) && fits(16, 1) ? 16 : fits(12, 1) ? 12 : fits(8, 1) ? 8 : fits(6, 1) ? 6 : 4;
-  static constexpr int S_WANT = (KIND == kE4M3 ? 96 : 128) * 1024 / (NW * PAGE);
-  static constexpr int S_LEAST = S_WANT > MIN_S ? S_WANT : MIN_S;
+  static constexpr int NW = PAGE <= 4096 && QREG && (NT == 1 || ES == 2) && fits(16, 1) ? 16 : fits(12, 1) ? 12 : fits(8, 1) ? 8 : fits(6, 1) ? 6 : 4;
+  static constexpr int S_WANT = (ES == 1 ? 96 : 128) * 1024 / (NW * PAGE);
+  static constexpr int S_LEAST = S_WANT > 8 ? 8 : S_WANT > MIN_S ? S_WANT : MIN_S;
   static constexpr int S = S_LEAST < stages(NW) ? S_LEAST : stages(NW);
   static_assert(S >= 1 && S <= 8, "one stage per warp fits");
   static constexpr int THREADS = NW * 32;
-  static_assert(HEADS * PITCH * 4 <= S * PAGE, "a warp's stages hold its last piece");
+  static_assert(SUMS <= S * PAGE, "a warp's stages hold its last piece");
   // dynamic shared memory, from a 1024-byte aligned base
   static constexpr int OFF_SLOT = NW * S * PAGE;                    // [NW][HEADS][PITCH]
-  static constexpr int OFF_ML = OFF_SLOT + NW * HEADS * PITCH * 4;  // [2][NW][HEADS] references and totals
-  static constexpr int OFF_REC = OFF_ML + NW * HEADS * 16;          // [2][NW] what the pieces are
-  static constexpr int OFF_Q = OFF_REC + NW * 32;
+  static constexpr int OFF_ML = OFF_SLOT + NW * SUMS;               // [2][NW][HEADS] references and totals
+  static constexpr int OFF_REC = OFF_ML + (KEYS ? 0 : NW * HEADS * 16);  // [2][NW] what the pieces are
+  static constexpr int OFF_Q = OFF_REC + (KEYS ? 0 : NW * 32);
   static constexpr int OFF_EXP = OFF_Q + NW * QBYTES;
   static constexpr int OFF_BAR = OFF_EXP + NW * S * EXP;
   static constexpr int OFF_PRE = OFF_BAR + NW * S * 16;
@@ -116,16 +125,16 @@ struct PagedCfg {
   static constexpr int OFF_WALK = (OFF_LEN + (LENS ? THREADS * 4 : 0) + 15) / 16 * 16;
   static constexpr int SMEM = OFF_WALK + (PARK ? NW * 48 : 0) + 1024;
   static_assert(SMEM <= 232448, "shared memory");
-  static constexpr int SWIZZLE_ROW = D * ES < 128 ? D * ES : 128;  // bytes of a row in one TMA box
-  static constexpr int BOXES = D * ES / SWIZZLE_ROW;               // boxes side by side in a page
+  static constexpr int SWIZZLE_ROW = ROW < 128 ? ROW : 128;  // bytes of a row in one TMA box
+  static constexpr int BOXES = ROW / SWIZZLE_ROW;            // boxes side by side in a page
   // With one stage keys and values are copied apart, so that the next keys come while the values are used (e4m3 at d = 512
   // 68.6 against 79.9 us); with more a page is one copy and one wait (fewer instructions: e4m3 at d = 64 55.9 against 64.9).
-  static constexpr bool APART = S == 1;
+  static constexpr bool APART = S == 1 && !KEYS;
   // The weights' total grows by every page: its rounding is the largest error of a long sequence (16 ragged sequences up
   // to 128K tokens: 1.2e-6 of the result, 4.2e-7 with what is lost kept; the same time).  8-bit pages with 16
   // heads or d = 512 go without (with it 87.5 against 85.6 us at d = 64, 74.1 against 72.9 at 128, 71.9 against 68.6 at 512).
-  static constexpr bool KEEP_LOST = KIND != kE4M3 || (NT == 1 && D < 512);
-  static constexpr int BOX_ROWS = APART ? kPage : 2 * kPage;
+  static constexpr bool KEEP_LOST = ES == 2 || (NT == 1 && D < 512);
+  static constexpr int BOX_ROWS = APART || KEYS ? kPage : 2 * kPage;
   static constexpr int BOX = BOX_ROWS * SWIZZLE_ROW;
 };
 
@@ -150,13 +159,22 @@ struct PagedWork {
   int q_bf16;
   int2* cuts;    // workspace: per segment the first and the last CTA with a piece of it, written by the first
   float* parts;  // workspace: per CTA the piece that comes from the CTA in front, and the one that goes on behind
+  float cap;            // 0: none
+  const float* slopes;  // NULL: none
+  // weights alone
+  int first;  // the launch's first query head of each KV head
+  const float* lse_in;
+  const float* w_in;  // NULL: zeros
+  float* w_out;
+  int64_t w_stride;
+  float decay;
 };
 
 struct Seq {
   int len, lo, first, pages;  // length, first position seen, first page, pages seen
 };
 __device__ __forceinline__ bool length_ok(const PagedArgs& a, int len) {
-  return len >= 0 && len <= (int64_t)a.max_blocks * kPage;
+  return len >= 0 && len <= a.max_len;
 }
 __device__ __forceinline__ Seq seq_of(const PagedArgs& a, int len) {
   Seq s;
@@ -309,6 +327,38 @@ __device__ __forceinline__ uint32_t f16_of_e4m3_high(uint32_t four) {
   asm("{ .reg .b16 lo, hi; mov.b32 {lo, hi}, %1; cvt.rn.f16x2.e4m3x2 %0, hi; }" : "=r"(r) : "r"(four));
   return r;
 }
+// Byte b of a word, two e2m1 codes (low nibble first), as two fp16.
+template <int B>
+__device__ __forceinline__ uint32_t f16_of_e2m1(uint32_t eight) {
+  uint32_t r;
+  if (B == 0) asm("{ .reg .b8 a, b, c, d; mov.b32 {a, b, c, d}, %1; cvt.rn.f16x2.e2m1x2 %0, a; }" : "=r"(r) : "r"(eight));
+  if (B == 1) asm("{ .reg .b8 a, b, c, d; mov.b32 {a, b, c, d}, %1; cvt.rn.f16x2.e2m1x2 %0, b; }" : "=r"(r) : "r"(eight));
+  if (B == 2) asm("{ .reg .b8 a, b, c, d; mov.b32 {a, b, c, d}, %1; cvt.rn.f16x2.e2m1x2 %0, c; }" : "=r"(r) : "r"(eight));
+  if (B == 3) asm("{ .reg .b8 a, b, c, d; mov.b32 {a, b, c, d}, %1; cvt.rn.f16x2.e2m1x2 %0, d; }" : "=r"(r) : "r"(eight));
+  return r;
+}
+__device__ __forceinline__ uint32_t mul_f16x2(uint32_t x, uint32_t y) {
+  uint32_t r;
+  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(x), "r"(y));
+  return r;
+}
+// N words at a shared address, 4 N bytes aligned (16 at most).
+template <int N>
+__device__ __forceinline__ void lds(uint32_t* r, uint32_t addr) {
+  if constexpr (N == 1) asm volatile("ld.shared.b32 %0, [%1];" : "=r"(r[0]) : "r"(addr) : "memory");
+  else if constexpr (N == 2) asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(r[0]), "=r"(r[1]) : "r"(addr) : "memory");
+  else asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
+}
+__device__ __forceinline__ uint32_t lds_u8(uint32_t addr) {
+  uint32_t r;
+  asm volatile("ld.shared.u8 %0, [%1];" : "=r"(r) : "r"(addr) : "memory");
+  return r;
+}
+__device__ __forceinline__ uint32_t lds_u16(uint32_t addr) {
+  uint32_t r;
+  asm volatile("ld.shared.u16 %0, [%1];" : "=r"(r) : "r"(addr) : "memory");
+  return r;
+}
 // 2^e for e in [-126, 127]; 0 for -127.
 __device__ __forceinline__ float power2(int e) { return __int_as_float((e + 127) << 23); }
 
@@ -343,6 +393,17 @@ __device__ __forceinline__ void turn(float& x, float& y) {
 __device__ __forceinline__ void tf32_parts(float x, uint32_t& high, uint32_t& low) {
   high = __float_as_uint(x) & 0xffffe000u;
   low = (__float_as_uint(x - __uint_as_float(high)) + 0x1000u) & 0xffffe000u;
+}
+
+// tanh x.  Below 1/2 in magnitude x + x y P(y), y = x^2, P fitted to (tanh x / x - 1) / y with a relative error of 1.5e-8;
+// above 1 - 2 / (e^2x + 1), where nothing cancels (e^2x may be infinite).  Within 4e-7 of the result (1.3e-7 below 1/2).
+__device__ __forceinline__ float tanh_of(float x) {
+  const float a = fabsf(x), y = x * x;
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(ex2(a * 2.88539008177792681472f) + 1.f));
+  const float far = copysignf(fmaf(-2.f, r, 1.f), x);
+  const float p = fmaf(fmaf(fmaf(0.01724148914f, y, -0.05304549262f), y, 0.13325878978f), y, -0.33333143592f);
+  return a < 0.5f ? fmaf(p * y, x, x) : far;
 }
 
 // ---------------------------------------------------------------- scan and walk over the line
@@ -432,11 +493,11 @@ __device__ __forceinline__ float lse_of(float M, float L) {
 __device__ __forceinline__ float inverse_of(float L) { return L == 0.f ? 0.f : kUp / L; }
 
 // ---------------------------------------------------------------- the kernel
-template <int KIND, int D, int NT>
-__global__ void __launch_bounds__(PagedCfg<KIND, D, NT>::THREADS, 1)
+template <int KIND, int D, int NT, int MODE>
+__global__ void __launch_bounds__(PagedCfg<KIND, D, NT, MODE>::THREADS, 1)
     paged_kernel(const __grid_constant__ CUtensorMap map, const __grid_constant__ PagedWork w) {
-  using C = PagedCfg<KIND, D, NT>;
-  constexpr bool BF = KIND == kBF16, F8 = KIND == kE4M3;
+  using C = PagedCfg<KIND, D, NT, MODE>;
+  constexpr bool BF = KIND == kBF16, F8 = KIND == kE4M3, F4 = KIND == kE2M1, XP = F8 || F4;  // XP: pages with exponents
   constexpr int NW = C::NW, S = C::S, KS = D / 16;
   extern __shared__ uint8_t raw[];
   uint8_t* sm = raw + ((1024 - (sm_addr(raw) & 1023)) & 1023);
@@ -455,7 +516,7 @@ __global__ void __launch_bounds__(PagedCfg<KIND, D, NT>::THREADS, 1)
   asm volatile("griddepcontrol.launch_dependents;");
   if (tid == 0 && a.num_blocks > 0) asm volatile("prefetch.tensormap [%0];" ::"l"(&map) : "memory");
   if (lane < 2 * S) bar_init(bar0 + 8 * lane, 1);
-  if (lane < 2) rec[lane * NW + wid] = make_int4(0, 0, 0, 0);
+  if (!C::KEYS && lane < 2) rec[lane * NW + wid] = make_int4(0, 0, 0, 0);
   asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");
 
@@ -544,7 +605,7 @@ __global__ void __launch_bounds__(PagedCfg<KIND, D, NT>::THREADS, 1)
   auto enter = [&](const Walk& in) {
     in_i = 0;
     next_kvh = kv_head(w.p, in.hg);
-    const int h0 = (in.hg - next_kvh * w.p.groups) * C::HEADS;
+    const int h0 = C::KEYS ? w.first : (in.hg - next_kvh * w.p.groups) * C::HEADS;
     const char* q = reinterpret_cast<const char*>(a.q + in.b * a.q_stride + ((int64_t)next_kvh * a.n_rep + h0) * D);
     for (int off = lane * 128; off < min(C::HEADS, a.n_rep - h0) * D * 2; off += 32 * 128)
       asm volatile("prefetch.global.L1 [%0];" ::"l"(q + off));
@@ -601,8 +662,15 @@ __global__ void __launch_bounds__(PagedCfg<KIND, D, NT>::THREADS, 1)
 #pragma unroll
     for (int j = 0; j < C::BOXES; ++j)
       tma_load(dst + j * C::BOX, &map, j * (C::SWIZZLE_ROW / C::ES), side * kPage, tile, bar);
-    if (F8 && side == 0)
-      bulk_load(exp0 + st * C::EXP, a.pool + (size_t)tile * (C::PAGE + C::EXP) + C::PAGE, C::EXP, bar);
+    if (XP && side == 0) {
+      const uint8_t* tail = a.pool + (size_t)tile * C::TILE + 2 * C::HALF;
+      if (!C::KEYS) {
+        bulk_load(exp0 + st * C::EXP, tail, C::EXP, bar);
+      } else {
+        if (F4) bulk_load(exp0 + st * C::EXP, tail, C::SCALES, bar);
+        bulk_load(exp0 + st * C::EXP + C::AT_EXP, tail + 2 * C::SCALES, 16, bar);
+      }
+    }
   };
   // Before a late lane 0 goes on, the copies that it has on their way come to their end: a phase of each barrier at most is
   // open, the keys' of the stages in `valid`, the values' of those in `values`.  The other lanes started none.
@@ -640,19 +708,33 @@ __global__ void __launch_bounds__(PagedCfg<KIND, D, NT>::THREADS, 1)
   const uint32_t v_off = F8 ? row_off(2 * ((lane & 15) >> 2) + (lane & 1) + (lane & 2) * 4, lane >> 4)
                             : row_off((lane & 7) + (lane >> 4) * 8, (lane >> 3) & 1);
 
+  // 4-bit pages are read without ldmatrix, a lane its own codes: row i of the keys' fragments is token turned(i), so that the
+  // rows that a load instruction takes together lie in different banks
+  auto turned = [](int i) -> int { return (C::ROW >= 128 ? 0x36147250u : C::ROW == 64 ? 0x65742130u : 0x53427160u) >> (4 * i) & 7; };
+  // 16-byte piece c of row r
+  auto piece4 = [&](uint32_t base, int r, int c) -> uint32_t {
+    const int x = C::SWIZZLE_ROW == 128 ? r & 7 : NARROW ? (r >> 1) & 3 : 0;
+    return base + (c >> 3) * C::BOX + r * C::SWIZZLE_ROW + (((c & 7) ^ x) << 4);
+  };
+
   uint32_t qf[C::QREG ? NT : 1][C::QREG ? KS : 1][2];
   uint2* q_sm = reinterpret_cast<uint2*>(sm + C::OFF_Q + wid * C::QBYTES);
   // m: reference of each of the lane's heads; qs: the score's factor.  8-bit pages: qh the part of that factor that
   // comes before the key's exponent, vr the values' reference (o is the sum times it), most what a score's place under
   // m and a value's exponent may come to together before vr is lowered
+  const int tok0 = F4 ? turned(g) : g;  // tokens of the lane's scores: this one and 8 behind it
   float o[KS][NT][4], m[NT][2], l[NT][2], lost[NT][2], qs[NT][2], qh[NT][2], vr[NT][2], most[NT][2];
-  const float log2e_scale = a.scale * 1.44269504088896340736f;
+  // capped scores are cap2 tanh(scale q . k / cap); slope: the bias per position
+  constexpr float kLog2e = 1.44269504088896340736f;
+  const bool capped = MODE != kAttend && w.cap > 0.f;
+  const float log2e_scale = capped ? a.scale / w.cap : a.scale * kLog2e, cap2 = MODE != kAttend ? w.cap * kLog2e : 0.f;
+  float slope[NT][2], lse_hi[NT][2], lse_lo[NT][2];
   int st = 0;
 
   // ================================================================ portions
 #pragma unroll 1
   for (bool more = busy; more; more = out.next(a, w.p, sc)) {
-    const int kvh = kv_head(w.p, out.hg), h0 = (out.hg - kvh * w.p.groups) * C::HEADS;
+    const int kvh = kv_head(w.p, out.hg), h0 = C::KEYS ? w.first : (out.hg - kvh * w.p.groups) * C::HEADS;
     const int nh = min(C::HEADS, a.n_rep - h0);
     const int64_t head0 = (int64_t)kvh * a.n_rep + h0;
     // ---- queries as B fragments: head g, dims 16 ks + 2 t, + 1 and + 8, + 9 (8-bit pages: 4 t .. 4 t + 3,
@@ -664,7 +746,7 @@ __global__ void __launch_bounds__(PagedCfg<KIND, D, NT>::THREADS, 1)
       const uint16_t* qr = a.q + out.b * a.q_stride + (head0 + (h < nh ? h : 0)) * D;
       const uint32_t keep = h < nh ? 0xffffffffu : 0u;
       int e_up = 0;
-      if (F8 && w.q_bf16) {
+      if (XP && w.q_bf16) {
         uint32_t top = 0;
 #pragma unroll 8
         for (int ks = 0; ks < KS; ++ks) {
@@ -684,11 +766,13 @@ __global__ void __launch_bounds__(PagedCfg<KIND, D, NT>::THREADS, 1)
         uint2 x;
         if (F8) {
           x = *reinterpret_cast<const uint2*>(qr + ks * 16 + 4 * t);
+        } else if (F4) {  // a lane's codes of a row are 32 dims in one place (16 at d = 64)
+          x = *reinterpret_cast<const uint2*>(qr + (D == 64 ? 16 * t + 4 * ks : 32 * (t + 4 * (ks >> 3)) + 4 * (ks & 7)));
         } else {
           x.x = *reinterpret_cast<const uint32_t*>(qr + ks * 16 + 2 * t);
           x.y = *reinterpret_cast<const uint32_t*>(qr + ks * 16 + 2 * t + 8);
         }
-        if (F8 && w.q_bf16) {
+        if (XP && w.q_bf16) {
           const __half2 u = __floats2half2_rn(__uint_as_float(x.x << 16) * up, __uint_as_float(x.x & 0xffff0000u) * up);
           const __half2 v = __floats2half2_rn(__uint_as_float(x.y << 16) * up, __uint_as_float(x.y & 0xffff0000u) * up);
           x = make_uint2(*reinterpret_cast<const uint32_t*>(&u), *reinterpret_cast<const uint32_t*>(&v));
@@ -704,12 +788,19 @@ __global__ void __launch_bounds__(PagedCfg<KIND, D, NT>::THREADS, 1)
       }
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        if (F8) {
+        if (XP) {
           const int e = __shfl_sync(kFull, e_up, (2 * t + i) * 4);
           qh[nt][i] = power2(-(e >> 1));
           qs[nt][i] = log2e_scale * power2((e >> 1) - e);
         } else {
           qs[nt][i] = log2e_scale;
+        }
+        const int hi = nt * 8 + 2 * t + i;
+        if (MODE != kAttend) slope[nt][i] = w.slopes && hi < nh ? w.slopes[head0 + hi] * kLog2e : 0.f;
+        if (C::KEYS) {  // in two parts; -inf, of a row without weights, makes them 0
+          const float x = hi < nh ? w.lse_in[(int64_t)out.b * a.hq + head0 + hi] : CUDART_INF_F;
+          lse_hi[nt][i] = x == -CUDART_INF_F ? CUDART_INF_F : x * kLog2e;
+          lse_lo[nt][i] = fabsf(lse_hi[nt][i]) < CUDART_INF_F ? fmaf(x, kLog2e, -lse_hi[nt][i]) : 0.f;
         }
         m[nt][i] = kNone;
         vr[nt][i] = power2(kValueTop);
@@ -731,6 +822,11 @@ __global__ void __launch_bounds__(PagedCfg<KIND, D, NT>::THREADS, 1)
 #pragma unroll 1
     for (int i = 0; i < out.take; ++i, st = st + 1 == S ? 0 : st + 1) {
       const bool here = valid >> st & 1;
+      // the weights' sums so far of tokens tok0 (lanes t = 0) and tok0 + 8 (t = 1)
+      const int pos = (out.s.first + out.p + i) * kPage + tok0;
+      const int64_t at = ((int64_t)out.b * a.hkv + kvh) * w.w_stride + pos + 8 * t;
+      float old = 0.f;
+      if (C::KEYS && t < 2 && pos + 8 * t < out.s.len && w.w_in) old = w.decay * w.w_in[at];
       const uint32_t kb = stage0 + st * C::PAGE, vb = kb + (C::APART ? C::HALF : kPage * C::SWIZZLE_ROW);
       float s[NT][4];
       if (here) {  // with a limit of 0 the first copy is waited for
@@ -740,12 +836,14 @@ __global__ void __launch_bounds__(PagedCfg<KIND, D, NT>::THREADS, 1)
       }
       int ek0 = 0, ek1 = 0, ev0 = 0, ev1 = 0;
       if (here) {
-        if (F8) {  // exponents of tokens g and g + 8, keys and values
-          const uint32_t ea = exp0 + st * C::EXP + g;
+        if (XP) {  // exponents of tokens g and g + 8, keys and values
+          const uint32_t ea = exp0 + st * C::EXP + C::AT_EXP + tok0;
           asm volatile("ld.shared.s8 %0, [%1];" : "=r"(ek0) : "r"(ea) : "memory");
           asm volatile("ld.shared.s8 %0, [%1];" : "=r"(ek1) : "r"(ea + 8) : "memory");
-          asm volatile("ld.shared.s8 %0, [%1];" : "=r"(ev0) : "r"(ea + 16) : "memory");
-          asm volatile("ld.shared.s8 %0, [%1];" : "=r"(ev1) : "r"(ea + 24) : "memory");
+          if (!C::KEYS) {
+            asm volatile("ld.shared.s8 %0, [%1];" : "=r"(ev0) : "r"(ea + 16) : "memory");
+            asm volatile("ld.shared.s8 %0, [%1];" : "=r"(ev1) : "r"(ea + 24) : "memory");
+          }
         }
         float s2[NT][4];
         auto score = [&](int ks, const uint32_t(&af)[4], float(&acc)[NT][4]) {
@@ -771,6 +869,30 @@ __global__ void __launch_bounds__(PagedCfg<KIND, D, NT>::THREADS, 1)
               else score(2 * j + c, af, s);
             }
           }
+        } else if constexpr (F4) {
+          // products of 16 dims: 4 of each lane's codes, an element being code x scale (6 bits, exact in fp16)
+          constexpr int W = D == 64 ? 2 : 4;  // words of a piece
+#pragma unroll
+          for (int i = 0; i < (D + 127) / 128; ++i) {
+            uint32_t r[2][W], sc[2];
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+              const int row = tok0 + 8 * x;
+              const uint32_t sa = exp0 + st * C::EXP + row * (D / 16);
+              lds<W>(r[x], D == 64 ? piece4(kb, row, t >> 1) + (t & 1) * 8 : piece4(kb, row, t + 4 * i));
+              sc[x] = f16_of_e4m3(D == 64 ? lds_u8(sa + t) : lds_u16(sa + 2 * (t + 4 * i)));
+            }
+#pragma unroll
+            for (int k = 0; k < W; ++k) {
+              const uint32_t s0 = __byte_perm(sc[0], 0, k < 2 ? 0x1010 : 0x3232), s1 = __byte_perm(sc[1], 0, k < 2 ? 0x1010 : 0x3232);
+              const uint32_t lo[4] = {mul_f16x2(f16_of_e2m1<0>(r[0][k]), s0), mul_f16x2(f16_of_e2m1<0>(r[1][k]), s1),
+                                      mul_f16x2(f16_of_e2m1<1>(r[0][k]), s0), mul_f16x2(f16_of_e2m1<1>(r[1][k]), s1)};
+              const uint32_t hi[4] = {mul_f16x2(f16_of_e2m1<2>(r[0][k]), s0), mul_f16x2(f16_of_e2m1<2>(r[1][k]), s1),
+                                      mul_f16x2(f16_of_e2m1<3>(r[0][k]), s0), mul_f16x2(f16_of_e2m1<3>(r[1][k]), s1)};
+              score(8 * i + 2 * k, lo, s);
+              score(8 * i + 2 * k + 1, hi, s2);
+            }
+          }
         } else {
 #pragma unroll
           for (int ks = 0; ks < KS; ++ks) {
@@ -792,7 +914,7 @@ __global__ void __launch_bounds__(PagedCfg<KIND, D, NT>::THREADS, 1)
         valid = again ? valid | 1u << st : valid & ~(1u << st);
         if (again && (parity & kLate) == 0 && lane == 0) fetch(st, 0);
       };
-      if (C::APART) next_page();  // the keys are read
+      if (C::APART || C::KEYS) next_page();  // the keys are read
 
       if (here) {
         // ---- weights
@@ -800,7 +922,7 @@ __global__ void __launch_bounds__(PagedCfg<KIND, D, NT>::THREADS, 1)
         const bool whole = rel != cut_first && rel != cut_last;
         const int t_lo = out.s.lo - (out.s.first + rel) * kPage, t_hi = out.s.len - (out.s.first + rel) * kPage;
         auto counts = [&](int tok) { return tok >= t_lo && tok < t_hi; };
-        if (F8) {
+        if (XP) {
           const float f0 = power2(ek0), f1 = power2(ek1);
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt)
@@ -812,8 +934,23 @@ __global__ void __launch_bounds__(PagedCfg<KIND, D, NT>::THREADS, 1)
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
           for (int k = 0; k < 4; ++k) s[nt][k] *= qs[nt][k & 1];
+        if constexpr (MODE != kAttend) {
+          if (capped) {
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+              for (int k = 0; k < 4; ++k) s[nt][k] = cap2 * tanh_of(s[nt][k]);
+          }
+          if (w.slopes) {
+            const float back0 = (float)(pos + 1 - out.s.len), back1 = (float)(pos + 9 - out.s.len);
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+              for (int k = 0; k < 4; ++k) s[nt][k] = fmaf(slope[nt][k & 1], k < 2 ? back0 : back1, s[nt][k]);
+          }
+        }
         if (!whole) {  // rows that do not count are whatever memory held
-          const bool ok0 = counts(g), ok1 = counts(g + 8);
+          const bool ok0 = counts(tok0), ok1 = counts(tok0 + 8);
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -821,6 +958,20 @@ __global__ void __launch_bounds__(PagedCfg<KIND, D, NT>::THREADS, 1)
           ev0 = ok0 ? ev0 : -127;
           ev1 = ok1 ? ev1 : -127;
         }
+        if constexpr (C::KEYS) {
+          float sum[2] = {0.f, 0.f};
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              if (nt * 8 + 2 * t + (k & 1) < nh) sum[k >> 1] += ex2(s[nt][k] - lse_hi[nt][k & 1] - lse_lo[nt][k & 1]);
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {
+            sum[x] += __shfl_xor_sync(kFull, sum[x], 1);
+            sum[x] += __shfl_xor_sync(kFull, sum[x], 2);
+          }
+          old += __any_sync(kFull, (parity & kLate) != 0) ? CUDART_NAN_F : t == 0 ? sum[0] : sum[1];
+        } else {
         const float fe0 = (float)ev0, fe1 = (float)ev1;
         float p[NT][4];
 #pragma unroll
@@ -829,7 +980,7 @@ __global__ void __launch_bounds__(PagedCfg<KIND, D, NT>::THREADS, 1)
           for (int k = 0; k < 4; ++k) {
             p[nt][k] = s[nt][k] - m[nt][k & 1];
             raise |= p[nt][k] > kLazy;
-            if (F8) raise |= p[nt][k] + (k < 2 ? fe0 : fe1) > most[nt][k & 1];
+            if (XP) raise |= p[nt][k] + (k < 2 ? fe0 : fe1) > most[nt][k & 1];
           }
         if (__any_sync(kFull, raise)) {  // all heads' references are set anew: fewer pages come here
 #pragma unroll
@@ -847,7 +998,7 @@ __global__ void __launch_bounds__(PagedCfg<KIND, D, NT>::THREADS, 1)
               p[nt][k] = s[nt][k] - mx;
               p[nt][k + 2] = s[nt][k + 2] - mx;
               float co = c;
-              if (F8) {  // the values' reference follows, and their sum takes what it does not
+              if (XP) {  // the values' reference follows, and their sum takes what it does not
                 float top = fmaxf(fmaxf(p[nt][k] + fe0, p[nt][k + 2] + fe1), -1000.f);
 #pragma unroll
                 for (int x = 4; x < 32; x <<= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, x));
@@ -865,7 +1016,7 @@ __global__ void __launch_bounds__(PagedCfg<KIND, D, NT>::THREADS, 1)
             }
         }
         // what a token's weight at its values has besides: 2^-8, and on 8-bit pages their exponent
-        const float w0 = F8 ? power2(ev0) * kDown : kDown, w1 = F8 ? power2(ev1) * kDown : kDown;
+        const float w0 = XP ? power2(ev0) * kDown : kDown, w1 = XP ? power2(ev1) * kDown : kDown;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
@@ -883,7 +1034,7 @@ __global__ void __launch_bounds__(PagedCfg<KIND, D, NT>::THREADS, 1)
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
             p[nt][k] *= k < 2 ? w0 : w1;
-            if (F8) p[nt][k] *= vr[nt][k & 1];
+            if (XP) p[nt][k] *= vr[nt][k & 1];
           }
         }
         constexpr int PARTS = BF ? 3 : 2;
@@ -909,7 +1060,15 @@ __global__ void __launch_bounds__(PagedCfg<KIND, D, NT>::THREADS, 1)
           vparity ^= 1u << st;
         }
         if (!whole) {
-          // value rows that do not count: a weight of 0 does not remove a NaN
+          // value rows that do not count: a weight of 0 does not remove a NaN (4-bit codes have none, their scales do)
+          if constexpr (F4) {
+#pragma unroll
+            for (int k = 0; k < (D + 127) / 128; ++k) {  // D bytes of scales, 4 a lane
+              const int at = (k * 32 + lane) * 4;
+              if (at < D && !counts(at / (D / 16)))
+                asm volatile("st.shared.b32 [%0], %1;" ::"r"(exp0 + st * C::EXP + D + at), "r"(0) : "memory");
+            }
+          } else {
 #pragma unroll
           for (int k = 0; k < C::HALF / 512; ++k) {
             const uint32_t row = (k * 32 + lane) * 16 / C::SWIZZLE_ROW, col = (k * 32 + lane) * 16 % C::SWIZZLE_ROW;
@@ -917,6 +1076,7 @@ __global__ void __launch_bounds__(PagedCfg<KIND, D, NT>::THREADS, 1)
               asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(vb + row / kPage * C::BOX + row % kPage * C::SWIZZLE_ROW + col),
                            "r"(0)
                            : "memory");
+          }
           }
           asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // before the stage's next copy
           __syncwarp();
@@ -957,6 +1117,43 @@ __global__ void __launch_bounds__(PagedCfg<KIND, D, NT>::THREADS, 1)
               add(2 * j + c, af);
             }
           }
+        } else if constexpr (F4) {
+          // tokens number 2 t, 2 t + 1, 2 t + 8, 2 t + 9 of the fragments, D / 8 dims each; nibbles of two tokens are paired before they
+          // become fp16: one product has dims 2 j (rows g) and 2 j + 1 (rows g + 8) of the lanes' shares
+          constexpr int W = D / 64 < 4 ? D / 64 : 4;  // words of a piece
+          const int ta = turned(2 * t), tb = turned(2 * t + 1);
+          const uint32_t sa = exp0 + st * C::EXP + D;
+#pragma unroll
+          for (int i = 0; i < (D + 255) / 256; ++i) {
+            uint32_t r[4][W];
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+              const int row = (x & 1 ? tb : ta) + (x >> 1) * 8;
+              lds<W>(r[x], W == 4 ? piece4(vb, row, g + 8 * i) : W == 2 ? piece4(vb, row, g >> 1) + (g & 1) * 8 : piece4(vb, row, g >> 2) + (g & 3) * 4);
+            }
+            uint32_t sc[2];
+#pragma unroll
+            for (int k = 0; k < W; ++k) {
+              if (k % 2 == 0) {  // scales of a pair of tokens
+                const int block = W == 4 ? 2 * (g + 8 * i) + k / 2 : W == 2 ? g : g >> 1;
+#pragma unroll
+                for (int x = 0; x < 2; ++x)
+                  sc[x] = f16_of_e4m3(lds_u8(sa + (ta + 8 * x) * (D / 16) + block) | lds_u8(sa + (tb + 8 * x) * (D / 16) + block) << 8);
+              }
+              constexpr uint32_t kLow = 0x0f0f0f0fu;
+              const uint32_t e0 = (r[0][k] & kLow) | (r[1][k] << 4 & ~kLow), o0 = (r[0][k] >> 4 & kLow) | (r[1][k] & ~kLow);
+              const uint32_t e1 = (r[2][k] & kLow) | (r[3][k] << 4 & ~kLow), o1 = (r[2][k] >> 4 & kLow) | (r[3][k] & ~kLow);
+              const int j = 16 * i + 4 * k;
+#define TQ_ADD4(B)                                                                                                     \
+  {                                                                                                                    \
+    const uint32_t af[4] = {mul_f16x2(f16_of_e2m1<B>(e0), sc[0]), mul_f16x2(f16_of_e2m1<B>(o0), sc[0]),                \
+                            mul_f16x2(f16_of_e2m1<B>(e1), sc[1]), mul_f16x2(f16_of_e2m1<B>(o1), sc[1])};               \
+    add(j + B, af);                                                                                                    \
+  }
+              TQ_ADD4(0) TQ_ADD4(1) TQ_ADD4(2) TQ_ADD4(3)
+#undef TQ_ADD4
+            }
+          }
         } else {
 #pragma unroll
           for (int j = 0; j < KS; ++j) {
@@ -965,8 +1162,11 @@ __global__ void __launch_bounds__(PagedCfg<KIND, D, NT>::THREADS, 1)
             add(j, r);
           }
         }
+        }
       }
-      if (C::APART) {
+      if (C::KEYS) {
+        if (t < 2 && pos + 8 * t < out.s.len) w.w_out[at] = old;
+      } else if (C::APART) {
         __syncwarp();
         if (again && (parity & kLate) == 0 && lane == 0) fetch(st, 1);
       } else {
@@ -975,6 +1175,7 @@ __global__ void __launch_bounds__(PagedCfg<KIND, D, NT>::THREADS, 1)
     }
 
     // ================================================================ the portion's result
+    if constexpr (!C::KEYS) {
     const bool dead = __any_sync(kFull, (parity & kLate) != 0);
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
@@ -996,12 +1197,20 @@ __global__ void __launch_bounds__(PagedCfg<KIND, D, NT>::THREADS, 1)
       for (int k = 0; k < 2; ++k) {
         const int h = nt * 8 + 2 * t + k;
         if (h >= nh) continue;
-        float* p = dst + h * pitch + g;  // accumulator rows g and g + 8 of tile j
-        const float f = (all ? inverse_of(l[nt][k]) : 1.f) * (F8 ? power2(-exponent_in(vr[nt][k])) : 1.f);
+        const float f = (all ? inverse_of(l[nt][k]) : 1.f) * (XP ? power2(-exponent_in(vr[nt][k])) : 1.f);
+        if constexpr (F4) {  // dims 2 j and 2 j + 1 of the lane's share of D / 8, or of 32 and 256 behind them 32
+          constexpr int SHARE = D / 8 < 32 ? D / 8 : 32;
+          float* p = dst + h * pitch + g * SHARE;
 #pragma unroll
-        for (int j = 0; j < KS; ++j) {
-          p[16 * j] = o[j][nt][k] * f;
-          p[16 * j + 8] = o[j][nt][k + 2] * f;
+          for (int j = 0; j < KS; ++j)
+            *reinterpret_cast<float2*>(p + 2 * j / SHARE * 8 * SHARE + 2 * j % SHARE) = make_float2(o[j][nt][k] * f, o[j][nt][k + 2] * f);
+        } else {
+          float* p = dst + h * pitch + g;  // accumulator rows g and g + 8 of tile j
+#pragma unroll
+          for (int j = 0; j < KS; ++j) {
+            p[16 * j] = o[j][nt][k] * f;
+            p[16 * j + 8] = o[j][nt][k + 2] * f;
+          }
         }
         if (g == 0) {
           if (!all) ml[(begins * NW + wid) * C::HEADS + h] = make_float2(m[nt][k], l[nt][k]);
@@ -1011,9 +1220,11 @@ __global__ void __launch_bounds__(PagedCfg<KIND, D, NT>::THREADS, 1)
     // sequence, segment, whether it ends here, and where it ends on the line
     if (!all && lane == 0)
       rec[begins * NW + wid] = make_int4(out.b, out.hg, 1 + (out.end == out.span), x_end - out.left - out.at + out.span);
+    }
   }
   if (parity & kLate) flag_error(a.err, TQ_DEVERR_TIMEOUT);
   if (bad_id) flag_error(a.err, TQ_DEVERR_BLOCK_ID);
+  if constexpr (C::KEYS) return;
 
   // ================================================================ the CTA's cut segments
   // A run: the piece that begins a segment (or the first warp's, if it continues one) and the pieces of
@@ -1216,9 +1427,9 @@ __global__ void __launch_bounds__((JOIN == 1 ? kMergeWarps : JOIN) * 32) paged_m
 }
 
 // ---------------------------------------------------------------- host side
-template <int KIND, int D, int NT>
+template <int KIND, int D, int NT, int MODE>
 PagedPlan plan_of(const tq_ctx* ctx) {
-  using C = PagedCfg<KIND, D, NT>;
+  using C = PagedCfg<KIND, D, NT, MODE>;
   PagedPlan p;
   const int n_rep = ctx->cfg.num_q_heads / ctx->cfg.num_kv_heads;
   p.groups = (n_rep + C::HEADS - 1) / C::HEADS;
@@ -1233,26 +1444,21 @@ inline size_t align256(size_t x) { return (x + 255) & ~(size_t)255; }
 // The CTAs' slots, then the segments' cuts.
 template <int KIND, int D, int NT>
 size_t parts_bytes(const PagedPlan& p) {
-  using C = PagedCfg<KIND, D, NT>;
+  using C = PagedCfg<KIND, D, NT, kAttend>;
   return align256((size_t)(p.teams / C::NW) * 2 * C::HEADS * (D + 2) * 4);
 }
 template <int KIND, int D, int NT>
 size_t workspace_of(const tq_ctx* ctx, int batch) {
-  const PagedPlan p = plan_of<KIND, D, NT>(ctx);
+  const PagedPlan p = plan_of<KIND, D, NT, kAttend>(ctx);
   return parts_bytes<KIND, D, NT>(p) + align256((size_t)batch * ctx->cfg.num_kv_heads * p.groups * sizeof(int2));
 }
 
-template <int KIND, int D, int NT>
-cudaError_t launch_one(tq_ctx* ctx, const PagedArgs& a, void* workspace, cudaStream_t s) {
-  using C = PagedCfg<KIND, D, NT>;
-  PagedWork w;
-  w.a = a;
-  w.p = plan_of<KIND, D, NT>(ctx);
-  w.q_bf16 = ctx->cfg.key_format == TQ_ELEM_BF16;
-  w.parts = static_cast<float*>(workspace);
-  w.cuts = reinterpret_cast<int2*>(static_cast<uint8_t*>(workspace) + parts_bytes<KIND, D, NT>(w.p));  // for all CTAs
-  // The longest line these arguments allow: the unit keeps it below 2^31, and a short one gets no more CTAs than
-  // it has use for.
+// The longest line these arguments allow: the unit keeps it below 2^31, and a short one gets no more CTAs than
+// it has use for.  Launches the kernel for w.
+template <int KIND, int D, int NT, int MODE>
+cudaError_t launch_line(tq_ctx* ctx, PagedWork& w, cudaStream_t s) {
+  using C = PagedCfg<KIND, D, NT, MODE>;
+  const PagedArgs& a = w.a;
   const int64_t all = (int64_t)a.batch * a.hkv * w.p.groups;
   int64_t pages = a.max_blocks;
   if (a.window && pages > ((int64_t)a.window + 2 * kPage - 2) / kPage) pages = ((int64_t)a.window + 2 * kPage - 2) / kPage;
@@ -1263,10 +1469,10 @@ cudaError_t launch_one(tq_ctx* ctx, const PagedArgs& a, void* workspace, cudaStr
   w.p.teams = ctas * C::NW;
   CUtensorMap map{};
   if (a.num_blocks > 0) {
-    const PagedTensorMap tm{a.pool, C::ES, D, (int64_t)a.num_blocks * a.hkv, C::PAGE + C::EXP, C::SWIZZLE_ROW, C::BOX_ROWS};
+    const PagedTensorMap tm{a.pool, C::ES, C::ROW / C::ES, (int64_t)a.num_blocks * a.hkv, C::TILE, C::SWIZZLE_ROW, C::BOX_ROWS};
     if (!encode_paged_map(tm, &map)) return cudaErrorInvalidValue;
   }
-  auto kern = paged_kernel<KIND, D, NT>;
+  auto kern = paged_kernel<KIND, D, NT, MODE>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
   if (e != cudaSuccess) return e;
   prof_start(ctx, kProfDecode, s);
@@ -1275,6 +1481,28 @@ cudaError_t launch_one(tq_ctx* ctx, const PagedArgs& a, void* workspace, cudaStr
   if (e != cudaSuccess) return e;
   ctx->launches++;
   ctx->decode_kernel = "paged_kernel";
+  return e;
+}
+
+template <int KIND, int D, int NT, int MODE>
+PagedWork work_of(const tq_ctx* ctx, const PagedArgs& a, const ScoreArgs& sc) {
+  PagedWork w{};
+  w.a = a;
+  w.p = plan_of<KIND, D, NT, MODE>(ctx);
+  w.q_bf16 = ctx->cfg.key_format == TQ_ELEM_BF16;
+  w.cap = sc.cap;
+  w.slopes = sc.slopes;
+  return w;
+}
+
+template <int KIND, int D, int NT, int MODE>
+cudaError_t launch_one(tq_ctx* ctx, const PagedArgs& a, const ScoreArgs& sc, void* workspace, cudaStream_t s) {
+  using C = PagedCfg<KIND, D, NT, MODE>;
+  PagedWork w = work_of<KIND, D, NT, MODE>(ctx, a, sc);
+  w.parts = static_cast<float*>(workspace);
+  w.cuts = reinterpret_cast<int2*>(static_cast<uint8_t*>(workspace) + parts_bytes<KIND, D, NT>(w.p));  // for all CTAs
+  cudaError_t e = launch_line<KIND, D, NT, MODE>(ctx, w, s);
+  if (e != cudaSuccess) return e;
 
   const int segments = a.batch * a.hkv * w.p.groups;
   const bool many = segments >= 4 * ctx->sm_count;
@@ -1292,15 +1520,48 @@ cudaError_t launch_one(tq_ctx* ctx, const PagedArgs& a, void* workspace, cudaStr
   return e;
 }
 
+// A launch for every C::HEADS query heads of a KV head: the first one fades what is there, all add to it.
+template <int KIND, int D, int NT>
+cudaError_t launch_weights_one(tq_ctx* ctx, const PagedArgs& a, const ScoreArgs& sc, const WeightArgs& wa, cudaStream_t s) {
+  using C = PagedCfg<KIND, D, NT, kWeights>;
+  PagedWork w = work_of<KIND, D, NT, kWeights>(ctx, a, sc);
+  const PagedPlan plan = w.p;
+  w.lse_in = wa.lse;
+  w.w_in = wa.in;
+  w.w_out = wa.out;
+  w.w_stride = wa.stride;
+  w.decay = wa.decay;
+  for (w.first = 0; w.first < a.n_rep; w.first += C::HEADS) {
+    w.p = plan;
+    w.p.groups = 1;
+    const cudaError_t e = launch_line<KIND, D, NT, kWeights>(ctx, w, s);
+    if (e != cudaSuccess) return e;
+    w.w_in = wa.out;
+    w.decay = 1.f;
+  }
+  return cudaSuccess;
+}
+
 // Query heads per segment: 8, or 16 when a KV head has more than 8 (d = 512: always 8, for want of registers).
-template <int KIND>
-cudaError_t launch_kind(tq_ctx* ctx, const PagedArgs& a, void* ws, cudaStream_t s) {
+template <int KIND, int MODE>
+cudaError_t launch_kind(tq_ctx* ctx, const PagedArgs& a, const ScoreArgs& sc, void* ws, cudaStream_t s) {
   const bool two = a.n_rep > 8;
   switch (ctx->cfg.head_dim) {
-    case 64: return two ? launch_one<KIND, 64, 2>(ctx, a, ws, s) : launch_one<KIND, 64, 1>(ctx, a, ws, s);
-    case 128: return two ? launch_one<KIND, 128, 2>(ctx, a, ws, s) : launch_one<KIND, 128, 1>(ctx, a, ws, s);
-    case 256: return two ? launch_one<KIND, 256, 2>(ctx, a, ws, s) : launch_one<KIND, 256, 1>(ctx, a, ws, s);
-    case 512: return launch_one<KIND, 512, 1>(ctx, a, ws, s);
+    case 64: return two ? launch_one<KIND, 64, 2, MODE>(ctx, a, sc, ws, s) : launch_one<KIND, 64, 1, MODE>(ctx, a, sc, ws, s);
+    case 128: return two ? launch_one<KIND, 128, 2, MODE>(ctx, a, sc, ws, s) : launch_one<KIND, 128, 1, MODE>(ctx, a, sc, ws, s);
+    case 256: return two ? launch_one<KIND, 256, 2, MODE>(ctx, a, sc, ws, s) : launch_one<KIND, 256, 1, MODE>(ctx, a, sc, ws, s);
+    case 512: return launch_one<KIND, 512, 1, MODE>(ctx, a, sc, ws, s);
+  }
+  return cudaErrorInvalidValue;
+}
+template <int KIND>
+cudaError_t launch_weights_kind(tq_ctx* ctx, const PagedArgs& a, const ScoreArgs& sc, const WeightArgs& w, cudaStream_t s) {
+  const bool two = a.n_rep > 8;
+  switch (ctx->cfg.head_dim) {
+    case 64: return two ? launch_weights_one<KIND, 64, 2>(ctx, a, sc, w, s) : launch_weights_one<KIND, 64, 1>(ctx, a, sc, w, s);
+    case 128: return two ? launch_weights_one<KIND, 128, 2>(ctx, a, sc, w, s) : launch_weights_one<KIND, 128, 1>(ctx, a, sc, w, s);
+    case 256: return two ? launch_weights_one<KIND, 256, 2>(ctx, a, sc, w, s) : launch_weights_one<KIND, 256, 1>(ctx, a, sc, w, s);
+    case 512: return launch_weights_one<KIND, 512, 1>(ctx, a, sc, w, s);
   }
   return cudaErrorInvalidValue;
 }

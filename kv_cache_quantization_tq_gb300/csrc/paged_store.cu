@@ -1,5 +1,5 @@
-// Writing keys and values into dense-layout pages (16-bit copies, or e4m3 codes with one power-of-two
-// exponent per vector).
+// Writing keys and values into dense-layout pages (16-bit copies, e4m3 codes with one power-of-two
+// exponent per vector, or e2m1 codes with an e4m3 scale per 16 elements and such an exponent).
 //
 // What bounds it: memory traffic, each element read once and written once.  A thread moves 32 bytes of a row
 // (16 elements: one 16-byte store of codes); the d / 16 lanes of a row are neighbours, so that a vector's
@@ -12,6 +12,13 @@
 // max|x| = m 2^x, 1 <= m < 2, it is x - 8 for m <= 1.75 and x - 7 otherwise (448 = 1.75 2^8).  A power of two
 // makes x 2^-e exact, so the only rounding is the one to e4m3 (3 fraction bits, relative 2^-4); e4m3 being a
 // floating type, a scale that is no power of two would buy no precision.
+//
+// 4 bits: e2m1 has the magnitudes 0, .5, 1, 1.5, 2, 3, 4, 6, so a scale does count; a thread's 16 elements are one block.
+//   e = min { e : max|x| <= 2688 2^e } (2688 = 6 x 448 = 1.3125 2^11),  s = e4m3(block's max|x| 2^-e / 6),  code = e2m1(x 2^-e / s)
+// The quotient y decides by comparison with the middles m between magnitudes (0.25 .. 5), and must do so as if it were
+// exact.  x has at most 11 bits and m s at most 7, so y = m or |y - m| >= 2^-11 m >= 2^-13; y is formed as x 2^-e (1 / s),
+// which is within 2^-21, and rounded to a multiple of 2^-14 (by adding 768 and taking it away), which moves it by
+// at most 2^-15: an exact m comes out as m, everything else stays on its side.
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>
 
@@ -54,6 +61,26 @@ __device__ __forceinline__ int exponent_of(float top) {
   const int e = (u & 0x7fffffu) <= 0x600000u ? x - 8 : x - 7;
   return max(e, -120);
 }
+__device__ __forceinline__ int exponent4_of(float top) {
+  const uint32_t u = __float_as_uint(top);
+  const int x = (int)(u >> 23) - 127;
+  const int e = (u & 0x7fffffu) <= 0x280000u ? x - 11 : x - 10;
+  return max(e, -120);
+}
+
+// Eight floats as e2m1 codes, the first in the lowest nibble.
+__device__ __forceinline__ uint32_t e2m1_of(const float (&f)[8]) {
+  uint32_t r;
+  asm("{ .reg .b8 a, b, c, d;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 a, %2, %1;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 b, %4, %3;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 c, %6, %5;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 d, %8, %7;\n\t"
+      "mov.b32 %0, {a, b, c, d}; }"
+      : "=r"(r)
+      : "f"(f[0]), "f"(f[1]), "f"(f[2]), "f"(f[3]), "f"(f[4]), "f"(f[5]), "f"(f[6]), "f"(f[7]));
+  return r;
+}
 
 // One thread's share of a row: 16 elements of one vector of one tile.
 struct Share {
@@ -62,7 +89,7 @@ struct Share {
   int at, i;      // row of the tile (token, values behind 16 keys), share of the row
 };
 
-template <int D, bool FP8>
+template <int D, int BITS>
 __device__ __forceinline__ Share share_of(const StoreArgs& a, const Divisor& rows, uint32_t u, bool& bad) {
   constexpr int L = D / 16;  // lanes of a row
   Share p{nullptr, nullptr, 0, 0};
@@ -80,12 +107,12 @@ __device__ __forceinline__ Share share_of(const StoreArgs& a, const Divisor& row
   p.i = u % L;
   p.at = (int)(slot % kPage) + (side ? kPage : 0);
   p.src = reinterpret_cast<const uint4*>((side ? a.v + tok * a.v_stride : a.k + tok * a.k_stride) + h * D + p.i * 16);
-  constexpr size_t tile = FP8 ? 32 * D + 32 : 64 * D;
+  constexpr size_t tile = BITS == 16 ? 64 * D : BITS == 8 ? 32 * D + 32 : 18 * D + 32;
   p.tile = a.pool + ((size_t)(slot / kPage) * a.hkv + h) * tile;
   return p;
 }
 
-template <int D, bool FP8, bool BF, int N>
+template <int D, int BITS, bool BF, int N>
 __global__ void __launch_bounds__(kStoreThreads) store_kernel(const StoreArgs a, const Divisor rows) {
   constexpr int L = D / 16;
   asm volatile("griddepcontrol.launch_dependents;");
@@ -95,7 +122,7 @@ __global__ void __launch_bounds__(kStoreThreads) store_kernel(const StoreArgs a,
   uint4 x[N][2];
 #pragma unroll
   for (int k = 0; k < N; ++k) {
-    p[k] = share_of<D, FP8>(a, rows, (blockIdx.x * N + k) * kStoreThreads + threadIdx.x, bad);
+    p[k] = share_of<D, BITS>(a, rows, (blockIdx.x * N + k) * kStoreThreads + threadIdx.x, bad);
     x[k][0] = x[k][1] = make_uint4(0, 0, 0, 0);
     if (p[k].tile) {
       x[k][0] = p[k].src[0];
@@ -104,7 +131,7 @@ __global__ void __launch_bounds__(kStoreThreads) store_kernel(const StoreArgs a,
   }
 #pragma unroll
   for (int k = 0; k < N; ++k) {
-    if constexpr (!FP8) {
+    if constexpr (BITS == 16) {
       if (p[k].tile) {
         uint4* dst = reinterpret_cast<uint4*>(p[k].tile + (size_t)p[k].at * D * 2) + p[k].i * 2;
         dst[0] = x[k][0];
@@ -114,12 +141,51 @@ __global__ void __launch_bounds__(kStoreThreads) store_kernel(const StoreArgs a,
       const uint32_t w[8] = {x[k][0].x, x[k][0].y, x[k][0].z, x[k][0].w, x[k][1].x, x[k][1].y, x[k][1].z, x[k][1].w};
       // the largest magnitude as 15-bit patterns, two at a time
       uint32_t m = 0;
+      constexpr uint32_t inf = BF ? 0x7f80u : 0x7c00u;
+      auto value = [](uint32_t bits) { return BF ? __uint_as_float(bits << 16) : __half2float(__ushort_as_half((unsigned short)bits)); };
 #pragma unroll
       for (int i = 0; i < 8; ++i) m = __vmaxu2(m, w[i] & 0x7fff7fffu);
+      if constexpr (BITS == 4) {
+        m = max(m & 0xffffu, m >> 16);
+        const uint32_t all = m;  // of the block
+        if (__any_sync(kFull, all >= inf)) {  // rare: an entry that is not finite; without those
+          m = 0;
+#pragma unroll
+          for (int i = 0; i < 8; ++i) m = __vmaxu2(m, finite_bits<BF>(w[i]));
+          m = max(m & 0xffffu, m >> 16);
+        }
+        uint32_t top = m;
+#pragma unroll
+        for (int o = 1; o < L; o <<= 1) top = max(top, __shfl_xor_sync(kFull, top, o));
+        const int e = exponent4_of(value(top));
+        const float down = __int_as_float((127 - e) << 23);
+        // a block with a NaN has the scale NaN and codes 0, one with an infinity the largest scale
+        uint32_t sc = __nv_cvt_float_to_fp8(__fdiv_rn(value(m) * down, 6.f), __NV_SATFINITE, __NV_E4M3);
+        if (all >= inf) sc = all > inf ? 0x7fu : 0x7eu;
+        const float scale = __half2float(__half(__nv_cvt_fp8_to_halfraw((__nv_fp8_storage_t)sc, __NV_E4M3)));
+        const float inverse = scale > 0.f ? __fdividef(1.f, scale) : 0.f;
+        uint32_t c[2];
+#pragma unroll
+        for (int k2 = 0; k2 < 2; ++k2) {
+          float y[8];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const float2 f = pair_of<BF>(w[4 * k2 + i]);
+            y[2 * i] = copysignf(fmaf(f.x * down, inverse, 768.f) - 768.f, f.x);
+            y[2 * i + 1] = copysignf(fmaf(f.y * down, inverse, 768.f) - 768.f, f.y);
+          }
+          c[k2] = all > inf ? 0u : e2m1_of(y);
+        }
+        if (p[k].tile) {
+          reinterpret_cast<uint2*>(p[k].tile + (size_t)p[k].at * (D / 2))[p[k].i] = make_uint2(c[0], c[1]);
+          p[k].tile[16 * D + p[k].at * L + p[k].i] = (uint8_t)sc;
+          if (p[k].i == 0) p[k].tile[18 * D + p[k].at] = (uint8_t)e;
+        }
+        continue;
+      }
 #pragma unroll
       for (int o = 1; o < L; o <<= 1) m = __vmaxu2(m, __shfl_xor_sync(kFull, m, o));
       m = max(m & 0xffffu, m >> 16);
-      constexpr uint32_t inf = BF ? 0x7f80u : 0x7c00u;
       if (__any_sync(kFull, m >= inf)) {  // rare: an entry that is not finite; without those
         m = 0;
 #pragma unroll
@@ -128,7 +194,7 @@ __global__ void __launch_bounds__(kStoreThreads) store_kernel(const StoreArgs a,
         for (int o = 1; o < L; o <<= 1) m = __vmaxu2(m, __shfl_xor_sync(kFull, m, o));
         m = max(m & 0xffffu, m >> 16);
       }
-      const int e = exponent_of(BF ? __uint_as_float(m << 16) : __half2float(__ushort_as_half((unsigned short)m)));
+      const int e = exponent_of(value(m));
       const float down = __int_as_float((127 - e) << 23);
       uint32_t c[4];
 #pragma unroll
@@ -148,22 +214,23 @@ __global__ void __launch_bounds__(kStoreThreads) store_kernel(const StoreArgs a,
   if (bad) flag_error(a.err, TQ_DEVERR_BLOCK_ID);
 }
 
-template <int D, bool FP8, bool BF>
+template <int D, int BITS, bool BF>
 cudaError_t launch_t(const StoreArgs& a, int sm_count, cudaStream_t s) {
   const int64_t units = (int64_t)a.n_tokens * 2 * a.hkv * (D / 16);
   const Divisor rows(2u * a.hkv);
   // two shares a thread once that still leaves every multiprocessor its full number of threads
   const int n = units >= (int64_t)sm_count * 4096 ? 2 : 1;
   const dim3 grid((unsigned)((units + n * kStoreThreads - 1) / (n * kStoreThreads)));
-  return n == 2 ? launch_early(store_kernel<D, FP8, BF, 2>, grid, dim3(kStoreThreads), 0, s, a, rows)
-                : launch_early(store_kernel<D, FP8, BF, 1>, grid, dim3(kStoreThreads), 0, s, a, rows);
+  return n == 2 ? launch_early(store_kernel<D, BITS, BF, 2>, grid, dim3(kStoreThreads), 0, s, a, rows)
+                : launch_early(store_kernel<D, BITS, BF, 1>, grid, dim3(kStoreThreads), 0, s, a, rows);
 }
 
 template <int D>
 cudaError_t launch_d(const tq_config& c, const StoreArgs& a, int sm_count, cudaStream_t s) {
   const bool bf = c.key_format == TQ_ELEM_BF16;
-  if (c.key_bits == 16) return launch_t<D, false, false>(a, sm_count, s);
-  return bf ? launch_t<D, true, true>(a, sm_count, s) : launch_t<D, true, false>(a, sm_count, s);
+  if (c.key_bits == 16) return launch_t<D, 16, false>(a, sm_count, s);
+  if (c.key_bits == 4) return bf ? launch_t<D, 4, true>(a, sm_count, s) : launch_t<D, 4, false>(a, sm_count, s);
+  return bf ? launch_t<D, 8, true>(a, sm_count, s) : launch_t<D, 8, false>(a, sm_count, s);
 }
 
 }  // namespace
