@@ -42,6 +42,10 @@
 // exponent is the size of a token's values, weight and exponent together say what the token is worth in the result: a
 // second reference per head, a power of two, holds the largest of these below 2^15 and, when it is set, at 2^12.  What
 // the parts leave out is 2^-37 of the largest token's share.
+//   Weights alone (kWeights) keep a score's whole error, so there every product of 16 dims leaves the tensor core and is added by
+// fp32 additions, and beside fp16 keys the queries have two parts, of 5 and 6 bits: products of 16 bits lie within what the
+// tensor core keeps of a sum, ones of 22 are cut, all in one direction (1 x 4K tokens of 16 / 4 heads: 1.2e-6 of the
+// result, 5e-7 in parts).
 //   bf16 queries on e4m3 pages are scaled by a power of two per head into fp16's range (exact down to 2^-31 of the
 // head's largest entry); half of its inverse comes before a key's exponent and half behind it, so that large
 // keys with small queries do not overflow on the way.
@@ -82,7 +86,9 @@ struct PagedCfg {
   static constexpr int EXP = ES == 1 ? AT_EXP + (KEYS ? 16 : 32) : 0;
   static constexpr int HEADS = 8 * NT;
   static constexpr bool QREG = D * NT <= 128;              // query fragments in registers
-  static constexpr int QBYTES = QREG ? 0 : HEADS * D * 2;  // else in shared memory, per warp
+  // The weights' scores from fp16 keys: queries in two parts (see the head of the kernel)
+  static constexpr int QPARTS = KEYS && KIND == kF16 ? 2 : 1;
+  static constexpr int QBYTES = QREG ? 0 : QPARTS * HEADS * D * 2;  // else in shared memory, per warp
   // A cut segment's sums: [HEADS][PITCH] floats (padded against bank conflicts where there is room) for the piece
   // that continues one; the piece that begins one is a warp's last, its stages are free to hold it.
   static constexpr int PITCH = D < 512 && (NT == 1 || D == 64) && !(KIND == kE4M3 && D == 128) ? D + 4 : D;
@@ -161,6 +167,7 @@ struct PagedWork {
   float* parts;  // workspace: per CTA the piece that comes from the CTA in front, and the one that goes on behind
   float cap;            // 0: none
   const float* slopes;  // NULL: none
+  float up_hi, up_lo;   // weights alone: scale x log2 e in two parts
   // weights alone
   int first;  // the launch's first query head of each KV head
   const float* lse_in;
@@ -365,6 +372,20 @@ __device__ __forceinline__ float power2(int e) { return __int_as_float((e + 127)
 // The exponent of a positive normal number, as of 2^e (of an infinity 128).
 __device__ __forceinline__ int exponent_in(float x) { return (__float_as_int(x) >> 23) - 127; }
 
+// What a pair of fp16 has beside its first 5 bits, which `two` keeps.  Numbers that have no such part (infinities, NaN, and
+// subnormal ones of so few bits) stay whole.
+__device__ __forceinline__ uint32_t low_part(uint32_t& two) {
+  uint32_t high = two & 0xffc0ffc0u;
+  if ((high & 0x7fffu) == 0 || (two & 0x7c00u) == 0x7c00u) high = (high & 0xffff0000u) | (two & 0xffffu);
+  if ((high & 0x7fff0000u) == 0 || (two & 0x7c000000u) == 0x7c000000u) high = (high & 0xffffu) | (two & 0xffff0000u);
+  uint32_t low;
+  asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(low) : "r"(two), "r"(high));
+  if ((two & 0x7c00u) == 0x7c00u) low &= 0xffff0000u;
+  if ((two & 0x7c000000u) == 0x7c000000u) low &= 0xffffu;
+  two = high;
+  return low;
+}
+
 // 16-bit parts of a pair of fp32 weights: each part rounds what the ones before leave.
 template <bool BF>
 __device__ __forceinline__ uint32_t take_part(float& x, float& y) {
@@ -395,15 +416,16 @@ __device__ __forceinline__ void tf32_parts(float x, uint32_t& high, uint32_t& lo
   low = (__float_as_uint(x - __uint_as_float(high)) + 0x1000u) & 0xffffe000u;
 }
 
-// tanh x.  Below 1/2 in magnitude x + x y P(y), y = x^2, P fitted to (tanh x / x - 1) / y with a relative error of 1.5e-8;
-// above 1 - 2 / (e^2x + 1), where nothing cancels (e^2x may be infinite).  Within 4e-7 of the result (1.3e-7 below 1/2).
+// tanh x.  Below 0.9 in magnitude x + x y P(y), y = x^2, P fitted to (tanh x / x - 1) / y with a relative error of 1.6e-8;
+// above 1 - 2 / (e^2x + 1), where little cancels (e^2x may be infinite).  Within 2.2e-7 of the result (8e-8 below 0.9).
 __device__ __forceinline__ float tanh_of(float x) {
   const float a = fabsf(x), y = x * x;
   float r;
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(ex2(a * 2.88539008177792681472f) + 1.f));
   const float far = copysignf(fmaf(-2.f, r, 1.f), x);
-  const float p = fmaf(fmaf(fmaf(0.01724148914f, y, -0.05304549262f), y, 0.13325878978f), y, -0.33333143592f);
-  return a < 0.5f ? fmaf(p * y, x, x) : far;
+  float p = fmaf(0.00130396f, y, -0.006860055f);
+  p = fmaf(fmaf(fmaf(fmaf(p, y, 0.020904126f), y, -0.05372149f), y, 0.1333036f), y, -0.33333212f);
+  return a < 0.9f ? fmaf(p * y, x, x) : far;
 }
 
 // ---------------------------------------------------------------- scan and walk over the line
@@ -717,7 +739,7 @@ __global__ void __launch_bounds__(PagedCfg<KIND, D, NT, MODE>::THREADS, 1)
     return base + (c >> 3) * C::BOX + r * C::SWIZZLE_ROW + (((c & 7) ^ x) << 4);
   };
 
-  uint32_t qf[C::QREG ? NT : 1][C::QREG ? KS : 1][2];
+  uint32_t qf[C::QREG ? NT : 1][C::QREG ? KS : 1][2], ql[C::QREG && C::QPARTS == 2 ? NT : 1][C::QREG && C::QPARTS == 2 ? KS : 1][2];
   uint2* q_sm = reinterpret_cast<uint2*>(sm + C::OFF_Q + wid * C::QBYTES);
   // m: reference of each of the lane's heads; qs: the score's factor.  8-bit pages: qh the part of that factor that
   // comes before the key's exponent, vr the values' reference (o is the sum times it), most what a score's place under
@@ -725,9 +747,13 @@ __global__ void __launch_bounds__(PagedCfg<KIND, D, NT, MODE>::THREADS, 1)
   const int tok0 = F4 ? turned(g) : g;  // tokens of the lane's scores: this one and 8 behind it
   float o[KS][NT][4], m[NT][2], l[NT][2], lost[NT][2], qs[NT][2], qh[NT][2], vr[NT][2], most[NT][2];
   // capped scores are cap2 tanh(scale q . k / cap); slope: the bias per position
-  constexpr float kLog2e = 1.44269504088896340736f;
-  const bool capped = MODE != kAttend && w.cap > 0.f;
-  const float log2e_scale = capped ? a.scale / w.cap : a.scale * kLog2e, cap2 = MODE != kAttend ? w.cap * kLog2e : 0.f;
+  constexpr float kLog2e = 1.44269504088896340736f, kLog2eLow = 1.92596299e-8f;  // log2 e = kLog2e + kLog2eLow
+  const bool capped = MODE != kAttend && w.cap > 0.f, scored = capped || (MODE != kAttend && w.slopes);
+  // Weights alone are not divided by their own sum, in which a score's error would largely go: there scores are kept in natural
+  // units and the factor to powers of two is applied in two parts, by a multiply-add with the log-sum-exp.
+  const float log2e_scale = capped ? a.scale / w.cap : C::KEYS ? (scored ? a.scale : 1.f) : a.scale * kLog2e;
+  const float cap2 = MODE != kAttend ? (C::KEYS ? w.cap : w.cap * kLog2e) : 0.f;
+  const float up_hi = scored ? kLog2e : w.up_hi, up_lo = scored ? kLog2eLow : w.up_lo;
   float slope[NT][2], lse_hi[NT][2], lse_lo[NT][2];
   int st = 0;
 
@@ -779,6 +805,17 @@ __global__ void __launch_bounds__(PagedCfg<KIND, D, NT, MODE>::THREADS, 1)
         }
         x.x &= keep;
         x.y &= keep;
+        if constexpr (C::QPARTS == 2) {
+          uint2 low;
+          low.x = low_part(x.x);
+          low.y = low_part(x.y);
+          if constexpr (C::QREG) {
+            ql[nt][ks][0] = low.x;
+            ql[nt][ks][1] = low.y;
+          } else {
+            q_sm[((NT + nt) * KS + ks) * 32 + lane] = low;
+          }
+        }
         if constexpr (C::QREG) {
           qf[nt][ks][0] = x.x;
           qf[nt][ks][1] = x.y;
@@ -796,11 +833,11 @@ __global__ void __launch_bounds__(PagedCfg<KIND, D, NT, MODE>::THREADS, 1)
           qs[nt][i] = log2e_scale;
         }
         const int hi = nt * 8 + 2 * t + i;
-        if (MODE != kAttend) slope[nt][i] = w.slopes && hi < nh ? w.slopes[head0 + hi] * kLog2e : 0.f;
+        if (MODE != kAttend) slope[nt][i] = w.slopes && hi < nh ? w.slopes[head0 + hi] * (C::KEYS ? 1.f : kLog2e) : 0.f;
         if (C::KEYS) {  // in two parts; -inf, of a row without weights, makes them 0
           const float x = hi < nh ? w.lse_in[(int64_t)out.b * a.hq + head0 + hi] : CUDART_INF_F;
           lse_hi[nt][i] = x == -CUDART_INF_F ? CUDART_INF_F : x * kLog2e;
-          lse_lo[nt][i] = fabsf(lse_hi[nt][i]) < CUDART_INF_F ? fmaf(x, kLog2e, -lse_hi[nt][i]) : 0.f;
+          lse_lo[nt][i] = fabsf(lse_hi[nt][i]) < CUDART_INF_F ? fmaf(x, kLog2eLow, fmaf(x, kLog2e, -lse_hi[nt][i])) : 0.f;
         }
         m[nt][i] = kNone;
         vr[nt][i] = power2(kValueTop);
@@ -845,15 +882,30 @@ __global__ void __launch_bounds__(PagedCfg<KIND, D, NT, MODE>::THREADS, 1)
             asm volatile("ld.shared.s8 %0, [%1];" : "=r"(ev1) : "r"(ea + 24) : "memory");
           }
         }
-        float s2[NT][4];
+        float s2[NT][4], sl[NT][4];
         auto score = [&](int ks, const uint32_t(&af)[4], float(&acc)[NT][4]) {
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt) {
             uint2 x;
             if constexpr (C::QREG) x = make_uint2(qf[nt][ks][0], qf[nt][ks][1]);
             else x = q_sm[(nt * KS + ks) * 32 + lane];
-            if (ks < 2) mma_first<BF>(acc[nt], af, x.x, x.y);
-            else mma<BF>(acc[nt], af, x.x, x.y);
+            if constexpr (C::QPARTS == 2) {
+              uint2 y;
+              if constexpr (C::QREG) y = make_uint2(ql[nt][ks][0], ql[nt][ks][1]);
+              else y = q_sm[((NT + nt) * KS + ks) * 32 + lane];
+              if (ks == 0) mma_first<BF>(sl[nt], af, y.x, y.y);
+              else mma<BF>(sl[nt], af, y.x, y.y);
+            }
+            if (C::KEYS && ks >= 2) {  // the tensor core cuts what it adds up
+              float one[4];
+              mma_first<BF>(one, af, x.x, x.y);
+#pragma unroll
+              for (int k = 0; k < 4; ++k) acc[nt][k] += one[k];
+            } else if (ks < 2) {
+              mma_first<BF>(acc[nt], af, x.x, x.y);
+            } else {
+              mma<BF>(acc[nt], af, x.x, x.y);
+            }
           }
         };
         if constexpr (F8) {
@@ -905,7 +957,11 @@ __global__ void __launch_bounds__(PagedCfg<KIND, D, NT, MODE>::THREADS, 1)
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-          for (int k = 0; k < 4; ++k) s[nt][k] += s2[nt][k];
+          for (int k = 0; k < 4; ++k) {
+            s[nt][k] += s2[nt][k];
+            // an infinite key times a part that is 0 is no number, and the first part has said what it is
+            if (C::QPARTS == 2) s[nt][k] = fabsf(s[nt][k]) < CUDART_INF_F ? s[nt][k] + sl[nt][k] : s[nt][k];
+          }
       }
       bool again = false;
       auto next_page = [&]() {
@@ -964,7 +1020,10 @@ __global__ void __launch_bounds__(PagedCfg<KIND, D, NT, MODE>::THREADS, 1)
           for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
             for (int k = 0; k < 4; ++k)
-              if (nt * 8 + 2 * t + (k & 1) < nh) sum[k >> 1] += ex2(s[nt][k] - lse_hi[nt][k & 1] - lse_lo[nt][k & 1]);
+              if (nt * 8 + 2 * t + (k & 1) < nh) {
+                const float z = s[nt][k], y = fmaf(z, up_hi, -lse_hi[nt][k & 1]);
+                sum[k >> 1] += ex2(fabsf(z) < CUDART_INF_F ? fmaf(z, up_lo, y) - lse_lo[nt][k & 1] : y);
+              }
 #pragma unroll
           for (int x = 0; x < 2; ++x) {
             sum[x] += __shfl_xor_sync(kFull, sum[x], 1);
@@ -1526,6 +1585,9 @@ cudaError_t launch_weights_one(tq_ctx* ctx, const PagedArgs& a, const ScoreArgs&
   using C = PagedCfg<KIND, D, NT, kWeights>;
   PagedWork w = work_of<KIND, D, NT, kWeights>(ctx, a, sc);
   const PagedPlan plan = w.p;
+  const double up = a.scale * 1.4426950408889634074;
+  w.up_hi = (float)up;
+  w.up_lo = (float)(up - w.up_hi);
   w.lse_in = wa.lse;
   w.w_in = wa.in;
   w.w_out = wa.out;
