@@ -71,24 +71,28 @@ constexpr float kNone = -3.402823466e38f;        // m before the first score
 // passes 2^15; it begins at 2^100 and stays within 2^-113 and 2^100
 constexpr int kValueAt = 12, kValueMost = 15, kValueTop = 100, kValueLeast = -113;
 
-template <int KIND, int D, int NT, int MODE>
+// N8: groups of 8 query heads of a segment (the columns of a product); 0: 4 heads, whose weights' parts share the columns.
+template <int KIND, int D, int N8, int MODE>
 struct PagedCfg {
+  static constexpr int NT = N8 > 0 ? N8 : 1;
   static constexpr int ES = KIND == kE4M3 || KIND == kE2M1 ? 1 : 2;  // bytes that TMA counts as one
   static constexpr int ROW = KIND == kE2M1 ? D / 2 : D * ES;
   static constexpr int HALF = kPage * ROW;  // keys or values of a page
   static constexpr bool KEYS = MODE == kWeights;  // keys alone
-  static constexpr int PAGE = (KEYS ? 1 : 2) * HALF;
+  static constexpr bool OWN = KEYS || KIND == kE2M1;       // every lane copies for itself, without TMA
+  static constexpr int PP = OWN && D <= 128 ? 2 : 1;       // pages of a step
+  static constexpr int PAGE1 = (KEYS ? 1 : 2) * HALF, PAGE = PP * PAGE1;  // bytes of one in a stage, and of a stage
   // What stands behind them in a tile: 4-bit pages' scales of the keys, of the values; the exponents of both.  Of that a stage has
-  // EXP bytes, the exponents from AT_EXP on.
+  // EXP1 bytes of each page, the exponents from AT_EXP on.
   static constexpr int SCALES = KIND == kE2M1 ? D : 0;
   static constexpr int TAIL = ES == 1 ? 2 * SCALES + 32 : 0, TILE = 2 * HALF + TAIL;
   static constexpr int AT_EXP = (KEYS ? 1 : 2) * SCALES;
-  static constexpr int EXP = ES == 1 ? AT_EXP + (KEYS ? 16 : 32) : 0;
-  static constexpr int HEADS = 8 * NT;
+  static constexpr int EXP1 = ES == 1 ? AT_EXP + (KEYS ? 16 : 32) : 0, EXP = PP * EXP1;
+  static constexpr int HEADS = N8 > 0 ? 8 * N8 : 4;
   static constexpr bool QREG = D * NT <= 128;              // query fragments in registers
   // The weights' scores from fp16 keys: queries in two parts (see the head of the kernel)
   static constexpr int QPARTS = KEYS && KIND == kF16 ? 2 : 1;
-  static constexpr int QBYTES = QREG ? 0 : QPARTS * HEADS * D * 2;  // else in shared memory, per warp
+  static constexpr int QBYTES = QREG ? 0 : QPARTS * 8 * NT * D * 2;  // else in shared memory, per warp
   // A cut segment's sums: [HEADS][PITCH] floats (padded against bank conflicts where there is room) for the piece
   // that continues one; the piece that begins one is a warp's last, its stages are free to hold it.
   static constexpr int PITCH = D < 512 && (NT == 1 || D == 64) && !(KIND == kE4M3 && D == 128) ? D + 4 : D;
@@ -109,7 +113,7 @@ struct PagedCfg {
   // 8 x 2 (128 KB) 87.0 and 634, 16 x 1 (128 KB) 88.7 and 644.  e4m3 pages of d = 128, 64 ragged sequences: 16 x 1 (64 KB)
   // 173 us, 16 x 2 (128 KB) 181.
   // (e4m3 at d = 64 with 16 query heads has no registers for 16 warps: 16 92.1 us, 12 87.2.)
-  static constexpr int NW = PAGE <= 4096 && QREG && (NT == 1 || ES == 2) && fits(16, 1) ? 16 : fits(12, 1) ? 12 : fits(8, 1) ? 8 : fits(6, 1) ? 6 : 4;
+  static constexpr int NW = PAGE1 <= 4096 && QREG && (KEYS || KIND != kE2M1) && (NT == 1 || ES == 2) && fits(16, 1) ? 16 : fits(12, 1) ? 12 : fits(8, 1) ? 8 : fits(6, 1) ? 6 : 4;
   static constexpr int S_WANT = (ES == 1 ? 96 : 128) * 1024 / (NW * PAGE);
   static constexpr int S_LEAST = S_WANT > 8 ? 8 : S_WANT > MIN_S ? S_WANT : MIN_S;
   static constexpr int S = S_LEAST < stages(NW) ? S_LEAST : stages(NW);
@@ -135,7 +139,7 @@ struct PagedCfg {
   static constexpr int BOXES = ROW / SWIZZLE_ROW;            // boxes side by side in a page
   // With one stage keys and values are copied apart, so that the next keys come while the values are used (e4m3 at d = 512
   // 68.6 against 79.9 us); with more a page is one copy and one wait (fewer instructions: e4m3 at d = 64 55.9 against 64.9).
-  static constexpr bool APART = S == 1 && !KEYS;
+  static constexpr bool APART = S == 1 && !OWN;
   // The weights' total grows by every page: its rounding is the largest error of a long sequence (16 ragged sequences up
   // to 128K tokens: 1.2e-6 of the result, 4.2e-7 with what is lost kept; the same time).  8-bit pages with 16
   // heads or d = 512 go without (with it 87.5 against 85.6 us at d = 64, 74.1 against 72.9 at 128, 71.9 against 68.6 at 512).
@@ -248,6 +252,9 @@ __device__ __forceinline__ void tma_load(uint32_t dst, const CUtensorMap* map, i
       "l"(map), "r"(x), "r"(y), "r"(z), "r"(bar)
       : "memory");
 }
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
 __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
   asm volatile("cp.async.bulk.shared::cta.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
                "l"(src), "r"(bytes), "r"(bar)
@@ -348,6 +355,14 @@ __device__ __forceinline__ uint32_t mul_f16x2(uint32_t x, uint32_t y) {
   uint32_t r;
   asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(x), "r"(y));
   return r;
+}
+// A fragment of values: byte B of two tokens' paired codes, even and odd dims, of 8 tokens and 8 behind them.
+template <int B>
+__device__ __forceinline__ void elements4(uint32_t (&af)[4], const uint32_t (&even)[2], const uint32_t (&odd)[2], const uint32_t (&scale)[2]) {
+  af[0] = mul_f16x2(f16_of_e2m1<B>(even[0]), scale[0]);
+  af[1] = mul_f16x2(f16_of_e2m1<B>(odd[0]), scale[0]);
+  af[2] = mul_f16x2(f16_of_e2m1<B>(even[1]), scale[1]);
+  af[3] = mul_f16x2(f16_of_e2m1<B>(odd[1]), scale[1]);
 }
 // N words at a shared address, 4 N bytes aligned (16 at most).
 template <int N>
@@ -515,12 +530,13 @@ __device__ __forceinline__ float lse_of(float M, float L) {
 __device__ __forceinline__ float inverse_of(float L) { return L == 0.f ? 0.f : kUp / L; }
 
 // ---------------------------------------------------------------- the kernel
-template <int KIND, int D, int NT, int MODE>
-__global__ void __launch_bounds__(PagedCfg<KIND, D, NT, MODE>::THREADS, 1)
+template <int KIND, int D, int N8, int MODE>
+__global__ void __launch_bounds__(PagedCfg<KIND, D, N8, MODE>::THREADS, 1)
     paged_kernel(const __grid_constant__ CUtensorMap map, const __grid_constant__ PagedWork w) {
-  using C = PagedCfg<KIND, D, NT, MODE>;
+  using C = PagedCfg<KIND, D, N8, MODE>;
   constexpr bool BF = KIND == kBF16, F8 = KIND == kE4M3, F4 = KIND == kE2M1, XP = F8 || F4;  // XP: pages with exponents
-  constexpr int NW = C::NW, S = C::S, KS = D / 16;
+  constexpr int NW = C::NW, S = C::S, KS = D / 16, NT = C::NT, PP = C::PP;
+  constexpr bool QUAD = N8 == 0;
   extern __shared__ uint8_t raw[];
   uint8_t* sm = raw + ((1024 - (sm_addr(raw) & 1023)) & 1023);
   unsigned* pre = reinterpret_cast<unsigned*>(sm + C::OFF_PRE);
@@ -536,8 +552,8 @@ __global__ void __launch_bounds__(PagedCfg<KIND, D, NT, MODE>::THREADS, 1)
 
   // what needs no input of the stream comes before the wait for the kernel in front
   asm volatile("griddepcontrol.launch_dependents;");
-  if (tid == 0 && a.num_blocks > 0) asm volatile("prefetch.tensormap [%0];" ::"l"(&map) : "memory");
-  if (lane < 2 * S) bar_init(bar0 + 8 * lane, 1);
+  if (!C::OWN && tid == 0 && a.num_blocks > 0) asm volatile("prefetch.tensormap [%0];" ::"l"(&map) : "memory");
+  if (!C::OWN && lane < 2 * S) bar_init(bar0 + 8 * lane, 1);
   if (!C::KEYS && lane < 2) rec[lane * NW + wid] = make_int4(0, 0, 0, 0);
   asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -616,9 +632,9 @@ __global__ void __launch_bounds__(PagedCfg<KIND, D, NT, MODE>::THREADS, 1)
   // Block ids are looked up by batches of up to 32 pages (one per lane), a batch ahead, and the queries of a new
   // portion are brought to L1 then: with every stage in flight a load waits its turn for microseconds.
   int in_i = 0, next_n = 0, next_id = -1, next_kvh = 0;
-  int cur_i = 0, cur_n = 0, tiles = -1, tile = -1;
+  int cur_i = 0, cur_n = 0, tiles = -1, tile = -1, tile2 = -1;
   bool in_done = !busy;
-  uint32_t valid = 0, parity = 0, vparity = 0;  // bit per stage: a page is there or on its way; phases of the barriers
+  uint32_t valid = 0, parity = 0, vparity = 0;  // bit per stage: a page is there or on its way (OWN: two bits); phases of the barriers
   bool bad_id = false;
   // A lane whose wait runs out is late (kLate in `parity`): it waits for nothing more, and lane 0 then starts no more
   // copies, but it goes on with the warp, which computes with whatever the stages hold: lanes near the limit can differ,
@@ -662,7 +678,8 @@ __global__ void __launch_bounds__(PagedCfg<KIND, D, NT, MODE>::THREADS, 1)
     enter(out);
     load_batch();
   }
-  // Step to the next page of this warp: its tile in `tile` (-1: a bad id); false when there is none.
+  // Step to the next page of this warp: its tile in `tile` (-1: a bad id); false when there is none.  In steps of two pages
+  // `tile2` is the second one's, -1 also where the portion has no second (batches of 32 begin with a first one).
   auto fetch_next = [&]() -> bool {
     if (cur_i == cur_n) {
       if (next_n == 0) return false;
@@ -675,8 +692,13 @@ __global__ void __launch_bounds__(PagedCfg<KIND, D, NT, MODE>::THREADS, 1)
     }
     tile = __shfl_sync(kFull, tiles, cur_i);
     ++cur_i;
+    if constexpr (C::PP == 2) {
+      tile2 = -1;
+      if (cur_i < cur_n) tile2 = __shfl_sync(kFull, tiles, cur_i++);
+    }
     return true;
   };
+  auto there = [&]() -> uint32_t { return (tile >= 0) + 2 * (tile2 >= 0); };
   // Lane 0 starts the copies of a page's keys (side 0) or values (1), or of the whole page (side 0).
   auto fetch = [&](int st, int side) {
     const uint32_t bar = bar0 + 16 * st + 8 * side, dst = stage0 + st * C::PAGE + side * C::HALF;
@@ -684,15 +706,39 @@ __global__ void __launch_bounds__(PagedCfg<KIND, D, NT, MODE>::THREADS, 1)
 #pragma unroll
     for (int j = 0; j < C::BOXES; ++j)
       tma_load(dst + j * C::BOX, &map, j * (C::SWIZZLE_ROW / C::ES), side * kPage, tile, bar);
-    if (XP && side == 0) {
-      const uint8_t* tail = a.pool + (size_t)tile * C::TILE + 2 * C::HALF;
-      if (!C::KEYS) {
-        bulk_load(exp0 + st * C::EXP, tail, C::EXP, bar);
-      } else {
-        if (F4) bulk_load(exp0 + st * C::EXP, tail, C::SCALES, bar);
-        bulk_load(exp0 + st * C::EXP + C::AT_EXP, tail + 2 * C::SCALES, 16, bar);
+    if (F8 && side == 0)
+      bulk_load(exp0 + st * C::EXP, a.pool + (size_t)tile * C::TILE + C::PAGE, C::EXP, bar);
+  };
+  // OWN: every lane copies its 16-byte pieces, swizzled as TMA would (rows of more than 128 bytes: keys alone
+  // as boxes side by side, 4-bit pages row by row).
+  auto fetch_own = [&](int st) {
+#pragma unroll
+    for (int pg = 0; pg < C::PP; ++pg) {
+      const int which = pg ? tile2 : tile;
+      if (which >= 0) {
+        const uint8_t* src = a.pool + (size_t)which * C::TILE + lane * 16;
+        const uint32_t dst = stage0 + st * C::PAGE + pg * C::PAGE1, tail = exp0 + st * C::EXP + pg * C::EXP1 + lane * 16;
+        constexpr int PR = C::ROW / 16, RS = PR < 32 ? 32 / PR : 1;  // pieces of a row, rows of a warp's copy
+#pragma unroll
+        for (int i = 0; i < C::PAGE1 / 512; ++i) {
+          const int row = PR <= 32 ? i * RS + lane / (PR <= 32 ? PR : 1) : i / (PR / 32);
+          const int c = PR <= 32 ? lane % PR : i % (PR / 32) * 32 + lane;
+          const int x = C::SWIZZLE_ROW == 128 ? row & 7 : C::SWIZZLE_ROW == 64 ? (row >> 1) & 3 : 0;
+          const int at = C::KEYS && !F4 ? (c >> 3) * C::BOX + row * C::SWIZZLE_ROW : row * C::ROW + (c >> 3) * 128;
+          copy16(dst + at + (((c & 7) ^ x) << 4), src + i * 512);
+        }
+        if constexpr (XP && !C::KEYS) {
+#pragma unroll
+          for (int i = 0; i < (C::EXP1 + 511) / 512; ++i)
+            if (i * 512 + lane * 16 < C::EXP1) copy16(tail + i * 512, src + 2 * C::HALF + i * 512);
+        }
+        if constexpr (F4 && C::KEYS)
+          if (lane * 16 < C::SCALES) copy16(tail, src + 2 * C::HALF);
+        if constexpr (XP && C::KEYS)
+          if (lane == 0) copy16(tail + C::AT_EXP, src + 2 * C::HALF + 2 * C::SCALES);
       }
     }
+    asm volatile("cp.async.commit_group;" ::: "memory");
   };
   // Before a late lane 0 goes on, the copies that it has on their way come to their end: a phase of each barrier at most is
   // open, the keys' of the stages in `valid`, the values' of those in `values`.  The other lanes started none.
@@ -705,14 +751,21 @@ __global__ void __launch_bounds__(PagedCfg<KIND, D, NT, MODE>::THREADS, 1)
     }
   };
 #pragma unroll 1
-  for (int st = 0; st < S; ++st)
-    if (fetch_next() && tile >= 0) {
-      valid |= 1u << st;
-      if (lane == 0) {
-        fetch(st, 0);
-        if (C::APART) fetch(st, 1);
+  for (int st = 0; st < S; ++st) {
+    if constexpr (!C::OWN) {
+      if (fetch_next() && tile >= 0) {
+        valid |= 1u << st;
+        if (lane == 0) {
+          fetch(st, 0);
+          if (C::APART) fetch(st, 1);
+        }
       }
+    } else {
+      if (!fetch_next()) tile = tile2 = -1;
+      valid |= there() << 2 * st;
+      fetch_own(st);
     }
+  }
 
   // ---- per-lane offsets of the ldmatrix rows (see the swizzle: 16-byte piece c of row r sits at c ^ (r & 7),
   // or c ^ ((r >> 1) & 3) in 64-byte rows)
@@ -736,7 +789,7 @@ __global__ void __launch_bounds__(PagedCfg<KIND, D, NT, MODE>::THREADS, 1)
   // 16-byte piece c of row r
   auto piece4 = [&](uint32_t base, int r, int c) -> uint32_t {
     const int x = C::SWIZZLE_ROW == 128 ? r & 7 : NARROW ? (r >> 1) & 3 : 0;
-    return base + (c >> 3) * C::BOX + r * C::SWIZZLE_ROW + (((c & 7) ^ x) << 4);
+    return base + r * C::ROW + (c >> 3) * 128 + (((c & 7) ^ x) << 4);
   };
 
   uint32_t qf[C::QREG ? NT : 1][C::QREG ? KS : 1][2], ql[C::QREG && C::QPARTS == 2 ? NT : 1][C::QREG && C::QPARTS == 2 ? KS : 1][2];
@@ -757,6 +810,91 @@ __global__ void __launch_bounds__(PagedCfg<KIND, D, NT, MODE>::THREADS, 1)
   float slope[NT][2], lse_hi[NT][2], lse_lo[NT][2];
   int st = 0;
 
+  // Scores of the 16 tokens of a page as the tensor core gives them: rows tok0 and tok0 + 8, heads 2 t and 2 t + 1.  kb: the keys
+  // in shared memory, tail: the scales of 4-bit pages.
+  auto scores = [&](uint32_t kb, uint32_t tail, float(&s)[NT][4]) {
+    float s2[NT][4], sl[NT][4];
+    auto score = [&](int ks, const uint32_t(&af)[4], float(&acc)[NT][4]) {
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        uint2 x;
+        if constexpr (C::QREG) x = make_uint2(qf[nt][ks][0], qf[nt][ks][1]);
+        else x = q_sm[(nt * KS + ks) * 32 + lane];
+        if constexpr (C::QPARTS == 2) {
+          uint2 y;
+          if constexpr (C::QREG) y = make_uint2(ql[nt][ks][0], ql[nt][ks][1]);
+          else y = q_sm[((NT + nt) * KS + ks) * 32 + lane];
+          if (ks == 0) mma_first<BF>(sl[nt], af, y.x, y.y);
+          else mma<BF>(sl[nt], af, y.x, y.y);
+        }
+        if (C::KEYS && C::ES == 2 && ks >= 2) {  // the tensor core cuts what it adds up
+          float one[4];
+          mma_first<BF>(one, af, x.x, x.y);
+#pragma unroll
+          for (int k = 0; k < 4; ++k) acc[nt][k] += one[k];
+        } else if (ks < 2) {
+          mma_first<BF>(acc[nt], af, x.x, x.y);
+        } else {
+          mma<BF>(acc[nt], af, x.x, x.y);
+        }
+      }
+    };
+    if constexpr (F8) {
+#pragma unroll
+      for (int j = 0; j < KS / 2; ++j) {
+        uint32_t r[4];
+        ldsm4(r, piece(kb, k_off, j));
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          const uint32_t af[4] = {f16_of_e4m3(r[2 * c]), f16_of_e4m3(r[2 * c + 1]), f16_of_e4m3_high(r[2 * c]),
+                                  f16_of_e4m3_high(r[2 * c + 1])};
+          if (c) score(2 * j + c, af, s2);
+          else score(2 * j + c, af, s);
+        }
+      }
+    } else if constexpr (F4) {
+      // products of 16 dims: 4 of each lane's codes, an element being code x scale (6 bits, exact in fp16)
+      constexpr int W = D == 64 ? 2 : 4;  // words of a piece
+#pragma unroll
+      for (int i = 0; i < (D + 127) / 128; ++i) {
+        uint32_t r[2][W], sc[2];
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          const int row = tok0 + 8 * x;
+          const uint32_t sa = tail + row * (D / 16);
+          lds<W>(r[x], D == 64 ? piece4(kb, row, t >> 1) + (t & 1) * 8 : piece4(kb, row, t + 4 * i));
+          sc[x] = f16_of_e4m3(D == 64 ? lds_u8(sa + t) : lds_u16(sa + 2 * (t + 4 * i)));
+        }
+#pragma unroll
+        for (int k = 0; k < W; ++k) {
+          const uint32_t s0 = __byte_perm(sc[0], 0, k < 2 ? 0x1010 : 0x3232), s1 = __byte_perm(sc[1], 0, k < 2 ? 0x1010 : 0x3232);
+          const uint32_t lo[4] = {mul_f16x2(f16_of_e2m1<0>(r[0][k]), s0), mul_f16x2(f16_of_e2m1<0>(r[1][k]), s1),
+                                  mul_f16x2(f16_of_e2m1<1>(r[0][k]), s0), mul_f16x2(f16_of_e2m1<1>(r[1][k]), s1)};
+          const uint32_t hi[4] = {mul_f16x2(f16_of_e2m1<2>(r[0][k]), s0), mul_f16x2(f16_of_e2m1<2>(r[1][k]), s1),
+                                  mul_f16x2(f16_of_e2m1<3>(r[0][k]), s0), mul_f16x2(f16_of_e2m1<3>(r[1][k]), s1)};
+          score(8 * i + 2 * k, lo, s);
+          score(8 * i + 2 * k + 1, hi, s2);
+        }
+      }
+    } else {
+#pragma unroll
+      for (int ks = 0; ks < KS; ++ks) {
+        uint32_t r[4];
+        ldsm4(r, piece(kb, k_off, ks));
+        if (ks & 1) score(ks, r, s2);
+        else score(ks, r, s);
+      }
+    }
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        s[nt][k] += s2[nt][k];
+        // an infinite key times a part that is 0 is no number, and the first part has said what it is
+        if (C::QPARTS == 2) s[nt][k] = fabsf(s[nt][k]) < CUDART_INF_F ? s[nt][k] + sl[nt][k] : s[nt][k];
+      }
+  };
+
   // ================================================================ portions
 #pragma unroll 1
   for (bool more = busy; more; more = out.next(a, w.p, sc)) {
@@ -767,7 +905,7 @@ __global__ void __launch_bounds__(PagedCfg<KIND, D, NT, MODE>::THREADS, 1)
     // the order in which ldmatrix hands out the bytes of a key row)
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
-      const int h = nt * 8 + g;
+      const int h = QUAD ? g & 3 : nt * 8 + g;
       // heads that are none read the first one's row and become zero: loads without a branch go out together
       const uint16_t* qr = a.q + out.b * a.q_stride + (head0 + (h < nh ? h : 0)) * D;
       const uint32_t keep = h < nh ? 0xffffffffu : 0u;
@@ -832,7 +970,7 @@ __global__ void __launch_bounds__(PagedCfg<KIND, D, NT, MODE>::THREADS, 1)
         } else {
           qs[nt][i] = log2e_scale;
         }
-        const int hi = nt * 8 + 2 * t + i;
+        const int hi = QUAD ? (2 * t + i) & 3 : nt * 8 + 2 * t + i;
         if (MODE != kAttend) slope[nt][i] = w.slopes && hi < nh ? w.slopes[head0 + hi] * (C::KEYS ? 1.f : kLog2e) : 0.f;
         if (C::KEYS) {  // in two parts; -inf, of a row without weights, makes them 0
           const float x = hi < nh ? w.lse_in[(int64_t)out.b * a.hq + head0 + hi] : CUDART_INF_F;
@@ -856,14 +994,10 @@ __global__ void __launch_bounds__(PagedCfg<KIND, D, NT, MODE>::THREADS, 1)
         for (int i = 0; i < 4; ++i) o[j][nt][i] = 0.f;
 
     // ================================================================ pages
+    if constexpr (!C::OWN) {
 #pragma unroll 1
     for (int i = 0; i < out.take; ++i, st = st + 1 == S ? 0 : st + 1) {
       const bool here = valid >> st & 1;
-      // the weights' sums so far of tokens tok0 (lanes t = 0) and tok0 + 8 (t = 1)
-      const int pos = (out.s.first + out.p + i) * kPage + tok0;
-      const int64_t at = ((int64_t)out.b * a.hkv + kvh) * w.w_stride + pos + 8 * t;
-      float old = 0.f;
-      if (C::KEYS && t < 2 && pos + 8 * t < out.s.len && w.w_in) old = w.decay * w.w_in[at];
       const uint32_t kb = stage0 + st * C::PAGE, vb = kb + (C::APART ? C::HALF : kPage * C::SWIZZLE_ROW);
       float s[NT][4];
       if (here) {  // with a limit of 0 the first copy is waited for
@@ -873,95 +1007,14 @@ __global__ void __launch_bounds__(PagedCfg<KIND, D, NT, MODE>::THREADS, 1)
       }
       int ek0 = 0, ek1 = 0, ev0 = 0, ev1 = 0;
       if (here) {
-        if (XP) {  // exponents of tokens g and g + 8, keys and values
-          const uint32_t ea = exp0 + st * C::EXP + C::AT_EXP + tok0;
+        if (F8) {  // exponents of tokens g and g + 8, keys and values
+          const uint32_t ea = exp0 + st * C::EXP + g;
           asm volatile("ld.shared.s8 %0, [%1];" : "=r"(ek0) : "r"(ea) : "memory");
           asm volatile("ld.shared.s8 %0, [%1];" : "=r"(ek1) : "r"(ea + 8) : "memory");
-          if (!C::KEYS) {
-            asm volatile("ld.shared.s8 %0, [%1];" : "=r"(ev0) : "r"(ea + 16) : "memory");
-            asm volatile("ld.shared.s8 %0, [%1];" : "=r"(ev1) : "r"(ea + 24) : "memory");
-          }
+          asm volatile("ld.shared.s8 %0, [%1];" : "=r"(ev0) : "r"(ea + 16) : "memory");
+          asm volatile("ld.shared.s8 %0, [%1];" : "=r"(ev1) : "r"(ea + 24) : "memory");
         }
-        float s2[NT][4], sl[NT][4];
-        auto score = [&](int ks, const uint32_t(&af)[4], float(&acc)[NT][4]) {
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt) {
-            uint2 x;
-            if constexpr (C::QREG) x = make_uint2(qf[nt][ks][0], qf[nt][ks][1]);
-            else x = q_sm[(nt * KS + ks) * 32 + lane];
-            if constexpr (C::QPARTS == 2) {
-              uint2 y;
-              if constexpr (C::QREG) y = make_uint2(ql[nt][ks][0], ql[nt][ks][1]);
-              else y = q_sm[((NT + nt) * KS + ks) * 32 + lane];
-              if (ks == 0) mma_first<BF>(sl[nt], af, y.x, y.y);
-              else mma<BF>(sl[nt], af, y.x, y.y);
-            }
-            if (C::KEYS && ks >= 2) {  // the tensor core cuts what it adds up
-              float one[4];
-              mma_first<BF>(one, af, x.x, x.y);
-#pragma unroll
-              for (int k = 0; k < 4; ++k) acc[nt][k] += one[k];
-            } else if (ks < 2) {
-              mma_first<BF>(acc[nt], af, x.x, x.y);
-            } else {
-              mma<BF>(acc[nt], af, x.x, x.y);
-            }
-          }
-        };
-        if constexpr (F8) {
-#pragma unroll
-          for (int j = 0; j < KS / 2; ++j) {
-            uint32_t r[4];
-            ldsm4(r, piece(kb, k_off, j));
-#pragma unroll
-            for (int c = 0; c < 2; ++c) {
-              const uint32_t af[4] = {f16_of_e4m3(r[2 * c]), f16_of_e4m3(r[2 * c + 1]), f16_of_e4m3_high(r[2 * c]),
-                                      f16_of_e4m3_high(r[2 * c + 1])};
-              if (c) score(2 * j + c, af, s2);
-              else score(2 * j + c, af, s);
-            }
-          }
-        } else if constexpr (F4) {
-          // products of 16 dims: 4 of each lane's codes, an element being code x scale (6 bits, exact in fp16)
-          constexpr int W = D == 64 ? 2 : 4;  // words of a piece
-#pragma unroll
-          for (int i = 0; i < (D + 127) / 128; ++i) {
-            uint32_t r[2][W], sc[2];
-#pragma unroll
-            for (int x = 0; x < 2; ++x) {
-              const int row = tok0 + 8 * x;
-              const uint32_t sa = exp0 + st * C::EXP + row * (D / 16);
-              lds<W>(r[x], D == 64 ? piece4(kb, row, t >> 1) + (t & 1) * 8 : piece4(kb, row, t + 4 * i));
-              sc[x] = f16_of_e4m3(D == 64 ? lds_u8(sa + t) : lds_u16(sa + 2 * (t + 4 * i)));
-            }
-#pragma unroll
-            for (int k = 0; k < W; ++k) {
-              const uint32_t s0 = __byte_perm(sc[0], 0, k < 2 ? 0x1010 : 0x3232), s1 = __byte_perm(sc[1], 0, k < 2 ? 0x1010 : 0x3232);
-              const uint32_t lo[4] = {mul_f16x2(f16_of_e2m1<0>(r[0][k]), s0), mul_f16x2(f16_of_e2m1<0>(r[1][k]), s1),
-                                      mul_f16x2(f16_of_e2m1<1>(r[0][k]), s0), mul_f16x2(f16_of_e2m1<1>(r[1][k]), s1)};
-              const uint32_t hi[4] = {mul_f16x2(f16_of_e2m1<2>(r[0][k]), s0), mul_f16x2(f16_of_e2m1<2>(r[1][k]), s1),
-                                      mul_f16x2(f16_of_e2m1<3>(r[0][k]), s0), mul_f16x2(f16_of_e2m1<3>(r[1][k]), s1)};
-              score(8 * i + 2 * k, lo, s);
-              score(8 * i + 2 * k + 1, hi, s2);
-            }
-          }
-        } else {
-#pragma unroll
-          for (int ks = 0; ks < KS; ++ks) {
-            uint32_t r[4];
-            ldsm4(r, piece(kb, k_off, ks));
-            if (ks & 1) score(ks, r, s2);
-            else score(ks, r, s);
-          }
-        }
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            s[nt][k] += s2[nt][k];
-            // an infinite key times a part that is 0 is no number, and the first part has said what it is
-            if (C::QPARTS == 2) s[nt][k] = fabsf(s[nt][k]) < CUDART_INF_F ? s[nt][k] + sl[nt][k] : s[nt][k];
-          }
+        scores(kb, exp0 + st * C::EXP, s);
       }
       bool again = false;
       auto next_page = [&]() {
@@ -970,7 +1023,7 @@ __global__ void __launch_bounds__(PagedCfg<KIND, D, NT, MODE>::THREADS, 1)
         valid = again ? valid | 1u << st : valid & ~(1u << st);
         if (again && (parity & kLate) == 0 && lane == 0) fetch(st, 0);
       };
-      if (C::APART || C::KEYS) next_page();  // the keys are read
+      if (C::APART) next_page();  // the keys are read
 
       if (here) {
         // ---- weights
@@ -978,7 +1031,7 @@ __global__ void __launch_bounds__(PagedCfg<KIND, D, NT, MODE>::THREADS, 1)
         const bool whole = rel != cut_first && rel != cut_last;
         const int t_lo = out.s.lo - (out.s.first + rel) * kPage, t_hi = out.s.len - (out.s.first + rel) * kPage;
         auto counts = [&](int tok) { return tok >= t_lo && tok < t_hi; };
-        if (XP) {
+        if (F8) {
           const float f0 = power2(ek0), f1 = power2(ek1);
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt)
@@ -998,7 +1051,7 @@ __global__ void __launch_bounds__(PagedCfg<KIND, D, NT, MODE>::THREADS, 1)
               for (int k = 0; k < 4; ++k) s[nt][k] = cap2 * tanh_of(s[nt][k]);
           }
           if (w.slopes) {
-            const float back0 = (float)(pos + 1 - out.s.len), back1 = (float)(pos + 9 - out.s.len);
+            const float back0 = (float)(g + 1 - t_hi), back1 = (float)(g + 9 - t_hi);
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -1006,7 +1059,7 @@ __global__ void __launch_bounds__(PagedCfg<KIND, D, NT, MODE>::THREADS, 1)
           }
         }
         if (!whole) {  // rows that do not count are whatever memory held
-          const bool ok0 = counts(tok0), ok1 = counts(tok0 + 8);
+          const bool ok0 = counts(g), ok1 = counts(g + 8);
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -1014,23 +1067,6 @@ __global__ void __launch_bounds__(PagedCfg<KIND, D, NT, MODE>::THREADS, 1)
           ev0 = ok0 ? ev0 : -127;
           ev1 = ok1 ? ev1 : -127;
         }
-        if constexpr (C::KEYS) {
-          float sum[2] = {0.f, 0.f};
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-              if (nt * 8 + 2 * t + (k & 1) < nh) {
-                const float z = s[nt][k], y = fmaf(z, up_hi, -lse_hi[nt][k & 1]);
-                sum[k >> 1] += ex2(fabsf(z) < CUDART_INF_F ? fmaf(z, up_lo, y) - lse_lo[nt][k & 1] : y);
-              }
-#pragma unroll
-          for (int x = 0; x < 2; ++x) {
-            sum[x] += __shfl_xor_sync(kFull, sum[x], 1);
-            sum[x] += __shfl_xor_sync(kFull, sum[x], 2);
-          }
-          old += __any_sync(kFull, (parity & kLate) != 0) ? CUDART_NAN_F : t == 0 ? sum[0] : sum[1];
-        } else {
         const float fe0 = (float)ev0, fe1 = (float)ev1;
         float p[NT][4];
 #pragma unroll
@@ -1039,7 +1075,7 @@ __global__ void __launch_bounds__(PagedCfg<KIND, D, NT, MODE>::THREADS, 1)
           for (int k = 0; k < 4; ++k) {
             p[nt][k] = s[nt][k] - m[nt][k & 1];
             raise |= p[nt][k] > kLazy;
-            if (XP) raise |= p[nt][k] + (k < 2 ? fe0 : fe1) > most[nt][k & 1];
+            if (F8) raise |= p[nt][k] + (k < 2 ? fe0 : fe1) > most[nt][k & 1];
           }
         if (__any_sync(kFull, raise)) {  // all heads' references are set anew: fewer pages come here
 #pragma unroll
@@ -1057,7 +1093,7 @@ __global__ void __launch_bounds__(PagedCfg<KIND, D, NT, MODE>::THREADS, 1)
               p[nt][k] = s[nt][k] - mx;
               p[nt][k + 2] = s[nt][k + 2] - mx;
               float co = c;
-              if (XP) {  // the values' reference follows, and their sum takes what it does not
+              if (F8) {  // the values' reference follows, and their sum takes what it does not
                 float top = fmaxf(fmaxf(p[nt][k] + fe0, p[nt][k + 2] + fe1), -1000.f);
 #pragma unroll
                 for (int x = 4; x < 32; x <<= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, x));
@@ -1075,7 +1111,7 @@ __global__ void __launch_bounds__(PagedCfg<KIND, D, NT, MODE>::THREADS, 1)
             }
         }
         // what a token's weight at its values has besides: 2^-8, and on 8-bit pages their exponent
-        const float w0 = XP ? power2(ev0) * kDown : kDown, w1 = XP ? power2(ev1) * kDown : kDown;
+        const float w0 = F8 ? power2(ev0) * kDown : kDown, w1 = F8 ? power2(ev1) * kDown : kDown;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
@@ -1093,7 +1129,7 @@ __global__ void __launch_bounds__(PagedCfg<KIND, D, NT, MODE>::THREADS, 1)
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
             p[nt][k] *= k < 2 ? w0 : w1;
-            if (XP) p[nt][k] *= vr[nt][k & 1];
+            if (F8) p[nt][k] *= vr[nt][k & 1];
           }
         }
         constexpr int PARTS = BF ? 3 : 2;
@@ -1119,15 +1155,7 @@ __global__ void __launch_bounds__(PagedCfg<KIND, D, NT, MODE>::THREADS, 1)
           vparity ^= 1u << st;
         }
         if (!whole) {
-          // value rows that do not count: a weight of 0 does not remove a NaN (4-bit codes have none, their scales do)
-          if constexpr (F4) {
-#pragma unroll
-            for (int k = 0; k < (D + 127) / 128; ++k) {  // D bytes of scales, 4 a lane
-              const int at = (k * 32 + lane) * 4;
-              if (at < D && !counts(at / (D / 16)))
-                asm volatile("st.shared.b32 [%0], %1;" ::"r"(exp0 + st * C::EXP + D + at), "r"(0) : "memory");
-            }
-          } else {
+          // value rows that do not count: a weight of 0 does not remove a NaN
 #pragma unroll
           for (int k = 0; k < C::HALF / 512; ++k) {
             const uint32_t row = (k * 32 + lane) * 16 / C::SWIZZLE_ROW, col = (k * 32 + lane) * 16 % C::SWIZZLE_ROW;
@@ -1135,7 +1163,6 @@ __global__ void __launch_bounds__(PagedCfg<KIND, D, NT, MODE>::THREADS, 1)
               asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(vb + row / kPage * C::BOX + row % kPage * C::SWIZZLE_ROW + col),
                            "r"(0)
                            : "memory");
-          }
           }
           asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // before the stage's next copy
           __syncwarp();
@@ -1176,43 +1203,6 @@ __global__ void __launch_bounds__(PagedCfg<KIND, D, NT, MODE>::THREADS, 1)
               add(2 * j + c, af);
             }
           }
-        } else if constexpr (F4) {
-          // tokens number 2 t, 2 t + 1, 2 t + 8, 2 t + 9 of the fragments, D / 8 dims each; nibbles of two tokens are paired before they
-          // become fp16: one product has dims 2 j (rows g) and 2 j + 1 (rows g + 8) of the lanes' shares
-          constexpr int W = D / 64 < 4 ? D / 64 : 4;  // words of a piece
-          const int ta = turned(2 * t), tb = turned(2 * t + 1);
-          const uint32_t sa = exp0 + st * C::EXP + D;
-#pragma unroll
-          for (int i = 0; i < (D + 255) / 256; ++i) {
-            uint32_t r[4][W];
-#pragma unroll
-            for (int x = 0; x < 4; ++x) {
-              const int row = (x & 1 ? tb : ta) + (x >> 1) * 8;
-              lds<W>(r[x], W == 4 ? piece4(vb, row, g + 8 * i) : W == 2 ? piece4(vb, row, g >> 1) + (g & 1) * 8 : piece4(vb, row, g >> 2) + (g & 3) * 4);
-            }
-            uint32_t sc[2];
-#pragma unroll
-            for (int k = 0; k < W; ++k) {
-              if (k % 2 == 0) {  // scales of a pair of tokens
-                const int block = W == 4 ? 2 * (g + 8 * i) + k / 2 : W == 2 ? g : g >> 1;
-#pragma unroll
-                for (int x = 0; x < 2; ++x)
-                  sc[x] = f16_of_e4m3(lds_u8(sa + (ta + 8 * x) * (D / 16) + block) | lds_u8(sa + (tb + 8 * x) * (D / 16) + block) << 8);
-              }
-              constexpr uint32_t kLow = 0x0f0f0f0fu;
-              const uint32_t e0 = (r[0][k] & kLow) | (r[1][k] << 4 & ~kLow), o0 = (r[0][k] >> 4 & kLow) | (r[1][k] & ~kLow);
-              const uint32_t e1 = (r[2][k] & kLow) | (r[3][k] << 4 & ~kLow), o1 = (r[2][k] >> 4 & kLow) | (r[3][k] & ~kLow);
-              const int j = 16 * i + 4 * k;
-#define TQ_ADD4(B)                                                                                                     \
-  {                                                                                                                    \
-    const uint32_t af[4] = {mul_f16x2(f16_of_e2m1<B>(e0), sc[0]), mul_f16x2(f16_of_e2m1<B>(o0), sc[0]),                \
-                            mul_f16x2(f16_of_e2m1<B>(e1), sc[1]), mul_f16x2(f16_of_e2m1<B>(o1), sc[1])};               \
-    add(j + B, af);                                                                                                    \
-  }
-              TQ_ADD4(0) TQ_ADD4(1) TQ_ADD4(2) TQ_ADD4(3)
-#undef TQ_ADD4
-            }
-          }
         } else {
 #pragma unroll
           for (int j = 0; j < KS; ++j) {
@@ -1221,19 +1211,307 @@ __global__ void __launch_bounds__(PagedCfg<KIND, D, NT, MODE>::THREADS, 1)
             add(j, r);
           }
         }
-        }
       }
-      if (C::KEYS) {
-        if (t < 2 && pos + 8 * t < out.s.len) w.w_out[at] = old;
-      } else if (C::APART) {
+      if (C::APART) {
         __syncwarp();
         if (again && (parity & kLate) == 0 && lane == 0) fetch(st, 1);
       } else {
         next_page();
       }
     }
+    } else {
+    // Up to d = 128 two pages a step: a page's share of the instructions that are not its own is halved.
+#pragma unroll 1
+    for (int i = 0; i < out.take; i += PP, st = st + 1 == S ? 0 : st + 1) {
+      const uint32_t here = valid >> 2 * st & 3;
+      const int rel = out.p + i, first = (out.s.first + rel) * kPage;  // page of the segment, position of its first token
+      // the weights' sums so far: a lane has token tok0 + 8 (t & 1) of page t >> 1
+      const int pos = first + 16 * (t >> 1) + tok0 + 8 * (t & 1);
+      const int64_t at = ((int64_t)out.b * a.hkv + kvh) * w.w_stride + pos;
+      const bool mine = C::KEYS && pos < out.s.len && (t < 2 || (PP == 2 && i + 1 < out.take));
+      float old = 0.f, added = 0.f;
+      if (mine && w.w_in) old = w.w_in[at];
+      asm volatile("cp.async.wait_group %0;" ::"n"(S - 1) : "memory");
+      __syncwarp();
+      auto next_pages = [&]() {
+        __syncwarp();  // every lane has read what the copy replaces
+        if (!fetch_next()) tile = tile2 = -1;
+        valid = (valid & ~(3u << 2 * st)) | there() << 2 * st;
+        fetch_own(st);
+      };
+      // a page that is not there counts as one whose tokens do not
+      float s[PP][NT][4];
+      int ek[PP][2] = {}, ev[PP][2] = {};
+      if (here) {
+#pragma unroll
+        for (int pg = 0; pg < PP; ++pg) {
+          const uint32_t tail = exp0 + st * C::EXP + pg * C::EXP1;
+          if (XP) {  // exponents of tokens tok0 and tok0 + 8, keys and values
+            const uint32_t ea = tail + C::AT_EXP + tok0;
+            asm volatile("ld.shared.s8 %0, [%1];" : "=r"(ek[pg][0]) : "r"(ea) : "memory");
+            asm volatile("ld.shared.s8 %0, [%1];" : "=r"(ek[pg][1]) : "r"(ea + 8) : "memory");
+            if (!C::KEYS) {
+              asm volatile("ld.shared.s8 %0, [%1];" : "=r"(ev[pg][0]) : "r"(ea + 16) : "memory");
+              asm volatile("ld.shared.s8 %0, [%1];" : "=r"(ev[pg][1]) : "r"(ea + 24) : "memory");
+            }
+          }
+          scores(stage0 + st * C::PAGE + pg * C::PAGE1, tail, s[pg]);
+        }
+      }
+      if (C::KEYS) next_pages();  // the keys are read
+      if (here) {
+        const bool whole = here == (1u << PP) - 1 && rel != cut_first && rel + PP - 1 != cut_last;
+        auto counts = [&](int pg, int tok) {
+          const int x = first + pg * kPage + tok;
+          return x >= out.s.lo && x < out.s.len && (here >> pg & 1);
+        };
+#pragma unroll
+        for (int pg = 0; pg < PP; ++pg) {
+          if (XP) {
+            const float f0 = power2(ek[pg][0]), f1 = power2(ek[pg][1]);
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+              for (int k = 0; k < 4; ++k) s[pg][nt][k] = s[pg][nt][k] * qh[nt][k & 1] * (k < 2 ? f0 : f1);
+          }
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int k = 0; k < 4; ++k) s[pg][nt][k] *= qs[nt][k & 1];
+          if constexpr (MODE != kAttend) {
+            if (capped) {
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int k = 0; k < 4; ++k) s[pg][nt][k] = cap2 * tanh_of(s[pg][nt][k]);
+            }
+            if (w.slopes) {
+              const int x = first + pg * kPage + tok0 + 1 - out.s.len;
+              const float back0 = (float)x, back1 = (float)(x + 8);
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int k = 0; k < 4; ++k) s[pg][nt][k] = fmaf(slope[nt][k & 1], k < 2 ? back0 : back1, s[pg][nt][k]);
+            }
+          }
+          if (!whole) {  // rows that do not count are whatever memory held
+            const bool ok0 = counts(pg, tok0), ok1 = counts(pg, tok0 + 8);
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+              for (int k = 0; k < 4; ++k) s[pg][nt][k] = (k < 2 ? ok0 : ok1) ? s[pg][nt][k] : -CUDART_INF_F;
+            ev[pg][0] = ok0 ? ev[pg][0] : -127;
+            ev[pg][1] = ok1 ? ev[pg][1] : -127;
+          }
+        }
+        if constexpr (C::KEYS) {
+          float sum[4] = {0.f, 0.f, 0.f, 0.f};  // tokens tok0, tok0 + 8 of the first page, of the second
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+#pragma unroll
+              for (int pg = 0; pg < PP; ++pg) {  // heads that are none have lse inf; their products with a key that is not finite do not count
+                const float z = nt * 8 + 2 * t + (k & 1) < nh ? s[pg][nt][k] : 0.f, y = fmaf(z, up_hi, -lse_hi[nt][k & 1]);
+                sum[2 * pg + (k >> 1)] += ex2(fabsf(z) < CUDART_INF_F ? fmaf(z, up_lo, y) - lse_lo[nt][k & 1] : y);
+              }
+          // lane t gets the total of sum[t] over the four lanes
+          const bool odd = t & 1, high = t & 2;
+          const float x0 = (odd ? sum[1] : sum[0]) + __shfl_xor_sync(kFull, odd ? sum[0] : sum[1], 1);
+          const float x1 = (odd ? sum[3] : sum[2]) + __shfl_xor_sync(kFull, odd ? sum[2] : sum[3], 1);
+          const float all = (high ? x1 : x0) + __shfl_xor_sync(kFull, high ? x0 : x1, 2);
+          added = all;
+        } else if constexpr (F4) {
+          float fe[PP][2], p[PP][NT][4];
+          bool raise = false;
+#pragma unroll
+          for (int pg = 0; pg < PP; ++pg) {
+            fe[pg][0] = (float)ev[pg][0];
+            fe[pg][1] = (float)ev[pg][1];
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+              for (int k = 0; k < 4; ++k) {
+                p[pg][nt][k] = s[pg][nt][k] - m[nt][k & 1];
+                raise |= p[pg][nt][k] > kLazy;
+                raise |= p[pg][nt][k] + fe[pg][k >> 1] > most[nt][k & 1];
+              }
+          }
+          if (__any_sync(kFull, raise)) {  // all heads' references are set anew: fewer pages come here
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+              for (int k = 0; k < 2; ++k) {
+                float mx = fmaxf(s[0][nt][k], s[0][nt][k + 2]);
+                if (PP == 2) mx = fmaxf(mx, fmaxf(s[PP - 1][nt][k], s[PP - 1][nt][k + 2]));
+#pragma unroll
+                for (int x = 4; x < 32; x <<= 1) mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, x));
+                mx = fmaxf(m[nt][k], ceilf(mx));
+                const float up = mx - m[nt][k], c = ex2(-up);
+                m[nt][k] = mx;
+                l[nt][k] *= c;
+                if (C::KEEP_LOST) lost[nt][k] *= c;
+                float top = -1000.f;
+#pragma unroll
+                for (int pg = 0; pg < PP; ++pg)
+#pragma unroll
+                  for (int x = 0; x < 2; ++x) {
+                    p[pg][nt][k + 2 * x] = s[pg][nt][k + 2 * x] - mx;
+                    top = fmaxf(top, p[pg][nt][k + 2 * x] + fe[pg][x]);
+                  }
+                // the values' reference follows, and their sum takes what it does not
+#pragma unroll
+                for (int x = 4; x < 32; x <<= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, x));
+                const int e = kValueMost + (int)kLazy - (int)most[nt][k], by = (int)fminf(up, 1000.f);
+                const int e1 = max(min(min(e + by, kValueTop), kValueAt + (int)kLazy - (int)floorf(top)), kValueLeast);
+                most[nt][k] = (float)(kValueMost + (int)kLazy - e1);
+                vr[nt][k] = power2(e1);
+                const float co = power2(max(e1 - e - by, -127));
+#pragma unroll
+                for (int j = 0; j < KS; ++j) {
+                  o[j][nt][k] *= co;
+                  o[j][nt][k + 2] *= co;
+                }
+              }
+          }
+          // Two fp16 parts of the weights of 8 tokens and 8 behind them.  With 4 heads columns 4 .. 7 are the same heads again, and
+          // take the second part: one product gives both sums.
+          constexpr int PARTS = QUAD ? 1 : 2;
+          uint32_t pf[PP][NT][PARTS][2];
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+            for (int pg = 0; pg < PP; ++pg)
+#pragma unroll
+              for (int k = 0; k < 4; ++k) p[pg][nt][k] = ex2(p[pg][nt][k]);
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+              float sum4 = p[0][nt][k] + p[0][nt][k + 2];
+              if (PP == 2) sum4 += p[PP - 1][nt][k] + p[PP - 1][nt][k + 2];
+              if constexpr (C::KEEP_LOST) {  // what an addition loses is kept for the next one (Kahan's sum)
+                const float y = sum4 - lost[nt][k], sum = l[nt][k] + y;
+                lost[nt][k] = sum - l[nt][k] - y;
+                l[nt][k] = sum;
+              } else {
+                l[nt][k] += sum4;
+              }
+            }
+#pragma unroll
+            for (int pg = 0; pg < PP; ++pg) {
+              // what a token's weight at its values has besides: 2^-8 and their exponent
+#pragma unroll
+              for (int k = 0; k < 4; ++k) p[pg][nt][k] = p[pg][nt][k] * (power2(ev[pg][k >> 1]) * kDown) * vr[nt][k & 1];
+#pragma unroll
+              for (int x = 0; x < 2; ++x) {
+                const uint32_t a1 = take_part<false>(p[pg][nt][2 * x], p[pg][nt][2 * x + 1]);
+                const uint32_t a2 = take_part<false>(p[pg][nt][2 * x], p[pg][nt][2 * x + 1]);
+                pf[pg][nt][0][x] = movmat(QUAD && t >= 2 ? a2 : a1);
+                if (!QUAD) pf[pg][nt][PARTS - 1][x] = movmat(a2);
+              }
+            }
+          }
+          if (!whole) {
+            // scales of values that do not count: a weight of 0 does not remove a NaN, which codes have not but scales do
+#pragma unroll
+            for (int pg = 0; pg < PP; ++pg)
+#pragma unroll
+              for (int k = 0; k < (D + 127) / 128; ++k) {  // D bytes of scales, 4 a lane
+                const int byte = (k * 32 + lane) * 4;
+                if (byte < D && !counts(pg, byte / (D / 16)))
+                  asm volatile("st.shared.b32 [%0], %1;" ::"r"(exp0 + st * C::EXP + pg * C::EXP1 + D + byte), "r"(0) : "memory");
+              }
+            __syncwarp();
+          }
+          // Tokens number 2 t, 2 t + 1, 2 t + 8, 2 t + 9 of the fragments, D / 8 dims each; nibbles of two tokens are paired before they
+          // become fp16: one product has dims 2 j (rows g) and 2 j + 1 (rows g + 8) of the lanes' shares.
+          constexpr int W = D / 64 < 4 ? D / 64 : 4;  // words of a piece
+          const int ta = turned(2 * t), tb = turned(2 * t + 1);
+#pragma unroll
+          for (int pi = 0; pi < (D + 255) / 256; ++pi) {
+            uint32_t r[PP][4][W];
+#pragma unroll
+            for (int pg = 0; pg < PP; ++pg)
+#pragma unroll
+              for (int x = 0; x < 4; ++x) {
+                const uint32_t vb = stage0 + st * C::PAGE + pg * C::PAGE1 + C::HALF;
+                const int row = (x & 1 ? tb : ta) + (x >> 1) * 8;
+                lds<W>(r[pg][x], W == 4 ? piece4(vb, row, g + 8 * pi) : W == 2 ? piece4(vb, row, g >> 1) + (g & 1) * 8 : piece4(vb, row, g >> 2) + (g & 3) * 4);
+              }
+            uint32_t sc[PP][2];
+#pragma unroll
+            for (int k = 0; k < W; ++k) {
+              uint32_t even[PP][2], odd[PP][2];
+#pragma unroll
+              for (int pg = 0; pg < PP; ++pg) {
+                if (k % 2 == 0) {  // scales of a pair of tokens
+                  const int block = W == 4 ? 2 * (g + 8 * pi) + k / 2 : W == 2 ? g : g >> 1;
+                  const uint32_t sa = exp0 + st * C::EXP + pg * C::EXP1 + D + block;
+#pragma unroll
+                  for (int x = 0; x < 2; ++x)
+                    sc[pg][x] = f16_of_e4m3(lds_u8(sa + (ta + 8 * x) * (D / 16)) | lds_u8(sa + (tb + 8 * x) * (D / 16)) << 8);
+                }
+                constexpr uint32_t kLow = 0x0f0f0f0fu;
+#pragma unroll
+                for (int x = 0; x < 2; ++x) {
+                  const uint32_t u = r[pg][2 * x][k], v = r[pg][2 * x + 1][k];
+                  even[pg][x] = (u & kLow) | (v << 4 & ~kLow);
+                  odd[pg][x] = (u >> 4 & kLow) | (v & ~kLow);
+                }
+              }
+              // chains of dependent products are interleaved, kAbreast of them
+              constexpr int kAbreast = 2;
+              auto add = [&](int j, const uint32_t(&af)[kAbreast][PP][4]) {
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) {
+                  float acc[kAbreast][4];
+#pragma unroll
+                  for (int part = PARTS - 1; part >= 0; --part)
+#pragma unroll
+                    for (int pg = 0; pg < PP; ++pg)
+#pragma unroll
+                      for (int y = 0; y < kAbreast; ++y) {
+                        if (part == PARTS - 1 && pg == 0) mma_first<false>(acc[y], af[y][pg], pf[pg][nt][part][0], pf[pg][nt][part][1]);
+                        else mma<false>(acc[y], af[y][pg], pf[pg][nt][part][0], pf[pg][nt][part][1]);
+                      }
+#pragma unroll
+                  for (int y = 0; y < kAbreast; ++y)
+#pragma unroll
+                    for (int x = 0; x < 4; ++x) o[j + y][nt][x] += acc[y][x];
+                }
+              };
+              const int j = 16 * pi + 4 * k;
+              uint32_t af[kAbreast][PP][4];
+#pragma unroll
+              for (int pg = 0; pg < PP; ++pg) {
+                elements4<0>(af[0][pg], even[pg], odd[pg], sc[pg]);
+                elements4<1>(af[1][pg], even[pg], odd[pg], sc[pg]);
+              }
+              add(j, af);
+#pragma unroll
+              for (int pg = 0; pg < PP; ++pg) {
+                elements4<2>(af[0][pg], even[pg], odd[pg], sc[pg]);
+                elements4<3>(af[1][pg], even[pg], odd[pg], sc[pg]);
+              }
+              add(j + 2, af);
+            }
+          }
+        }
+      }
+      if (C::KEYS) {
+        if (mine) w.w_out[at] = fmaf(w.decay, old, added);
+      } else {
+        next_pages();
+      }
+    }
+    }
 
     // ================================================================ the portion's result
+    if constexpr (QUAD) {  // the sums of both parts
+#pragma unroll
+      for (int j = 0; j < KS; ++j)
+#pragma unroll
+        for (int x = 0; x < 4; ++x) o[j][0][x] += __shfl_xor_sync(kFull, o[j][0][x], 2);
+    }
     if constexpr (!C::KEYS) {
     const bool dead = __any_sync(kFull, (parity & kLate) != 0);
 #pragma unroll
@@ -1527,7 +1805,7 @@ cudaError_t launch_line(tq_ctx* ctx, PagedWork& w, cudaStream_t s) {
   const int ctas = want < ctx->sm_count ? (int)want : ctx->sm_count;
   w.p.teams = ctas * C::NW;
   CUtensorMap map{};
-  if (a.num_blocks > 0) {
+  if (!C::OWN && a.num_blocks > 0) {
     const PagedTensorMap tm{a.pool, C::ES, C::ROW / C::ES, (int64_t)a.num_blocks * a.hkv, C::TILE, C::SWIZZLE_ROW, C::BOX_ROWS};
     if (!encode_paged_map(tm, &map)) return cudaErrorInvalidValue;
   }
@@ -1604,10 +1882,18 @@ cudaError_t launch_weights_one(tq_ctx* ctx, const PagedArgs& a, const ScoreArgs&
   return cudaSuccess;
 }
 
-// Query heads per segment: 8, or 16 when a KV head has more than 8 (d = 512: always 8, for want of registers).
+// Query heads per segment: 8, or 16 when a KV head has more than 8 (d = 512: always 8, for want of registers); from 4-bit pages
+// 4 where a KV head has no more.
 template <int KIND, int MODE>
 cudaError_t launch_kind(tq_ctx* ctx, const PagedArgs& a, const ScoreArgs& sc, void* ws, cudaStream_t s) {
   const bool two = a.n_rep > 8;
+  if constexpr (KIND == kE2M1)
+    if (a.n_rep <= 4) switch (ctx->cfg.head_dim) {
+        case 64: return launch_one<KIND, 64, 0, MODE>(ctx, a, sc, ws, s);
+        case 128: return launch_one<KIND, 128, 0, MODE>(ctx, a, sc, ws, s);
+        case 256: return launch_one<KIND, 256, 0, MODE>(ctx, a, sc, ws, s);
+        case 512: return launch_one<KIND, 512, 0, MODE>(ctx, a, sc, ws, s);
+      }
   switch (ctx->cfg.head_dim) {
     case 64: return two ? launch_one<KIND, 64, 2, MODE>(ctx, a, sc, ws, s) : launch_one<KIND, 64, 1, MODE>(ctx, a, sc, ws, s);
     case 128: return two ? launch_one<KIND, 128, 2, MODE>(ctx, a, sc, ws, s) : launch_one<KIND, 128, 1, MODE>(ctx, a, sc, ws, s);
@@ -1630,7 +1916,15 @@ cudaError_t launch_weights_kind(tq_ctx* ctx, const PagedArgs& a, const ScoreArgs
 
 template <int KIND>
 size_t workspace_kind(const tq_ctx* ctx, int batch) {
-  const bool two = ctx->cfg.num_q_heads / ctx->cfg.num_kv_heads > 8;
+  const int n_rep = ctx->cfg.num_q_heads / ctx->cfg.num_kv_heads;
+  const bool two = n_rep > 8;
+  if constexpr (KIND == kE2M1)
+    if (n_rep <= 4) switch (ctx->cfg.head_dim) {
+        case 64: return workspace_of<KIND, 64, 0>(ctx, batch);
+        case 128: return workspace_of<KIND, 128, 0>(ctx, batch);
+        case 256: return workspace_of<KIND, 256, 0>(ctx, batch);
+        case 512: return workspace_of<KIND, 512, 0>(ctx, batch);
+      }
   switch (ctx->cfg.head_dim) {
     case 64: return two ? workspace_of<KIND, 64, 2>(ctx, batch) : workspace_of<KIND, 64, 1>(ctx, batch);
     case 128: return two ? workspace_of<KIND, 128, 2>(ctx, batch) : workspace_of<KIND, 128, 1>(ctx, batch);

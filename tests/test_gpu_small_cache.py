@@ -413,45 +413,25 @@ def test_weights_of_infinite_keys():
     assert torch.isfinite(got[0, 0, :20]).all() and got[0, 0, 4] == 0 and abs(float(got[0, 0, :20].sum()) - 2) < 1e-5
 
 
-@pytest.mark.parametrize("hq,hkv,d", [(2, 2, 64), (8, 2, 128), (32, 2, 128), (4, 1, 512)])
-@pytest.mark.parametrize("bits,bf16", [(16, True), (8, False), (4, False)])
-def test_weights_waits_that_run_out(bits, bf16, hq, hkv, d):
-    e = weights_case(d + hq, [200, 130], hq, hkv, d, bits, bf16)
+@pytest.mark.parametrize("bits,d,rep", [(4, 64, 4), (4, 128, 8), (4, 256, 16), (4, 512, 4), (16, 128, 8), (8, 512, 4)])
+def test_the_wait_limit_is_for_other_pages(bits, d, rep):
+    """Long sequences over the same few pages, many rounds of copies a warp: weight sums, and attention from 4-bit pages, wait by
+    counting their copies and know no limit."""
+    e = weights_case(d + rep, [200, 130], rep, 1, d, bits, False)
     ctx, held = e["ctx"], np.concatenate([e["bt"][0, :12], e["bt"][1, :8]])
-    e["lengths"] = np.array([60000, 0, 17, 20000], np.int32)
-    e["bt"] = np.resize(held, (4, 60000 // 16)).astype(np.int32)
-    e["q"] = torch.randn(4, hq, d, generator=torch.Generator().manual_seed(d)).to(e["q"].dtype)
-    e["before"] = torch.zeros(4, hkv, 60000)
-    _, lse = attend(e)
-    ref = add_weights(e, lse)
-    assert ctx.device_errors() == 0 and torch.isfinite(ref).all()
-    ctx.set_wait_limit(0)
-    got = add_weights(e, lse)
-    assert ctx.device_errors() == tq.binding.TQ_DEVERR_TIMEOUT
-    late = torch.isnan(got)
-    assert late.any() and torch.equal(got[~late], ref[~late])
-    ctx.set_wait_limit(10 ** 9)
-    assert torch.equal(add_weights(e, lse), ref) and ctx.device_errors() == 0
-
-
-@pytest.mark.parametrize("d,rep", [(64, 4), (128, 8), (256, 16), (512, 4)])
-def test_attention4_waits_that_run_out(d, rep):
-    e = make_case(d + rep, [200, 130], rep, 1, d, 4, False)
-    ctx, held = e["ctx"], np.concatenate([e["bt"][0, :12], e["bt"][1, :8]])
-    e["lengths"] = np.array([200000, 0, 17, 120000, 190000], np.int32)
-    e["bt"] = np.resize(held, (5, 200000 // 16)).astype(np.int32)
+    e["lengths"] = np.array([60000, 0, 17, 20000, 31000], np.int32)
+    e["bt"] = np.resize(held, (5, 60000 // 16)).astype(np.int32)
     e["q"] = torch.randn(5, rep, d, generator=torch.Generator().manual_seed(d)).half()
-    ref, ref_lse = attend(e)
-    assert ctx.device_errors() == 0 and torch.isfinite(ref).all()
+    e["before"] = torch.zeros(5, 1, 60000)
+    ref = attend(e)
+    sums = add_weights(e, ref[1])
+    assert ctx.device_errors() == 0 and torch.isfinite(sums).all() and torch.isfinite(ref[0]).all()
     ctx.set_wait_limit(0)
-    out, lse = attend(e)
-    assert ctx.device_errors() == tq.binding.TQ_DEVERR_TIMEOUT
-    late = torch.isnan(lse)
-    assert late.any() and not late[1].any() and torch.isnan(out[late]).all()
-    assert torch.equal(out[~late], ref[~late]) and torch.equal(lse[~late], ref_lse[~late])
-    ctx.set_wait_limit(10 ** 9)
-    again = attend(e)
-    assert ctx.device_errors() == 0 and torch.equal(again[0], ref) and torch.equal(again[1], ref_lse)
+    assert torch.equal(add_weights(e, ref[1]), sums)
+    if bits == 4:
+        again = attend(e)
+        assert torch.equal(again[0], ref[0]) and torch.equal(again[1], ref[1])
+    assert ctx.device_errors() == 0
 
 
 # ---------------------------------------------------------------- eviction
