@@ -22,16 +22,25 @@ namespace {
 namespace cg = cooperative_groups;
 
 constexpr int kEvictThreads = 512, kEvictWarps = kEvictThreads / 32;
-constexpr int kHeld = 10 * 1024;   // keys of a CTA's slice that are kept in shared memory
+constexpr int kHeld = 10 * 1024;   // weights of a CTA's slice that are kept in shared memory
 constexpr int kInFlight = 8;       // 16-byte pieces of a thread and round
 constexpr int kDigits = 256;
+static_assert(kEvictThreads == 2 * kDigits, "half of the threads add up, the others clear");
 
+// Where a token comes from and goes to: byte offsets of the tiles in the pool with the slots in their low 4 bits; -1: no move.
+struct __align__(16) Move {
+  int64_t src, dst;
+};
 struct EvictSmem {
-  uint32_t key[kHeld];
-  uint32_t hist[kDigits];      // of this CTA
+  union {
+    float held[kHeld];
+    Move move[2][1024];  // of a round and the next
+  };
+  uint32_t hist[2][kDigits];   // of this CTA; two passes' by turns
   uint32_t total[kDigits];     // of the cluster
   uint32_t above[kEvictWarps], on[kEvictWarps];  // per warp: keys above the threshold, and equal to it
   uint32_t cta_above, cta_on;
+  int first_gone;  // lowest slot of the slice that does not stay
   uint32_t digit, left;
 };
 
@@ -50,6 +59,7 @@ struct Tile {
   static constexpr int AT_SCALE = 2 * kPage * ROW, AT_EXP = AT_SCALE + 2 * kPage * SCALE;
   static constexpr int BYTES = AT_EXP + (BITS < 16 ? 2 * kPage : 0);
   static constexpr int TOKENS = kEvictThreads * kInFlight / PIECES;  // of a CTA and round
+  static_assert(TOKENS <= 1024 && BYTES % 16 == 0, "the moves' list");
 };
 
 // A token's scales of one side as one value.
@@ -100,29 +110,42 @@ __global__ void __launch_bounds__(kEvictThreads, 2) evict_kernel(const EvictArgs
   const int each = (hi - lo + ctas - 1) / ctas;
   const int s0 = (int)min((int64_t)hi, lo + (int64_t)rank * each), size = min(each, hi - s0);
   const bool held = size <= kHeld;
-  if (held)
-    for (int i = tid; i < size; i += kEvictThreads) sm.key[i] = key_of(w[s0 + i]);
-  auto key_at = [&](int i) { return held ? sm.key[i] : key_of(w[s0 + i]); };
+  if (held) {
+#pragma unroll 1
+    for (int i = tid; i < size; i += 8 * kEvictThreads) {
+      float x[8];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) x[k] = i + k * kEvictThreads < size ? w[s0 + i + k * kEvictThreads] : 0.f;
+#pragma unroll
+      for (int k = 0; k < 8; ++k)
+        if (i + k * kEvictThreads < size) sm.held[i + k * kEvictThreads] = x[k];
+    }
+  }
+  auto weight_at = [&](int i) { return held ? sm.held[i] : w[s0 + i]; };
+  auto key_at = [&](int i) { return key_of(weight_at(i)); };
 
   // ---- the threshold: `prefix` collects the digits of the m-th largest key, m what is still to be found below it
   uint32_t prefix = 0;
   const bool all = m >= hi - lo, none = m == 0;
   if (!all && !none) {
+    for (int i = tid; i < 2 * kDigits; i += kEvictThreads) sm.hist[i / kDigits][i % kDigits] = 0;
+    __syncthreads();
 #pragma unroll 1
     for (int shift = 24; shift >= 0; shift -= 8) {
-      for (int i = tid; i < kDigits; i += kEvictThreads) sm.hist[i] = 0;
-      __syncthreads();
+      uint32_t* hist = sm.hist[shift >> 3 & 1];
       for (int i = tid; i < size; i += kEvictThreads) {
         const uint32_t k = key_at(i);
-        if (shift == 24 || k >> (shift + 8) == prefix >> (shift + 8)) atomicAdd(&sm.hist[k >> shift & 255], 1u);
+        if (shift == 24 || k >> (shift + 8) == prefix >> (shift + 8)) atomicAdd(&hist[k >> shift & 255], 1u);
       }
       meet();
       if (tid < kDigits) {
         uint32_t t = 0;
-        for (int c = 0; c < ctas; ++c) t += ctas > 1 ? cluster.map_shared_rank(sm.hist, c)[tid] : sm.hist[tid];
+        for (int c = 0; c < ctas; ++c) t += ctas > 1 ? cluster.map_shared_rank(hist, c)[tid] : hist[tid];
         sm.total[tid] = t;
+      } else {
+        sm.hist[~shift >> 3 & 1][tid - kDigits] = 0;  // the pass before: everyone has read it, and the next one wants it clear
       }
-      meet();  // the histograms are read: the next pass may clear them
+      __syncthreads();
       if (wid == 0) {  // the digit with which the count from above reaches m: lane 0 has the top 8
         uint32_t c[8], sum = 0;
 #pragma unroll
@@ -171,6 +194,7 @@ __global__ void __launch_bounds__(kEvictThreads, 2) evict_kernel(const EvictArgs
     sm.above[wid] = ca;
     sm.on[wid] = co;
   }
+  if (tid == 0) sm.first_gone = keep;
   __syncthreads();
   if (wid == 0) {
     const uint32_t x = __reduce_add_sync(kFull, lane < kEvictWarps ? sm.above[lane] : 0u);
@@ -193,15 +217,23 @@ __global__ void __launch_bounds__(kEvictThreads, 2) evict_kernel(const EvictArgs
   int32_t* kept = a.kept + (int64_t)row * a.stride;
   float* out = a.weights_out + (int64_t)row * a.stride;
   const uint32_t before = (1u << lane) - 1;
+  int first = keep;  // the warp's first slot that does not stay
   for (int i = i0; i < i1; i += 32) {
-    const uint32_t k = i + lane < i1 ? key_at(i + lane) : 0u;
+    const float x = i + lane < i1 ? weight_at(i + lane) : 0.f;
+    const uint32_t k = key_of(x);
     const uint32_t va = __ballot_sync(kFull, i + lane < i1 && above(k)), vo = __ballot_sync(kFull, i + lane < i1 && on(k));
     const uint32_t ra = fa + __popc(va & before), ro = fo + __popc(vo & before);
     const bool tie = vo >> lane & 1;
-    if ((va >> lane & 1) || (tie && ro < (uint32_t)m)) {
+    const bool stays = (va >> lane & 1) || (tie && ro < (uint32_t)m);
+    const uint32_t gone = __ballot_sync(kFull, i + lane < i1 && !stays);
+    if (gone && first == keep) {
+      first = min(first, s0 + i + __ffs(gone) - 1);
+      if (lane == 0) atomicMin(&sm.first_gone, first);
+    }
+    if (stays) {
       const int at = lead + ra + min(ro, all || none ? 0u : (uint32_t)m);
       kept[at] = s0 + i + lane;
-      out[at] = w[s0 + i + lane];
+      out[at] = x;
     }
     fa += __popc(va);
     fo += __popc(vo);
@@ -223,89 +255,110 @@ __global__ void __launch_bounds__(kEvictThreads, 2) evict_kernel(const EvictArgs
   __threadfence();
   meet();  // the list is there
 
-  // ---- moving, from the first token that does not stay where it is (the list is i up to there, and above i behind it)
-  int from = lead, to = keep;
-  while (from < to) {
-    const int mid = from + (to - from) / 2;
-    if (__ldcg(kept + mid) == mid) from = mid + 1;
-    else to = mid;
+  // ---- moving, from the first token that does not stay where it is: the list is i below the first slot that goes
+  int from = keep;
+  for (int c = 0; c < ctas; ++c) from = min(from, *cluster.map_shared_rank(&sm.first_gone, c));
+  if (from >= keep) {
+    meet();  // before a CTA leaves
+    return;
   }
   const int32_t* table = a.block_table + (int64_t)b * a.max_blocks;
   bool bad = false;
-  // where slot p of this head is; -1: its page is none
-  auto tile_of = [&](int p) -> int64_t {
-    const int id = table[p / kPage];
-    if (id >= 0 && id < a.num_blocks) return ((int64_t)id * a.hkv + h) * T::BYTES;
-    bad = true;
-    return -1;
+  // The moves of the round that begins at token `first`, listed by a thread per token; all loads of a step before the next.
+  auto list = [&](int first, Move* to) {
+    constexpr int EACH = (T::TOKENS + kEvictThreads - 1) / kEvictThreads;
+    int p[EACH], from_id[EACH], to_id[EACH];
+#pragma unroll
+    for (int u = 0; u < EACH; ++u) p[u] = __ldcg(kept + min(first + u * kEvictThreads + tid, keep - 1));
+#pragma unroll
+    for (int u = 0; u < EACH; ++u) {
+      from_id[u] = table[p[u] / kPage];
+      to_id[u] = table[min(first + u * kEvictThreads + tid, keep - 1) / kPage];
+    }
+#pragma unroll
+    for (int u = 0; u < EACH; ++u) {
+      const int k = u * kEvictThreads + tid, i = first + k;
+      const bool ok = (unsigned)from_id[u] < (unsigned)a.num_blocks && (unsigned)to_id[u] < (unsigned)a.num_blocks;
+      bad |= i < keep && k < T::TOKENS && !ok;
+      Move m{-1, -1};
+      if (ok && i < keep) {
+        m.src = ((int64_t)from_id[u] * a.hkv + h) * T::BYTES + p[u] % kPage;
+        m.dst = ((int64_t)to_id[u] * a.hkv + h) * T::BYTES + i % kPage;
+      }
+      if (k < T::TOKENS) to[k] = m;
+    }
   };
+  int turn = 0;
+  list(from + rank * T::TOKENS, sm.move[0]);
+  __syncthreads();
 #pragma unroll 1
-  for (int first = from + rank * T::TOKENS; first - rank * T::TOKENS < keep; first += ctas * T::TOKENS) {
+  for (int first = from + rank * T::TOKENS; first - rank * T::TOKENS < keep; first += ctas * T::TOKENS, turn ^= 1) {
+    const Move* moves = sm.move[turn];
     uint4 x[kInFlight];
-    int64_t to_at[kInFlight];
 #pragma unroll
     for (int u = 0; u < kInFlight; ++u) {
-      const int unit = u * kEvictThreads + tid, i = first + unit / T::PIECES, piece = unit % T::PIECES;
-      to_at[u] = -1;
-      if (i < keep) {
-        const int p = __ldcg(kept + i);
-        const int64_t src = tile_of(p), dst = tile_of(i);
-        const int side = piece / (T::PIECES / 2), col = (side * kPage * T::ROW) + piece % (T::PIECES / 2) * 16;
-        if (src >= 0 && dst >= 0) {
-          x[u] = *reinterpret_cast<const uint4*>(a.pool + src + col + p % kPage * T::ROW);
-          to_at[u] = dst + col + i % kPage * T::ROW;
-        }
-      }
+      const int unit = u * kEvictThreads + tid, piece = unit % T::PIECES, side = piece / (T::PIECES / 2);
+      const int64_t src = moves[unit / T::PIECES].src;
+      if (src >= 0)
+        x[u] = *reinterpret_cast<const uint4*>(a.pool + (src & ~15ll) + (side * kPage + (src & 15)) * T::ROW + piece % (T::PIECES / 2) * 16);
     }
     // scales and exponents: a token per thread, TOKENS of them
-    constexpr int SMALL = BITS == 16 ? 0 : (T::TOKENS + kEvictThreads - 1) / kEvictThreads;
-    Scales<BITS == 4 ? T::SCALE : 4> sc[SMALL > 0 ? SMALL : 1][2];
-    uint8_t ex[SMALL > 0 ? SMALL : 1][2];
-    int64_t tail[SMALL > 0 ? SMALL : 1];
+    constexpr int SMALL = BITS == 16 ? 1 : (T::TOKENS + kEvictThreads - 1) / kEvictThreads;
+    Scales<BITS == 4 ? T::SCALE : 4> sc[SMALL][2];
+    uint8_t ex[SMALL][2];
     if constexpr (BITS < 16) {
 #pragma unroll
       for (int u = 0; u < SMALL; ++u) {
-        const int k = u * kEvictThreads + tid, i = first + k;
-        tail[u] = -1;
-        if (k < T::TOKENS && i < keep) {
-          const int p = __ldcg(kept + i), q = p % kPage;
-          const int64_t src = tile_of(p), dst = tile_of(i);
-          if (src >= 0 && dst >= 0) {
-            tail[u] = dst;
+        const int k = u * kEvictThreads + tid;
+        const int64_t src = k < T::TOKENS ? moves[k].src : -1;
+        if (src >= 0) {
+          const uint8_t* tile = a.pool + (src & ~15ll);
 #pragma unroll
-            for (int side = 0; side < 2; ++side) {
-              ex[u][side] = a.pool[src + T::AT_EXP + side * kPage + q];
-              if constexpr (BITS == 4)
-                sc[u][side] = *reinterpret_cast<const Scales<T::SCALE>*>(a.pool + src + T::AT_SCALE + (side * kPage + q) * T::SCALE);
-            }
+          for (int side = 0; side < 2; ++side) {
+            const int row = side * kPage + (int)(src & 15);
+            ex[u][side] = tile[T::AT_EXP + row];
+            if constexpr (BITS == 4) sc[u][side] = *reinterpret_cast<const Scales<T::SCALE>*>(tile + T::AT_SCALE + row * T::SCALE);
           }
         }
       }
     }
+    const int next = first + ctas * T::TOKENS;
+    if (next < keep) list(next, sm.move[turn ^ 1]);
+    else {  // this CTA is through, the cluster may not be
+      for (int k = tid; k < T::TOKENS; k += kEvictThreads) sm.move[turn ^ 1][k] = Move{-1, -1};
+    }
     meet();
 #pragma unroll
-    for (int u = 0; u < kInFlight; ++u)
-      if (to_at[u] >= 0) *reinterpret_cast<uint4*>(a.pool + to_at[u]) = x[u];
+    for (int u = 0; u < kInFlight; ++u) {
+      const int unit = u * kEvictThreads + tid, piece = unit % T::PIECES, side = piece / (T::PIECES / 2);
+      const int64_t dst = moves[unit / T::PIECES].dst;
+      if (dst >= 0)
+        *reinterpret_cast<uint4*>(a.pool + (dst & ~15ll) + (side * kPage + (dst & 15)) * T::ROW + piece % (T::PIECES / 2) * 16) = x[u];
+    }
     if constexpr (BITS < 16) {
 #pragma unroll
       for (int u = 0; u < SMALL; ++u) {
-        if (tail[u] < 0) continue;
-        const int q = (first + u * kEvictThreads + tid) % kPage;
+        const int k = u * kEvictThreads + tid;
+        const int64_t dst = k < T::TOKENS ? moves[k].dst : -1;
+        if (dst >= 0) {
+          uint8_t* tile = a.pool + (dst & ~15ll);
 #pragma unroll
-        for (int side = 0; side < 2; ++side) {
-          a.pool[tail[u] + T::AT_EXP + side * kPage + q] = ex[u][side];
-          if constexpr (BITS == 4)
-            *reinterpret_cast<Scales<T::SCALE>*>(a.pool + tail[u] + T::AT_SCALE + (side * kPage + q) * T::SCALE) = sc[u][side];
+          for (int side = 0; side < 2; ++side) {
+            const int row = side * kPage + (int)(dst & 15);
+            tile[T::AT_EXP + row] = ex[u][side];
+            if constexpr (BITS == 4) *reinterpret_cast<Scales<T::SCALE>*>(tile + T::AT_SCALE + row * T::SCALE) = sc[u][side];
+          }
         }
       }
     }
+    __syncthreads();  // the list is read before the round after the next one writes it
   }
   if (bad) flag_error(a.err, TQ_DEVERR_BLOCK_ID);
 }
 
 // Pages that hold no token any more, behind the queue's end in order.  A CTA has a stretch of the requests and adds up itself
 // what those in front give back: a few bytes per request from L2, against a second launch or CTAs that wait for one another.
-constexpr int kReleaseThreads = 256;
+constexpr int kReleaseThreads = 1024;
 
 __global__ void __launch_bounds__(kReleaseThreads) release_kernel(const ReleaseArgs a) {
   __shared__ int64_t part[kReleaseThreads / 32];
@@ -347,7 +400,8 @@ __global__ void __launch_bounds__(kReleaseThreads) release_kernel(const ReleaseA
         break;
       }
       if (id < 0 || id >= a.num_blocks) flags |= TQ_DEVERR_BLOCK_ID;
-      a.queue[((int64_t)head + count + at + j) % a.queue_cap] = id;
+      const int64_t to = (int64_t)head + count + at + j;  // below twice the capacity
+      a.queue[to < a.queue_cap ? to : to - a.queue_cap] = id;
     }
     at += max(gone, 0);
   }
@@ -362,7 +416,7 @@ __global__ void __launch_bounds__(kReleaseThreads) release_kernel(const ReleaseA
 template <int BITS, int D>
 cudaError_t launch_evict_t(tq_ctx* ctx, const EvictArgs& a, cudaStream_t s) {
   const int64_t rows = (int64_t)a.batch * a.hkv;
-  // CTAs per row: enough for two on every multiprocessor, up to the portable cluster
+  // CTAs per row: enough for two on every multiprocessor, up to the portable cluster (16: 1 x 32K to 2K 29.3 us against 26.6)
   int ctas = 1;
   while (ctas < 8 && rows * ctas * 2 <= 2 * (int64_t)ctx->sm_count) ctas *= 2;
   auto kern = evict_kernel<BITS, D>;

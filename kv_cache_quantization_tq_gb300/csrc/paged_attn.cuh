@@ -113,7 +113,7 @@ struct PagedCfg {
   // 8 x 2 (128 KB) 87.0 and 634, 16 x 1 (128 KB) 88.7 and 644.  e4m3 pages of d = 128, 64 ragged sequences: 16 x 1 (64 KB)
   // 173 us, 16 x 2 (128 KB) 181.
   // (e4m3 at d = 64 with 16 query heads has no registers for 16 warps: 16 92.1 us, 12 87.2.)
-  static constexpr int NW = PAGE1 <= 4096 && QREG && (KEYS || KIND != kE2M1) && (NT == 1 || ES == 2) && fits(16, 1) ? 16 : fits(12, 1) ? 12 : fits(8, 1) ? 8 : fits(6, 1) ? 6 : 4;
+  static constexpr int NW = PAGE1 <= 4096 && QREG && (KEYS || KIND != kE2M1 || D == 64) && (NT == 1 || ES == 2) && fits(16, 1) ? 16 : fits(12, 1) ? 12 : fits(8, 1) ? 8 : fits(6, 1) ? 6 : 4;
   static constexpr int S_WANT = (ES == 1 ? 96 : 128) * 1024 / (NW * PAGE);
   static constexpr int S_LEAST = S_WANT > 8 ? 8 : S_WANT > MIN_S ? S_WANT : MIN_S;
   static constexpr int S = S_LEAST < stages(NW) ? S_LEAST : stages(NW);
@@ -431,16 +431,33 @@ __device__ __forceinline__ void tf32_parts(float x, uint32_t& high, uint32_t& lo
   low = (__float_as_uint(x - __uint_as_float(high)) + 0x1000u) & 0xffffe000u;
 }
 
-// tanh x.  Below 0.9 in magnitude x + x y P(y), y = x^2, P fitted to (tanh x / x - 1) / y with a relative error of 1.6e-8;
-// above 1 - 2 / (e^2x + 1), where little cancels (e^2x may be infinite).  Within 2.2e-7 of the result (8e-8 below 0.9).
-__device__ __forceinline__ float tanh_of(float x) {
-  const float a = fabsf(x), y = x * x;
-  float r;
-  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(ex2(a * 2.88539008177792681472f) + 1.f));
-  const float far = copysignf(fmaf(-2.f, r, 1.f), x);
-  float p = fmaf(0.00130396f, y, -0.006860055f);
-  p = fmaf(fmaf(fmaf(fmaf(p, y, 0.020904126f), y, -0.05372149f), y, 0.1333036f), y, -0.33333212f);
-  return a < 0.9f ? fmaf(p * y, x, x) : far;
+// cap tanh x of N values, for a whole warp.  Below 0.9 in magnitude tanh x = x + x y P(y), y = x^2, P fitted to
+// (tanh x / x - 1) / y with a relative error of 1.6e-8; above 1 - 2 / (e^2x + 1), where little cancels (e^2x may be
+// infinite).  Within 2.2e-7 of the result (8e-8 below 0.9).  Scores are mostly far below the cap: the second form is left
+// out where no lane needs it.
+template <int N>
+__device__ __forceinline__ void cap_scores(float (&x)[N], float cap) {
+  bool beyond = false;
+  float near[N];
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    const float y = x[i] * x[i];
+    float p = fmaf(0.00130396f, y, -0.006860055f);
+    p = fmaf(fmaf(fmaf(fmaf(p, y, 0.020904126f), y, -0.05372149f), y, 0.1333036f), y, -0.33333212f);
+    near[i] = fmaf(p * y, x[i], x[i]);
+    beyond |= !(fabsf(x[i]) < 0.9f);
+  }
+  if (__any_sync(kFull, beyond)) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const float a = fabsf(x[i]);
+      float r;
+      asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(ex2(a * 2.88539008177792681472f) + 1.f));
+      near[i] = a < 0.9f ? near[i] : copysignf(fmaf(-2.f, r, 1.f), x[i]);
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < N; ++i) x[i] = cap * near[i];
 }
 
 // ---------------------------------------------------------------- scan and walk over the line
@@ -628,6 +645,10 @@ __global__ void __launch_bounds__(PagedCfg<KIND, D, N8, MODE>::THREADS, 1)
     }
   }
 
+  // Scores that are biased by distance mostly grow from page to page: from the newest page on the references stand, where
+  // the other way they would be raised every time (64 ragged sequences, e4m3, slopes down to 2^-0.25: 200 us).
+  const bool back = MODE == kScored && w.slopes != nullptr;
+
   // ---- fetching
   // Block ids are looked up by batches of up to 32 pages (one per lane), a batch ahead, and the queries of a new
   // portion are brought to L1 then: with every stage in flight a load waits its turn for microseconds.
@@ -665,7 +686,7 @@ __global__ void __launch_bounds__(PagedCfg<KIND, D, N8, MODE>::THREADS, 1)
       in_reg = in;
     }
     next_n = in_done ? 0 : min(in.take - in_i, 32);
-    if (lane < next_n) next_id = a.block_table[(int64_t)in.b * a.max_blocks + in.s.first + in.p + in_i + lane];
+    if (lane < next_n) next_id = a.block_table[(int64_t)in.b * a.max_blocks + in.s.first + in.p + (back ? in.take - 1 - in_i - lane : in_i + lane)];
     in_i += next_n;
   };
   if (busy) {
@@ -1027,7 +1048,7 @@ __global__ void __launch_bounds__(PagedCfg<KIND, D, N8, MODE>::THREADS, 1)
 
       if (here) {
         // ---- weights
-        const int rel = out.p + i;  // page of the segment
+        const int rel = out.p + (back ? out.take - 1 - i : i);  // page of the segment
         const bool whole = rel != cut_first && rel != cut_last;
         const int t_lo = out.s.lo - (out.s.first + rel) * kPage, t_hi = out.s.len - (out.s.first + rel) * kPage;
         auto counts = [&](int tok) { return tok >= t_lo && tok < t_hi; };
@@ -1046,9 +1067,7 @@ __global__ void __launch_bounds__(PagedCfg<KIND, D, N8, MODE>::THREADS, 1)
         if constexpr (MODE != kAttend) {
           if (capped) {
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-              for (int k = 0; k < 4; ++k) s[nt][k] = cap2 * tanh_of(s[nt][k]);
+            for (int nt = 0; nt < NT; ++nt) cap_scores(s[nt], cap2);
           }
           if (w.slopes) {
             const float back0 = (float)(g + 1 - t_hi), back1 = (float)(g + 9 - t_hi);
@@ -1224,7 +1243,9 @@ __global__ void __launch_bounds__(PagedCfg<KIND, D, N8, MODE>::THREADS, 1)
 #pragma unroll 1
     for (int i = 0; i < out.take; i += PP, st = st + 1 == S ? 0 : st + 1) {
       const uint32_t here = valid >> 2 * st & 3;
-      const int rel = out.p + i, first = (out.s.first + rel) * kPage;  // page of the segment, position of its first token
+      // page of the segment, position of its first token; and of the second page of the step
+      const int rel = out.p + (back ? out.take - 1 - i : i), rel2 = back ? rel - 1 : rel + 1;
+      const int first = (out.s.first + rel) * kPage, on = back ? -kPage : kPage;
       // the weights' sums so far: a lane has token tok0 + 8 (t & 1) of page t >> 1
       const int pos = first + 16 * (t >> 1) + tok0 + 8 * (t & 1);
       const int64_t at = ((int64_t)out.b * a.hkv + kvh) * w.w_stride + pos;
@@ -1260,9 +1281,9 @@ __global__ void __launch_bounds__(PagedCfg<KIND, D, N8, MODE>::THREADS, 1)
       }
       if (C::KEYS) next_pages();  // the keys are read
       if (here) {
-        const bool whole = here == (1u << PP) - 1 && rel != cut_first && rel + PP - 1 != cut_last;
+        const bool whole = here == (1u << PP) - 1 && rel != cut_first && rel != cut_last && (PP == 1 || (rel2 != cut_first && rel2 != cut_last));
         auto counts = [&](int pg, int tok) {
-          const int x = first + pg * kPage + tok;
+          const int x = first + pg * on + tok;
           return x >= out.s.lo && x < out.s.len && (here >> pg & 1);
         };
 #pragma unroll
@@ -1281,12 +1302,10 @@ __global__ void __launch_bounds__(PagedCfg<KIND, D, N8, MODE>::THREADS, 1)
           if constexpr (MODE != kAttend) {
             if (capped) {
 #pragma unroll
-              for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                for (int k = 0; k < 4; ++k) s[pg][nt][k] = cap2 * tanh_of(s[pg][nt][k]);
+              for (int nt = 0; nt < NT; ++nt) cap_scores(s[pg][nt], cap2);
             }
             if (w.slopes) {
-              const int x = first + pg * kPage + tok0 + 1 - out.s.len;
+              const int x = first + pg * on + tok0 + 1 - out.s.len;
               const float back0 = (float)x, back1 = (float)(x + 8);
 #pragma unroll
               for (int nt = 0; nt < NT; ++nt)

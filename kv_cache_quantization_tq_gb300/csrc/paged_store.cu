@@ -163,16 +163,22 @@ __global__ void __launch_bounds__(kStoreThreads) store_kernel(const StoreArgs a,
         uint32_t sc = __nv_cvt_float_to_fp8(__fdiv_rn(value(m) * down, 6.f), __NV_SATFINITE, __NV_E4M3);
         if (all >= inf) sc = all > inf ? 0x7fu : 0x7eu;
         const float scale = __half2float(__half(__nv_cvt_fp8_to_halfraw((__nv_fp8_storage_t)sc, __NV_E4M3)));
-        const float inverse = scale > 0.f ? __fdividef(1.f, scale) : 0.f;
+        // 2^-e / s in one factor where that is a number: s >= 2^-9
+        const bool tiny = __any_sync(kFull, e < -110);
+        const float inverse = scale > 0.f ? __fdividef(tiny ? 1.f : down, scale) : 0.f;
         uint32_t c[2];
 #pragma unroll
         for (int k2 = 0; k2 < 2; ++k2) {
           float y[8];
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            const float2 f = pair_of<BF>(w[4 * k2 + i]);
-            y[2 * i] = copysignf(fmaf(f.x * down, inverse, 768.f) - 768.f, f.x);
-            y[2 * i + 1] = copysignf(fmaf(f.y * down, inverse, 768.f) - 768.f, f.y);
+            float2 f = pair_of<BF>(w[4 * k2 + i]);
+            if (tiny) {
+              f.x *= down;
+              f.y *= down;
+            }
+            y[2 * i] = copysignf(fmaf(f.x, inverse, 768.f) - 768.f, f.x);
+            y[2 * i + 1] = copysignf(fmaf(f.y, inverse, 768.f) - 768.f, f.y);
           }
           c[k2] = all > inf ? 0u : e2m1_of(y);
         }
