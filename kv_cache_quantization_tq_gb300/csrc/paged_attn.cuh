@@ -252,8 +252,11 @@ __device__ __forceinline__ void tma_load(uint32_t dst, const CUtensorMap* map, i
       "l"(map), "r"(x), "r"(y), "r"(z), "r"(bar)
       : "memory");
 }
-__device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+// 16 bytes of a lane, where `there`: a predicate, not a branch.
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool there) {
+  asm volatile("{ .reg .pred p; setp.ne.b32 p, %2, 0; @p cp.async.cg.shared.global [%0], [%1], 16; }" ::"r"(dst), "l"(src),
+               "r"((int)there)
+               : "memory");
 }
 __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
   asm volatile("cp.async.bulk.shared::cta.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
@@ -736,28 +739,25 @@ __global__ void __launch_bounds__(PagedCfg<KIND, D, N8, MODE>::THREADS, 1)
 #pragma unroll
     for (int pg = 0; pg < C::PP; ++pg) {
       const int which = pg ? tile2 : tile;
-      if (which >= 0) {
-        const uint8_t* src = a.pool + (size_t)which * C::TILE + lane * 16;
-        const uint32_t dst = stage0 + st * C::PAGE + pg * C::PAGE1, tail = exp0 + st * C::EXP + pg * C::EXP1 + lane * 16;
-        constexpr int PR = C::ROW / 16, RS = PR < 32 ? 32 / PR : 1;  // pieces of a row, rows of a warp's copy
+      const bool has = which >= 0;
+      const uint8_t* src = a.pool + (size_t)which * C::TILE + lane * 16;
+      const uint32_t dst = stage0 + st * C::PAGE + pg * C::PAGE1, tail = exp0 + st * C::EXP + pg * C::EXP1 + lane * 16;
+      constexpr int PR = C::ROW / 16, RS = PR < 32 ? 32 / PR : 1;  // pieces of a row, rows of a warp's copy
 #pragma unroll
-        for (int i = 0; i < C::PAGE1 / 512; ++i) {
-          const int row = PR <= 32 ? i * RS + lane / (PR <= 32 ? PR : 1) : i / (PR / 32);
-          const int c = PR <= 32 ? lane % PR : i % (PR / 32) * 32 + lane;
-          const int x = C::SWIZZLE_ROW == 128 ? row & 7 : C::SWIZZLE_ROW == 64 ? (row >> 1) & 3 : 0;
-          const int at = C::KEYS && !F4 ? (c >> 3) * C::BOX + row * C::SWIZZLE_ROW : row * C::ROW + (c >> 3) * 128;
-          copy16(dst + at + (((c & 7) ^ x) << 4), src + i * 512);
-        }
-        if constexpr (XP && !C::KEYS) {
-#pragma unroll
-          for (int i = 0; i < (C::EXP1 + 511) / 512; ++i)
-            if (i * 512 + lane * 16 < C::EXP1) copy16(tail + i * 512, src + 2 * C::HALF + i * 512);
-        }
-        if constexpr (F4 && C::KEYS)
-          if (lane * 16 < C::SCALES) copy16(tail, src + 2 * C::HALF);
-        if constexpr (XP && C::KEYS)
-          if (lane == 0) copy16(tail + C::AT_EXP, src + 2 * C::HALF + 2 * C::SCALES);
+      for (int i = 0; i < C::PAGE1 / 512; ++i) {
+        const int row = PR <= 32 ? i * RS + lane / (PR <= 32 ? PR : 1) : i / (PR / 32);
+        const int c = PR <= 32 ? lane % PR : i % (PR / 32) * 32 + lane;
+        const int x = C::SWIZZLE_ROW == 128 ? row & 7 : C::SWIZZLE_ROW == 64 ? (row >> 1) & 3 : 0;
+        const int at = C::KEYS && !F4 ? (c >> 3) * C::BOX + row * C::SWIZZLE_ROW : row * C::ROW + (c >> 3) * 128;
+        copy16(dst + at + (((c & 7) ^ x) << 4), src + i * 512, has);
       }
+      if constexpr (XP && !C::KEYS) {
+#pragma unroll
+        for (int i = 0; i < (C::EXP1 + 511) / 512; ++i)
+          copy16(tail + i * 512, src + 2 * C::HALF + i * 512, has && i * 512 + lane * 16 < C::EXP1);
+      }
+      if constexpr (F4 && C::KEYS) copy16(tail, src + 2 * C::HALF, has && lane * 16 < C::SCALES);
+      if constexpr (XP && C::KEYS) copy16(tail + C::AT_EXP, src + 2 * C::HALF + 2 * C::SCALES, has && lane == 0);
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
   };
@@ -1239,6 +1239,9 @@ __global__ void __launch_bounds__(PagedCfg<KIND, D, N8, MODE>::THREADS, 1)
       }
     }
     } else {
+    const int64_t w_row = ((int64_t)out.b * a.hkv + kvh) * w.w_stride;
+    const float* row_in = w.w_in ? w.w_in + w_row : nullptr;
+    float* row_out = w.w_out + w_row;
     // Up to d = 128 two pages a step: a page's share of the instructions that are not its own is halved.
 #pragma unroll 1
     for (int i = 0; i < out.take; i += PP, st = st + 1 == S ? 0 : st + 1) {
@@ -1248,10 +1251,9 @@ __global__ void __launch_bounds__(PagedCfg<KIND, D, N8, MODE>::THREADS, 1)
       const int first = (out.s.first + rel) * kPage, on = back ? -kPage : kPage;
       // the weights' sums so far: a lane has token tok0 + 8 (t & 1) of page t >> 1
       const int pos = first + 16 * (t >> 1) + tok0 + 8 * (t & 1);
-      const int64_t at = ((int64_t)out.b * a.hkv + kvh) * w.w_stride + pos;
       const bool mine = C::KEYS && pos < out.s.len && (t < 2 || (PP == 2 && i + 1 < out.take));
       float old = 0.f, added = 0.f;
-      if (mine && w.w_in) old = w.w_in[at];
+      if (mine && row_in) old = row_in[pos];
       asm volatile("cp.async.wait_group %0;" ::"n"(S - 1) : "memory");
       __syncwarp();
       auto next_pages = [&]() {
@@ -1263,7 +1265,7 @@ __global__ void __launch_bounds__(PagedCfg<KIND, D, N8, MODE>::THREADS, 1)
       // a page that is not there counts as one whose tokens do not
       float s[PP][NT][4];
       int ek[PP][2] = {}, ev[PP][2] = {};
-      if (here) {
+      {
 #pragma unroll
         for (int pg = 0; pg < PP; ++pg) {
           const uint32_t tail = exp0 + st * C::EXP + pg * C::EXP1;
@@ -1280,7 +1282,7 @@ __global__ void __launch_bounds__(PagedCfg<KIND, D, N8, MODE>::THREADS, 1)
         }
       }
       if (C::KEYS) next_pages();  // the keys are read
-      if (here) {
+      {
         const bool whole = here == (1u << PP) - 1 && rel != cut_first && rel != cut_last && (PP == 1 || (rel2 != cut_first && rel2 != cut_last));
         auto counts = [&](int pg, int tok) {
           const int x = first + pg * on + tok;
@@ -1313,7 +1315,10 @@ __global__ void __launch_bounds__(PagedCfg<KIND, D, N8, MODE>::THREADS, 1)
                 for (int k = 0; k < 4; ++k) s[pg][nt][k] = fmaf(slope[nt][k & 1], k < 2 ? back0 : back1, s[pg][nt][k]);
             }
           }
-          if (!whole) {  // rows that do not count are whatever memory held
+        }
+        if (!whole) {  // rows that do not count are whatever memory held
+#pragma unroll
+          for (int pg = 0; pg < PP; ++pg) {
             const bool ok0 = counts(pg, tok0), ok1 = counts(pg, tok0 + 8);
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
@@ -1330,9 +1335,10 @@ __global__ void __launch_bounds__(PagedCfg<KIND, D, N8, MODE>::THREADS, 1)
 #pragma unroll
             for (int k = 0; k < 4; ++k)
 #pragma unroll
-              for (int pg = 0; pg < PP; ++pg) {  // heads that are none have lse inf; their products with a key that is not finite do not count
-                const float z = nt * 8 + 2 * t + (k & 1) < nh ? s[pg][nt][k] : 0.f, y = fmaf(z, up_hi, -lse_hi[nt][k & 1]);
-                sum[2 * pg + (k >> 1)] += ex2(fabsf(z) < CUDART_INF_F ? fmaf(z, up_lo, y) - lse_lo[nt][k & 1] : y);
+              for (int pg = 0; pg < PP; ++pg) {
+                // heads that are none have lse inf and scores 0, but of a 16-bit key that is infinite
+                const float z = C::ES == 1 || nt * 8 + 2 * t + (k & 1) < nh ? s[pg][nt][k] : 0.f;
+                sum[2 * pg + (k >> 1)] += ex2(fmaf(z, up_lo, fmaf(z, up_hi, -lse_hi[nt][k & 1])) - lse_lo[nt][k & 1]);
               }
           // lane t gets the total of sum[t] over the four lanes
           const bool odd = t & 1, high = t & 2;
@@ -1517,7 +1523,7 @@ __global__ void __launch_bounds__(PagedCfg<KIND, D, N8, MODE>::THREADS, 1)
         }
       }
       if (C::KEYS) {
-        if (mine) w.w_out[at] = fmaf(w.decay, old, added);
+        if (mine) row_out[pos] = fmaf(w.decay, old, added);
       } else {
         next_pages();
       }
@@ -1882,9 +1888,12 @@ cudaError_t launch_weights_one(tq_ctx* ctx, const PagedArgs& a, const ScoreArgs&
   using C = PagedCfg<KIND, D, NT, kWeights>;
   PagedWork w = work_of<KIND, D, NT, kWeights>(ctx, a, sc);
   const PagedPlan plan = w.p;
+  // both of one sign, none 0: an infinite score stays what it is
   const double up = a.scale * 1.4426950408889634074;
   w.up_hi = (float)up;
+  if (fabs((double)w.up_hi) > fabs(up)) w.up_hi = nextafterf(w.up_hi, 0.f);
   w.up_lo = (float)(up - w.up_hi);
+  if (w.up_lo == 0.f) w.up_lo = copysignf(1e-37f, a.scale);
   w.lse_in = wa.lse;
   w.w_in = wa.in;
   w.w_out = wa.out;

@@ -167,21 +167,22 @@ __global__ void __launch_bounds__(kStoreThreads) store_kernel(const StoreArgs a,
         const bool tiny = __any_sync(kFull, e < -110);
         const float inverse = scale > 0.f ? __fdividef(tiny ? 1.f : down, scale) : 0.f;
         uint32_t c[2];
+        auto codes = [&](float first) {
 #pragma unroll
-        for (int k2 = 0; k2 < 2; ++k2) {
-          float y[8];
+          for (int k2 = 0; k2 < 2; ++k2) {
+            float y[8];
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            float2 f = pair_of<BF>(w[4 * k2 + i]);
-            if (tiny) {
-              f.x *= down;
-              f.y *= down;
+            for (int i = 0; i < 4; ++i) {
+              float2 f = pair_of<BF>(w[4 * k2 + i]);
+              y[2 * i] = copysignf(fmaf(f.x * first, inverse, 768.f) - 768.f, f.x);
+              y[2 * i + 1] = copysignf(fmaf(f.y * first, inverse, 768.f) - 768.f, f.y);
             }
-            y[2 * i] = copysignf(fmaf(f.x, inverse, 768.f) - 768.f, f.x);
-            y[2 * i + 1] = copysignf(fmaf(f.y, inverse, 768.f) - 768.f, f.y);
+            c[k2] = e2m1_of(y);
           }
-          c[k2] = all > inf ? 0u : e2m1_of(y);
-        }
+        };
+        if (tiny) codes(down);
+        else codes(1.f);
+        if (all > inf) c[0] = c[1] = 0u;
         if (p[k].tile) {
           reinterpret_cast<uint2*>(p[k].tile + (size_t)p[k].at * (D / 2))[p[k].i] = make_uint2(c[0], c[1]);
           p[k].tile[16 * D + p[k].at * L + p[k].i] = (uint8_t)sc;
