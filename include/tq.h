@@ -449,7 +449,7 @@ tq_status tq_paged_workspace_size(const tq_ctx* ctx, int batch, size_t* bytes);
  * TQ_DEVERR_TIMEOUT, and the rows it has a part in become NaN.  A NaN or an infinity in a row that counts makes
  * what depends on it NaN (weights are multiplied in parts).  Sums are held in 32 bits: they overflow where the
  * number of positions times the largest |value| passes 2^127, and weights below about 2^-100 of a row's largest and values
- * whose vector is below about 2^-100 (8-bit pages: 2^-78) count with fewer bits or not at all.  On 8-bit pages a position counts to within 2^-36 of the
+ * whose vector is below about 2^-100 (8-bit pages: 2^-78, 4-bit pages: 2^-75) count with fewer bits or not at all.  On 8- and 4-bit pages a position counts to within 2^-36 of the
  * row's largest weight times |value|, and a bf16 query entry to within 2^-39 of its head's largest.  num_blocks * Hkv must be below 2^31.  The current device
  * must be the context's (TQ_ERR_INVALID_ARG), here and in the two calls above. */
 tq_status tq_paged_attention(tq_ctx* ctx, const void* q, int64_t q_stride, int batch, const void* pool, int num_blocks,
@@ -475,8 +475,8 @@ tq_status tq_paged_attention_scored(tq_ctx* ctx, const void* q, int64_t q_stride
  *                that does not overlap it
  *   decay        any finite number
  * A length beyond weights_stride or the block table, or negative, counts as 0 with TQ_DEVERR_POSITION; tokens of a page whose
- * id is outside [0, num_blocks) get no weight, with TQ_DEVERR_BLOCK_ID; after TQ_DEVERR_TIMEOUT the sums of the tokens
- * concerned are NaN.  Needs no workspace. */
+ * id is outside [0, num_blocks) get no weight, with TQ_DEVERR_BLOCK_ID.  A NaN in a key, query or lse makes the sums that
+ * depend on it NaN.  Needs no workspace. */
 tq_status tq_paged_weights(tq_ctx* ctx, const void* q, int64_t q_stride, int batch, const void* pool, int num_blocks,
                            const int32_t* block_table, int max_blocks, const int32_t* lengths, int window, float scale,
                            float cap, const float* slopes, const float* lse, const float* weights, float decay,
@@ -512,8 +512,9 @@ tq_status tq_release_pages(tq_ctx* ctx, const int32_t* lengths, const int32_t* n
                            const int32_t* block_table, int max_blocks, int num_blocks, int32_t* queue, int queue_cap,
                            const int32_t* queue_state, int32_t* queue_state_out, cudaStream_t stream);
 
-/* How long later tq_paged_attention, _scored and tq_paged_weights calls (and graphs captured later) wait for a copy of their own before they give
- * up with TQ_DEVERR_TIMEOUT; 10^9 nanoseconds unless set.  Meant for tests of that path: with 0 a warp's first
+/* How long later tq_paged_attention calls (and _scored ones, and graphs captured later) wait for a copy of their own before they give
+ * up with TQ_DEVERR_TIMEOUT; 10^9 nanoseconds unless set.  4-bit pages and tq_paged_weights wait by counting their
+ * copies, without a limit.  Meant for tests of that path: with 0 a warp's first
  * copy is waited for as usual and the next one counts as late.  Host only. */
 tq_status tq_set_wait_limit(tq_ctx* ctx, uint32_t nanoseconds);
 

@@ -484,15 +484,15 @@ class Context:
         """tq_paged_store: k, v [n_tokens, Hkv, d] of the context's 16-bit type (rows may be strided) into the pages;
         slots int64 [n_tokens], negative to skip a token."""
         _, i64, _, u8 = self._types or self._look_up()
-        elem, n = self._elem, k.shape[0]
+        elem, n = self._elem, k.size(0)
         kp, ks = self._rows_of(k, self.num_kv_heads, elem, "k")
         vp, vs = self._rows_of(v, self.num_kv_heads, elem, "v")
-        if v.shape[0] != n or slots.numel() != n:
+        if v.size(0) != n or slots.numel() != n:
             raise ValueError("k, v must be [n_tokens, Hkv, d] and slots [n_tokens]")
         self._check_pool(pool)
         a_slots, = self._addrs(i64, "slots", slots)
         a_pool, = self._addrs(u8, "pool", pool)
-        st = lib.tq_paged_store(self.ptr, kp, vp, ks, vs, a_slots, n, a_pool, pool.shape[0],
+        st = lib.tq_paged_store(self.ptr, kp, vp, ks, vs, a_slots, n, a_pool, pool.size(0),
                                 self._raw(self._device) if stream is None else _stream(stream))
         if st:
             raise TQError(st, "tq_paged_store")
@@ -509,8 +509,9 @@ class Context:
         slopes (fp32 [Hq]) tq_paged_attention_scored: scores cap * tanh(score / cap) + slope * (position - newest position)."""
         i32, _, f32, u8 = self._types or self._look_up()
         qp, qs = self._rows_of(q, self.num_q_heads, self._elem, "q")
-        bsz = q.shape[0]
-        if out.shape != q.shape or lengths.numel() != bsz or (lse is not None and lse.shape != q.shape[:2]):
+        shape = q.shape
+        bsz = shape[0]
+        if out.shape != shape or lengths.numel() != bsz or (lse is not None and lse.shape != shape[:2]):
             raise ValueError("out must be [batch, Hq, d], lengths [batch] and lse [batch, Hq]")
         if not 0 <= window < 2 ** 31:
             raise ValueError("window must be 0 or a count below 2^31")
@@ -523,11 +524,11 @@ class Context:
         a_out, a_lse, a_slopes = self._addrs(f32, "out lse slopes", out, lse, slopes)
         stream = self._raw(self._device) if stream is None else _stream(stream)
         if cap or slopes is not None:
-            st, name = lib.tq_paged_attention_scored(self.ptr, qp, qs, bsz, a_pool, pool.shape[0], a_table, block_table.shape[1], a_len,
+            st, name = lib.tq_paged_attention_scored(self.ptr, qp, qs, bsz, a_pool, pool.size(0), a_table, block_table.size(1), a_len,
                                                      window, scale, cap, a_slopes, a_out, a_lse, a_ws, workspace.numel(),
                                                      stream), "tq_paged_attention_scored"
         else:
-            st, name = lib.tq_paged_attention(self.ptr, qp, qs, bsz, a_pool, pool.shape[0], a_table, block_table.shape[1], a_len, window,
+            st, name = lib.tq_paged_attention(self.ptr, qp, qs, bsz, a_pool, pool.size(0), a_table, block_table.size(1), a_len, window,
                                               scale, a_out, a_lse, a_ws, workspace.numel(), stream), "tq_paged_attention"
         if st:
             raise TQError(st, name)
@@ -539,11 +540,11 @@ class Context:
         paged_attention gives it with the same window, scale, cap and slopes."""
         i32, _, f32, u8 = self._types or self._look_up()
         qp, qs = self._rows_of(q, self.num_q_heads, self._elem, "q")
-        bsz = q.shape[0]
-        if lengths.numel() != bsz or lse.shape != q.shape[:2]:
+        bsz = q.size(0)
+        if lengths.numel() != bsz or lse.dim() != 2 or lse.size(0) != bsz or lse.size(1) != self.num_q_heads:
             raise ValueError("lengths must be [batch] and lse [batch, Hq]")
-        self._check_weights(weights_out, bsz, "weights_out")
-        if weights is not None and weights.shape != weights_out.shape:
+        shape = self._check_weights(weights_out, bsz, "weights_out")
+        if weights is not None and weights.shape != shape:
             raise ValueError("weights must be of the shape of weights_out")
         if not 0 <= window < 2 ** 31:
             raise ValueError("window must be 0 or a count below 2^31")
@@ -554,15 +555,17 @@ class Context:
         a_pool, = self._addrs(u8, "pool", pool)
         a_table, a_len = self._addrs(i32, "block_table lengths", block_table, lengths)
         a_lse, a_in, a_out, a_slopes = self._addrs(f32, "lse weights weights_out slopes", lse, weights, weights_out, slopes)
-        st = lib.tq_paged_weights(self.ptr, qp, qs, bsz, a_pool, pool.shape[0], a_table, block_table.shape[1], a_len, window, scale, cap,
-                                  a_slopes, a_lse, a_in, decay, a_out, weights_out.shape[2],
+        st = lib.tq_paged_weights(self.ptr, qp, qs, bsz, a_pool, pool.size(0), a_table, block_table.size(1), a_len, window, scale, cap,
+                                  a_slopes, a_lse, a_in, decay, a_out, shape[2],
                                   self._raw(self._device) if stream is None else _stream(stream))
         if st:
             raise TQError(st, "tq_paged_weights")
 
     def _check_weights(self, t, batch, name):
-        if len(t.shape) != 3 or t.shape[0] != batch or t.shape[1] != self.num_kv_heads:
+        shape = t.shape
+        if len(shape) != 3 or shape[0] != batch or shape[1] != self.num_kv_heads:
             raise ValueError(f"{name} must be [batch, {self.num_kv_heads}, n]")
+        return shape
 
     def paged_evict(self, weights, pool, block_table, lengths, keep, weights_out, lengths_out, kept, sinks=0, recent=0, stream=None):
         """tq_paged_evict: the keep[b] tokens with the largest weights (and the newest `recent`, the oldest `sinks`) move to
@@ -572,8 +575,8 @@ class Context:
         bsz = lengths.numel()
         if keep.numel() != bsz or lengths_out.numel() != bsz:
             raise ValueError("keep and lengths_out must be [batch]")
-        self._check_weights(weights, bsz, "weights")
-        if weights_out.shape != weights.shape or kept.shape != weights.shape:
+        shape = self._check_weights(weights, bsz, "weights")
+        if weights_out.shape != shape or kept.shape != shape:
             raise ValueError("weights_out and kept must be of the shape of weights")
         if not (0 <= sinks < 2 ** 31 and 0 <= recent < 2 ** 31):
             raise ValueError("sinks and recent must be counts below 2^31")
@@ -583,7 +586,7 @@ class Context:
         a_w, a_wo = self._addrs(f32, "weights weights_out", weights, weights_out)
         a_table, a_len, a_keep, a_lo, a_kept = self._addrs(i32, "block_table lengths keep lengths_out kept", block_table, lengths, keep,
                                                            lengths_out, kept)
-        st = lib.tq_paged_evict(self.ptr, a_w, weights.shape[2], bsz, a_pool, pool.shape[0], a_table, block_table.shape[1], a_len, a_keep,
+        st = lib.tq_paged_evict(self.ptr, a_w, shape[2], bsz, a_pool, pool.size(0), a_table, block_table.size(1), a_len, a_keep,
                                 sinks, recent, a_wo, a_lo, a_kept, self._raw(self._device) if stream is None else _stream(stream))
         if st:
             raise TQError(st, "tq_paged_evict")
@@ -603,7 +606,7 @@ class Context:
         a_len, a_new, a_table, a_queue, a_state, a_out = self._addrs(
             i32, "lengths new_lengths block_table queue queue_state queue_state_out", lengths, new_lengths, block_table, queue,
             queue_state, queue_state_out)
-        st = lib.tq_release_pages(self.ptr, a_len, a_new, bsz, a_table, block_table.shape[1], num_blocks, a_queue, queue.numel(),
+        st = lib.tq_release_pages(self.ptr, a_len, a_new, bsz, a_table, block_table.size(1), num_blocks, a_queue, queue.numel(),
                                   a_state, a_out, self._raw(self._device) if stream is None else _stream(stream))
         if st:
             raise TQError(st, "tq_release_pages")

@@ -1,7 +1,9 @@
-// Attention of one new token per sequence over dense-layout pages: kernels, included by one
-// translation unit per element type (paged_attn_f16.cu, paged_attn_bf16.cu, paged_attn_e4m3.cu).
+// Attention of one new token per sequence over dense-layout pages, and the weights of it added up per token: kernels,
+// included by one translation unit per element type and kind of call (paged_attn_*.cu, paged_scored_*.cu, paged_weights_*.cu).
 //
 //   s_p = scale q . k_p,  out = sum_p 2^(s_p log2(e) - m) v_p / sum_p 2^(s_p log2(e) - m)
+//   scored:  s_p = cap tanh(scale q . k_p / cap) + slope (p - newest position)
+//   weights: sums[p] = decay sums[p] + sum over a KV head's query heads of exp(s_p - lse)
 //
 // What bounds it: reading the cache once.  A step does 4 d operations per query head for the 4 d bytes (16
 // bits) of a token's key and value, far below what the tensor cores do in that time, so everything here
@@ -25,6 +27,19 @@
 // With tokens and dims on the 16-row side, 8 query heads per KV head fill the 8-column side and no row of the
 // products is padding; the accumulators are d / 4 registers.
 //
+// 4-bit pages (and weights alone) are bound by instructions: a page of d = 128 has 2.3 KB for the 4 KB of e4m3, and as many
+// elements to be made fp16 (code x scale, exact: one conversion and one multiplication per two, 128 a lane and page).  What was
+// taken off the rest, on 64 ragged sequences of 32 / 8 heads (614 MB, 92 us at the copy rate):
+//   one page a step, TMA, like e4m3                                             172 us, 538 warp instructions a page
+//   two pages a step up to d = 128, their products with V in one chain           163       494
+//   every lane copies its own 16-byte pieces (TMA needs its operands in uniform registers: 62 instructions a page)  153  435
+//   with up to 4 heads per KV head, both parts of the weights in the 8 columns of one product (24 -> 16 products a page)  137  416
+//   predicates in place of branches                                              131       402
+// Codes need no ldmatrix: a lane loads the codes of its own rows, of keys 32 dims in one place, of values D / 8 dims of 4
+// tokens, whose nibbles are paired by token before they are converted.  What is left: 65% of the issue slots with 3 warps per
+// scheduler (16 warps of 128 registers spill: 151 us); loading codes earlier, or more products abreast, changed nothing.
+// Weights alone: 147 us in the first form, 77 now (51 at the copy rate; the same from fp16 keys 173 of 165).
+//
 // Precision: q and k products are exact and summed in fp32.  A weight is split into parts whose products with V are
 // exact.  Each page's sum leaves the tensor core and is added to the running sum by an fp32 addition that rounds to
 // nearest (the tensor core cuts, which over thousands of pages would pull the sum towards zero); the weights' total is a
@@ -37,16 +52,16 @@
 // it does not matter what a token's values are worth beside its neighbours'.  (Two fp16 parts end at 2^-25, and a token
 // of small weight and large values then loses its bits.)  Two fp16 parts take the same time: 16 ragged sequences
 // 624 us, tf32 parts 622.
-//   e4m3 pages: codes are exact in fp16, and tf32 parts would cost their widening (64 ragged sequences 186 against
+//   e4m3 and 4-bit pages: elements are exact in fp16, and tf32 parts would cost their widening (64 ragged sequences 186 against
 // 173 us), so the weights have two fp16 parts.  Key exponents scale the fp32 scores, value exponents the weights.  As the
 // exponent is the size of a token's values, weight and exponent together say what the token is worth in the result: a
 // second reference per head, a power of two, holds the largest of these below 2^15 and, when it is set, at 2^12.  What
 // the parts leave out is 2^-37 of the largest token's share.
 //   Weights alone (kWeights) keep a score's whole error, so there every product of 16 dims leaves the tensor core and is added by
-// fp32 additions, and beside fp16 keys the queries have two parts, of 5 and 6 bits: products of 16 bits lie within what the
-// tensor core keeps of a sum, ones of 22 are cut, all in one direction (1 x 4K tokens of 16 / 4 heads: 1.2e-6 of the
-// result, 5e-7 in parts).
-//   bf16 queries on e4m3 pages are scaled by a power of two per head into fp16's range (exact down to 2^-31 of the
+// fp32 additions (4-bit keys: not needed, 5e-7 of the result), and beside fp16 keys the queries have two parts, of 5 and 6 bits:
+// products of 16 bits lie within what the tensor core keeps of a sum, ones of 22 are cut, all in one direction (1 x 4K
+// tokens of 16 / 4 heads: 1.2e-6 of the result, 8e-7 in parts).
+//   bf16 queries on these pages are scaled by a power of two per head into fp16's range (exact down to 2^-31 of the
 // head's largest entry); half of its inverse comes before a key's exponent and half behind it, so that large
 // keys with small queries do not overflow on the way.
 #pragma once
@@ -79,8 +94,10 @@ struct PagedCfg {
   static constexpr int ROW = KIND == kE2M1 ? D / 2 : D * ES;
   static constexpr int HALF = kPage * ROW;  // keys or values of a page
   static constexpr bool KEYS = MODE == kWeights;  // keys alone
-  static constexpr bool OWN = KEYS || KIND == kE2M1;       // every lane copies for itself, without TMA
-  static constexpr int PP = OWN && D <= 128 ? 2 : 1;       // pages of a step
+  static constexpr bool OWN = KEYS || KIND == kE2M1;  // every lane copies for itself, without TMA
+  // Pages of a step: two where a stage of two leaves room for 8 warps and more (d = 256, 8 x 32K of 40 / 8 heads, 4 bits: 6 warps
+  // with two 174 us, 8 with one 141).
+  static constexpr int PP = OWN && D <= 128 ? 2 : 1;
   static constexpr int PAGE1 = (KEYS ? 1 : 2) * HALF, PAGE = PP * PAGE1;  // bytes of one in a stage, and of a stage
   // What stands behind them in a tile: 4-bit pages' scales of the keys, of the values; the exponents of both.  Of that a stage has
   // EXP1 bytes of each page, the exponents from AT_EXP on.
@@ -112,7 +129,8 @@ struct PagedCfg {
   // them ends late.  16-bit pages of d = 128, 8 x 32K and 16 ragged sequences: 12 warps x 1 stage (96 KB) 85.8 and 622 us,
   // 8 x 2 (128 KB) 87.0 and 634, 16 x 1 (128 KB) 88.7 and 644.  e4m3 pages of d = 128, 64 ragged sequences: 16 x 1 (64 KB)
   // 173 us, 16 x 2 (128 KB) 181.
-  // (e4m3 at d = 64 with 16 query heads has no registers for 16 warps: 16 92.1 us, 12 87.2.)
+  // (e4m3 at d = 64 with 16 query heads has no registers for 16 warps: 16 92.1 us, 12 87.2.  4-bit pages have them at d = 64 only:
+  // 64 ragged sequences of 4 heads per KV head, d = 64 12 98.6 us, 16 92.3; d = 128 137 and 151.)
   static constexpr int NW = PAGE1 <= 4096 && QREG && (KEYS || KIND != kE2M1 || D == 64) && (NT == 1 || ES == 2) && fits(16, 1) ? 16 : fits(12, 1) ? 12 : fits(8, 1) ? 8 : fits(6, 1) ? 6 : 4;
   static constexpr int S_WANT = (ES == 1 ? 96 : 128) * 1024 / (NW * PAGE);
   static constexpr int S_LEAST = S_WANT > 8 ? 8 : S_WANT > MIN_S ? S_WANT : MIN_S;
@@ -848,7 +866,7 @@ __global__ void __launch_bounds__(PagedCfg<KIND, D, N8, MODE>::THREADS, 1)
           if (ks == 0) mma_first<BF>(sl[nt], af, y.x, y.y);
           else mma<BF>(sl[nt], af, y.x, y.y);
         }
-        if (C::KEYS && C::ES == 2 && ks >= 2) {  // the tensor core cuts what it adds up
+        if (C::KEYS && !F4 && ks >= 2) {  // the tensor core cuts what it adds up
           float one[4];
           mma_first<BF>(one, af, x.x, x.y);
 #pragma unroll
