@@ -10,7 +10,10 @@
 // registers hold: load, barrier, store.  kept[i] >= i, so a round's stores touch no token that a later round loads, and the
 // one barrier per round is all the order that is needed.
 //
-// What bounds it: the tokens that move, read once and written once; for a single sequence the chain of passes.
+// What bounds it: the tokens that move, read once and written once; in front of that, and for a single sequence all in all,
+// the chain of passes.  64 sequences of 8 heads from 4.2K to 4K tokens, e4m3 (a sixth of the tokens moves, 211 MB, 31 us at
+// the copy rate): 6 us to the weights, 10 to the threshold, 9 to the places, 29 of moves; 1 x 32K to 2K, fp16: 4.5, 7, 5.5
+// and 7 us.
 #include <cooperative_groups.h>
 
 #include "common.cuh"
@@ -21,11 +24,10 @@ namespace {
 
 namespace cg = cooperative_groups;
 
-constexpr int kEvictThreads = 512, kEvictWarps = kEvictThreads / 32;
+constexpr int kMostWarps = 16;
 constexpr int kHeld = 10 * 1024;   // weights of a CTA's slice that are kept in shared memory
 constexpr int kInFlight = 8;       // 16-byte pieces of a thread and round
 constexpr int kDigits = 256;
-static_assert(kEvictThreads == 2 * kDigits, "half of the threads add up, the others clear");
 
 // Where a token comes from and goes to: byte offsets of the tiles in the pool with the slots in their low 4 bits; -1: no move.
 struct __align__(16) Move {
@@ -38,7 +40,7 @@ struct EvictSmem {
   };
   uint32_t hist[2][kDigits];   // of this CTA; two passes' by turns
   uint32_t total[kDigits];     // of the cluster
-  uint32_t above[kEvictWarps], on[kEvictWarps];  // per warp: keys above the threshold, and equal to it
+  uint32_t above[kMostWarps], on[kMostWarps];  // per warp: keys above the threshold, and equal to it
   uint32_t cta_above, cta_on;
   int first_gone;  // lowest slot of the slice that does not stay
   uint32_t digit, left;
@@ -52,13 +54,13 @@ __device__ __forceinline__ uint32_t key_of(float x) {
 }
 
 // Byte layout of a tile: rows of keys, rows of values, 4-bit scales of both, exponents of both.
-template <int BITS, int D>
+template <int BITS, int D, int THREADS>
 struct Tile {
   static constexpr int ROW = D * BITS / 8, PIECES = 2 * ROW / 16;  // 16-byte pieces of a token's key and value
   static constexpr int SCALE = BITS == 4 ? D / 16 : 0;             // bytes of a token's scales on a side
   static constexpr int AT_SCALE = 2 * kPage * ROW, AT_EXP = AT_SCALE + 2 * kPage * SCALE;
   static constexpr int BYTES = AT_EXP + (BITS < 16 ? 2 * kPage : 0);
-  static constexpr int TOKENS = kEvictThreads * kInFlight / PIECES;  // of a CTA and round
+  static constexpr int TOKENS = THREADS * kInFlight / PIECES;  // of a CTA and round
   static_assert(TOKENS <= 1024 && BYTES % 16 == 0, "the moves' list");
 };
 
@@ -76,9 +78,10 @@ struct Scales<8> {
   uint2 v;
 };
 
-template <int BITS, int D>
-__global__ void __launch_bounds__(kEvictThreads, 2) evict_kernel(const EvictArgs a) {
-  using T = Tile<BITS, D>;
+template <int BITS, int D, int THREADS>
+__global__ void __launch_bounds__(THREADS, 1024 / THREADS) evict_kernel(const EvictArgs a) {
+  using T = Tile<BITS, D, THREADS>;
+  constexpr int WARPS = THREADS / 32;
   extern __shared__ __align__(16) uint8_t raw[];
   EvictSmem& sm = *reinterpret_cast<EvictSmem*>(raw);
   cg::cluster_group cluster = cg::this_cluster();
@@ -112,13 +115,13 @@ __global__ void __launch_bounds__(kEvictThreads, 2) evict_kernel(const EvictArgs
   const bool held = size <= kHeld;
   if (held) {
 #pragma unroll 1
-    for (int i = tid; i < size; i += 8 * kEvictThreads) {
+    for (int i = tid; i < size; i += 8 * THREADS) {
       float x[8];
 #pragma unroll
-      for (int k = 0; k < 8; ++k) x[k] = i + k * kEvictThreads < size ? w[s0 + i + k * kEvictThreads] : 0.f;
+      for (int k = 0; k < 8; ++k) x[k] = i + k * THREADS < size ? w[s0 + i + k * THREADS] : 0.f;
 #pragma unroll
       for (int k = 0; k < 8; ++k)
-        if (i + k * kEvictThreads < size) sm.held[i + k * kEvictThreads] = x[k];
+        if (i + k * THREADS < size) sm.held[i + k * THREADS] = x[k];
     }
   }
   auto weight_at = [&](int i) { return held ? sm.held[i] : w[s0 + i]; };
@@ -128,22 +131,23 @@ __global__ void __launch_bounds__(kEvictThreads, 2) evict_kernel(const EvictArgs
   uint32_t prefix = 0;
   const bool all = m >= hi - lo, none = m == 0;
   if (!all && !none) {
-    for (int i = tid; i < 2 * kDigits; i += kEvictThreads) sm.hist[i / kDigits][i % kDigits] = 0;
+    for (int i = tid; i < 2 * kDigits; i += THREADS) sm.hist[i / kDigits][i % kDigits] = 0;
     __syncthreads();
 #pragma unroll 1
     for (int shift = 24; shift >= 0; shift -= 8) {
       uint32_t* hist = sm.hist[shift >> 3 & 1];
-      for (int i = tid; i < size; i += kEvictThreads) {
+#pragma unroll 4
+      for (int i = tid; i < size; i += THREADS) {
         const uint32_t k = key_at(i);
         if (shift == 24 || k >> (shift + 8) == prefix >> (shift + 8)) atomicAdd(&hist[k >> shift & 255], 1u);
       }
       meet();
-      if (tid < kDigits) {
+      for (int i = tid; i < kDigits; i += THREADS) {
         uint32_t t = 0;
-        for (int c = 0; c < ctas; ++c) t += ctas > 1 ? cluster.map_shared_rank(hist, c)[tid] : hist[tid];
-        sm.total[tid] = t;
-      } else {
-        sm.hist[~shift >> 3 & 1][tid - kDigits] = 0;  // the pass before: everyone has read it, and the next one wants it clear
+        for (int c = 0; c < ctas; ++c) t += ctas > 1 ? cluster.map_shared_rank(hist, c)[i] : hist[i];
+        sm.total[i] = t;
+        // the pass before: everyone has read it, and the next one wants it clear
+        sm.hist[~shift >> 3 & 1][i] = 0;
       }
       __syncthreads();
       if (wid == 0) {  // the digit with which the count from above reaches m: lane 0 has the top 8
@@ -180,9 +184,10 @@ __global__ void __launch_bounds__(kEvictThreads, 2) evict_kernel(const EvictArgs
   auto on = [&](uint32_t k) { return !all && !none && k == prefix; };
 
   // ---- places: a warp has a stretch of the slice
-  const int stretch = (size + kEvictThreads - 1) / kEvictThreads * 32;  // stride <= 2^30: nothing here passes 31 bits
+  const int stretch = (size + THREADS - 1) / THREADS * 32;  // stride <= 2^30: nothing here passes 31 bits
   const int i0 = min(wid * stretch, size), i1 = min(i0 + stretch, size);
   uint32_t ca = 0, co = 0;
+#pragma unroll 4
   for (int i = i0 + lane; i < i1; i += 32) {
     const uint32_t k = key_at(i);
     ca += above(k);
@@ -197,8 +202,8 @@ __global__ void __launch_bounds__(kEvictThreads, 2) evict_kernel(const EvictArgs
   if (tid == 0) sm.first_gone = keep;
   __syncthreads();
   if (wid == 0) {
-    const uint32_t x = __reduce_add_sync(kFull, lane < kEvictWarps ? sm.above[lane] : 0u);
-    const uint32_t y = __reduce_add_sync(kFull, lane < kEvictWarps ? sm.on[lane] : 0u);
+    const uint32_t x = __reduce_add_sync(kFull, lane < WARPS ? sm.above[lane] : 0u);
+    const uint32_t y = __reduce_add_sync(kFull, lane < WARPS ? sm.on[lane] : 0u);
     if (lane == 0) {
       sm.cta_above = x;
       sm.cta_on = y;
@@ -218,6 +223,7 @@ __global__ void __launch_bounds__(kEvictThreads, 2) evict_kernel(const EvictArgs
   float* out = a.weights_out + (int64_t)row * a.stride;
   const uint32_t before = (1u << lane) - 1;
   int first = keep;  // the warp's first slot that does not stay
+#pragma unroll 2
   for (int i = i0; i < i1; i += 32) {
     const float x = i + lane < i1 ? weight_at(i + lane) : 0.f;
     const uint32_t k = key_of(x);
@@ -238,7 +244,7 @@ __global__ void __launch_bounds__(kEvictThreads, 2) evict_kernel(const EvictArgs
     fa += __popc(va);
     fo += __popc(vo);
   }
-  const int self = rank * kEvictThreads + tid, everyone = ctas * kEvictThreads;
+  const int self = rank * THREADS + tid, everyone = ctas * THREADS;
   for (int i = self; i < lead; i += everyone) {
     kept[i] = i;
     out[i] = w[i];
@@ -266,18 +272,18 @@ __global__ void __launch_bounds__(kEvictThreads, 2) evict_kernel(const EvictArgs
   bool bad = false;
   // The moves of the round that begins at token `first`, listed by a thread per token; all loads of a step before the next.
   auto list = [&](int first, Move* to) {
-    constexpr int EACH = (T::TOKENS + kEvictThreads - 1) / kEvictThreads;
+    constexpr int EACH = (T::TOKENS + THREADS - 1) / THREADS;
     int p[EACH], from_id[EACH], to_id[EACH];
 #pragma unroll
-    for (int u = 0; u < EACH; ++u) p[u] = __ldcg(kept + min(first + u * kEvictThreads + tid, keep - 1));
+    for (int u = 0; u < EACH; ++u) p[u] = __ldcg(kept + min(first + u * THREADS + tid, keep - 1));
 #pragma unroll
     for (int u = 0; u < EACH; ++u) {
       from_id[u] = table[p[u] / kPage];
-      to_id[u] = table[min(first + u * kEvictThreads + tid, keep - 1) / kPage];
+      to_id[u] = table[min(first + u * THREADS + tid, keep - 1) / kPage];
     }
 #pragma unroll
     for (int u = 0; u < EACH; ++u) {
-      const int k = u * kEvictThreads + tid, i = first + k;
+      const int k = u * THREADS + tid, i = first + k;
       const bool ok = (unsigned)from_id[u] < (unsigned)a.num_blocks && (unsigned)to_id[u] < (unsigned)a.num_blocks;
       bad |= i < keep && k < T::TOKENS && !ok;
       Move m{-1, -1};
@@ -297,19 +303,19 @@ __global__ void __launch_bounds__(kEvictThreads, 2) evict_kernel(const EvictArgs
     uint4 x[kInFlight];
 #pragma unroll
     for (int u = 0; u < kInFlight; ++u) {
-      const int unit = u * kEvictThreads + tid, piece = unit % T::PIECES, side = piece / (T::PIECES / 2);
+      const int unit = u * THREADS + tid, piece = unit % T::PIECES, side = piece / (T::PIECES / 2);
       const int64_t src = moves[unit / T::PIECES].src;
       if (src >= 0)
         x[u] = *reinterpret_cast<const uint4*>(a.pool + (src & ~15ll) + (side * kPage + (src & 15)) * T::ROW + piece % (T::PIECES / 2) * 16);
     }
     // scales and exponents: a token per thread, TOKENS of them
-    constexpr int SMALL = BITS == 16 ? 1 : (T::TOKENS + kEvictThreads - 1) / kEvictThreads;
+    constexpr int SMALL = BITS == 16 ? 1 : (T::TOKENS + THREADS - 1) / THREADS;
     Scales<BITS == 4 ? T::SCALE : 4> sc[SMALL][2];
     uint8_t ex[SMALL][2];
     if constexpr (BITS < 16) {
 #pragma unroll
       for (int u = 0; u < SMALL; ++u) {
-        const int k = u * kEvictThreads + tid;
+        const int k = u * THREADS + tid;
         const int64_t src = k < T::TOKENS ? moves[k].src : -1;
         if (src >= 0) {
           const uint8_t* tile = a.pool + (src & ~15ll);
@@ -325,12 +331,12 @@ __global__ void __launch_bounds__(kEvictThreads, 2) evict_kernel(const EvictArgs
     const int next = first + ctas * T::TOKENS;
     if (next < keep) list(next, sm.move[turn ^ 1]);
     else {  // this CTA is through, the cluster may not be
-      for (int k = tid; k < T::TOKENS; k += kEvictThreads) sm.move[turn ^ 1][k] = Move{-1, -1};
+      for (int k = tid; k < T::TOKENS; k += THREADS) sm.move[turn ^ 1][k] = Move{-1, -1};
     }
     meet();
 #pragma unroll
     for (int u = 0; u < kInFlight; ++u) {
-      const int unit = u * kEvictThreads + tid, piece = unit % T::PIECES, side = piece / (T::PIECES / 2);
+      const int unit = u * THREADS + tid, piece = unit % T::PIECES, side = piece / (T::PIECES / 2);
       const int64_t dst = moves[unit / T::PIECES].dst;
       if (dst >= 0)
         *reinterpret_cast<uint4*>(a.pool + (dst & ~15ll) + (side * kPage + (dst & 15)) * T::ROW + piece % (T::PIECES / 2) * 16) = x[u];
@@ -338,7 +344,7 @@ __global__ void __launch_bounds__(kEvictThreads, 2) evict_kernel(const EvictArgs
     if constexpr (BITS < 16) {
 #pragma unroll
       for (int u = 0; u < SMALL; ++u) {
-        const int k = u * kEvictThreads + tid;
+        const int k = u * THREADS + tid;
         const int64_t dst = k < T::TOKENS ? moves[k].dst : -1;
         if (dst >= 0) {
           uint8_t* tile = a.pool + (dst & ~15ll);
@@ -413,13 +419,10 @@ __global__ void __launch_bounds__(kReleaseThreads) release_kernel(const ReleaseA
   if (flags) flag_error(a.err, flags);
 }
 
-template <int BITS, int D>
-cudaError_t launch_evict_t(tq_ctx* ctx, const EvictArgs& a, cudaStream_t s) {
+template <int BITS, int D, int THREADS>
+cudaError_t launch_evict_t(tq_ctx* ctx, const EvictArgs& a, int ctas, cudaStream_t s) {
   const int64_t rows = (int64_t)a.batch * a.hkv;
-  // CTAs per row: enough for two on every multiprocessor, up to the portable cluster (16: 1 x 32K to 2K 29.3 us against 26.6)
-  int ctas = 1;
-  while (ctas < 8 && rows * ctas * 2 <= 2 * (int64_t)ctx->sm_count) ctas *= 2;
-  auto kern = evict_kernel<BITS, D>;
+  auto kern = evict_kernel<BITS, D, THREADS>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(EvictSmem));
   if (e != cudaSuccess) return e;
   cudaLaunchAttribute attr[2]{};
@@ -430,7 +433,7 @@ cudaError_t launch_evict_t(tq_ctx* ctx, const EvictArgs& a, cudaStream_t s) {
   attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3((unsigned)(rows * ctas));
-  cfg.blockDim = dim3(kEvictThreads);
+  cfg.blockDim = dim3(THREADS);
   cfg.dynamicSmemBytes = sizeof(EvictSmem);
   cfg.stream = s;
   cfg.attrs = attr;
@@ -440,13 +443,25 @@ cudaError_t launch_evict_t(tq_ctx* ctx, const EvictArgs& a, cudaStream_t s) {
   return e;
 }
 
+// Rows enough for every multiprocessor twice are CTAs of 256 threads, four resident on each (64 sequences of 8 heads from 4.2K
+// to 4K tokens, e4m3: 67 us, with 512 threads 74); fewer rows are clusters of CTAs of 512, enough for two on every
+// multiprocessor, up to the portable cluster of 8 (1 x 32K to 2K, 8 heads: 26.6 us, with 256 threads 32, with 16 CTAs 29).
+template <int BITS, int D>
+cudaError_t launch_evict_rows(tq_ctx* ctx, const EvictArgs& a, cudaStream_t s) {
+  const int64_t rows = (int64_t)a.batch * a.hkv;
+  if (rows >= 2 * ctx->sm_count) return launch_evict_t<BITS, D, 256>(ctx, a, 1, s);
+  int ctas = 1;
+  while (ctas < 8 && rows * ctas <= ctx->sm_count) ctas *= 2;
+  return launch_evict_t<BITS, D, 512>(ctx, a, ctas, s);
+}
+
 template <int BITS>
 cudaError_t launch_evict_d(tq_ctx* ctx, const EvictArgs& a, cudaStream_t s) {
   switch (ctx->cfg.head_dim) {
-    case 64: return launch_evict_t<BITS, 64>(ctx, a, s);
-    case 128: return launch_evict_t<BITS, 128>(ctx, a, s);
-    case 256: return launch_evict_t<BITS, 256>(ctx, a, s);
-    case 512: return launch_evict_t<BITS, 512>(ctx, a, s);
+    case 64: return launch_evict_rows<BITS, 64>(ctx, a, s);
+    case 128: return launch_evict_rows<BITS, 128>(ctx, a, s);
+    case 256: return launch_evict_rows<BITS, 256>(ctx, a, s);
+    case 512: return launch_evict_rows<BITS, 512>(ctx, a, s);
   }
   return cudaErrorInvalidValue;
 }
