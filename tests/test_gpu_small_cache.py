@@ -518,6 +518,74 @@ def test_evict_batches_of_every_cluster_size(rows, hkv):
     check_evict(e, run_evict(e, keep, 2, 16), keep, 2, 16)
 
 
+def test_evict_many_rows_with_long_ones_among_them():
+    """More rows than the GPU has room for at once, some longer than a CTA holds."""
+    lengths = [(i * 37) % 90 for i in range(160)]
+    lengths[3], lengths[77], lengths[159] = 11003, 20001, 10241
+    e = evict_case(17, lengths, 2, 64, 4)
+    keep = [40] * 160
+    keep[3], keep[77], keep[159] = 5000, 19990, 1
+    check_evict(e, run_evict(e, keep, 3, 9), keep, 3, 9)
+
+
+@pytest.mark.parametrize("bits", [16, 4])
+def test_evict_and_weights_in_a_pool_beyond_32_bits(bits):
+    """Tiles whose place in the pool passes 2^31 and 2^32 bytes: the same as in a small pool."""
+    hkv, d = 4, 128
+    small = evict_case(19, [100, 70], hkv, d, bits, kind="plain")
+    ctx = small["ctx"]
+    nb = (5 << 30) // (hkv * ctx.page_bytes)
+    rng = np.random.default_rng(3)
+    # pages of real keys and values, for the weights
+    gen = torch.Generator().manual_seed(3)
+    k, v = torch.randn(170, hkv, d, generator=gen).half().cuda(), torch.randn(170, hkv, d, generator=gen).half().cuda()
+    slots = np.concatenate([small["bt"][b, np.arange(n) // 16].astype(np.int64) * 16 + np.arange(n) % 16 for b, n in enumerate([100, 70])])
+    pool = torch.from_numpy(small["pool"]).cuda()
+    ctx.paged_store(k, v, torch.from_numpy(slots).cuda(), pool)
+    small["pool"] = pool.cpu().numpy()
+    far = np.concatenate([np.linspace(0, nb - 1, len(small["pool"]), dtype=np.int64)])
+    far = rng.permutation(far).astype(np.int32)
+    big_pool = torch.zeros(nb, hkv, ctx.page_bytes, dtype=torch.uint8, device="cuda")
+    big_pool[torch.from_numpy(far).long().cuda()] = pool
+    bt = np.where(small["bt"] >= 0, far[small["bt"]], -1).astype(np.int32)
+    q = torch.randn(2, hkv, d, generator=gen).half().cuda()
+    lens, n = i32(small["lengths"]), small["w"].shape[2]
+    got = []
+    for p, t in ((pool, small["bt"]), (big_pool, bt)):
+        out, lse = torch.zeros(2, hkv, d, device="cuda"), torch.zeros(2, hkv, device="cuda")
+        ws = torch.zeros(ctx.paged_workspace_size(2), dtype=torch.uint8, device="cuda")
+        ctx.paged_attention(q, p, i32(t), lens, out, ws, lse=lse)
+        w, w2 = torch.zeros(2, hkv, n, device="cuda"), torch.zeros(2, hkv, n, device="cuda")
+        ctx.paged_weights(q, p, i32(t), lens, lse, w)
+        kept, new = torch.zeros(2, hkv, n, dtype=torch.int32, device="cuda"), i32([0, 0])
+        ctx.paged_evict(w, p, i32(t), lens, i32([50, 33]), w2, new, kept, sinks=2, recent=10)
+        ctx.paged_attention(q, p, i32(t), new, out, ws, lse=lse)
+        got.append((out, lse, w, w2, kept, new))
+    assert ctx.device_errors() == 0
+    for x, y in zip(*got):
+        assert torch.equal(x, y)
+
+
+def test_two_calls_at_once():
+    """The same context on two streams: calls that share only what they read."""
+    e = weights_case(101, [3000, 130, 9, 2000], 8, 2, 128, 4, False)
+    f = evict_case(23, [700, 90, 300], 4, 128, 8, kind="plain")
+    ref, lse = attend_scored(e, 10.0, slopes_of(8))
+    sums = add_weights(e, lse)
+    gone = run_evict(f, 60, 1, 8)
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(3)]
+    got = []
+    for _ in range(10):
+        for i, s in enumerate(streams):
+            with torch.cuda.stream(s):
+                got.append((attend_scored(e, 10.0, slopes_of(8))[0], add_weights(e, lse), *run_evict(f, 60, 1, 8)))
+    torch.cuda.synchronize()
+    for out, w, *rest in got:
+        assert torch.equal(out, ref) and torch.equal(w, sums)
+        assert all(torch.equal(x, y) for x, y in zip(rest, gone))
+
+
 def test_evict_rows_longer_and_shorter_than_the_table():
     e = evict_case(5, [100, 37], 2, 64, 16, max_blocks=9, n=300)
     check_evict(e, run_evict(e, 30, 0, 5), 30, 0, 5)
