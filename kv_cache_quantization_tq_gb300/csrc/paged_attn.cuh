@@ -1371,15 +1371,23 @@ __global__ void __launch_bounds__(PagedCfg<KIND, D, N8, MODE>::THREADS, 1)
           for (int pg = 0; pg < PP; ++pg) {
             fe[pg][0] = (float)ev[pg][0];
             fe[pg][1] = (float)ev[pg][1];
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-              for (int k = 0; k < 4; ++k) {
-                p[pg][nt][k] = s[pg][nt][k] - m[nt][k & 1];
-                raise |= p[pg][nt][k] > kLazy;
-                raise |= p[pg][nt][k] + fe[pg][k >> 1] > most[nt][k & 1];
-              }
           }
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+              float high = -CUDART_INF_F, worth = -CUDART_INF_F;  // largest score, and largest product with the values
+#pragma unroll
+              for (int pg = 0; pg < PP; ++pg)
+#pragma unroll
+                for (int x = 0; x < 2; ++x) {
+                  const float y = s[pg][nt][k + 2 * x] - m[nt][k];
+                  p[pg][nt][k + 2 * x] = y;
+                  high = fmaxf(high, y);
+                  worth = fmaxf(worth, y + fe[pg][x]);
+                }
+              raise |= high > kLazy || worth > most[nt][k];
+            }
           if (__any_sync(kFull, raise)) {  // all heads' references are set anew: fewer pages come here
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
@@ -1443,7 +1451,7 @@ __global__ void __launch_bounds__(PagedCfg<KIND, D, N8, MODE>::THREADS, 1)
             for (int pg = 0; pg < PP; ++pg) {
               // what a token's weight at its values has besides: 2^-8 and their exponent
 #pragma unroll
-              for (int k = 0; k < 4; ++k) p[pg][nt][k] = p[pg][nt][k] * (power2(ev[pg][k >> 1]) * kDown) * vr[nt][k & 1];
+              for (int k = 0; k < 4; ++k) p[pg][nt][k] = p[pg][nt][k] * (power2(ev[pg][k >> 1]) * (kDown * vr[nt][k & 1]));
 #pragma unroll
               for (int x = 0; x < 2; ++x) {
                 const uint32_t a1 = take_part<false>(p[pg][nt][2 * x], p[pg][nt][2 * x + 1]);
