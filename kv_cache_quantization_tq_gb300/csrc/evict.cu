@@ -258,8 +258,7 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) evict_kernel(const Ev
     meet();
     return;
   }
-  __threadfence();
-  meet();  // the list is there
+  meet();  // the list is there, for all of the cluster
 
   // ---- moving, from the first token that does not stay where it is: the list is i below the first slot that goes
   int from = keep;
