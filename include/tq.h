@@ -493,7 +493,8 @@ tq_status tq_paged_weights(tq_ctx* ctx, const void* q, int64_t q_stride, int bat
  *   weights_out  as weights, another array: entries 0 .. K - 1 are those of the kept tokens, K .. L - 1 become 0
  *   lengths_out  device int32 [batch]: K
  *   kept         device int32 [batch][Hkv][weights_stride]: entries 0 .. K - 1 are the slots that the tokens come from
- * Slots K .. L - 1 of the pages are no longer defined.  A length that is negative, or beyond the block table or weights_stride,
+ * Slots K .. L - 1 of the pages are no longer defined.  Keys are moved as they are, with the positions that were worked into
+ * them; the positions that tq_plan_pages gives afterwards count slots.  A length that is negative, or beyond the block table or weights_stride,
  * counts as 0 with TQ_DEVERR_POSITION; a token is not moved from or to a page whose id is outside [0, num_blocks)
  * (TQ_DEVERR_BLOCK_ID).  batch * Hkv must be below 2^28.  Calls that share pages, and the calls that read them, must be ordered. */
 tq_status tq_paged_evict(tq_ctx* ctx, const float* weights, int64_t weights_stride, int batch, void* pool, int num_blocks,

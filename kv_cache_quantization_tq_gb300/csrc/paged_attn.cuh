@@ -840,9 +840,11 @@ __global__ void __launch_bounds__(PagedCfg<KIND, D, N8, MODE>::THREADS, 1)
   float o[KS][NT][4], m[NT][2], l[NT][2], lost[NT][2], qs[NT][2], qh[NT][2], vr[NT][2], most[NT][2];
   // capped scores are cap2 tanh(scale q . k / cap); slope: the bias per position
   constexpr float kLog2e = 1.44269504088896340736f, kLog2eLow = 1.92596299e-8f;  // log2 e = kLog2e + kLog2eLow
-  const bool capped = MODE != kAttend && w.cap > 0.f, scored = capped || (MODE != kAttend && w.slopes);
+  const bool capped = MODE != kAttend && w.cap > 0.f;
   // Weights alone are not divided by their own sum, in which a score's error would largely go: there scores are kept in natural
-  // units and the factor to powers of two is applied in two parts, by a multiply-add with the log-sum-exp.
+  // units and the factor to powers of two is applied in two parts, by a multiply-add with the log-sum-exp.  The factor has the
+  // scale in it where that is all, and is not negative: a score of -inf stands for a token that does not count.
+  const bool scored = MODE != kAttend && (capped || w.slopes || (C::KEYS && a.scale < 0.f));
   const float log2e_scale = capped ? a.scale / w.cap : C::KEYS ? (scored ? a.scale : 1.f) : a.scale * kLog2e;
   const float cap2 = MODE != kAttend ? (C::KEYS ? w.cap : w.cap * kLog2e) : 0.f;
   const float up_hi = scored ? kLog2e : w.up_hi, up_lo = scored ? kLog2eLow : w.up_lo;
@@ -1035,255 +1037,254 @@ __global__ void __launch_bounds__(PagedCfg<KIND, D, N8, MODE>::THREADS, 1)
     // ================================================================ pages
     if constexpr (!C::OWN) {
 #pragma unroll 1
-    for (int i = 0; i < out.take; ++i, st = st + 1 == S ? 0 : st + 1) {
-      const bool here = valid >> st & 1;
-      const uint32_t kb = stage0 + st * C::PAGE, vb = kb + (C::APART ? C::HALF : kPage * C::SWIZZLE_ROW);
-      float s[NT][4];
-      if (here) {  // with a limit of 0 the first copy is waited for
-        const uint32_t limit = w.p.wait_limit || parity ? w.p.wait_limit : kDrainLimit;
-        if ((parity & kLate) == 0 && !bar_wait(bar0 + 16 * st, parity >> st & 1, limit)) give_up(valid);
-        parity ^= 1u << st;
-      }
-      int ek0 = 0, ek1 = 0, ev0 = 0, ev1 = 0;
-      if (here) {
-        if (F8) {  // exponents of tokens g and g + 8, keys and values
-          const uint32_t ea = exp0 + st * C::EXP + g;
-          asm volatile("ld.shared.s8 %0, [%1];" : "=r"(ek0) : "r"(ea) : "memory");
-          asm volatile("ld.shared.s8 %0, [%1];" : "=r"(ek1) : "r"(ea + 8) : "memory");
-          asm volatile("ld.shared.s8 %0, [%1];" : "=r"(ev0) : "r"(ea + 16) : "memory");
-          asm volatile("ld.shared.s8 %0, [%1];" : "=r"(ev1) : "r"(ea + 24) : "memory");
+      for (int i = 0; i < out.take; ++i, st = st + 1 == S ? 0 : st + 1) {
+        const bool here = valid >> st & 1;
+        const uint32_t kb = stage0 + st * C::PAGE, vb = kb + (C::APART ? C::HALF : kPage * C::SWIZZLE_ROW);
+        float s[NT][4];
+        if (here) {  // with a limit of 0 the first copy is waited for
+          const uint32_t limit = w.p.wait_limit || parity ? w.p.wait_limit : kDrainLimit;
+          if ((parity & kLate) == 0 && !bar_wait(bar0 + 16 * st, parity >> st & 1, limit)) give_up(valid);
+          parity ^= 1u << st;
         }
-        scores(kb, exp0 + st * C::EXP, s);
-      }
-      bool again = false;
-      auto next_page = [&]() {
-        __syncwarp();  // every lane has read what the copy replaces
-        again = fetch_next() && tile >= 0;
-        valid = again ? valid | 1u << st : valid & ~(1u << st);
-        if (again && (parity & kLate) == 0 && lane == 0) fetch(st, 0);
-      };
-      if (C::APART) next_page();  // the keys are read
-
-      if (here) {
-        // ---- weights
-        const int rel = out.p + (back ? out.take - 1 - i : i);  // page of the segment
-        const bool whole = rel != cut_first && rel != cut_last;
-        const int t_lo = out.s.lo - (out.s.first + rel) * kPage, t_hi = out.s.len - (out.s.first + rel) * kPage;
-        auto counts = [&](int tok) { return tok >= t_lo && tok < t_hi; };
-        if (F8) {
-          const float f0 = power2(ek0), f1 = power2(ek1);
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-            for (int k = 0; k < 4; ++k) s[nt][k] = s[nt][k] * qh[nt][k & 1] * (k < 2 ? f0 : f1);
-        }
-        bool raise = false;
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-          for (int k = 0; k < 4; ++k) s[nt][k] *= qs[nt][k & 1];
-        if constexpr (MODE != kAttend) {
-          if (capped) {
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt) cap_scores(s[nt], cap2);
+        int ek0 = 0, ek1 = 0, ev0 = 0, ev1 = 0;
+        if (here) {
+          if (F8) {  // exponents of tokens g and g + 8, keys and values
+            const uint32_t ea = exp0 + st * C::EXP + g;
+            asm volatile("ld.shared.s8 %0, [%1];" : "=r"(ek0) : "r"(ea) : "memory");
+            asm volatile("ld.shared.s8 %0, [%1];" : "=r"(ek1) : "r"(ea + 8) : "memory");
+            asm volatile("ld.shared.s8 %0, [%1];" : "=r"(ev0) : "r"(ea + 16) : "memory");
+            asm volatile("ld.shared.s8 %0, [%1];" : "=r"(ev1) : "r"(ea + 24) : "memory");
           }
-          if (w.slopes) {
-            const float back0 = (float)(g + 1 - t_hi), back1 = (float)(g + 9 - t_hi);
+          scores(kb, exp0 + st * C::EXP, s);
+        }
+        bool again = false;
+        auto next_page = [&]() {
+          __syncwarp();  // every lane has read what the copy replaces
+          again = fetch_next() && tile >= 0;
+          valid = again ? valid | 1u << st : valid & ~(1u << st);
+          if (again && (parity & kLate) == 0 && lane == 0) fetch(st, 0);
+        };
+        if (C::APART) next_page();  // the keys are read
+
+        if (here) {
+          // ---- weights
+          const int rel = out.p + (back ? out.take - 1 - i : i);  // page of the segment
+          const bool whole = rel != cut_first && rel != cut_last;
+          const int t_lo = out.s.lo - (out.s.first + rel) * kPage, t_hi = out.s.len - (out.s.first + rel) * kPage;
+          auto counts = [&](int tok) { return tok >= t_lo && tok < t_hi; };
+          if (F8) {
+            const float f0 = power2(ek0), f1 = power2(ek1);
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-              for (int k = 0; k < 4; ++k) s[nt][k] = fmaf(slope[nt][k & 1], k < 2 ? back0 : back1, s[nt][k]);
+              for (int k = 0; k < 4; ++k) s[nt][k] = s[nt][k] * qh[nt][k & 1] * (k < 2 ? f0 : f1);
           }
-        }
-        if (!whole) {  // rows that do not count are whatever memory held
-          const bool ok0 = counts(g), ok1 = counts(g + 8);
+          bool raise = false;
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-            for (int k = 0; k < 4; ++k) s[nt][k] = (k < 2 ? ok0 : ok1) ? s[nt][k] : -CUDART_INF_F;
-          ev0 = ok0 ? ev0 : -127;
-          ev1 = ok1 ? ev1 : -127;
-        }
-        const float fe0 = (float)ev0, fe1 = (float)ev1;
-        float p[NT][4];
+            for (int k = 0; k < 4; ++k) s[nt][k] *= qs[nt][k & 1];
+          if constexpr (MODE != kAttend) {
+            if (capped) {
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
+              for (int nt = 0; nt < NT; ++nt) cap_scores(s[nt], cap2);
+            }
+            if (w.slopes) {
+              const float back0 = (float)(g + 1 - t_hi), back1 = (float)(g + 9 - t_hi);
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            p[nt][k] = s[nt][k] - m[nt][k & 1];
-            raise |= p[nt][k] > kLazy;
-            if (F8) raise |= p[nt][k] + (k < 2 ? fe0 : fe1) > most[nt][k & 1];
+              for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int k = 0; k < 4; ++k) s[nt][k] = fmaf(slope[nt][k & 1], k < 2 ? back0 : back1, s[nt][k]);
+            }
           }
-        if (__any_sync(kFull, raise)) {  // all heads' references are set anew: fewer pages come here
+          if (!whole) {  // rows that do not count are whatever memory held
+            const bool ok0 = counts(g), ok1 = counts(g + 8);
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+              for (int k = 0; k < 4; ++k) s[nt][k] = (k < 2 ? ok0 : ok1) ? s[nt][k] : -CUDART_INF_F;
+            ev0 = ok0 ? ev0 : -127;
+            ev1 = ok1 ? ev1 : -127;
+          }
+          const float fe0 = (float)ev0, fe1 = (float)ev1;
+          float p[NT][4];
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              p[nt][k] = s[nt][k] - m[nt][k & 1];
+              raise |= p[nt][k] > kLazy;
+              if (F8) raise |= p[nt][k] + (k < 2 ? fe0 : fe1) > most[nt][k & 1];
+            }
+          if (__any_sync(kFull, raise)) {  // all heads' references are set anew: fewer pages come here
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+              for (int k = 0; k < 2; ++k) {
+                float mx = fmaxf(s[nt][k], s[nt][k + 2]);
+#pragma unroll
+                for (int x = 4; x < 32; x <<= 1) mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, x));
+                mx = fmaxf(m[nt][k], ceilf(mx));
+                const float up = mx - m[nt][k], c = ex2(-up);
+                m[nt][k] = mx;
+                l[nt][k] *= c;
+                if (C::KEEP_LOST) lost[nt][k] *= c;
+                p[nt][k] = s[nt][k] - mx;
+                p[nt][k + 2] = s[nt][k + 2] - mx;
+                float co = c;
+                if (F8) {  // the values' reference follows, and their sum takes what it does not
+                  float top = fmaxf(fmaxf(p[nt][k] + fe0, p[nt][k + 2] + fe1), -1000.f);
+#pragma unroll
+                  for (int x = 4; x < 32; x <<= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, x));
+                  const int e = kValueMost + (int)kLazy - (int)most[nt][k], by = (int)fminf(up, 1000.f);
+                  const int e1 = max(min(min(e + by, kValueTop), kValueAt + (int)kLazy - (int)floorf(top)), kValueLeast);
+                  most[nt][k] = (float)(kValueMost + (int)kLazy - e1);
+                  vr[nt][k] = power2(e1);
+                  co = power2(max(e1 - e - by, -127));
+                }
+#pragma unroll
+                for (int j = 0; j < KS; ++j) {
+                  o[j][nt][k] *= co;
+                  o[j][nt][k + 2] *= co;
+                }
+              }
+          }
+          // what a token's weight at its values has besides: 2^-8, and on 8-bit pages their exponent
+          const float w0 = F8 ? power2(ev0) * kDown : kDown, w1 = F8 ? power2(ev1) * kDown : kDown;
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k) p[nt][k] = ex2(p[nt][k]);
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
-              float mx = fmaxf(s[nt][k], s[nt][k + 2]);
-#pragma unroll
-              for (int x = 4; x < 32; x <<= 1) mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, x));
-              mx = fmaxf(m[nt][k], ceilf(mx));
-              const float up = mx - m[nt][k], c = ex2(-up);
-              m[nt][k] = mx;
-              l[nt][k] *= c;
-              if (C::KEEP_LOST) lost[nt][k] *= c;
-              p[nt][k] = s[nt][k] - mx;
-              p[nt][k + 2] = s[nt][k + 2] - mx;
-              float co = c;
-              if (F8) {  // the values' reference follows, and their sum takes what it does not
-                float top = fmaxf(fmaxf(p[nt][k] + fe0, p[nt][k + 2] + fe1), -1000.f);
-#pragma unroll
-                for (int x = 4; x < 32; x <<= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, x));
-                const int e = kValueMost + (int)kLazy - (int)most[nt][k], by = (int)fminf(up, 1000.f);
-                const int e1 = max(min(min(e + by, kValueTop), kValueAt + (int)kLazy - (int)floorf(top)), kValueLeast);
-                most[nt][k] = (float)(kValueMost + (int)kLazy - e1);
-                vr[nt][k] = power2(e1);
-                co = power2(max(e1 - e - by, -127));
-              }
-#pragma unroll
-              for (int j = 0; j < KS; ++j) {
-                o[j][nt][k] *= co;
-                o[j][nt][k + 2] *= co;
+              if constexpr (C::KEEP_LOST) {  // what an addition loses is kept for the next one (Kahan's sum)
+                const float y = p[nt][k] + p[nt][k + 2] - lost[nt][k], sum = l[nt][k] + y;
+                lost[nt][k] = sum - l[nt][k] - y;
+                l[nt][k] = sum;
+              } else {
+                l[nt][k] += p[nt][k] + p[nt][k + 2];
               }
             }
-        }
-        // what a token's weight at its values has besides: 2^-8, and on 8-bit pages their exponent
-        const float w0 = F8 ? power2(ev0) * kDown : kDown, w1 = F8 ? power2(ev1) * kDown : kDown;
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
+            for (int k = 0; k < 4; ++k) {
+              p[nt][k] *= k < 2 ? w0 : w1;
+              if (F8) p[nt][k] *= vr[nt][k & 1];
+            }
+          }
+          constexpr int PARTS = BF ? 3 : 2;
+          // 16-bit parts of tokens 0 .. 7 and 8 .. 15, or tf32 parts of tokens 2 t, 2 t + 1, 2 t + 8, 2 t + 9
+          uint32_t pf[KIND == kF16 ? 1 : NT][PARTS][2], wh[KIND == kF16 ? NT : 1][4], wl[KIND == kF16 ? NT : 1][4];
 #pragma unroll
-          for (int k = 0; k < 4; ++k) p[nt][k] = ex2(p[nt][k]);
+          for (int nt = 0; nt < NT; ++nt) {
+            if constexpr (KIND == kF16) {
+              turn(p[nt][0], p[nt][1]);
+              turn(p[nt][2], p[nt][3]);
 #pragma unroll
-          for (int k = 0; k < 2; ++k) {
-            if constexpr (C::KEEP_LOST) {  // what an addition loses is kept for the next one (Kahan's sum)
-              const float y = p[nt][k] + p[nt][k + 2] - lost[nt][k], sum = l[nt][k] + y;
-              lost[nt][k] = sum - l[nt][k] - y;
-              l[nt][k] = sum;
+              for (int k = 0; k < 4; ++k) tf32_parts(p[nt][k], wh[nt][k], wl[nt][k]);
             } else {
-              l[nt][k] += p[nt][k] + p[nt][k + 2];
+#pragma unroll
+              for (int k = 0; k < PARTS; ++k) {
+                pf[nt][k][0] = movmat(take_part<BF>(p[nt][0], p[nt][1]));
+                pf[nt][k][1] = movmat(take_part<BF>(p[nt][2], p[nt][3]));
+              }
             }
           }
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            p[nt][k] *= k < 2 ? w0 : w1;
-            if (F8) p[nt][k] *= vr[nt][k & 1];
+          if (C::APART) {
+            if ((parity & kLate) == 0 && !bar_wait(bar0 + 16 * st + 8, vparity >> st & 1, w.p.wait_limit)) give_up(valid | 1u << st);
+            vparity ^= 1u << st;
           }
-        }
-        constexpr int PARTS = BF ? 3 : 2;
-        // 16-bit parts of tokens 0 .. 7 and 8 .. 15, or tf32 parts of tokens 2 t, 2 t + 1, 2 t + 8, 2 t + 9
-        uint32_t pf[KIND == kF16 ? 1 : NT][PARTS][2], wh[KIND == kF16 ? NT : 1][4], wl[KIND == kF16 ? NT : 1][4];
+          if (!whole) {
+            // value rows that do not count: a weight of 0 does not remove a NaN
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-          if constexpr (KIND == kF16) {
-            turn(p[nt][0], p[nt][1]);
-            turn(p[nt][2], p[nt][3]);
+            for (int k = 0; k < C::HALF / 512; ++k) {
+              const uint32_t row = (k * 32 + lane) * 16 / C::SWIZZLE_ROW, col = (k * 32 + lane) * 16 % C::SWIZZLE_ROW;
+              if (!counts(row % kPage))
+                asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(vb + row / kPage * C::BOX + row % kPage * C::SWIZZLE_ROW + col),
+                             "r"(0)
+                             : "memory");
+            }
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // before the stage's next copy
+            __syncwarp();
+          }
+          auto add = [&](int j, const uint32_t(&af)[4]) {
+            // af: dims g, g + 8 of tokens 2 t, 2 t + 1 (first two), 2 t + 8, 2 t + 9; a product of 8 tokens takes a
+            // pair's first token as number t and its second as number t + 4
+            uint32_t va[2][4];
+            if constexpr (KIND == kF16)
 #pragma unroll
-            for (int k = 0; k < 4; ++k) tf32_parts(p[nt][k], wh[nt][k], wl[nt][k]);
+              for (int k = 0; k < 4; ++k) widen(af[k], va[k >> 1][k & 1], va[k >> 1][(k & 1) + 2]);
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+              float acc[4];
+              if constexpr (KIND != kF16) {
+                mma_first<BF>(acc, af, pf[nt][PARTS - 1][0], pf[nt][PARTS - 1][1]);
+#pragma unroll
+                for (int k = PARTS - 2; k >= 0; --k) mma<BF>(acc, af, pf[nt][k][0], pf[nt][k][1]);
+              } else {
+                mma_tf32_first(acc, va[0], wl[nt][0], wl[nt][1]);
+                mma_tf32(acc, va[1], wl[nt][2], wl[nt][3]);
+                mma_tf32(acc, va[0], wh[nt][0], wh[nt][1]);
+                mma_tf32(acc, va[1], wh[nt][2], wh[nt][3]);
+              }
+#pragma unroll
+              for (int k = 0; k < 4; ++k) o[j][nt][k] += acc[k];
+            }
+          };
+          if constexpr (F8) {
+#pragma unroll
+            for (int j = 0; j < KS / 2; ++j) {
+              uint32_t r[4];
+              ldsm2t8(r, piece(vb, v_off, j));
+#pragma unroll
+              for (int c = 0; c < 2; ++c) {
+                const uint32_t af[4] = {f16_of_e4m3(r[2 * c]), f16_of_e4m3(r[2 * c + 1]), f16_of_e4m3_high(r[2 * c]),
+                                        f16_of_e4m3_high(r[2 * c + 1])};
+                add(2 * j + c, af);
+              }
+            }
           } else {
 #pragma unroll
-            for (int k = 0; k < PARTS; ++k) {
-              pf[nt][k][0] = movmat(take_part<BF>(p[nt][0], p[nt][1]));
-              pf[nt][k][1] = movmat(take_part<BF>(p[nt][2], p[nt][3]));
+            for (int j = 0; j < KS; ++j) {
+              uint32_t r[4];
+              ldsm4t(r, piece(vb, v_off, j));
+              add(j, r);
             }
           }
         }
         if (C::APART) {
-          if ((parity & kLate) == 0 && !bar_wait(bar0 + 16 * st + 8, vparity >> st & 1, w.p.wait_limit)) give_up(valid | 1u << st);
-          vparity ^= 1u << st;
-        }
-        if (!whole) {
-          // value rows that do not count: a weight of 0 does not remove a NaN
-#pragma unroll
-          for (int k = 0; k < C::HALF / 512; ++k) {
-            const uint32_t row = (k * 32 + lane) * 16 / C::SWIZZLE_ROW, col = (k * 32 + lane) * 16 % C::SWIZZLE_ROW;
-            if (!counts(row % kPage))
-              asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(vb + row / kPage * C::BOX + row % kPage * C::SWIZZLE_ROW + col),
-                           "r"(0)
-                           : "memory");
-          }
-          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // before the stage's next copy
           __syncwarp();
-        }
-        auto add = [&](int j, const uint32_t(&af)[4]) {
-          // af: dims g, g + 8 of tokens 2 t, 2 t + 1 (first two), 2 t + 8, 2 t + 9; a product of 8 tokens takes a
-          // pair's first token as number t and its second as number t + 4
-          uint32_t va[2][4];
-          if constexpr (KIND == kF16)
-#pragma unroll
-            for (int k = 0; k < 4; ++k) widen(af[k], va[k >> 1][k & 1], va[k >> 1][(k & 1) + 2]);
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt) {
-            float acc[4];
-            if constexpr (KIND != kF16) {
-              mma_first<BF>(acc, af, pf[nt][PARTS - 1][0], pf[nt][PARTS - 1][1]);
-#pragma unroll
-              for (int k = PARTS - 2; k >= 0; --k) mma<BF>(acc, af, pf[nt][k][0], pf[nt][k][1]);
-            } else {
-              mma_tf32_first(acc, va[0], wl[nt][0], wl[nt][1]);
-              mma_tf32(acc, va[1], wl[nt][2], wl[nt][3]);
-              mma_tf32(acc, va[0], wh[nt][0], wh[nt][1]);
-              mma_tf32(acc, va[1], wh[nt][2], wh[nt][3]);
-            }
-#pragma unroll
-            for (int k = 0; k < 4; ++k) o[j][nt][k] += acc[k];
-          }
-        };
-        if constexpr (F8) {
-#pragma unroll
-          for (int j = 0; j < KS / 2; ++j) {
-            uint32_t r[4];
-            ldsm2t8(r, piece(vb, v_off, j));
-#pragma unroll
-            for (int c = 0; c < 2; ++c) {
-              const uint32_t af[4] = {f16_of_e4m3(r[2 * c]), f16_of_e4m3(r[2 * c + 1]), f16_of_e4m3_high(r[2 * c]),
-                                      f16_of_e4m3_high(r[2 * c + 1])};
-              add(2 * j + c, af);
-            }
-          }
+          if (again && (parity & kLate) == 0 && lane == 0) fetch(st, 1);
         } else {
-#pragma unroll
-          for (int j = 0; j < KS; ++j) {
-            uint32_t r[4];
-            ldsm4t(r, piece(vb, v_off, j));
-            add(j, r);
-          }
+          next_page();
         }
       }
-      if (C::APART) {
-        __syncwarp();
-        if (again && (parity & kLate) == 0 && lane == 0) fetch(st, 1);
-      } else {
-        next_page();
-      }
-    }
     } else {
-    const int64_t w_row = ((int64_t)out.b * a.hkv + kvh) * w.w_stride;
-    const float* row_in = w.w_in ? w.w_in + w_row : nullptr;
-    float* row_out = w.w_out + w_row;
-    // Up to d = 128 two pages a step: a page's share of the instructions that are not its own is halved.
+      const int64_t w_row = ((int64_t)out.b * a.hkv + kvh) * w.w_stride;
+      const float* row_in = w.w_in ? w.w_in + w_row : nullptr;
+      float* row_out = w.w_out + w_row;
+      // Up to d = 128 two pages a step: a page's share of the instructions that are not its own is halved.
 #pragma unroll 1
-    for (int i = 0; i < out.take; i += PP, st = st + 1 == S ? 0 : st + 1) {
-      const uint32_t here = valid >> 2 * st & 3;
-      // page of the segment, position of its first token; and of the second page of the step
-      const int rel = out.p + (back ? out.take - 1 - i : i), rel2 = back ? rel - 1 : rel + 1;
-      const int first = (out.s.first + rel) * kPage, on = back ? -kPage : kPage;
-      // the weights' sums so far: a lane has token tok0 + 8 (t & 1) of page t >> 1
-      const int pos = first + 16 * (t >> 1) + tok0 + 8 * (t & 1);
-      const bool mine = C::KEYS && pos < out.s.len && (t < 2 || (PP == 2 && i + 1 < out.take));
-      float old = 0.f, added = 0.f;
-      if (mine && row_in) old = row_in[pos];
-      asm volatile("cp.async.wait_group %0;" ::"n"(S - 1) : "memory");
-      __syncwarp();
-      auto next_pages = [&]() {
-        __syncwarp();  // every lane has read what the copy replaces
-        if (!fetch_next()) tile = tile2 = -1;
-        valid = (valid & ~(3u << 2 * st)) | there() << 2 * st;
-        fetch_own(st);
-      };
-      // a page that is not there counts as one whose tokens do not
-      float s[PP][NT][4];
-      int ek[PP][2] = {}, ev[PP][2] = {};
-      {
+      for (int i = 0; i < out.take; i += PP, st = st + 1 == S ? 0 : st + 1) {
+        const uint32_t here = valid >> 2 * st & 3;
+        // page of the segment, position of its first token; and of the second page of the step
+        const int rel = out.p + (back ? out.take - 1 - i : i), rel2 = back ? rel - 1 : rel + 1;
+        const int first = (out.s.first + rel) * kPage, on = back ? -kPage : kPage;
+        // the weights' sums so far: a lane has token tok0 + 8 (t & 1) of page t >> 1
+        const int pos = first + 16 * (t >> 1) + tok0 + 8 * (t & 1);
+        const bool mine = C::KEYS && pos < out.s.len && (t < 2 || (PP == 2 && i + 1 < out.take));
+        float old = 0.f, added = 0.f;
+        if (mine && row_in) old = row_in[pos];
+        asm volatile("cp.async.wait_group %0;" ::"n"(S - 1) : "memory");
+        __syncwarp();
+        auto next_pages = [&]() {
+          __syncwarp();  // every lane has read what the copy replaces
+          if (!fetch_next()) tile = tile2 = -1;
+          valid = (valid & ~(3u << 2 * st)) | there() << 2 * st;
+          fetch_own(st);
+        };
+        // a page that is not there counts as one whose tokens do not
+        float s[PP][NT][4];
+        int ek[PP][2] = {}, ev[PP][2] = {};
 #pragma unroll
         for (int pg = 0; pg < PP; ++pg) {
           const uint32_t tail = exp0 + st * C::EXP + pg * C::EXP1;
@@ -1298,9 +1299,7 @@ __global__ void __launch_bounds__(PagedCfg<KIND, D, N8, MODE>::THREADS, 1)
           }
           scores(stage0 + st * C::PAGE + pg * C::PAGE1, tail, s[pg]);
         }
-      }
-      if (C::KEYS) next_pages();  // the keys are read
-      {
+        if (C::KEYS) next_pages();  // the keys are read
         const bool whole = here == (1u << PP) - 1 && rel != cut_first && rel != cut_last && (PP == 1 || (rel2 != cut_first && rel2 != cut_last));
         auto counts = [&](int pg, int tok) {
           const int x = first + pg * on + tok;
@@ -1547,13 +1546,12 @@ __global__ void __launch_bounds__(PagedCfg<KIND, D, N8, MODE>::THREADS, 1)
             }
           }
         }
+        if (C::KEYS) {
+          if (mine) row_out[pos] = fmaf(w.decay, old, added);
+        } else {
+          next_pages();
+        }
       }
-      if (C::KEYS) {
-        if (mine) row_out[pos] = fmaf(w.decay, old, added);
-      } else {
-        next_pages();
-      }
-    }
     }
 
     // ================================================================ the portion's result
@@ -1564,50 +1562,50 @@ __global__ void __launch_bounds__(PagedCfg<KIND, D, N8, MODE>::THREADS, 1)
         for (int x = 0; x < 4; ++x) o[j][0][x] += __shfl_xor_sync(kFull, o[j][0][x], 2);
     }
     if constexpr (!C::KEYS) {
-    const bool dead = __any_sync(kFull, (parity & kLate) != 0);
+      const bool dead = __any_sync(kFull, (parity & kLate) != 0);
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
+      for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-      for (int k = 0; k < 2; ++k) {
+        for (int k = 0; k < 2; ++k) {
 #pragma unroll
-        for (int x = 4; x < 32; x <<= 1) l[nt][k] += __shfl_xor_sync(kFull, l[nt][k], x);
-        if (dead) l[nt][k] = CUDART_NAN_F;
-      }
-    // The rows: to the outputs when the warp had the whole segment, else to its slot of shared memory.
-    const bool begins = out.at == 0, all = begins && out.end == out.span;
-    if (all && lane == 0) w.cuts[(int64_t)out.b * heads + out.hg] = make_int2(0, 0);
-    const int64_t row = (int64_t)out.b * a.hq + head0;
-    float* dst = all ? a.out + row * D : begins ? own_stage : own_slot;
-    const int pitch = all ? D : C::PITCH;
+          for (int x = 4; x < 32; x <<= 1) l[nt][k] += __shfl_xor_sync(kFull, l[nt][k], x);
+          if (dead) l[nt][k] = CUDART_NAN_F;
+        }
+      // The rows: to the outputs when the warp had the whole segment, else to its slot of shared memory.
+      const bool begins = out.at == 0, all = begins && out.end == out.span;
+      if (all && lane == 0) w.cuts[(int64_t)out.b * heads + out.hg] = make_int2(0, 0);
+      const int64_t row = (int64_t)out.b * a.hq + head0;
+      float* dst = all ? a.out + row * D : begins ? own_stage : own_slot;
+      const int pitch = all ? D : C::PITCH;
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
+      for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        const int h = nt * 8 + 2 * t + k;
-        if (h >= nh) continue;
-        const float f = (all ? inverse_of(l[nt][k]) : 1.f) * (XP ? power2(-exponent_in(vr[nt][k])) : 1.f);
-        if constexpr (F4) {  // dims 2 j and 2 j + 1 of the lane's share of D / 8, or of 32 and 256 behind them 32
-          constexpr int SHARE = D / 8 < 32 ? D / 8 : 32;
-          float* p = dst + h * pitch + g * SHARE;
+        for (int k = 0; k < 2; ++k) {
+          const int h = nt * 8 + 2 * t + k;
+          if (h >= nh) continue;
+          const float f = (all ? inverse_of(l[nt][k]) : 1.f) * (XP ? power2(-exponent_in(vr[nt][k])) : 1.f);
+          if constexpr (F4) {  // dims 2 j and 2 j + 1 of the lane's share of D / 8, or of 32 and 256 behind them 32
+            constexpr int SHARE = D / 8 < 32 ? D / 8 : 32;
+            float* p = dst + h * pitch + g * SHARE;
 #pragma unroll
-          for (int j = 0; j < KS; ++j)
-            *reinterpret_cast<float2*>(p + 2 * j / SHARE * 8 * SHARE + 2 * j % SHARE) = make_float2(o[j][nt][k] * f, o[j][nt][k + 2] * f);
-        } else {
-          float* p = dst + h * pitch + g;  // accumulator rows g and g + 8 of tile j
+            for (int j = 0; j < KS; ++j)
+              *reinterpret_cast<float2*>(p + 2 * j / SHARE * 8 * SHARE + 2 * j % SHARE) = make_float2(o[j][nt][k] * f, o[j][nt][k + 2] * f);
+          } else {
+            float* p = dst + h * pitch + g;  // accumulator rows g and g + 8 of tile j
 #pragma unroll
-          for (int j = 0; j < KS; ++j) {
-            p[16 * j] = o[j][nt][k] * f;
-            p[16 * j + 8] = o[j][nt][k + 2] * f;
+            for (int j = 0; j < KS; ++j) {
+              p[16 * j] = o[j][nt][k] * f;
+              p[16 * j + 8] = o[j][nt][k + 2] * f;
+            }
+          }
+          if (g == 0) {
+            if (!all) ml[(begins * NW + wid) * C::HEADS + h] = make_float2(m[nt][k], l[nt][k]);
+            else if (a.lse) a.lse[row + h] = lse_of(m[nt][k], l[nt][k]);
           }
         }
-        if (g == 0) {
-          if (!all) ml[(begins * NW + wid) * C::HEADS + h] = make_float2(m[nt][k], l[nt][k]);
-          else if (a.lse) a.lse[row + h] = lse_of(m[nt][k], l[nt][k]);
-        }
-      }
-    // sequence, segment, whether it ends here, and where it ends on the line
-    if (!all && lane == 0)
-      rec[begins * NW + wid] = make_int4(out.b, out.hg, 1 + (out.end == out.span), x_end - out.left - out.at + out.span);
+      // sequence, segment, whether it ends here, and where it ends on the line
+      if (!all && lane == 0)
+        rec[begins * NW + wid] = make_int4(out.b, out.hg, 1 + (out.end == out.span), x_end - out.left - out.at + out.span);
     }
   }
   if (parity & kLate) flag_error(a.err, TQ_DEVERR_TIMEOUT);

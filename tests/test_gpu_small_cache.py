@@ -364,6 +364,17 @@ def test_weights_window_cap_and_slopes(window, bits, bf16):
         check_weights(e, got, lse, window=window, cap=20.0, slopes=s, **kw)
 
 
+@pytest.mark.parametrize("bits", [16, 8, 4])
+@pytest.mark.parametrize("scale", [0.03, 1.0, -0.2, -1.0])
+def test_weights_scale(scale, bits):
+    """Any factor, with tokens in front of the window that must get nothing whatever its sign."""
+    e = weights_case(103, [100, 33, 7], 8, 2, 64, bits, False)
+    for window, cap, s in ((0, 0.0, None), (21, 0.0, None), (21, 10.0, None), (21, 0.0, slopes_of(8))):
+        _, lse = attend_scored(e, cap, s, window=window, scale=scale)
+        got = add_weights(e, lse, decay=0.5, window=window, scale=scale, cap=cap, slopes=s)
+        check_weights(e, got, lse, decay=0.5, window=window, scale=scale, cap=cap, slopes=s)
+
+
 @pytest.mark.parametrize("bits,bf16", ALL)
 @pytest.mark.parametrize("d,rep", [(128, 8), (64, 16), (128, 20)])
 def test_weights_long(d, rep, bits, bf16):
