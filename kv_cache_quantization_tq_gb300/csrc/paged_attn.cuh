@@ -1861,12 +1861,12 @@ cudaError_t launch_line(tq_ctx* ctx, PagedWork& w, cudaStream_t s) {
   auto kern = paged_kernel<KIND, D, NT, MODE>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
   if (e != cudaSuccess) return e;
-  prof_start(ctx, kProfDecode, s);
+  if (MODE != kWeights) prof_start(ctx, kProfDecode, s);
   e = launch_early(kern, dim3(ctas), dim3(C::THREADS), C::SMEM, s, map, w);
-  prof_stop(ctx, kProfDecode, s);
+  if (MODE != kWeights) prof_stop(ctx, kProfDecode, s);
   if (e != cudaSuccess) return e;
   ctx->launches++;
-  ctx->decode_kernel = "paged_kernel";
+  if (MODE != kWeights) ctx->decode_kernel = "paged_kernel";
   return e;
 }
 

@@ -728,6 +728,18 @@ def test_a_side_stream_and_repeated_calls_agree():
         assert torch.equal(got[0], ref[0]) and torch.equal(got[1], ref[1]) and torch.equal(more, sums)
 
 
+def test_the_profile_counts_attention_alone():
+    e = weights_case(107, [300, 20], 8, 2, 64, 16, False)
+    ctx = e["ctx"]
+    _, lse = attend_scored(e, 5.0)
+    ctx.profile_begin()
+    attend_scored(e, 5.0)
+    for _ in range(3):
+        add_weights(e, lse, cap=5.0)
+    p = ctx.profile_end()
+    assert p["decode_launches"] == 1 and p["merge_launches"] == 1 and p["decode_kernel"] == "paged_kernel"
+
+
 # ---------------------------------------------------------------- refusals
 def test_refusals():
     ctx = dense(64, 4, 2, 4)
