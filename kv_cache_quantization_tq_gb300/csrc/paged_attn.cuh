@@ -34,7 +34,7 @@
 //   two pages a step up to d = 128, their products with V in one chain           163       494
 //   every lane copies its own 16-byte pieces (TMA needs its operands in uniform registers: 62 instructions a page)  153  435
 //   with up to 4 heads per KV head, both parts of the weights in the 8 columns of one product (24 -> 16 products a page)  137  416
-//   predicates in place of branches                                              131       402
+//   predicates in place of branches, one test of the references per head         130       402
 // Codes need no ldmatrix: a lane loads the codes of its own rows, of keys 32 dims in one place, of values D / 8 dims of 4
 // tokens, whose nibbles are paired by token before they are converted.  What is left: 65% of the issue slots with 3 warps per
 // scheduler (16 warps of 128 registers spill: 151 us); loading codes earlier, or more products abreast, changed nothing.
@@ -58,7 +58,7 @@
 // second reference per head, a power of two, holds the largest of these below 2^15 and, when it is set, at 2^12.  What
 // the parts leave out is 2^-37 of the largest token's share.
 //   Weights alone (kWeights) keep a score's whole error, so there every product of 16 dims leaves the tensor core and is added by
-// fp32 additions (4-bit keys: not needed, 5e-7 of the result), and beside fp16 keys the queries have two parts, of 5 and 6 bits:
+// fp32 additions (4-bit keys: every four products; 16 of them at d = 512 were up to 1.8e-6 of the result off, four 7e-7), and beside fp16 keys the queries have two parts, of 5 and 6 bits:
 // products of 16 bits lie within what the tensor core keeps of a sum, ones of 22 are cut, all in one direction (1 x 4K
 // tokens of 16 / 4 heads: 1.2e-6 of the result, 8e-7 in parts).
 //   bf16 queries on these pages are scaled by a power of two per head into fp16's range (exact down to 2^-31 of the
@@ -854,7 +854,7 @@ __global__ void __launch_bounds__(PagedCfg<KIND, D, N8, MODE>::THREADS, 1)
   // Scores of the 16 tokens of a page as the tensor core gives them: rows tok0 and tok0 + 8, heads 2 t and 2 t + 1.  kb: the keys
   // in shared memory, tail: the scales of 4-bit pages.
   auto scores = [&](uint32_t kb, uint32_t tail, float(&s)[NT][4]) {
-    float s2[NT][4], sl[NT][4];
+    float s2[NT][4], sl[NT][4], four[NT][4];
     auto score = [&](int ks, const uint32_t(&af)[4], float(&acc)[NT][4]) {
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
@@ -873,6 +873,10 @@ __global__ void __launch_bounds__(PagedCfg<KIND, D, N8, MODE>::THREADS, 1)
           mma_first<BF>(one, af, x.x, x.y);
 #pragma unroll
           for (int k = 0; k < 4; ++k) acc[nt][k] += one[k];
+        } else if (C::KEYS && ks >= 8 && ks % 8 < 2) {  // from 4-bit keys it cuts little: sums of 4 products are left to it
+#pragma unroll
+          for (int k = 0; k < 4; ++k) four[nt][k] = ks == 8 ? acc[nt][k] : four[nt][k] + acc[nt][k];
+          mma_first<BF>(acc[nt], af, x.x, x.y);
         } else if (ks < 2) {
           mma_first<BF>(acc[nt], af, x.x, x.y);
         } else {
@@ -931,6 +935,7 @@ __global__ void __launch_bounds__(PagedCfg<KIND, D, N8, MODE>::THREADS, 1)
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
         s[nt][k] += s2[nt][k];
+        if (C::KEYS && F4 && KS > 8) s[nt][k] += four[nt][k];
         // an infinite key times a part that is 0 is no number, and the first part has said what it is
         if (C::QPARTS == 2) s[nt][k] = fabsf(s[nt][k]) < CUDART_INF_F ? s[nt][k] + sl[nt][k] : s[nt][k];
       }
