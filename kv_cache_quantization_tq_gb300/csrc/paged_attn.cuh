@@ -29,7 +29,8 @@
 //
 // 4-bit pages (and weights alone) are bound by instructions: a page of d = 128 has 2.3 KB for the 4 KB of e4m3, and as many
 // elements to be made fp16 (code x scale, exact: one conversion and one multiplication per two, 128 a lane and page).  What was
-// taken off the rest, on 64 ragged sequences of 32 / 8 heads (614 MB, 92 us at the copy rate):
+// taken off the rest, on 64 ragged sequences of 32 / 8 heads (614 MB, 92 us at the copy rate; replayed graphs, 3 us
+// above the kernels' own time):
 //   one page a step, TMA, like e4m3                                             172 us, 538 warp instructions a page
 //   two pages a step up to d = 128, their products with V in one chain           163       494
 //   every lane copies its own 16-byte pieces (TMA needs its operands in uniform registers: 62 instructions a page)  153  435
@@ -58,9 +59,9 @@
 // second reference per head, a power of two, holds the largest of these below 2^15 and, when it is set, at 2^12.  What
 // the parts leave out is 2^-37 of the largest token's share.
 //   Weights alone (kWeights) keep a score's whole error, so there every product of 16 dims leaves the tensor core and is added by
-// fp32 additions (4-bit keys: every four products; 16 of them at d = 512 were up to 1.8e-6 of the result off, four 7e-7), and beside fp16 keys the queries have two parts, of 5 and 6 bits:
-// products of 16 bits lie within what the tensor core keeps of a sum, ones of 22 are cut, all in one direction (1 x 4K
-// tokens of 16 / 4 heads: 1.2e-6 of the result, 8e-7 in parts).
+// fp32 additions (4-bit keys: every four products; sums of 16 at d = 512 were up to 1.8e-6 of the result off, of four 7e-7).
+// Beside fp16 keys the queries have two parts, of 5 and 6 bits: products of 16 bits lie within what the tensor core keeps of
+// a sum, ones of 22 are cut, all in one direction (1 x 4K tokens of 16 / 4 heads: 1.2e-6 of the result, 8e-7 in parts).
 //   bf16 queries on these pages are scaled by a power of two per head into fp16's range (exact down to 2^-31 of the
 // head's largest entry); half of its inverse comes before a key's exponent and half behind it, so that large
 // keys with small queries do not overflow on the way.
