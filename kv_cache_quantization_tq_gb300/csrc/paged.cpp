@@ -20,8 +20,8 @@ bool aligned16(const void* p) { return (((uintptr_t)p) & 15) == 0; }
 
 // Checks that attention and weight sums share, and the arguments they share.
 tq_status paged_args(tq_ctx* ctx, const void* q, int64_t q_stride, int batch, const void* pool, int num_blocks,
-                            const int32_t* block_table, int max_blocks, const int32_t* lengths, int window, float scale,
-                            float cap, const float* slopes, tq::PagedArgs& a, tq::ScoreArgs& sc) {
+                     const int32_t* block_table, int max_blocks, const int32_t* lengths, int window, float scale,
+                     float cap, const float* slopes, tq::PagedArgs& a, tq::ScoreArgs& sc) {
   const tq_config& c = ctx->cfg;
   if (scale == 0.f) scale = (float)(1.0 / sqrt((double)c.head_dim));
   // far caps would leave scale / cap, or the tanh, without bits
@@ -110,10 +110,10 @@ cudaError_t launch_weights(tq_ctx* ctx, const PagedArgs& a, const ScoreArgs& sc,
     const cudaError_t e = launch_fade(ctx, a, w, s);
     if (e != cudaSuccess) return e;
   }
-  return c.key_bits == 4                    ? launch_weights_e2m1(ctx, a, sc, w, s)
-         : c.key_bits == 8                  ? launch_weights_e4m3(ctx, a, sc, w, s)
-         : c.key_format == TQ_ELEM_BF16     ? launch_weights_bf16(ctx, a, sc, w, s)
-                                            : launch_weights_f16(ctx, a, sc, w, s);
+  return c.key_bits == 4                ? launch_weights_e2m1(ctx, a, sc, w, s)
+         : c.key_bits == 8              ? launch_weights_e4m3(ctx, a, sc, w, s)
+         : c.key_format == TQ_ELEM_BF16 ? launch_weights_bf16(ctx, a, sc, w, s)
+                                        : launch_weights_f16(ctx, a, sc, w, s);
 }
 
 }  // namespace tq
