@@ -35,7 +35,7 @@
 //   two pages a step up to d = 128, their products with V in one chain           163       494
 //   every lane copies its own 16-byte pieces (TMA needs its operands in uniform registers: 62 instructions a page)  153  435
 //   with up to 4 heads per KV head, both parts of the weights in the 8 columns of one product (24 -> 16 products a page)  137  416
-//   predicates in place of branches, one test of the references per head         130       402
+//   predicates in place of branches, one test of the references per head         130       399
 // Codes need no ldmatrix: a lane loads the codes of its own rows, of keys 32 dims in one place, of values D / 8 dims of 4
 // tokens, whose nibbles are paired by token before they are converted.  What is left: 65% of the issue slots with 3 warps per
 // scheduler (16 warps of 128 registers spill: 151 us); loading codes earlier, or more products abreast, changed nothing.

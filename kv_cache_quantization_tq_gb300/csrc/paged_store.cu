@@ -177,7 +177,7 @@ __global__ void __launch_bounds__(kStoreThreads) store_kernel(const StoreArgs a,
 }
 
 // 4 bits: a thread has two blocks of 16 of a vector, so that what it does once per vector is shared by them (32768 tokens x 8
-// heads x 128: 34.8 us; one block a thread 39.1, two vectors a thread 35.1).  What bounds it is instructions, about 100 per
+// heads x 128: 34.8 us; one block a thread 39.1, two vectors a thread 35.1).  What bounds it is instructions, 180 per
 // block: 16 entries unpacked, scaled, rounded and signed one by one.
 template <int D, bool BF>
 __global__ void __launch_bounds__(kStoreThreads) store4_kernel(const StoreArgs a, const Divisor rows) {
