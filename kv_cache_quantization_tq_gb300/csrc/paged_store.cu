@@ -47,6 +47,15 @@ __device__ __forceinline__ float2 pair_of(uint32_t w) {
   return __half22float2(*reinterpret_cast<const __half2*>(&w));
 }
 
+// The larger magnitudes of two pairs; NaN where there is one.
+template <bool BF>
+__device__ __forceinline__ uint32_t max_magnitudes(uint32_t x, uint32_t y) {
+  uint32_t r;
+  if (BF) asm("{ .reg .b32 a; abs.bf16x2 a, %2; max.NaN.bf16x2 %0, %1, a; }" : "=r"(r) : "r"(x), "r"(y));
+  else asm("{ .reg .b32 a; abs.f16x2 a, %2; max.NaN.f16x2 %0, %1, a; }" : "=r"(r) : "r"(x), "r"(y));
+  return r;
+}
+
 // Magnitudes of a pair's entries with the ones that are not finite as 0.
 template <bool BF>
 __device__ __forceinline__ uint32_t finite_bits(uint32_t w) {
@@ -177,7 +186,7 @@ __global__ void __launch_bounds__(kStoreThreads) store_kernel(const StoreArgs a,
 }
 
 // 4 bits: a thread has two blocks of 16 of a vector, so that what it does once per vector is shared by them (32768 tokens x 8
-// heads x 128: 34.8 us; one block a thread 39.1, two vectors a thread 35.1).  What bounds it is instructions, 180 per
+// heads x 128: 33.5 us as replayed graphs, 31.0 by itself; one block a thread 39.1, two vectors a thread 35.1).  What bounds it is instructions, 180 per
 // block: 16 entries unpacked, scaled, rounded and signed one by one.
 template <int D, bool BF>
 __global__ void __launch_bounds__(kStoreThreads) store4_kernel(const StoreArgs a, const Divisor rows) {
@@ -201,7 +210,7 @@ __global__ void __launch_bounds__(kStoreThreads) store4_kernel(const StoreArgs a
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       w[b][i] = y[i];
-      m[b] = __vmaxu2(m[b], y[i] & 0x7fff7fffu);
+      m[b] = max_magnitudes<BF>(m[b], y[i]);
     }
     all[b] = m[b] = max(m[b] & 0xffffu, m[b] >> 16);
   }
