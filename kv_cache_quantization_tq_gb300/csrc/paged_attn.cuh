@@ -1454,9 +1454,10 @@ __global__ void __launch_bounds__(PagedCfg<KIND, D, N8, MODE>::THREADS, 1)
             }
 #pragma unroll
             for (int pg = 0; pg < PP; ++pg) {
-              // what a token's weight at its values has besides: 2^-8 and their exponent
+              // What a token's weight at its values has besides: the head's reference with 2^-8, then the values' exponent.  Those two
+              // alone can pass 2^127, for a token of little weight and large values; a weight times the reference cannot (2^8 2^92).
 #pragma unroll
-              for (int k = 0; k < 4; ++k) p[pg][nt][k] = p[pg][nt][k] * (power2(ev[pg][k >> 1]) * (kDown * vr[nt][k & 1]));
+              for (int k = 0; k < 4; ++k) p[pg][nt][k] = p[pg][nt][k] * (kDown * vr[nt][k & 1]) * power2(ev[pg][k >> 1]);
 #pragma unroll
               for (int x = 0; x < 2; ++x) {
                 const uint32_t a1 = take_part<false>(p[pg][nt][2 * x], p[pg][nt][2 * x + 1]);
