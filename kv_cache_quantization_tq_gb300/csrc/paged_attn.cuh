@@ -1020,7 +1020,11 @@ __global__ void __launch_bounds__(PagedCfg<KIND, D, N8, MODE>::THREADS, 1)
         const int hi = QUAD ? (2 * t + i) & 3 : nt * 8 + 2 * t + i;
         if (MODE != kAttend) slope[nt][i] = w.slopes && hi < nh ? w.slopes[head0 + hi] * (C::KEYS ? 1.f : kLog2e) : 0.f;
         if (C::KEYS) {  // in two parts; -inf, of a row without weights, makes them 0
-          const float x = hi < nh ? w.lse_in[(int64_t)out.b * a.hq + head0 + hi] : CUDART_INF_F;
+          float x = hi < nh ? w.lse_in[(int64_t)out.b * a.hq + head0 + hi] : CUDART_INF_F;
+          if (x != x) {  // NaN goes into the scores, where it is replaced for tokens that do not count
+            qs[nt][i] = x;
+            x = 0.f;
+          }
           lse_hi[nt][i] = x == -CUDART_INF_F ? CUDART_INF_F : x * kLog2e;
           lse_lo[nt][i] = fabsf(lse_hi[nt][i]) < CUDART_INF_F ? fmaf(x, kLog2eLow, fmaf(x, kLog2e, -lse_hi[nt][i])) : 0.f;
         }
