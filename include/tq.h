@@ -470,7 +470,7 @@ tq_status tq_paged_attention_scored(tq_ctx* ctx, const void* q, int64_t q_stride
  *   weights_out[b][kvh][p] = decay * weights[b][kvh][p] + sum over the query heads h of kvh of exp(z_hp - lse[b][h])
  * for p < lengths[b], z as in tq_paged_attention_scored (0 for p in front of the window); entries from lengths[b] on are left as
  * they were.  Reads the keys alone.  Arguments as there, and
- *   lse          device float32 [batch][Hq], what the attention call gave (-inf: the row's weights are 0)
+ *   lse          device float32 [batch][Hq], what the attention call gave (-inf: the row's weights are 0, whatever the keys are)
  *   weights      device float32 [batch][Hkv][weights_stride], NULL for zeros; weights_out: likewise, the same array or one
  *                that does not overlap it
  *   decay        any finite number

@@ -948,6 +948,7 @@ __global__ void __launch_bounds__(PagedCfg<KIND, D, N8, MODE>::THREADS, 1)
     const int kvh = kv_head(w.p, out.hg), h0 = C::KEYS ? w.first : (out.hg - kvh * w.p.groups) * C::HEADS;
     const int nh = min(C::HEADS, a.n_rep - h0);
     const int64_t head0 = (int64_t)kvh * a.n_rep + h0;
+    bool bare = false;  // weights alone: a head's lse is -inf, it has no weights
     // ---- queries as B fragments: head g, dims 16 ks + 2 t, + 1 and + 8, + 9 (8-bit pages: 4 t .. 4 t + 3,
     // the order in which ldmatrix hands out the bytes of a key row)
 #pragma unroll
@@ -1021,6 +1022,7 @@ __global__ void __launch_bounds__(PagedCfg<KIND, D, N8, MODE>::THREADS, 1)
         if (MODE != kAttend) slope[nt][i] = w.slopes && hi < nh ? w.slopes[head0 + hi] * (C::KEYS ? 1.f : kLog2e) : 0.f;
         if (C::KEYS) {  // in two parts; -inf, of a row without weights, makes them 0
           float x = hi < nh ? w.lse_in[(int64_t)out.b * a.hq + head0 + hi] : CUDART_INF_F;
+          bare |= x == -CUDART_INF_F;
           if (x != x) {  // NaN goes into the scores, where it is replaced for tokens that do not count
             qs[nt][i] = x;
             x = 0.f;
@@ -1032,6 +1034,33 @@ __global__ void __launch_bounds__(PagedCfg<KIND, D, N8, MODE>::THREADS, 1)
         vr[nt][i] = power2(kValueTop);
         most[nt][i] = kValueMost + kLazy - kValueTop;
         l[nt][i] = lost[nt][i] = 0.f;
+      }
+    }
+    // A score that is not finite must not meet such a head's lse.  Beside 16-bit keys each is replaced; beside the others, of which
+    // only NaN can come, the query becomes 0, and where no head has weights no position counts.  (64 ragged sequences, 4-bit keys:
+    // with any choice in the loop 80 us and more, so 76.5.)
+    uint32_t full = (1u << PP) - 1;
+    int seen_from = out.s.lo;
+    if constexpr (C::KEYS && C::ES == 1) {
+      if (__any_sync(kFull, bare)) {
+        bool none = true;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          const float x = __shfl_sync(kFull, lse_hi[nt][0], g >> 1), y = __shfl_sync(kFull, lse_hi[nt][1], g >> 1);
+          if ((g & 1 ? y : x) == CUDART_INF_F) {
+#pragma unroll
+            for (int ks = 0; ks < KS; ++ks) {
+              if constexpr (C::QREG) qf[nt][ks][0] = qf[nt][ks][1] = 0;
+              else q_sm[(nt * KS + ks) * 32 + lane] = make_uint2(0, 0);
+            }
+          } else {
+            none = false;
+          }
+        }
+        if (__all_sync(kFull, none)) {
+          full = 4;  // no page is whole
+          seen_from = 0x7fffffff;
+        }
       }
     }
     // pages of the segment that the sequence's end or the window cuts
@@ -1310,10 +1339,10 @@ __global__ void __launch_bounds__(PagedCfg<KIND, D, N8, MODE>::THREADS, 1)
           scores(stage0 + st * C::PAGE + pg * C::PAGE1, tail, s[pg]);
         }
         if (C::KEYS) next_pages();  // the keys are read
-        const bool whole = here == (1u << PP) - 1 && rel != cut_first && rel != cut_last && (PP == 1 || (rel2 != cut_first && rel2 != cut_last));
+        const bool whole = here == full && rel != cut_first && rel != cut_last && (PP == 1 || (rel2 != cut_first && rel2 != cut_last));
         auto counts = [&](int pg, int tok) {
           const int x = first + pg * on + tok;
-          return x >= out.s.lo && x < out.s.len && (here >> pg & 1);
+          return x >= seen_from && x < out.s.len && (here >> pg & 1);
         };
 #pragma unroll
         for (int pg = 0; pg < PP; ++pg) {
@@ -1363,8 +1392,8 @@ __global__ void __launch_bounds__(PagedCfg<KIND, D, N8, MODE>::THREADS, 1)
             for (int k = 0; k < 4; ++k)
 #pragma unroll
               for (int pg = 0; pg < PP; ++pg) {
-                // heads that are none have lse inf and scores 0, but of a 16-bit key that is infinite
-                const float z = C::ES == 1 || nt * 8 + 2 * t + (k & 1) < nh ? s[pg][nt][k] : 0.f;
+                // heads without weights, and heads that are none, have lse inf
+                const float z = C::ES == 2 && lse_hi[nt][k & 1] == CUDART_INF_F ? 0.f : s[pg][nt][k];
                 sum[2 * pg + (k >> 1)] += ex2(fmaf(z, up_lo, fmaf(z, up_hi, -lse_hi[nt][k & 1])) - lse_lo[nt][k & 1]);
               }
           // lane t gets the total of sum[t] over the four lanes

@@ -1,4 +1,4 @@
-"""Weight sums where a log-sum-exp is NaN: what gets no weight keeps its sum."""
+"""Weight sums where a log-sum-exp is NaN or -inf: what gets no weight keeps its sum."""
 import pytest
 import torch
 
@@ -12,7 +12,7 @@ if torch.cuda.is_available():
 
     build()
     from test_gpu_paged import attend
-    from test_gpu_small_cache import add_weights, weights_case
+    from test_gpu_small_cache import add_weights, rewrite, slopes_of, weights_case
 
 
 @pytest.fixture(autouse=True)
@@ -50,3 +50,26 @@ def test_a_nan_reaches_only_tokens_that_count(hq, hkv, d, bits, bf16, cap):
             others = [x for x in range(hkv) if x != h // rep]
             for b, n in enumerate(e["lengths"]):
                 assert torch.equal(got[b, others, :n], ref[b, others, :n])
+
+
+@pytest.mark.parametrize("bits,bf16", ALL)
+@pytest.mark.parametrize("cap,biased", [(0.0, False), (20.0, True)])
+def test_a_row_without_weights_adds_nothing_whatever_its_keys_hold(cap, biased, bits, bf16):
+    """A log-sum-exp of -inf against keys that are NaN and infinite (8- and 4-bit pages: as large as they get)."""
+    e = weights_case(17, [50, 20], 6, 2, 64, bits, bf16)
+    s = slopes_of(6) if biased else None
+    k = torch.randn(50, 2, 64)
+    k[3, 0, 5], k[20, 0], k[21, 0], k[40, 1, 1] = float("nan"), float("inf"), float("-inf"), float("inf")
+    rewrite(e, 0, k, torch.randn(50, 2, 64))
+    lse = torch.zeros(2, 6, device="cuda")
+    lse[0, :3] = -float("inf")
+    got = add_weights(e, lse, decay=0.5, cap=cap, slopes=s)
+    assert e["ctx"].device_errors() == 0
+    assert torch.equal(got[0, 0, :50], 0.5 * e["before"][0, 0, :50].cuda())
+    # beside a head that has weights the others still add nothing
+    lse[0, :3] = torch.tensor([-float("inf"), 0.0, -float("inf")])
+    one = add_weights(e, lse, decay=0.5, cap=cap, slopes=s, before=False)
+    lse[0, :3] = torch.tensor([float("inf"), 0.0, float("inf")])
+    ref = add_weights(e, lse, decay=0.5, cap=cap, slopes=s, before=False)
+    finite = torch.isfinite(ref[0, 0, :50])
+    assert int(finite.sum()) >= 45 and torch.equal(one[0, 0, :50][finite], ref[0, 0, :50][finite])
