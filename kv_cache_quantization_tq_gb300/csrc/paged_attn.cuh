@@ -455,7 +455,7 @@ __device__ __forceinline__ void tf32_parts(float x, uint32_t& high, uint32_t& lo
 
 // cap tanh x of N values, for a whole warp.  Below 0.9 in magnitude tanh x = x + x y P(y), y = x^2, P fitted to
 // (tanh x / x - 1) / y with a relative error of 1.6e-8; above 1 - 2 / (e^2x + 1), where little cancels (e^2x may be
-// infinite).  Within 2.2e-7 of the result (8e-8 below 0.9).  Scores are mostly far below the cap: the second form is left
+// infinite).  Within 2.7e-7 of the result by the roundings of its steps (1.3e-7 below 0.9, evaluated 9e-8).  Scores are mostly far below the cap: the second form is left
 // out where no lane needs it.
 template <int N>
 __device__ __forceinline__ void cap_scores(float (&x)[N], float cap) {
