@@ -459,7 +459,7 @@ tq_status tq_paged_attention(tq_ctx* ctx, const void* q, int64_t q_stride, int b
 
 /* tq_paged_attention with other scores: z = scale * q . k_p, then with cap > 0 z = cap * tanh(z / cap), then with slopes (device
  * float32 [Hq], NULL: none) z += slopes[h] * (p - (L - 1)), which is 0 at the new token.  out and lse are those of z.  cap 0 and
- * no slopes: tq_paged_attention.  cap: 0, or in [2^-60, 2^60].  p counts the sequence's slots: behind tq_paged_evict the
+ * no slopes: tq_paged_attention.  cap: 0, or in [2^-60, 2^60] with |scale| / cap in [2^-66, 2^66].  p counts the sequence's slots: behind tq_paged_evict the
  * distance (and the window) is one in the tokens that are left. */
 tq_status tq_paged_attention_scored(tq_ctx* ctx, const void* q, int64_t q_stride, int batch, const void* pool, int num_blocks,
                                     const int32_t* block_table, int max_blocks, const int32_t* lengths, int window,

@@ -24,8 +24,9 @@ tq_status paged_args(tq_ctx* ctx, const void* q, int64_t q_stride, int batch, co
                      float cap, const float* slopes, tq::PagedArgs& a, tq::ScoreArgs& sc) {
   const tq_config& c = ctx->cfg;
   if (scale == 0.f) scale = (float)(1.0 / sqrt((double)c.head_dim));
-  // far caps would leave scale / cap, or the tanh, without bits
-  if (!isfinite(scale) || !(cap == 0.f || (cap >= 0x1p-60f && cap <= 0x1p60f && isfinite(scale / cap)))) return TQ_ERR_INVALID_ARG;
+  // Far caps would leave the tanh, or scale / cap, without bits: beside 8- and 4-bit pages up to 2^63 of a bf16 query's size joins that factor.
+  const float ratio = cap > 0.f ? fabsf(scale / cap) : 1.f;
+  if (!isfinite(scale) || !(cap == 0.f || (cap >= 0x1p-60f && cap <= 0x1p60f)) || !(ratio >= 0x1p-66f && ratio <= 0x1p66f)) return TQ_ERR_INVALID_ARG;
   if (batch == 0) return TQ_OK;
   if (!q || !lengths || (max_blocks > 0 && !block_table) || (num_blocks > 0 && !pool)) return TQ_ERR_INVALID_ARG;
   if (!aligned16(q) || !aligned16(pool) || (q_stride & 7) || q_stride < (int64_t)c.num_q_heads * c.head_dim)

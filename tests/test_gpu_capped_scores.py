@@ -73,3 +73,27 @@ def test_capped_scores_are_exact_to_the_tanh(cap, scale, bits, bf16):
         err, tol = np.abs(w[:, :, 0].double().cpu().numpy() - ref), np.abs(z) * E + 2.0 ** -21
         assert np.all(err <= tol), f"weight sums: {np.max(err / tol):.3g} of the bound"
     assert ctx.device_errors() == 0
+
+
+@pytest.mark.parametrize("bits,bf16", ALL)
+def test_factors_far_from_the_cap_are_refused(bits, bf16):
+    """Where scale / cap has no bits left in fp32 every score would be 0, or 0 times infinity."""
+    import kv_cache_quantization_tq_gb300 as tq
+
+    ctx = dense(64, 2, 1, bits, bf16)
+    pool = torch.zeros(1, 1, ctx.page_bytes, dtype=torch.uint8, device="cuda")
+    table, lens = i32([[0]]), i32([5])
+    q, out, lse = torch.ones(1, 2, 64, dtype=elem(bf16), device="cuda"), torch.zeros(1, 2, 64, device="cuda"), torch.zeros(1, 2, device="cuda")
+    ws, w = torch.zeros(ctx.paged_workspace_size(1), dtype=torch.uint8, device="cuda"), torch.zeros(1, 1, 16, device="cuda")
+    for cap, scale, ok in ((2.0 ** 60, 2.0 ** -90, False), (2.0 ** 60, -2.0 ** -90, False), (2.0 ** 60, 2.0 ** -7, False), (2.0 ** 60, 2.0 ** -6, True),
+                           (2.0 ** -60, 2.0 ** 7, False), (2.0 ** -60, -2.0 ** 80, False), (2.0 ** -60, 2.0 ** 6, True), (1.0, 2.0 ** -66, True),
+                           (1.0, 2.0 ** 66, True), (1.0, 2.0 ** 67, False)):
+        for call in (lambda: ctx.paged_attention(q, pool, table, lens, out, ws, lse=lse, scale=scale, cap=cap),
+                     lambda: ctx.paged_weights(q, pool, table, lens, lse, w, scale=scale, cap=cap)):
+            if ok:
+                call()
+            else:
+                with pytest.raises(tq.TQError) as x:
+                    call()
+                assert x.value.status == tq.binding.TQ_ERR_INVALID_ARG
+    assert ctx.device_errors() == 0 and torch.isfinite(out).all() and torch.isfinite(w).all()
