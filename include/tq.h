@@ -469,7 +469,8 @@ tq_status tq_paged_attention_scored(tq_ctx* ctx, const void* q, int64_t q_stride
 /* The attention weights of one new token per sequence, added up per cached token and KV head:
  *   weights_out[b][kvh][p] = decay * weights[b][kvh][p] + sum over the query heads h of kvh of exp(z_hp - lse[b][h])
  * for p < lengths[b], z as in tq_paged_attention_scored (0 for p in front of the window); entries from lengths[b] on are left as
- * they were.  Reads the keys alone.  Arguments as there, and
+ * they were.  A token's sum goes on from what its entry holds: entries that a sequence has not reached have to be 0 before it grows
+ * into them, also where a request takes over the row of another one.  Reads the keys alone.  Arguments as there, and
  *   lse          device float32 [batch][Hq], what the attention call gave (-inf: the row's weights are 0, whatever the keys are)
  *   weights      device float32 [batch][Hkv][weights_stride], NULL for zeros; weights_out: likewise, the same array or one
  *                that does not overlap it
@@ -490,7 +491,9 @@ tq_status tq_paged_weights(tq_ctx* ctx, const void* q, int64_t q_stride, int bat
  *   weights      device float32 [batch][Hkv][weights_stride] (tq_paged_weights); weights_stride at most 2^30
  *   pool, block_table  as for tq_paged_attention; the pool is changed in place, so no page may belong to two sequences
  *   lengths, keep      device int32 [batch]
- *   weights_out  as weights, another array: entries 0 .. K - 1 are those of the kept tokens, K .. L - 1 become 0
+ *   weights_out  as weights, another array: entries 0 .. K - 1 are those of the kept tokens, K .. L - 1 become 0, and what
+ *                is behind stays: a buffer that an earlier call read has to be cleared before it is written here, if the
+ *                sequence then grows beyond L
  *   lengths_out  device int32 [batch]: K
  *   kept         device int32 [batch][Hkv][weights_stride]: entries 0 .. K - 1 are the slots that the tokens come from
  * Slots K .. L - 1 of the pages are no longer defined.  Keys are moved as they are, with the positions that were worked into
