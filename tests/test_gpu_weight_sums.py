@@ -1,4 +1,4 @@
-"""Weight sums where a log-sum-exp is NaN or -inf: what gets no weight keeps its sum."""
+"""Weight sums: what gets no weight keeps its sum, also where a log-sum-exp is NaN or -inf; the roundings of a score."""
 import pytest
 import torch
 
@@ -73,3 +73,25 @@ def test_a_row_without_weights_adds_nothing_whatever_its_keys_hold(cap, biased, 
     ref = add_weights(e, lse, decay=0.5, cap=cap, slopes=s, before=False)
     finite = torch.isfinite(ref[0, 0, :50])
     assert int(finite.sum()) >= 45 and torch.equal(one[0, 0, :50][finite], ref[0, 0, :50][finite])
+
+
+@pytest.mark.parametrize("d", [64, 128, 256, 512])
+def test_fp16_scores_are_rounded_once(d):
+    """A score of 1024 and two small parts, each less than half a step of it: one in a product of its own, one in the bits behind a
+    query entry's first five.  Together they count: the score is off by half a step of 1024 (2^-14), the exponential by 2^-21."""
+    gen = torch.Generator().manual_seed(d)
+    n, step = 96, 2.0 ** -13
+    a, b = 0.3 + 0.19 * torch.rand(n, generator=gen), 0.3 + 0.19 * torch.rand(n, generator=gen)
+    sign = torch.where(torch.arange(n) % 2 == 0, 1.0, -1.0)
+    k = torch.zeros(n, 1, d)
+    k[:, 0, 0] = 32.0
+    k[:, 0, 16] = sign * a * step * 128
+    k[:, 0, 17] = k[:, 0, 18] = sign * b * step * 128
+    e = weights_case(d, [n], 1, 1, d, 16, False)
+    rewrite(e, 0, k, torch.zeros(n, 1, d))
+    e["q"][:] = 0
+    e["q"][0, 0, 0], e["q"][0, 0, 16], e["q"][0, 0, 17], e["q"][0, 0, 18] = 32.0, 2.0 ** -7, 1 + 2.0 ** -7, -1.0
+    got = add_weights(e, torch.full((1, 1), 1024.0, device="cuda"), before=False, scale=1.0)[0, 0, :n].double().cpu()
+    z = (k[:, 0].half().double() * e["q"][0, 0].double()).sum(1) - 1024
+    assert (z.abs() > 0.6 * step).all()
+    assert ((got - torch.exp(z)).abs() <= 2.0 ** -14 * (1 + 2.0 ** -10) + 2.0 ** -21).all()
