@@ -449,15 +449,15 @@ tq_status tq_paged_workspace_size(const tq_ctx* ctx, int batch, size_t* bytes);
  * TQ_DEVERR_TIMEOUT, and the rows it has a part in become NaN.  A NaN or an infinity in a row that counts makes
  * what depends on it NaN (weights are multiplied in parts).  Sums are held in 32 bits: they overflow where the
  * number of positions times the largest |value| passes 2^127, and weights below about 2^-100 of a row's largest and values
- * whose vector is below about 2^-100 (8-bit pages: 2^-78, 4-bit pages: 2^-75) count with fewer bits or not at all.  On 8- and 4-bit pages a position counts to within 2^-36 of the
- * row's largest weight times |value|, and a bf16 query entry to within 2^-39 of its head's largest.  num_blocks * Hkv must be below 2^31.  The current device
+ * whose vector is below about 2^-100 (8-bit pages: 2^-78, 4-bit pages: 2^-75) count with fewer bits or not at all.  On 8-bit pages a position counts to within 2^-36 of the
+ * row's largest weight times |value| (4-bit pages: 2^-35), and on both a bf16 query entry to within 2^-39 of its head's largest.  num_blocks * Hkv must be below 2^31.  The current device
  * must be the context's (TQ_ERR_INVALID_ARG), here and in the two calls above. */
 tq_status tq_paged_attention(tq_ctx* ctx, const void* q, int64_t q_stride, int batch, const void* pool, int num_blocks,
                              const int32_t* block_table, int max_blocks, const int32_t* lengths, int window,
                              float scale, float* out, float* lse, void* workspace, size_t ws_bytes,
                              cudaStream_t stream);
 
-/* tq_paged_attention with other scores: z = scale * q . k_p, then with cap > 0 z = cap * tanh(z / cap), then with slopes (device
+/* tq_paged_attention with other scores: z = scale * q . k_p, then with cap > 0 z = cap * tanh(z / cap) (within 2.7e-7 of it), then with slopes (device
  * float32 [Hq], NULL: none) z += slopes[h] * (p - (L - 1)), which is 0 at the new token.  out and lse are those of z.  cap 0 and
  * no slopes: tq_paged_attention.  cap: 0, or in [2^-60, 2^60] with |scale| / cap in [2^-66, 2^66].  p counts the sequence's slots: behind tq_paged_evict the
  * distance (and the window) is one in the tokens that are left. */
@@ -476,8 +476,8 @@ tq_status tq_paged_attention_scored(tq_ctx* ctx, const void* q, int64_t q_stride
  *                that does not overlap it
  *   decay        any finite number
  * A length beyond weights_stride or the block table, or negative, counts as 0 with TQ_DEVERR_POSITION; tokens of a page whose
- * id is outside [0, num_blocks) get no weight, with TQ_DEVERR_BLOCK_ID.  A NaN in a key, query or lse makes the sums that
- * depend on it NaN.  Needs no workspace. */
+ * id is outside [0, num_blocks) get no weight, with TQ_DEVERR_BLOCK_ID.  Weights below 2^-126 are 0.  A NaN in a key, query or lse
+ * makes the sums that depend on it NaN.  Needs no workspace. */
 tq_status tq_paged_weights(tq_ctx* ctx, const void* q, int64_t q_stride, int batch, const void* pool, int num_blocks,
                            const int32_t* block_table, int max_blocks, const int32_t* lengths, int window, float scale,
                            float cap, const float* slopes, const float* lse, const float* weights, float decay,

@@ -11,9 +11,11 @@
 // one barrier per round is all the order that is needed.
 //
 // What bounds it: the tokens that move, read once and written once; in front of that, and for a single sequence all in all,
-// the chain of passes.  64 sequences of 8 heads from 4.2K to 4K tokens, e4m3 (a sixth of the tokens moves, 211 MB, 31 us at
-// the copy rate): 6 us to the weights, 10 to the threshold, 9 to the places, 29 of moves; 1 x 32K to 2K, fp16: 4.5, 7, 5.5
-// and 7 us.
+// the chain of passes.  64 sequences of 8 heads from 4.2K to 4K tokens as replayed graphs, 3 us above the kernel's own time:
+//   many equal sums, so that the newest of them go and a sixth of the tokens moves   e4m3 62 us (31.5 at the copy rate), 16 bits 89 (59), 4 bits 48 (19)
+//   sums that are all different: nearly all tokens move                              e4m3 208 (162), 16 bits 364 (318), 4 bits 132 (94)
+// The first of these by phases: 6 us to the weights, 10 to the threshold, 9 to the places, 29 of moves; 1 x 32K to 2K, fp16
+// (23 us): 4.5, 7, 5.5 and 7.
 #include <cooperative_groups.h>
 
 #include "common.cuh"
@@ -443,8 +445,10 @@ cudaError_t launch_evict_t(tq_ctx* ctx, const EvictArgs& a, int ctas, cudaStream
 }
 
 // Rows enough for every multiprocessor twice are CTAs of 256 threads, four resident on each (64 sequences of 8 heads from 4.2K
-// to 4K tokens, e4m3: 67 us, with 512 threads 74); fewer rows are clusters of CTAs of 512, enough for two on every
-// multiprocessor, up to the portable cluster of 8 (1 x 32K to 2K, 8 heads: 26.6 us, with 256 threads 32, with 16 CTAs 29).
+// to 4K tokens, e4m3: 67 us with the return of the pages, with 512 threads 74); fewer rows are clusters of CTAs of 512, enough
+// for two on every multiprocessor, up to the portable cluster of 8 (1 x 32K to 2K, 8 heads, likewise: 26.6 us, with 256 threads 32, with
+// 16 CTAs 29).  The rule looks at the number of rows alone: a CTA with more than kHeld weights reads them from memory in every pass
+// (64 x 32K to 2K, e4m3: 343 us for 678 MB, 101 at the copy rate), and a long row among many short ones ends late.
 template <int BITS, int D>
 cudaError_t launch_evict_rows(tq_ctx* ctx, const EvictArgs& a, cudaStream_t s) {
   const int64_t rows = (int64_t)a.batch * a.hkv;

@@ -627,7 +627,7 @@ static tq_status dequantize_common(tq_ctx* ctx, const void* pool, int num_blocks
                                    const int32_t* n_buf, int batch, int max_tokens, void* k_out, void* v_out, bool bf16,
                                    cudaStream_t stream) {
   if (!ctx || batch < 0 || max_blocks < 0 || num_blocks < 0 || max_tokens < 0) return TQ_ERR_INVALID_ARG;
-  if (ctx->cfg.layout == TQ_LAYOUT_DENSE) return TQ_ERR_UNSUPPORTED;  // dense pages hold the elements already
+  if (ctx->cfg.layout == TQ_LAYOUT_DENSE) return TQ_ERR_UNSUPPORTED;  // materialisation is for the compressed layouts
   if (batch == 0 || max_tokens == 0) return TQ_OK;
   if (!k_out || !v_out || !n_compressed || !block_table || !pool) return TQ_ERR_INVALID_ARG;
   if (n_buf && (!ring_k || !ring_v)) return TQ_ERR_INVALID_ARG;

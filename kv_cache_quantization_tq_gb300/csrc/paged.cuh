@@ -1,5 +1,5 @@
 // Arguments and launchers of the page plan and the dense-layout page kernels
-// (page_plan.cu, paged_store.cu, paged_attn.cu; entry checks in paged.cpp).
+// (page_plan.cu, paged_store.cu, paged_attn.cuh, paged_fade.cu, evict.cu; entry checks in paged.cpp).
 #pragma once
 
 #include <cuda.h>

@@ -27,7 +27,7 @@
 // With tokens and dims on the 16-row side, 8 query heads per KV head fill the 8-column side and no row of the
 // products is padding; the accumulators are d / 4 registers.
 //
-// 4-bit pages (and weights alone) are bound by instructions: a page of d = 128 has 2.3 KB for the 4 KB of e4m3, and as many
+// 4-bit pages (and weights alone) wait for instructions, not for memory: a page of d = 128 has 2.3 KB for the 4 KB of e4m3, and as many
 // elements to be made fp16 (code x scale, exact: one conversion and one multiplication per two, 128 a lane and page).  What was
 // taken off the rest, on 64 ragged sequences of 32 / 8 heads (614 MB, 92 us at the copy rate; replayed graphs, 3 us
 // above the kernels' own time):
@@ -35,11 +35,14 @@
 //   two pages a step up to d = 128, their products with V in one chain           163       494
 //   every lane copies its own 16-byte pieces (TMA needs its operands in uniform registers: 62 instructions a page)  153  435
 //   with up to 4 heads per KV head, both parts of the weights in the 8 columns of one product (24 -> 16 products a page)  137  416
-//   predicates in place of branches, one test of the references per head         130       399
+//   predicates in place of branches, one test of the references per head         131       399
 // Codes need no ldmatrix: a lane loads the codes of its own rows, of keys 32 dims in one place, of values D / 8 dims of 4
-// tokens, whose nibbles are paired by token before they are converted.  What is left: 65% of the issue slots with 3 warps per
-// scheduler (16 warps of 128 registers spill: 151 us); loading codes earlier, or more products abreast, changed nothing.
-// Weights alone: 147 us in the first form, 77 now (51 at the copy rate; the same from fp16 keys 173 of 165).
+// tokens, whose nibbles are paired by token before they are converted.  What is left: no pipe is full (65% of the issue slots, ALU
+// 51%, FMA 39%, tensor cores 21%, DRAM 52%), and the stalls are spread over fixed latencies, the pipes and the choice
+// between warps: chains of dependent instructions with 3 warps per scheduler (16 warps of 128 registers spill: 151 us).  Loading codes
+// earlier, or more products abreast, changed nothing.
+// Weights alone, timed in the same way: 147 us in the first form, 77 now (51 at the copy rate; from e4m3 keys 105 of 86, from bf16
+// and fp16 ones 174 and 178 of 165).
 //
 // Precision: q and k products are exact and summed in fp32.  A weight is split into parts whose products with V are
 // exact.  Each page's sum leaves the tensor core and is added to the running sum by an fp32 addition that rounds to
@@ -131,7 +134,7 @@ struct PagedCfg {
   // 8 x 2 (128 KB) 87.0 and 634, 16 x 1 (128 KB) 88.7 and 644.  e4m3 pages of d = 128, 64 ragged sequences: 16 x 1 (64 KB)
   // 173 us, 16 x 2 (128 KB) 181.
   // (e4m3 at d = 64 with 16 query heads has no registers for 16 warps: 16 92.1 us, 12 87.2.  4-bit pages have them at d = 64 only:
-  // 64 ragged sequences of 4 heads per KV head, d = 64 12 98.6 us, 16 92.3; d = 128 137 and 151.)
+  // 64 ragged sequences of 4 heads per KV head, each when it was tried: d = 64 12 98.6 us, 16 92.3; d = 128 137 and 151.)
   static constexpr int NW = PAGE1 <= 4096 && QREG && (KEYS || KIND != kE2M1 || D == 64) && (NT == 1 || ES == 2) && fits(16, 1) ? 16 : fits(12, 1) ? 12 : fits(8, 1) ? 8 : fits(6, 1) ? 6 : 4;
   static constexpr int S_WANT = (ES == 1 ? 96 : 128) * 1024 / (NW * PAGE);
   static constexpr int S_LEAST = S_WANT > 8 ? 8 : S_WANT > MIN_S ? S_WANT : MIN_S;
@@ -455,8 +458,9 @@ __device__ __forceinline__ void tf32_parts(float x, uint32_t& high, uint32_t& lo
 
 // cap tanh x of N values, for a whole warp.  Below 0.9 in magnitude tanh x = x + x y P(y), y = x^2, P fitted to
 // (tanh x / x - 1) / y with a relative error of 1.6e-8; above 1 - 2 / (e^2x + 1), where little cancels (e^2x may be
-// infinite).  Within 2.7e-7 of the result by the roundings of its steps (1.3e-7 below 0.9, evaluated 9e-8).  Scores are mostly far below the cap: the second form is left
-// out where no lane needs it.
+// infinite).  Within 2.7e-7 of the result by the roundings of its steps (1.3e-7 below 0.9, evaluated 9e-8).  Scores are
+// mostly far below the cap: the second form is left out where no lane needs it (64 ragged sequences, e4m3, cap and slopes: 184 us
+// with scores below 0.9 of the cap, 189 with queries 8 times as large).
 template <int N>
 __device__ __forceinline__ void cap_scores(float (&x)[N], float cap) {
   bool beyond = false;
